@@ -445,6 +445,160 @@ const char *fi_dd_last_error(const fi_dd *ctx);
  * for a null context, FI_EDEVICE if the synchronisation fails. */
 fi_status fi_dd_destroy(fi_dd *ctx);
 
+/* ------------------------------------------------------------------------
+ * Operators of a recurrent block: what a caller that runs its own block
+ * between mixers (FI_MAP_EXTERNAL, fi_layer_red / fi_tiles) or trains one
+ * needs next to the long convolution.  They hold no context: every call takes
+ * its sizes, device pointers and stream, allocates nothing, waits for nothing
+ * and may be captured into a graph.
+ *
+ * Conventions shared by these calls.
+ *  - Tensors are row-major; a row is `channels` contiguous values and rows are
+ *    a pitch (ld_*, in elements, 0 = densely packed) apart, so a tensor may be
+ *    a column slice of a wider one.  Sequences are [T][B][D]: row t*B + b.
+ *  - Types: FI_F32, FI_BF16, FI_F16.  Arithmetic, states, sums and statistics
+ *    are fp32; a value is rounded once, when it is stored.
+ *  - An output may not share an element with an input or another output,
+ *    unless stated (FI_EINVAL); column slices of one tensor are separate.
+ *  - A workspace (256-byte aligned) belongs to one call until its work on the
+ *    stream is done; its contents need no initialisation and do not survive.
+ *  - FI_EINVAL for a bad argument, FI_EDEVICE for a failed launch; nothing is
+ *    launched when FI_EINVAL is returned.  fi_op_last_error() describes the
+ *    calling thread's last failure.
+ * ------------------------------------------------------------------------ */
+enum { FI_F32 = 0, FI_BF16 = 1, FI_F16 = 2 };
+
+/* Message of the calling thread's last failed operator call ("" if none). */
+const char *fi_op_last_error(void);
+
+/* The gated linear recurrence, per batch row b and channel c:
+ *
+ *     z_t = gate_t + bias[c],  d_t = 1 - sigmoid(z_t)  (the decay's complement),
+ *     s_t = (1 - d_t) s_{t-1} + e(d_t) x_t,            y_t = s_t,
+ *
+ * with the input factor e = 1 (PLAIN), d (CONVEX: a running average) or
+ * sqrt(d (2 - d)) (ENERGY: keeps the variance of independent inputs). */
+enum { FI_SCAN_PLAIN = 0, FI_SCAN_CONVEX = 1, FI_SCAN_ENERGY = 2 };
+
+typedef struct fi_scan_desc {
+    int64_t T;             /* positions, >= 0 */
+    int batch, channels;   /* B, D >= 1 */
+    int dtype;             /* of x, gate, y and their gradients */
+    int input;             /* FI_SCAN_* */
+    int64_t ld_x, ld_gate, ld_y;            /* row pitches, elements; 0 = channels */
+    int64_t ld_dy, ld_dx, ld_dgate;
+    int reserved[4];       /* must be zero */
+} fi_scan_desc;
+
+/* Bytes of the states the forward pass keeps for the backward pass (`saved`),
+ * and of the workspace of either pass; 0 for a bad descriptor.  256 means that
+ * the workspace is not used and may be NULL. */
+size_t fi_scan_saved_bytes(const fi_scan_desc *desc);
+size_t fi_scan_workspace_bytes(const fi_scan_desc *desc, int backward);
+
+/* y [T][B][D] and, where not NULL, final [B][D] fp32 (the state after the last
+ * position) and saved (for fi_scan_backward).  bias [D] fp32 or NULL (zeros);
+ * state [B][D] fp32, the state before the first position, or NULL (zeros);
+ * lengths [B] int32 (device) or NULL: row b has positions t < lengths[b] (taken
+ * into [0, T]); later rows are not read, give y = 0 and leave the state as it
+ * is.  final may be state.  T = 1 is the form for one token: one launch. */
+fi_status fi_scan_forward(const fi_scan_desc *desc, const void *x, const void *gate, const float *bias,
+                          const float *state, const int32_t *lengths, void *y, float *final, void *saved,
+                          void *workspace, void *stream);
+
+/* Gradients of sum(y . dy) + sum(final . dfinal): dx, dgate [T][B][D] (0 past a
+ * row's length), and where not NULL dbias [D] fp32 (summed over t and b in a
+ * fixed order) and dstate [B][D] fp32.  The other arguments are those of the
+ * forward call that wrote `saved`; dfinal may be NULL (zeros). */
+fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *gate, const float *bias,
+                           const float *state, const int32_t *lengths, const void *saved, const void *dy,
+                           const float *dfinal, void *dx, void *dgate, float *dbias, float *dstate,
+                           void *workspace, void *stream);
+
+/* The norms around a block, with the block's gate, residual and residual scale,
+ * per row of `channels` values (each factor that is NULL is left out):
+ *
+ *     v = post_norm ? o / sqrt(mean(o^2) + eps) * post_weight : o
+ *     m = v * act(gate)            act: FI_GATE_LINEAR, _SIGMOID, _SILU
+ *     r = res + scale * m          the residual stream after the block
+ *     a = r / sqrt(mean(r^2) + eps) * pre_weight     the next block's input
+ *
+ * o NULL (then gate, scale and post_norm are too): r = res, the norm before a
+ * first block.  post_weight needs post_norm.  The mean is over the row; a is formed from r before r is
+ * rounded. */
+enum { FI_GATE_LINEAR = 0, FI_GATE_SIGMOID = 1, FI_GATE_SILU = 2 };
+
+typedef struct fi_norm_desc {
+    int64_t rows;          /* >= 0 */
+    int channels;          /* 1 .. 16384 */
+    int dtype;             /* of o, gate, a and their gradients */
+    int res_dtype;         /* of res, r and their gradients: dtype or FI_F32 */
+    int post_norm;         /* 0 or 1 */
+    int act;               /* FI_GATE_*, used where gate is given */
+    float eps;             /* >= 0 */
+    int64_t ld_o, ld_gate, ld_res, ld_r, ld_a;   /* row pitches, elements; 0 = channels */
+    int64_t ld_dr, ld_da, ld_do, ld_dgate, ld_dres;
+    int reserved[4];       /* must be zero */
+} fi_norm_desc;
+
+/* Workspace of fi_norm_backward; 0 for a bad descriptor. */
+size_t fi_norm_workspace_bytes(const fi_norm_desc *desc);
+
+/* r and a (either may be NULL), and where not NULL saved [2][rows] fp32 (the
+ * two reciprocal norms, for the backward pass).  Weights and scale are fp32
+ * [channels] or NULL.  r may be res itself (same pointer and pitch). */
+fi_status fi_norm_forward(const fi_norm_desc *desc, const void *o, const void *gate, const void *res,
+                          const float *post_weight, const float *scale, const float *pre_weight, void *r, void *a,
+                          float *saved, void *stream);
+
+/* Gradients of sum(r . dr) + sum(a . da) (dr or da may be NULL: zeros): where
+ * not NULL d_o, dgate, dres per row and dpost, dscale, dpre fp32 [channels]
+ * (summed over the rows in a fixed order).  A gradient can be asked for only
+ * where its input is given, except that unit weights have gradients too: dpost
+ * needs post_norm, dscale needs o, dpre needs da.  dres may be dr itself. */
+fi_status fi_norm_backward(const fi_norm_desc *desc, const void *o, const void *gate, const void *res,
+                           const float *post_weight, const float *scale, const float *pre_weight, const float *saved,
+                           const void *dr, const void *da, void *d_o, void *dgate, void *dres, float *dpost,
+                           float *dscale, float *dpre, void *workspace, void *stream);
+
+/* Matrix-vector products with 4-bit weights and group scales, for the block's
+ * projections on the few rows of one position:
+ *
+ *     y[b][n] = sum_k x[b][k] scale[n][k / group] (code[n][k] - zero[n][k / group])
+ *
+ * codes 0..15; zero 0..15, or 8 everywhere where none are given.  The weights
+ * are laid out once (fi_q4_pack) for the matrix instructions. */
+typedef struct fi_q4_desc {
+    int N, K;              /* outputs, inputs: 1 .. 2^20 each */
+    int group;             /* 32, 64 or 128 values along K share a scale */
+    int scale_dtype;       /* FI_F32, FI_BF16 or FI_F16 */
+    int has_zeros;         /* 0: every zero is 8 */
+    int reserved[3];       /* must be zero */
+} fi_q4_desc;
+
+/* Device bytes of the packed weights; 0 for a bad descriptor. */
+size_t fi_q4_packed_bytes(const fi_q4_desc *desc);
+
+/* codes [N][K] uint8 (the low four bits count), scales [N][ceil(K/group)] of
+ * scale_dtype, zeros [N][ceil(K/group)] uint8 (NULL unless has_zeros), all
+ * device memory, densely packed; packed 256-byte aligned. */
+fi_status fi_q4_pack(const fi_q4_desc *desc, const uint8_t *codes, const void *scales, const uint8_t *zeros,
+                     void *packed, void *stream);
+
+/* Codes and scales of a weight matrix w [N][K] of w_dtype (row pitch ld_w
+ * elements, 0 = K), zeros all 8: scale = max|w| of the group / 7 rounded to
+ * scale_dtype, code = 8 + w / scale rounded to nearest even, in 1..15.  A
+ * group of zeros, or one whose scale rounds to zero, gets scale 0 and codes 8. */
+fi_status fi_q4_quantize(const fi_q4_desc *desc, int w_dtype, const void *w, int64_t ld_w, uint8_t *codes,
+                         void *scales, void *stream);
+
+/* y [rows][N] = x [rows][K] times the packed weights; rows 1 .. 16, x and y of
+ * `dtype`.  fp32 inputs are multiplied in full (as three bf16 terms), 16-bit
+ * ones exactly too; sums are fp32.  A row of x with an infinity or NaN gives
+ * non-finite values in its row of y only.  |x| stays below 2^120. */
+fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int dtype, const void *x, int64_t ld_x,
+                       void *y, int64_t ld_y, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

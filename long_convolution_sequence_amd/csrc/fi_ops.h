@@ -1,0 +1,71 @@
+// Shared by the operators of a recurrent block (scan, norms, 4-bit products):
+// value types, argument checks and the calling thread's error message.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cstdio>
+
+#include "../../include/fi.h"
+
+namespace fi {
+
+using bf16_t = __bf16;
+using f16_t = _Float16;
+
+// ---- host side ---------------------------------------------------------------
+
+char *op_error();                             // the calling thread's message, kOpErrorBytes long
+constexpr size_t kOpErrorBytes = 160;
+
+inline fi_status op_fail(fi_status s, const char *call, const char *what) {
+    std::snprintf(op_error(), kOpErrorBytes, "%s: %s", call, what);
+    return s;
+}
+
+inline fi_status op_launched(const char *call) {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? FI_OK : op_fail(FI_EDEVICE, call, hipGetErrorString(e));
+}
+
+inline size_t value_bytes(int dtype) { return dtype == FI_F32 ? 4 : 2; }
+inline bool value_type(int dtype) { return dtype >= FI_F32 && dtype <= FI_F16; }
+
+// One tensor argument as `rows` rows of `width` bytes, `pitch` bytes apart.
+struct View {
+    const void *p;
+    int64_t rows;
+    size_t width, pitch;
+};
+
+// Whether two views may share a byte.  Rows of equal pitch are compared by
+// their places within the pitch, so column slices of one tensor are separate;
+// views of different pitch whose extents meet are taken to overlap.
+inline bool views_meet(const View &a, const View &b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    const uintptr_t ea = pa + (size_t)(a.rows - 1) * a.pitch + a.width;
+    const uintptr_t eb = pb + (size_t)(b.rows - 1) * b.pitch + b.width;
+    if (ea <= pb || eb <= pa) return false;
+    if (a.pitch != b.pitch) return true;
+    const size_t delta = pb >= pa ? (pb - pa) % a.pitch : (a.pitch - (pa - pb) % a.pitch) % a.pitch;
+    return !(delta >= a.width && delta + b.width <= a.pitch);
+}
+
+inline bool same_view(const View &a, const View &b) { return a.p == b.p && a.pitch == b.pitch; }
+
+// Whether any output meets an input or another output (null views never do).
+inline bool outputs_meet(const View *out, int nout, const View *in, int nin) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = i + 1; j < nout; ++j)
+            if (views_meet(out[i], out[j])) return true;
+        for (int j = 0; j < nin; ++j)
+            if (views_meet(out[i], in[j])) return true;
+    }
+    return false;
+}
+
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace fi

@@ -100,6 +100,19 @@ def load_library():
         "fi_dd_position": (I64, [P]),
         "fi_dd_last_error": (ctypes.c_char_p, [P]),
         "fi_dd_destroy": (I, [P]),
+        # operators of a recurrent block (ops.py)
+        "fi_op_last_error": (ctypes.c_char_p, []),
+        "fi_scan_saved_bytes": (S, [P]),
+        "fi_scan_workspace_bytes": (S, [P, I]),
+        "fi_scan_forward": (I, [P] * 11),
+        "fi_scan_backward": (I, [P] * 15),
+        "fi_norm_workspace_bytes": (S, [P]),
+        "fi_norm_forward": (I, [P] * 11),
+        "fi_norm_backward": (I, [P] * 18),
+        "fi_q4_packed_bytes": (S, [P]),
+        "fi_q4_pack": (I, [P] * 6),
+        "fi_q4_quantize": (I, [P, I, P, I64, P, P, P]),
+        "fi_q4_matvec": (I, [P, P, I, I, P, I64, P, I64, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

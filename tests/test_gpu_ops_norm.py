@@ -1,0 +1,224 @@
+"""The norms around a block on the GPU against the 64-bit definition, within the
+bounds that tests/_ops_ref.py derives."""
+import pytest
+import torch
+
+from long_convolution_sequence_amd import fi, ops
+from tests import _ops_ref as ref
+from tests._parity import say
+
+pytestmark = pytest.mark.gpu
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+EPS = 1e-6
+
+
+def _inputs(N, D, dtype, rt, seed=0):
+    gen = torch.Generator().manual_seed(977 * seed + N + 31 * D)
+    r = lambda *s: torch.randn(*s, generator=gen)                   # noqa: E731
+    return {"o": r(N, D).to(dtype), "gate": r(N, D).to(dtype), "res": (2 * r(N, D)).to(rt), "w1": 1 + r(D) / 8,
+            "k": 0.5 + r(D) / 8, "w2": 1 + r(D) / 8, "dr": r(N, D).to(rt), "da": r(N, D).to(dtype)}
+
+
+def _cuda(v):
+    return {k: t.cuda() if t is not None else None for k, t in v.items()}
+
+
+def _run(c, post, act, eps=EPS, **kw):
+    w = dict(post_weight=c["w1"], scale=c["k"], pre_weight=c["w2"], post_norm=post, act=act, eps=eps)
+    r, a, saved = ops.block_norm(c["o"], c["res"], c["gate"], save=True, **w)
+    g = ops.block_norm_backward(c["dr"], c["da"], c["o"], c["res"], c["gate"], saved, **w, **kw)
+    return {"r": r, "a": a, "do": g.o, "dres": g.res, "dgate": g.gate, "dpost": g.post_weight, "dscale": g.scale,
+            "dpre": g.pre_weight}
+
+
+def _check(got, v, post, act, dtype, rt, eps=EPS):
+    want = ref.norm(v["o"], v["res"], v["gate"], v["w1"], v["k"], v["w2"], post, act, eps, v["dr"], v["da"], True)
+    types = {"r": rt, "a": dtype, "do": dtype, "dres": rt, "dgate": dtype}
+    for name, g in got.items():
+        if g is None:
+            continue
+        if name not in want:
+            assert (g == 0).all(), name
+            continue
+        value, tol = want[name]
+        assert g.shape == value.shape and g.dtype == types.get(name, F32)
+        w = ref.worst(g, value, ref.stored(value, tol, types.get(name, F32)))
+        assert w <= 1.0, f"{name}: {w:.3g} of its bound"
+
+
+CASES = [(1, 1, F32, F32, True, 2), (1, 864, BF16, F32, True, 2), (8, 864, BF16, BF16, True, 1), (3, 7, F16, F16, True, 0),
+         (5, 64, F32, F32, False, 2), (33, 100, BF16, F32, True, 2), (17, 255, F16, F32, False, 1),
+         (70, 256, F32, F32, True, 2), (9, 257, BF16, BF16, True, 2), (4, 1000, F16, F32, True, 0),
+         (3, 1024, F32, F32, True, 1), (6, 1025, BF16, F32, False, 0), (2, 2050, F32, F32, True, 2),
+         (3, 4100, F16, F16, True, 2), (2, 8191, BF16, F32, True, 2), (2, 16384, F32, F32, True, 2),
+         (3, 16383, F16, F32, True, 1), (2500, 40, F32, F32, True, 2), (1300, 96, BF16, F32, True, 2)]
+
+
+@pytest.mark.parametrize("N,D,dtype,rt,post,act", CASES)
+def test_forward_and_gradients(N, D, dtype, rt, post, act):
+    say(f"case norm N={N} D={D} {dtype}/{rt} post={post} act={act}")
+    v = _inputs(N, D, dtype, rt)
+    if not post:
+        v["w1"] = None
+    _check(_run(_cuda(v), post, act), v, post, act, dtype, rt)
+
+
+@pytest.mark.parametrize("gone", [("gate",), ("res",), ("w1",), ("k",), ("w2",), ("dr",), ("da",), ("gate", "k", "res"),
+                                  ("w1", "k", "w2", "gate"), ("o", "gate", "w1", "k"), ("o", "gate", "w1", "k", "w2", "dr")])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_left_out_factors(gone, dtype):
+    say(f"case norm without {gone} {dtype}")
+    v = _inputs(12, 300, dtype, dtype if "o" in gone or "res" in gone else F32, seed=1)
+    for k in gone:
+        v[k] = None
+    post = v["o"] is not None
+    rt = v["res"].dtype if v["res"] is not None else dtype
+    got = _run(_cuda(v), post, ops.GATE_SILU)
+    for name, k in (("do", "o"), ("dres", "res"), ("dgate", "gate"), ("dpost", "w1"), ("dscale", "k"), ("dpre", "w2")):
+        assert (got[name] is None) == (v[k] is None)
+    _check(got, v, post, ops.GATE_SILU, dtype, rt)
+
+
+def test_zero_rows_and_no_rows():
+    """A row of zeros: finite with eps; an empty tensor: empty results, column gradients of zero."""
+    say("case norm zero rows")
+    v = _inputs(4, 130, F32, F32, seed=2)
+    v["o"][1], v["res"][1], v["res"][2], v["o"][2] = 0.0, 0.0, 0.0, 0.0
+    _check(_run(_cuda(v), True, ops.GATE_SILU), v, True, ops.GATE_SILU, F32, F32)
+    got = _run(_cuda(_inputs(0, 130, BF16, F32)), True, ops.GATE_SILU)
+    assert got["r"].shape == (0, 130) and got["do"].shape == (0, 130)
+    assert all((got[k] == 0).all() for k in ("dpost", "dscale", "dpre"))
+
+
+def test_bad_values_stay_in_their_row():
+    """A NaN or an infinity in one row leaves the others as they were."""
+    say("case norm bad rows")
+    v = _inputs(6, 200, BF16, F32, seed=3)
+    clean = _run(_cuda(v), True, ops.GATE_SILU)
+    v["o"][2, 5], v["res"][4, 0] = float("nan"), float("inf")
+    got = _run(_cuda(v), True, ops.GATE_SILU)
+    for name in ("r", "a", "do", "dres", "dgate"):
+        for i in (0, 1, 3, 5):
+            assert torch.equal(got[name][i], clean[name][i])
+    assert got["a"][2].isnan().any() and not torch.isfinite(got["a"][4]).all()
+
+
+@pytest.mark.parametrize("D,dtype,rt", [(40, BF16, F32), (864, BF16, BF16), (33, F32, F32), (1200, F16, F32)])
+def test_column_slices(D, dtype, rt):
+    """o and gate (and their gradients) as column slices; no other column is written."""
+    say(f"case norm slices D={D} {dtype}/{rt}")
+    N = 37
+    v = _inputs(N, D, dtype, rt, seed=4)
+    c = _cuda(v)
+    for lead in (0, 1, 8):
+        wide = torch.full((N, 2 * D + 3 + lead), 7.0, dtype=dtype, device="cuda")
+        grads = torch.full((N, 2 * D + 3 + lead), 9.0, dtype=dtype, device="cuda")
+        cols = (slice(lead, lead + D), slice(lead + D + 2, lead + 2 * D + 2))
+        s = dict(c, o=wide[:, cols[0]], gate=wide[:, cols[1]])
+        s["o"].copy_(c["o"]), s["gate"].copy_(c["gate"])
+        got = _run(s, True, ops.GATE_SILU, do=grads[:, cols[0]], dgate=grads[:, cols[1]])
+        _check(got, v, True, ops.GATE_SILU, dtype, rt)
+        mask = torch.ones(wide.shape[1], dtype=torch.bool, device="cuda")
+        mask[cols[0]] = mask[cols[1]] = False
+        assert (wide[:, mask] == 7).all() and (grads[:, mask] == 9).all()
+
+
+def test_in_place_residual_and_gradient():
+    say("case norm in place")
+    for D, rt in ((130, F32), (864, BF16), (2000, F32), (9000, F32)):
+        v = _inputs(21, D, BF16, rt, seed=5)
+        c = _cuda(v)
+        want = _run(c, True, ops.GATE_SILU)
+        dr = c["dr"].clone()
+        got = _run(dict(c, dr=dr), True, ops.GATE_SILU, dres=dr)
+        assert got["dres"] is dr
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        res = c["res"].clone()
+        r, a = ops.block_norm(c["o"], res, c["gate"], post_weight=c["w1"], scale=c["k"], pre_weight=c["w2"],
+                              post_norm=True, eps=EPS, r=res)
+        assert r is res and torch.equal(r, want["r"]) and torch.equal(a, want["a"])
+
+
+def test_leading_dimensions_and_repeats():
+    say("case norm [T][B][D]")
+    v = _inputs(60, 96, F32, F32, seed=6)
+    c = _cuda(v)
+    flat = _run(c, True, ops.GATE_SIGMOID)
+    deep = {k: (t.reshape(20, 3, 96) if t.dim() == 2 else t) for k, t in c.items()}
+    for _ in range(3):
+        got = _run(deep, True, ops.GATE_SIGMOID)
+        assert got["r"].shape == (20, 3, 96)
+        assert all(torch.equal(got[k].reshape(flat[k].shape), flat[k]) for k in flat)
+
+
+def test_captured_and_replayed():
+    say("case norm graph")
+    c = _cuda(_inputs(500, 96, BF16, F32, seed=7))
+    _run(c, True, ops.GATE_SILU)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = _run(c, True, ops.GATE_SILU)
+    for i in range(4):
+        new = _cuda(_inputs(500, 96, BF16, F32, seed=8 + i))
+        for k, t in new.items():
+            c[k].copy_(t)
+        g.replay()
+        eager = _run(new, True, ops.GATE_SILU)
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[k], eager[k]) for k in out)
+
+
+def test_on_another_stream():
+    say("case norm on a side stream")
+    v = _inputs(300, 864, BF16, F32, seed=9)
+    c = _cuda(v)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = _run(c, True, ops.GATE_SILU)
+    s.synchronize()
+    _check(got, v, True, ops.GATE_SILU, BF16, F32)
+
+
+def test_offsets_past_32_bits():
+    say("case norm far rows")
+    N, D, pitch = 1100, 24, 1 << 21
+    v = _inputs(N, D, BF16, BF16, seed=10)
+    c = _cuda(v)
+    buf = torch.empty(N * pitch, dtype=BF16, device="cuda")
+    far = lambda at: buf.as_strided((N, D), (pitch, 1), at)          # noqa: E731
+    s = dict(c)
+    for i, k in enumerate(("o", "gate", "res", "dr", "da")):
+        s[k] = far(64 * i)
+        s[k].copy_(c[k])
+    got = _run(s, True, ops.GATE_SILU, do=far(512), dgate=far(640), dres=far(768))
+    _check(got, v, True, ops.GATE_SILU, BF16, BF16)
+
+
+def test_many_rows():
+    """More rows than any grid has workgroups: the sums of a sample of columns, and every row's a."""
+    say("case norm 200000 rows")
+    N, D = 200_000, 16
+    v = _inputs(N, D, F32, F32, seed=11)
+    _check(_run(_cuda(v), True, ops.GATE_SILU), v, True, ops.GATE_SILU, F32, F32)
+
+
+def test_binding_refuses_mismatches():
+    say("case norm refusals")
+    o = torch.zeros(4, 8, device="cuda")
+    w = torch.ones(8, device="cuda")
+    saved = torch.zeros(2, 4, device="cuda")
+    for call in (lambda: ops.block_norm(o, o[:3]), lambda: ops.block_norm(o, o.half()), lambda: ops.block_norm(o.double()),
+                 lambda: ops.block_norm(o, o.cpu()), lambda: ops.block_norm(o, gate=o.half()),
+                 lambda: ops.block_norm(o, pre_weight=w[:7]), lambda: ops.block_norm(o, pre_weight=w.half()),
+                 lambda: ops.block_norm(o, post_weight=w), lambda: ops.block_norm(None, o, o),
+                 lambda: ops.block_norm(o, act=9), lambda: ops.block_norm(o, eps=-1.0), lambda: ops.block_norm(o, a=o),
+                 lambda: ops.block_norm(torch.zeros(2, 16385, device="cuda")),
+                 lambda: ops.block_norm(o[:, ::2]), lambda: ops.block_norm_backward(o, o, o, None, None, None),
+                 lambda: ops.block_norm_backward(o, o, o, None, None, saved[:, :3]),
+                 lambda: ops.block_norm_backward(o, o[:2], o, None, None, saved),
+                 lambda: ops.block_norm_backward(o, o, o, None, None, saved, do=o)):
+        with pytest.raises(fi.FiError) as e:
+            call()
+        assert e.value.status == fi.FI_EINVAL

@@ -1,0 +1,302 @@
+"""The gated linear recurrence on the GPU against the 64-bit definition, within
+the bounds that tests/_ops_ref.py derives."""
+import math
+
+import pytest
+import torch
+
+from long_convolution_sequence_amd import fi, ops
+from tests import _ops_ref as ref
+from tests._parity import say
+
+pytestmark = pytest.mark.gpu
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+def _inputs(T, B, D, dtype, seed=0, lengths=None, bias=True, state=True):
+    gen = torch.Generator().manual_seed(1000 * seed + T + 7 * B + 13 * D)
+    r = lambda *s: torch.randn(*s, generator=gen)                   # noqa: E731
+    v = {"x": r(T, B, D).to(dtype), "gate": r(T, B, D).to(dtype), "dy": r(T, B, D).to(dtype), "dfinal": r(B, D),
+         "bias": (torch.rand(D, generator=gen) * math.log(1000.0)) if bias else None,
+         "state": r(B, D) if state else None,
+         "lengths": torch.tensor(lengths, dtype=torch.int32) if lengths is not None else None}
+    if lengths is not None:                                          # masked places hold what must not be used
+        for b, n in enumerate(lengths):
+            n = min(max(n, 0), T)
+            v["x"][n:, b], v["gate"][n:, b], v["dy"][n:, b] = float("nan"), float("inf"), float("-inf")
+    return v
+
+
+def _cuda(v):
+    return {k: t.cuda() if t is not None else None for k, t in v.items()}
+
+
+def _run(c, kind, **kw):
+    y, final, saved = ops.gated_scan(c["x"], c["gate"], c["bias"], c["state"], c["lengths"], input=kind, save=True)
+    dx, dg, db, ds = ops.gated_scan_backward(c["dy"], c["x"], c["gate"], saved, c["bias"], c["state"], c["lengths"],
+                                             dfinal=c["dfinal"], input=kind, **kw)
+    return {"y": y, "final": final, "dx": dx, "dgate": dg, "dbias": db, "dstate": ds}
+
+
+def _check(got, v, kind, dtype):
+    want = ref.scan(v["x"], v["gate"], v["bias"], v["state"], v["lengths"], kind, v["dy"], v["dfinal"])
+    for name, g in got.items():
+        if g is None:
+            continue
+        value, tol = want[name]
+        assert g.shape == value.shape
+        w = ref.worst(g, value, ref.stored(value, tol, dtype if name in ("y", "dx", "dgate") else F32))
+        assert w <= 1.0, f"{name}: {w:.3g} of its bound"
+
+
+CASES = [(1, 1, 1, F32, 1), (1, 8, 864, BF16, 1), (2, 3, 5, F16, 2), (7, 1, 64, F32, 0), (31, 2, 33, BF16, 2),
+         (64, 4, 8, F16, 1), (65, 1, 257, F32, 2), (127, 2, 100, BF16, 0), (128, 1, 66, F32, 1), (129, 3, 12, F16, 0),
+         (255, 2, 7, F32, 2), (256, 1, 130, BF16, 1), (257, 1, 3, F32, 1), (511, 3, 20, F32, 0), (513, 2, 65, F16, 2),
+         (1025, 1, 16, BF16, 2), (3001, 2, 9, F32, 1), (5000, 1, 65, F32, 2)]
+
+
+@pytest.mark.parametrize("T,B,D,dtype,kind", CASES)
+def test_forward_and_gradients(T, B, D, dtype, kind):
+    say(f"case scan T={T} B={B} D={D} {dtype} input={kind}")
+    v = _inputs(T, B, D, dtype)
+    _check(_run(_cuda(v), kind), v, kind, dtype)
+
+
+@pytest.mark.parametrize("T,B,D,dtype,lengths", [
+    (1, 3, 8, F32, [1, 0, 1]), (40, 4, 5, BF16, [40, 0, 1, 39]), (300, 3, 40, F32, [0, 0, 0]),
+    (600, 5, 66, F16, [600, 256, 255, 257, 0]), (1300, 3, 7, F32, [512, 1300, 3]), (90, 2, 16, F32, [-5, 1000])])
+def test_lengths(T, B, D, dtype, lengths):
+    say(f"case scan lengths T={T} B={B} D={D} {dtype} {lengths}")
+    v = _inputs(T, B, D, dtype, seed=1, lengths=lengths)
+    got = _run(_cuda(v), ops.SCAN_CONVEX)
+    _check(got, v, ops.SCAN_CONVEX, dtype)
+    for b, n in enumerate(lengths):
+        n = min(max(n, 0), T)
+        for name in ("y", "dx", "dgate"):
+            assert (got[name][n:, b] == 0).all()
+        if n == 0:                                                   # an empty row hands its state through, bit for bit
+            assert torch.equal(got["final"][b].cpu(), v["state"][b])
+            assert torch.equal(got["dstate"][b].cpu(), v["dfinal"][b])
+
+
+@pytest.mark.parametrize("bias,state", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("T", [1, 700])
+def test_without_bias_or_state(bias, state, T):
+    say(f"case scan T={T} bias={bias} state={state}")
+    v = _inputs(T, 2, 35, F32, seed=2, bias=bias, state=state)
+    got = _run(_cuda(v), ops.SCAN_ENERGY)
+    assert (got["dbias"] is None) == (not bias) and (got["dstate"] is None) == (not state)
+    _check(got, v, ops.SCAN_ENERGY, F32)
+
+
+def test_no_final_gradient():
+    say("case scan dfinal None")
+    v = _inputs(530, 2, 35, F32, seed=3)
+    v["dfinal"] = None
+    _check(_run(_cuda(v), ops.SCAN_PLAIN), v, ops.SCAN_PLAIN, F32)
+
+
+def test_no_positions():
+    """T = 0: the state and its gradient pass through."""
+    say("case scan T=0")
+    c = _cuda(_inputs(0, 2, 5, F32))
+    got = _run(c, ops.SCAN_CONVEX)
+    assert got["y"].shape == (0, 2, 5) and torch.equal(got["final"], c["state"])
+    assert torch.equal(got["dstate"], c["dfinal"]) and (got["dbias"] == 0).all()
+    assert ops.gated_scan(c["x"], c["gate"], c["bias"], c["state"], final=c["state"])[1] is c["state"]
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("T", [5, 900])
+def test_gates_at_the_ends(kind, T):
+    """Gates from -120 to 120 and infinite ones: a decay of exactly 0 or 1, no NaN."""
+    say(f"case scan extreme gates T={T} input={kind}")
+    v = _inputs(T, 1, 12, F32, seed=4, bias=False)
+    v["gate"] *= 40
+    for c, g in enumerate((float("inf"), float("-inf"), 1e30, -1e30, 90.0, -90.0)):
+        v["gate"][::2, 0, c] = g
+    got = _run(_cuda(v), kind)
+    finite = v["gate"].clone().clamp(-700, 700)                     # the same decays in fp64, without inf * 0
+    want = ref.scan(v["x"], finite, None, v["state"], None, kind, v["dy"], v["dfinal"])
+    for name in ("y", "final", "dx", "dgate", "dstate"):
+        w = ref.worst(got[name], want[name][0], ref.stored(*want[name], F32))
+        assert w <= 1.0, f"{name}: {w:.3g} of its bound"
+
+
+@pytest.mark.parametrize("T,B,D,dtype", [(37, 2, 24, BF16), (600, 1, 20, F32), (300, 3, 17, F16), (700, 2, 64, BF16)])
+def test_column_slices(T, B, D, dtype):
+    """x, gate and y as column slices of one tensor, the gradients of another: the same values as
+    packed ones, and no other column is written."""
+    say(f"case scan slices T={T} B={B} D={D} {dtype}")
+    v = _inputs(T, B, D, dtype, seed=5)
+    c = _cuda(v)
+    want = _run(c, ops.SCAN_CONVEX)
+    for lead in (0, 1, 8):
+        wide = torch.full((T, B, 3 * D + 3 + lead), 7.0, dtype=dtype, device="cuda")
+        grads = torch.full((T, B, 2 * D + 5 + lead), 9.0, dtype=dtype, device="cuda")
+        x, gate, y = (wide[..., lead + i * (D + 1):lead + i * (D + 1) + D] for i in range(3))
+        dx, dg = grads[..., lead + 1:lead + 1 + D], grads[..., lead + D + 3:lead + 2 * D + 3]
+        x.copy_(c["x"]), gate.copy_(c["gate"])
+        _, final, saved = ops.gated_scan(x, gate, c["bias"], c["state"], save=True, y=y)
+        _, _, db, ds = ops.gated_scan_backward(c["dy"], x, gate, saved, c["bias"], c["state"], dfinal=c["dfinal"],
+                                               dx=dx, dgate=dg)
+        _check({"y": y, "final": final, "dx": dx, "dgate": dg, "dbias": db, "dstate": ds}, v, ops.SCAN_CONVEX, dtype)
+        assert torch.equal(y, want["y"]) or lead       # another alignment may take another variant
+        mask = torch.ones(wide.shape[-1], dtype=torch.bool)
+        for i in range(3):
+            mask[lead + i * (D + 1):lead + i * (D + 1) + D] = False
+        assert (wide[..., mask.cuda()] == 7).all()
+        mask = torch.ones(grads.shape[-1], dtype=torch.bool)
+        mask[lead + 1:lead + 1 + D] = mask[lead + D + 3:lead + 2 * D + 3] = False
+        assert (grads[..., mask.cuda()] == 9).all()
+
+
+def test_steps_continue_a_sequence():
+    """Position by position in place, from the state a prompt left, against the whole sequence."""
+    say("case scan steps")
+    v = _inputs(330, 3, 40, F32, seed=6)
+    c = _cuda(v)
+    want = ref.scan(v["x"], v["gate"], v["bias"], v["state"], None, ops.SCAN_CONVEX)
+    state = c["state"].clone()
+    y0, state = ops.gated_scan(c["x"][:300], c["gate"][:300], c["bias"], state, final=state)
+    ys = [ops.gated_scan_step(c["x"][t], c["gate"][t], state, c["bias"]) for t in range(300, 330)]
+    y = torch.cat((y0, torch.stack(ys)))
+    for got, name in ((y, "y"), (state, "final")):
+        value, tol = want[name]
+        assert ref.worst(got, value, ref.stored(value, tol, F32)) <= 1.0
+
+
+def test_step_leaves_empty_slots():
+    say("case scan step with empty slots")
+    v = _inputs(1, 4, 24, BF16, seed=7, lengths=[1, 0, 1, 0])
+    c = _cuda(v)
+    state = c["state"].clone()
+    y = ops.gated_scan_step(c["x"][0], c["gate"][0], state, c["bias"], c["lengths"])
+    assert (y[1::2] == 0).all() and torch.equal(state[1::2], c["state"][1::2])
+    want = ref.scan(v["x"], v["gate"], v["bias"], v["state"], v["lengths"], ops.SCAN_CONVEX)
+    assert ref.worst(state, want["final"][0], ref.stored(*want["final"], F32)) <= 1.0
+
+
+@pytest.mark.parametrize("T", [5, 40, 700, 3000])
+def test_final_in_place_of_the_state(T):
+    say(f"case scan in place T={T}")
+    v = _inputs(T, 2, 70, F32, seed=8)
+    c = _cuda(v)
+    y, final = ops.gated_scan(c["x"], c["gate"], c["bias"], c["state"])
+    state = c["state"].clone()
+    y2, got = ops.gated_scan(c["x"], c["gate"], c["bias"], state, final=state)
+    assert got is state and torch.equal(state, final) and torch.equal(y, y2)
+
+
+def test_results_repeat():
+    say("case scan repeats")
+    c = _cuda(_inputs(4000, 2, 96, BF16, seed=9))
+    first = _run(c, ops.SCAN_ENERGY)
+    for _ in range(3):
+        again = _run(c, ops.SCAN_ENERGY)
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_on_another_stream():
+    say("case scan on a side stream")
+    v = _inputs(900, 2, 48, F32, seed=10)
+    c = _cuda(v)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = _run(c, ops.SCAN_CONVEX)
+    s.synchronize()
+    _check(got, v, ops.SCAN_CONVEX, F32)
+
+
+def test_two_streams_at_once():
+    """Two long calls side by side, each with its own workspace."""
+    say("case scan two streams")
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    v = [_inputs(6000, 1, 200, F32, seed=20 + i) for i in range(2)]
+    c = [_cuda(u) for u in v]
+    alone = [_run(u, ops.SCAN_CONVEX) for u in c]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(sides):
+            with torch.cuda.stream(s):
+                got[i].append(_run(c[i], ops.SCAN_CONVEX))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(g[k], alone[i][k]) for k in g)
+
+
+@pytest.mark.parametrize("T", [1, 200, 2500])
+def test_captured_and_replayed(T):
+    """A training pass in a graph, replayed with new inputs and eager work between the replays."""
+    say(f"case scan graph T={T}")
+    c = _cuda(_inputs(T, 2, 40, BF16, seed=11))
+    _run(c, ops.SCAN_CONVEX)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = _run(c, ops.SCAN_CONVEX)
+    for i in range(4):
+        new = _cuda(_inputs(T, 2, 40, BF16, seed=12 + i))
+        for k, t in new.items():
+            if t is not None:
+                c[k].copy_(t)
+        g.replay()
+        eager = _run(new, ops.SCAN_CONVEX)
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[k], eager[k]) for k in out)
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^21 elements apart: element offsets pass 2^31 (and bytes 2^32) within the sequence."""
+    say("case scan far rows")
+    T, B, D, pitch = 1100, 1, 20, 1 << 21
+    v = _inputs(T, B, D, BF16, seed=13)
+    c = _cuda(v)
+    buf = torch.empty(T * pitch, dtype=BF16, device="cuda")
+    far = lambda at: buf.as_strided((T, B, D), (pitch, pitch, 1), at)       # noqa: E731
+    for at, t in ((0, c["x"]), (64, c["gate"]), (256, c["dy"])):
+        far(at).copy_(t)
+    y, final, saved = ops.gated_scan(far(0), far(64), c["bias"], c["state"], save=True, y=far(128))
+    dx, dg, db, ds = ops.gated_scan_backward(far(256), far(0), far(64), saved, c["bias"], c["state"],
+                                             dfinal=c["dfinal"], dx=far(320), dgate=far(384))
+    _check({"y": y, "final": final, "dx": dx, "dgate": dg, "dbias": db, "dstate": ds}, v, ops.SCAN_CONVEX, BF16)
+
+
+def test_long_memory():
+    """Decays next to one: a memory of 2^14 positions over 2^16, a constant input, exact limit 1 - (1-d)^t."""
+    say("case scan long memory")
+    T = 1 << 16
+    z = math.log((1 << 14) - 1)                                      # d = 2^-14
+    x = torch.ones(T, 1, 4, device="cuda")
+    gate = torch.full((T, 1, 4), z, device="cuda")
+    y, _ = ops.gated_scan(x, gate)
+    d = torch.sigmoid(-gate[:, 0, 0].double().cpu())
+    want = 1 - torch.exp(torch.cumsum(torch.log1p(-d), 0))
+    # the gate's exponential is off by (3|z| + 5) U of d; the state rounds 3 U a position over 1/d positions,
+    # and a joint of chunks 10 U
+    tol = (3 * z + 5 + 3 / float(d[0]) + 10) * ref.U
+    assert float((y[:, 0, 0].double().cpu() - want).abs().max()) < tol
+
+
+def test_binding_refuses_mismatches():
+    say("case scan refusals")
+    x = torch.zeros(4, 2, 8, device="cuda")
+    st = torch.zeros(2, 8, device="cuda")
+    for call in (lambda: ops.gated_scan(x, x[:3]), lambda: ops.gated_scan(x, x.half()), lambda: ops.gated_scan(x, None),
+                 lambda: ops.gated_scan(x, x.cpu()), lambda: ops.gated_scan(x[0], x[0]),
+                 lambda: ops.gated_scan(x.double(), x.double()), lambda: ops.gated_scan(x, x, st),
+                 lambda: ops.gated_scan(x, x, None, st[:1]), lambda: ops.gated_scan(x, x, None, st.half()),
+                 lambda: ops.gated_scan(x, x, None, None, torch.zeros(2, device="cuda")),
+                 lambda: ops.gated_scan(x, x, None, None, torch.zeros(3, dtype=torch.int32, device="cuda")),
+                 lambda: ops.gated_scan(x, x, y=x), lambda: ops.gated_scan(x, x, input=3),
+                 lambda: ops.gated_scan(x.transpose(0, 1), x.transpose(0, 1)),
+                 lambda: ops.gated_scan(x, x[:1].expand(4, 2, 8)),
+                 lambda: ops.gated_scan_step(x[0], x[0], None), lambda: ops.gated_scan_step(x, x, st),
+                 lambda: ops.gated_scan_backward(x, x, x, None), lambda: ops.gated_scan_backward(x, x, x, st),
+                 lambda: ops.gated_scan_backward(None, x, x, ops.gated_scan(x, x, save=True)[2])):
+        with pytest.raises(fi.FiError) as e:
+            call()
+        assert e.value.status == fi.FI_EINVAL
