@@ -66,6 +66,52 @@ inline bool outputs_meet(const View *out, int nout, const View *in, int nin) {
     return false;
 }
 
+inline int64_t pitch_or(int64_t ld, int64_t width) { return ld ? ld : width; }
+
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// ---- device side -------------------------------------------------------------
+
+// CH values side by side.  The pitch and the start of a row are any number of
+// elements, so a chunk is aligned to its element only; global loads and stores
+// of 4 to 16 bytes need no more on this target.
+template <typename T, int CH>
+using Chunk __attribute__((aligned(sizeof(T)))) = T __attribute__((ext_vector_type(CH)));
+
+// Values p[0 .. min(n, CH)) of a chunk, zeros behind them.
+template <typename T, int CH>
+__device__ __forceinline__ Chunk<T, CH> load_chunk(const T *p, int n) {
+    if (n >= CH) return *reinterpret_cast<const Chunk<T, CH> *>(p);
+    Chunk<T, CH> v;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = i < n ? p[i] : (T)0.f;
+    return v;
+}
+
+template <typename T, int CH>
+__device__ __forceinline__ void store_chunk(T *p, int n, Chunk<T, CH> v) {
+    if (n >= CH) {
+        *reinterpret_cast<Chunk<T, CH> *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+        if (i < n) p[i] = v[i];
+}
+
+// Sum over the 64 lanes, in every lane: shifts within rows of 16 lanes, then
+// across the rows, on the vector ALU's lane shifts (no LDS traffic).
+__device__ __forceinline__ float lanes_sum(float v) {
+#define FI_LANE_ADD(ctrl, rows) \
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false))
+    FI_LANE_ADD(0x111, 0xf);   // from 1, 2, 4, 8 lanes below, in the row
+    FI_LANE_ADD(0x112, 0xf);
+    FI_LANE_ADD(0x114, 0xf);
+    FI_LANE_ADD(0x118, 0xf);
+    FI_LANE_ADD(0x142, 0xa);   // a row's last lane into the next row
+    FI_LANE_ADD(0x143, 0xc);   // the lower half's last lane into the upper half
+#undef FI_LANE_ADD
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
 
 }  // namespace fi

@@ -5,7 +5,7 @@
 // Backwards, with u = da w2:
 //   dR = dr + p (u - r p mean(u r p)),  dm = k dR,  dv = dm act(g),
 //   dg = dm v act'(g),  do = q (dv w1 - o q mean(dv w1 o q)),
-//   dk = sum m dR, dw1 = sum dv o q, dw2 = sum da r p   (over the rows).
+//   dw1 = k P, dk = w1 P with P = sum dR act(g) o q,  dw2 = sum da r p   (over the rows).
 // r is formed again from o, g and res in fp32, not read back rounded.
 #include "fi_ops.h"
 
@@ -13,34 +13,24 @@ namespace fi {
 
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr int kNormMaxD = 16384;
-constexpr int kNormGroups = 1024;      // workgroups of the backward pass at most, each with its own column sums
+constexpr int kNormLane = 16;          // values of a row per lane at most
+constexpr int kNormForwardGroups = 2048;
+constexpr int kNormGroups = 512;       // workgroups of the backward pass at most, each with its own column sums
 
 struct NormArgs {
     const void *o, *gate, *res, *dr, *da;
     void *r, *a, *d_o, *dgate, *dres;
     const float *w1, *k, *w2;
     float *saved;            // [2][rows]
-    float *part;             // [groups][3][D] column sums of dw1, dk, dw2
+    float *part;             // [groups][2][D] column sums of dR act o q and of da r p
     int64_t rows;
     int64_t ldo, ldg, ldres, ldr, lda, lddr, ldda, lddo, lddg, lddres;
     int D;
     int post, act;
     float eps;
-    bool col1, colk, col2;   // column sums wanted
+    bool columns;            // column sums wanted
 };
-
-__device__ __forceinline__ float block_sum(float v, float *lds) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < (int)(blockDim.x >> 6); ++i) s += lds[i];
-    return s;
-}
 
 __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896f));
@@ -61,131 +51,262 @@ __device__ __forceinline__ float act_of(int act, float g, float &slope) {
     return g * s;
 }
 
-template <typename V>
-__device__ __forceinline__ float ld(const void *p, int64_t i) {
-    return (float)static_cast<const V *>(p)[i];
+// A row is held in registers by a team: one wave up to 1024 values (four teams
+// to a workgroup, no barrier), else a workgroup of as many waves as the row
+// needs.  A lane holds NC chunks of CH neighbouring values, CH chosen so that
+// the widest tensor of the row is read 16 bytes at a time; a team's waves take
+// alternate stretches.  A team keeps its columns' weights (and, backwards,
+// their column sums) in registers over all its rows.
+template <int CH, int NC, bool MULTI>
+struct Team {
+    int start, step;       // first column of this lane, columns between its chunks
+    int waves, wave, lane;
+    int64_t row, rows_step;
+    int turn;
+
+    __device__ __forceinline__ Team() {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        waves = blockDim.x >> 6;
+        turn = 0;
+        if (MULTI) {
+            start = (wave * 64 + lane) * CH;
+            step = waves * 64 * CH;
+            row = blockIdx.x;
+            rows_step = gridDim.x;
+        } else {
+            start = lane * CH;
+            step = 64 * CH;
+            row = blockIdx.x * (int64_t)waves + wave;
+            rows_step = gridDim.x * (int64_t)waves;
+        }
+    }
+    // Sum over the team, in every lane.  Two sets of slots by turns: a wave that
+    // writes a set has passed the barrier after everybody's reads of that set.
+    __device__ __forceinline__ float sum(float v, float (*slots)[16]) {
+        v = lanes_sum(v);
+        if (!MULTI) return v;
+        if (lane == 0) slots[turn][wave] = v;
+        __syncthreads();
+        v = 0.f;
+        for (int i = 0; i < waves; ++i) v += slots[turn][i];
+        turn ^= 1;
+        return v;
+    }
+};
+
+template <typename T, int CH, int NC, bool MULTI>
+__device__ __forceinline__ void load_row(float (&v)[NC * CH], const void *p, int64_t ld, const Team<CH, NC, MULTI> &t,
+                                         int D) {
+    const T *from = static_cast<const T *>(p) + t.row * ld;
+    Chunk<T, CH> raw[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int c = t.start + j * t.step;
+        raw[j] = load_chunk<T, CH>(from + c, D - c);
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) v[j * CH + i] = (float)raw[j][i];
 }
 
-// One element's m (and what the backward pass needs of it).
-template <typename V>
-__device__ __forceinline__ float block_out(const NormArgs &p, int64_t row, int c, float q, float &unit, float &act,
-                                           float &slope) {
-    unit = act = slope = 0.f;
-    if (!p.o) return 0.f;
-    unit = ld<V>(p.o, row * p.ldo + c) * q;
-    float v = unit * (p.w1 ? p.w1[c] : 1.f);
-    act = 1.f;
-    if (p.gate) act = act_of(p.act, ld<V>(p.gate, row * p.ldg + c), slope);
-    return v * act;
+template <typename T, int CH, int NC, bool MULTI>
+__device__ __forceinline__ void store_row(const float (&v)[NC * CH], void *p, int64_t ld,
+                                          const Team<CH, NC, MULTI> &t, int D) {
+    T *to = static_cast<T *>(p) + t.row * ld;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int c = t.start + j * t.step;
+        Chunk<T, CH> raw;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) raw[i] = (T)v[j * CH + i];
+        store_chunk<T, CH>(to + c, D - c, raw);
+    }
 }
 
-template <typename V, typename W>
-__device__ __forceinline__ float stream_out(const NormArgs &p, int64_t row, int c, float m) {
-    const float r = p.res ? ld<W>(p.res, row * p.ldres + c) : 0.f;
-    return p.o ? fmaf(p.k ? p.k[c] : 1.f, m, r) : r;
+template <int CH, int NC, bool MULTI>
+__device__ __forceinline__ void load_weights(float (&v)[NC * CH], const float *w, const Team<CH, NC, MULTI> &t,
+                                             int D) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int c = t.start + j * t.step;
+        Chunk<float, CH> raw;
+        if (w) raw = load_chunk<float, CH>(w + c, D - c);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) v[j * CH + i] = w ? raw[i] : 1.f;
+    }
 }
 
-template <typename V, typename W>
-__global__ void __launch_bounds__(kNormThreads) k_norm(NormArgs p) {
-    __shared__ float lds[kNormThreads / 64];
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        float q = 1.f, unit, act, slope;
+// k w1: the two weights of a column meet in every use of them in a row
+template <int CH, int NC, bool MULTI>
+__device__ __forceinline__ void load_product(float (&v)[NC * CH], const float *k, const float *w1,
+                                             const Team<CH, NC, MULTI> &t, int D) {
+    float w[NC * CH];
+    load_weights(v, k, t, D);
+    load_weights(w, w1, t, D);
+#pragma unroll
+    for (int i = 0; i < NC * CH; ++i) v[i] *= w[i];
+}
+
+__device__ __forceinline__ float rnorm(float squares, const NormArgs &p) {
+    return 1.f / sqrtf(squares / (float)p.D + p.eps);
+}
+
+// Forward: HBM-bound, every tensor once.
+template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
+    constexpr int N = CH * NC;
+    __shared__ float slots[2][16];
+    Team<CH, NC, MULTI> t;
+    float kw[N], w2[N];
+    load_product(kw, p.k, p.w1, t, p.D);
+    load_weights(w2, p.w2, t, p.D);
+    for (; t.row < p.rows; t.row += t.rows_step) {
+        float o[N], g[N], r[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = 0.f, g[i] = 0.f, r[i] = 0.f;
+        if (p.o) load_row<V>(o, p.o, p.ldo, t, p.D);
+        if (p.gate) load_row<V>(g, p.gate, p.ldg, t, p.D);
+        if (p.res) load_row<W>(r, p.res, p.ldres, t, p.D);
+        float q = 1.f;
         if (p.post) {
             float s = 0.f;
-            for (int c = threadIdx.x; c < p.D; c += kNormThreads) {
-                const float v = ld<V>(p.o, row * p.ldo + c);
-                s = fmaf(v, v, s);
-            }
-            q = 1.f / sqrtf(block_sum(s, lds) / (float)p.D + p.eps);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s = fmaf(o[i], o[i], s);
+            q = rnorm(t.sum(s, slots), p);
         }
         float s = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += kNormThreads) {
-            const float r = stream_out<V, W>(p, row, c, block_out<V>(p, row, c, q, unit, act, slope));
-            s = fmaf(r, r, s);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float m = o[i] * q;
+            if (p.gate) {
+                float slope;
+                m *= act_of(p.act, g[i], slope);
+            }
+            r[i] = fmaf(kw[i], m, r[i]);
+            s = fmaf(r[i], r[i], s);
         }
-        const float n = 1.f / sqrtf(block_sum(s, lds) / (float)p.D + p.eps);
-        for (int c = threadIdx.x; c < p.D; c += kNormThreads) {
-            const float r = stream_out<V, W>(p, row, c, block_out<V>(p, row, c, q, unit, act, slope));
-            if (p.r) static_cast<W *>(p.r)[row * p.ldr + c] = (W)r;
-            if (p.a) static_cast<V *>(p.a)[row * p.lda + c] = (V)(r * n * (p.w2 ? p.w2[c] : 1.f));
+        const float n = rnorm(t.sum(s, slots), p);
+        if (p.r) store_row<W>(r, p.r, p.ldr, t, p.D);
+        if (p.a) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i] = r[i] * n * w2[i];
+            store_row<V>(r, p.a, p.lda, t, p.D);
         }
-        if (p.saved && threadIdx.x == 0) {
-            p.saved[row] = q;
-            p.saved[p.rows + row] = n;
+        if (p.saved && (t.start == 0)) {
+            p.saved[t.row] = q;
+            p.saved[p.rows + t.row] = n;
         }
     }
 }
 
-template <typename V, typename W>
-__global__ void __launch_bounds__(kNormThreads) k_norm_back(NormArgs p) {
-    __shared__ float lds[kNormThreads / 64];
-    float *part = p.part + (size_t)blockIdx.x * 3 * p.D;
-    for (int c = threadIdx.x; c < 3 * p.D; c += kNormThreads) part[c] = 0.f;
-    __syncthreads();
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const float q = p.post ? p.saved[row] : 1.f, n = p.saved[p.rows + row];
-        float unit, act, slope;
-        float mean2 = 0.f;
-        if (p.da) {
-            float s = 0.f;
-            for (int c = threadIdx.x; c < p.D; c += kNormThreads) {
-                const float r = stream_out<V, W>(p, row, c, block_out<V>(p, row, c, q, unit, act, slope));
-                s = fmaf(ld<V>(p.da, row * p.ldda + c) * (p.w2 ? p.w2[c] : 1.f), r * n, s);
-            }
-            mean2 = block_sum(s, lds) / (float)p.D;
+// Backward: every tensor of the row once, two row means, one after the other;
+// the column sums of a team's rows in registers, its workgroup's joined in LDS
+// (team after team, so the order is fixed) and written once.
+template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_norm_back(NormArgs p) {
+    constexpr int N = CH * NC;
+    __shared__ float slots[2][16];
+    __shared__ float join[MULTI ? 1 : 2 * 64 * N];
+    Team<CH, NC, MULTI> t;
+    float kw[N], w2[N], c1[N], c2[N];
+    load_product(kw, p.k, p.w1, t, p.D);
+    load_weights(w2, p.w2, t, p.D);
+#pragma unroll
+    for (int i = 0; i < N; ++i) c1[i] = c2[i] = 0.f;
+    for (; t.row < p.rows; t.row += t.rows_step) {
+        float o[N], g[N], r[N], dr[N], da[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = g[i] = r[i] = dr[i] = da[i] = 0.f;
+        if (p.o) load_row<V>(o, p.o, p.ldo, t, p.D);
+        if (p.gate) load_row<V>(g, p.gate, p.ldg, t, p.D);
+        if (p.res) load_row<W>(r, p.res, p.ldres, t, p.D);
+        if (p.da) load_row<V>(da, p.da, p.ldda, t, p.D);
+        if (p.dr) load_row<W>(dr, p.dr, p.lddr, t, p.D);
+        const float q = p.post ? p.saved[t.row] : 1.f, n = p.saved[p.rows + t.row];
+        float act[N];
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            o[i] *= q;                                   // unit o
+            float slope = 0.f;
+            act[i] = 1.f;
+            if (p.gate) act[i] = act_of(p.act, g[i], slope);
+            g[i] = slope;
+            r[i] = fmaf(kw[i], o[i] * act[i], r[i]) * n;   // unit r
+            c2[i] = fmaf(da[i], r[i], c2[i]);
+            da[i] *= w2[i];
+            s = fmaf(da[i], r[i], s);
         }
-        // dR at one element, and its unit r
-        const auto grad = [&](int c, float m, float &da, float &ru) {
-            const float r = stream_out<V, W>(p, row, c, m);
-            float g = p.dr ? ld<W>(p.dr, row * p.lddr + c) : 0.f;
-            da = 0.f;
-            ru = r * n;
-            if (p.da) {
-                da = ld<V>(p.da, row * p.ldda + c);
-                g = fmaf(n, fmaf(-ru, mean2, da * (p.w2 ? p.w2[c] : 1.f)), g);
-            }
-            return g;
-        };
-        float mean1 = 0.f;
-        if (p.post && p.d_o) {
-            float s = 0.f;
-            for (int c = threadIdx.x; c < p.D; c += kNormThreads) {
-                float da, ru;
-                const float m = block_out<V>(p, row, c, q, unit, act, slope);
-                const float dm = grad(c, m, da, ru) * (p.k ? p.k[c] : 1.f);
-                s = fmaf(dm * act * (p.w1 ? p.w1[c] : 1.f), unit, s);
-            }
-            mean1 = block_sum(s, lds) / (float)p.D;
+        const float mean2 = p.da ? t.sum(s, slots) / (float)p.D : 0.f;
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            dr[i] = fmaf(n, fmaf(-r[i], mean2, da[i]), dr[i]);   // dR
+            const float e = dr[i] * act[i];
+            c1[i] = fmaf(e, o[i], c1[i]);
+            act[i] = e * kw[i];
+            s = fmaf(act[i], o[i], s);
         }
-        __syncthreads();   // dres may be dr: every read of the row is done
-        for (int c = threadIdx.x; c < p.D; c += kNormThreads) {
-            float da, ru;
-            const float m = block_out<V>(p, row, c, q, unit, act, slope);
-            const float g = grad(c, m, da, ru);
-            const float w1 = p.w1 ? p.w1[c] : 1.f;
-            const float dm = g * (p.k ? p.k[c] : 1.f);
-            const float dv = dm * act;
-            if (p.dres) static_cast<W *>(p.dres)[row * p.lddres + c] = (W)g;
-            if (p.dgate) static_cast<V *>(p.dgate)[row * p.lddg + c] = (V)(dm * unit * w1 * slope);
-            if (p.d_o)
-                static_cast<V *>(p.d_o)[row * p.lddo + c] = (V)(p.post ? q * fmaf(-unit, mean1, dv * w1) : dv * w1);
-            if (p.col1) part[c] = fmaf(dv, unit, part[c]);
-            if (p.colk) part[p.D + c] = fmaf(m, g, part[p.D + c]);
-            if (p.col2) part[2 * p.D + c] = fmaf(da, ru, part[2 * p.D + c]);
+        if (p.dres) store_row<W>(dr, p.dres, p.lddres, t, p.D);
+        const float mean1 = p.post && p.d_o ? t.sum(s, slots) / (float)p.D : 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            g[i] *= dr[i] * kw[i] * o[i];
+            o[i] = p.post ? q * fmaf(-o[i], mean1, act[i]) : act[i];
         }
+        if (p.dgate) store_row<V>(g, p.dgate, p.lddg, t, p.D);
+        if (p.d_o) store_row<V>(o, p.d_o, p.lddo, t, p.D);
+    }
+    if (!p.columns) return;
+    float *part = p.part + (size_t)blockIdx.x * 2 * p.D;
+    if (!MULTI) {
+        for (int w = 0; w < t.waves; ++w) {
+            if (t.wave == w) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int at = i * 64 + t.lane;
+                    if (w) c1[i] += join[at], c2[i] += join[64 * N + at];
+                    join[at] = c1[i], join[64 * N + at] = c2[i];
+                }
+            }
+            __syncthreads();
+        }
+        if (t.wave != t.waves - 1) return;
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int c = t.start + j * t.step;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (c + i < p.D) {
+                part[c + i] = c1[j * CH + i];
+                part[p.D + c + i] = c2[j * CH + i];
+            }
     }
 }
 
-// The workgroups' column sums, in their order.
-__global__ void __launch_bounds__(64) k_norm_columns(const float *part, int groups, int D, float *dw1, float *dk,
-                                                     float *dw2) {
-    const int i = blockIdx.x * 64 + threadIdx.x;
-    if (i >= 3 * D) return;
-    float *to = i < D ? dw1 : i < 2 * D ? dk : dw2;
-    if (!to) return;
+// The workgroups' column sums: 64 columns a workgroup, its four waves take
+// every fourth group and are added in their order.  dw1 and dk are the one sum
+// of dR act o q times k and w1.
+__global__ void __launch_bounds__(256) k_norm_columns(NormArgs p, int groups, float *dw1, float *dk, float *dw2) {
+    __shared__ float join[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int i = blockIdx.x * 64 + lane;
     float s = 0.f;
-    for (int g = 0; g < groups; ++g) s += part[(size_t)g * 3 * D + i];
-    to[i % D] = s;
+    if (i < 2 * p.D)
+        for (int g = wave; g < groups; g += 4) s += p.part[(size_t)g * 2 * p.D + i];
+    join[wave][lane] = s;
+    __syncthreads();
+    if (wave || i >= 2 * p.D) return;
+    s = (join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]);
+    if (i >= p.D) {
+        if (dw2) dw2[i - p.D] = s;
+        return;
+    }
+    if (dw1) dw1[i] = p.k ? p.k[i] * s : s;
+    if (dk) dk[i] = p.w1 ? p.w1[i] * s : s;
 }
 
 const char *norm_check(const fi_norm_desc *q) {
@@ -206,9 +327,15 @@ const char *norm_check(const fi_norm_desc *q) {
     return nullptr;
 }
 
-int norm_groups(int64_t rows) { return (int)(rows < kNormGroups ? (rows < 1 ? 1 : rows) : kNormGroups); }
+// Waves of a team, and workgroups over `rows`: at most `most`, the rows spread evenly.
+int team_waves(int D) { return (D + 64 * kNormLane - 1) / (64 * kNormLane); }
 
-int64_t pitch(int64_t ld, int64_t width) { return ld ? ld : width; }
+unsigned norm_groups(int64_t rows, int D, int64_t most) {
+    const int64_t need = team_waves(D) > 1 ? rows : (rows + 3) / 4;
+    if (need <= most) return (unsigned)(need < 1 ? 1 : need);
+    const int64_t turns = (need + most - 1) / most;
+    return (unsigned)((need + turns - 1) / turns);
+}
 
 void norm_args(const fi_norm_desc *q, NormArgs &a) {
     a.rows = q->rows;
@@ -216,24 +343,40 @@ void norm_args(const fi_norm_desc *q, NormArgs &a) {
     a.post = q->post_norm;
     a.act = q->act;
     a.eps = q->eps;
-    a.ldo = pitch(q->ld_o, a.D);
-    a.ldg = pitch(q->ld_gate, a.D);
-    a.ldres = pitch(q->ld_res, a.D);
-    a.ldr = pitch(q->ld_r, a.D);
-    a.lda = pitch(q->ld_a, a.D);
-    a.lddr = pitch(q->ld_dr, a.D);
-    a.ldda = pitch(q->ld_da, a.D);
-    a.lddo = pitch(q->ld_do, a.D);
-    a.lddg = pitch(q->ld_dgate, a.D);
-    a.lddres = pitch(q->ld_dres, a.D);
+    a.ldo = pitch_or(q->ld_o, a.D);
+    a.ldg = pitch_or(q->ld_gate, a.D);
+    a.ldres = pitch_or(q->ld_res, a.D);
+    a.ldr = pitch_or(q->ld_r, a.D);
+    a.lda = pitch_or(q->ld_a, a.D);
+    a.lddr = pitch_or(q->ld_dr, a.D);
+    a.ldda = pitch_or(q->ld_da, a.D);
+    a.lddo = pitch_or(q->ld_do, a.D);
+    a.lddg = pitch_or(q->ld_dgate, a.D);
+    a.lddres = pitch_or(q->ld_dres, a.D);
+}
+
+template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
+void launch(const NormArgs &a, bool backward, unsigned groups, unsigned threads, hipStream_t st) {
+    if (backward)
+        hipLaunchKernelGGL((k_norm_back<V, W, CH, NC, MULTI, THREADS>), dim3(groups), dim3(threads), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_norm<V, W, CH, NC, MULTI, THREADS>), dim3(groups), dim3(threads), 0, st, a);
 }
 
 template <typename V, typename W>
 void launch(const NormArgs &a, bool backward, unsigned groups, hipStream_t st) {
-    if (backward)
-        hipLaunchKernelGGL((k_norm_back<V, W>), dim3(groups), dim3(kNormThreads), 0, st, a);
+    constexpr int CH = sizeof(W) == 2 ? 8 : 4;
+    const int waves = team_waves(a.D);
+    if (a.D <= 64 * CH)
+        launch<V, W, CH, 1, false, 256>(a, backward, groups, 256, st);
+    else if (a.D <= 128 * CH)
+        launch<V, W, CH, 2, false, 256>(a, backward, groups, 256, st);
+    else if (waves == 1)
+        launch<V, W, CH, kNormLane / CH, false, 256>(a, backward, groups, 256, st);
+    else if (waves <= 8)
+        launch<V, W, CH, kNormLane / CH, true, 512>(a, backward, groups, waves * 64, st);
     else
-        hipLaunchKernelGGL((k_norm<V, W>), dim3(groups), dim3(kNormThreads), 0, st, a);
+        launch<V, W, CH, kNormLane / CH, true, 1024>(a, backward, groups, waves * 64, st);
 }
 
 void launch(const fi_norm_desc *q, const NormArgs &a, bool backward, unsigned groups, hipStream_t st) {
@@ -266,7 +409,7 @@ extern "C" {
 
 size_t fi_norm_workspace_bytes(const fi_norm_desc *desc) {
     if (norm_check(desc)) return 0;
-    return up256((size_t)norm_groups(desc->rows) * 3 * desc->channels * sizeof(float));
+    return up256((size_t)norm_groups(desc->rows, desc->channels, kNormGroups) * 2 * desc->channels * sizeof(float));
 }
 
 fi_status fi_norm_forward(const fi_norm_desc *desc, const void *o, const void *gate, const void *res,
@@ -288,7 +431,7 @@ fi_status fi_norm_forward(const fi_norm_desc *desc, const void *o, const void *g
         return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
     n.o = o, n.gate = gate, n.res = res, n.w1 = post_weight, n.k = scale, n.w2 = pre_weight;
     n.r = r, n.a = a, n.saved = saved;
-    launch(desc, n, false, (unsigned)std::min<int64_t>(n.rows, 1 << 20), (hipStream_t)stream);
+    launch(desc, n, false, norm_groups(n.rows, n.D, kNormForwardGroups), (hipStream_t)stream);
     return op_launched(call);
 }
 
@@ -322,13 +465,12 @@ fi_status fi_norm_backward(const fi_norm_desc *desc, const void *o, const void *
         return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
     n.o = o, n.gate = gate, n.res = res, n.w1 = post_weight, n.k = scale, n.w2 = pre_weight;
     n.saved = (float *)saved, n.dr = dr, n.da = da, n.d_o = d_o, n.dgate = dgate, n.dres = dres;
-    n.part = (float *)workspace, n.col1 = dpost, n.colk = dscale, n.col2 = dpre;
+    n.part = (float *)workspace, n.columns = dpost || dscale || dpre;
     const hipStream_t st = (hipStream_t)stream;
-    const int groups = n.rows > 0 ? norm_groups(n.rows) : 0;
-    if (groups) launch(desc, n, true, (unsigned)groups, st);
-    if (dpost || dscale || dpre)
-        hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)((3 * D + 63) / 64)), dim3(64), 0, st, (const float *)workspace,
-                           groups, n.D, dpost, dscale, dpre);
+    const unsigned groups = n.rows > 0 ? norm_groups(n.rows, n.D, kNormGroups) : 0;
+    if (groups) launch(desc, n, true, groups, st);
+    if (n.columns)
+        hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)((2 * D + 63) / 64)), dim3(256), 0, st, n, (int)groups, dpost, dscale, dpre);
     return op_launched(call);
 }
 

@@ -268,19 +268,17 @@ size_t scan_workspace(const Plan &p, bool backward) {
     return std::max<size_t>(backward ? p.part * 3 : p.chunks > 1 ? p.part * 2 : 0, 256);
 }
 
-int64_t pitch(int64_t ld, int64_t width) { return ld ? ld : width; }
-
 void scan_args(const fi_scan_desc *q, const Plan &pl, ScanArgs &a) {
     a.T = q->T;
     a.B = q->batch;
     a.D = q->channels;
     a.chunks = (int)pl.chunks;
-    a.ldx = pitch(q->ld_x, a.D);
-    a.ldg = pitch(q->ld_gate, a.D);
-    a.ldy = pitch(q->ld_y, a.D);
-    a.lddy = pitch(q->ld_dy, a.D);
-    a.lddx = pitch(q->ld_dx, a.D);
-    a.lddg = pitch(q->ld_dgate, a.D);
+    a.ldx = pitch_or(q->ld_x, a.D);
+    a.ldg = pitch_or(q->ld_gate, a.D);
+    a.ldy = pitch_or(q->ld_y, a.D);
+    a.lddy = pitch_or(q->ld_dy, a.D);
+    a.lddx = pitch_or(q->ld_dx, a.D);
+    a.lddg = pitch_or(q->ld_dgate, a.D);
 }
 
 template <typename V, int IN>
