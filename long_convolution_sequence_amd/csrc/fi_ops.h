@@ -78,25 +78,52 @@ inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 template <typename T, int CH>
 using Chunk __attribute__((aligned(sizeof(T)))) = T __attribute__((ext_vector_type(CH)));
 
-// Values p[0 .. min(n, CH)) of a chunk, zeros behind them.
-template <typename T, int CH>
-__device__ __forceinline__ Chunk<T, CH> load_chunk(const T *p, int n) {
-    if (n >= CH) return *reinterpret_cast<const Chunk<T, CH> *>(p);
-    Chunk<T, CH> v;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) v[i] = i < n ? p[i] : (T)0.f;
-    return v;
+// A lane's chunk of a row of D >= CH columns that would begin at column c: it is
+// read from `at` = min(c, D - CH), so always whole and inside the row, without a
+// branch (a lane-by-lane tail costs its wave a wait for memory at every tensor).
+// The lane owns the elements from `skip` on; the others are a neighbour's.
+template <int CH>
+struct Place {
+    unsigned at;
+    int skip;
+    __device__ __forceinline__ Place() {}
+    __device__ __forceinline__ Place(int c, int D) {
+        const int a = c < D - CH ? c : D - CH;
+        at = (unsigned)a;
+        skip = c - a < CH ? c - a : CH;
+        // kept as a value of its own: as a sum the compiler would carry it, and
+        // with it every address, in 64 bits a lane
+        asm("" : "+v"(at));
+    }
+};
+
+// The address of a row's element as a row address for the whole wave and a
+// 32-bit byte offset of the lane.
+template <typename T>
+__device__ __forceinline__ const T *in_row(const T *row, unsigned at) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + at * (unsigned)sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ T *in_row(T *row, unsigned at) {
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(row) + at * (unsigned)sizeof(T));
 }
 
 template <typename T, int CH>
-__device__ __forceinline__ void store_chunk(T *p, int n, Chunk<T, CH> v) {
-    if (n >= CH) {
-        *reinterpret_cast<Chunk<T, CH> *>(p) = v;
-        return;
-    }
+__device__ __forceinline__ Chunk<T, CH> load_chunk(const T *row, const Place<CH> &w) {
+    return *reinterpret_cast<const Chunk<T, CH> *>(in_row(row, w.at));
+}
+
+// TAIL: a chunk may be owned in part (D is no multiple of CH).
+template <bool TAIL, typename T, int CH>
+__device__ __forceinline__ void store_chunk(T *row, const Place<CH> &w, Chunk<T, CH> v) {
+    if (w.skip == 0)
+        *reinterpret_cast<Chunk<T, CH> *>(in_row(row, w.at)) = v;
+    else if (TAIL && w.skip < CH) {
+        T *to = in_row(row, w.at);
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
-        if (i < n) p[i] = v[i];
+        for (int i = 1; i < CH; ++i)
+            if (i >= w.skip) to[i] = v[i];
+    }
 }
 
 // Sum over the 64 lanes, in every lane: shifts within rows of 16 lanes, then

@@ -59,27 +59,23 @@ __device__ __forceinline__ float act_of(int act, float g, float &slope) {
 // their column sums) in registers over all its rows.
 template <int CH, int NC, bool MULTI>
 struct Team {
-    int start, step;       // first column of this lane, columns between its chunks
+    Place<CH> at[NC];      // this lane's chunks
+    bool first;            // the lane of column 0
     int waves, wave, lane;
     int64_t row, rows_step;
     int turn;
 
-    __device__ __forceinline__ Team() {
+    __device__ __forceinline__ Team(int D) {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         waves = blockDim.x >> 6;
         turn = 0;
-        if (MULTI) {
-            start = (wave * 64 + lane) * CH;
-            step = waves * 64 * CH;
-            row = blockIdx.x;
-            rows_step = gridDim.x;
-        } else {
-            start = lane * CH;
-            step = 64 * CH;
-            row = blockIdx.x * (int64_t)waves + wave;
-            rows_step = gridDim.x * (int64_t)waves;
-        }
+        const int start = ((MULTI ? wave * 64 : 0) + lane) * CH, step = (MULTI ? waves : 1) * 64 * CH;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) at[j] = Place<CH>(start + j * step, D);
+        first = start == 0;
+        row = MULTI ? blockIdx.x : blockIdx.x * (int64_t)waves + wave;
+        rows_step = MULTI ? gridDim.x : gridDim.x * (int64_t)waves;
     }
     // Sum over the team, in every lane.  Two sets of slots by turns: a wave that
     // writes a set has passed the barrier after everybody's reads of that set.
@@ -95,106 +91,137 @@ struct Team {
     }
 };
 
-template <typename T, int CH, int NC, bool MULTI>
-__device__ __forceinline__ void load_row(float (&v)[NC * CH], const void *p, int64_t ld, const Team<CH, NC, MULTI> &t,
-                                         int D) {
-    const T *from = static_cast<const T *>(p) + t.row * ld;
-    Chunk<T, CH> raw[NC];
+// A row's values as they are loaded.  ALL: the tensor is there; else a null one
+// reads as zeros.
+template <bool ALL, typename T, int CH, int NC>
+struct Raw {
+    Chunk<T, CH> v[NC];
+
+    template <bool MULTI>
+    __device__ __forceinline__ void load(const void *p, int64_t ld, int64_t row, const Team<CH, NC, MULTI> &t) {
+        if (!ALL && !p) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) v[j] = (Chunk<T, CH>)(T)0.f;
+            return;
+        }
+        const T *from = static_cast<const T *>(p) + row * ld;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = load_chunk<T, CH>(from, t.at[j]);
+    }
+    __device__ __forceinline__ void get(float (&f)[NC * CH]) const {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int i = 0; i < CH; ++i) f[j * CH + i] = (float)v[j][i];
+    }
+};
+
+template <bool TAIL, typename T, int CH, int NC, bool MULTI>
+__device__ __forceinline__ void store_row(const float (&v)[NC * CH], void *p, int64_t ld,
+                                          const Team<CH, NC, MULTI> &t) {
+    T *to = static_cast<T *>(p) + t.row * ld;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        const int c = t.start + j * t.step;
-        raw[j] = load_chunk<T, CH>(from + c, D - c);
+        Chunk<T, CH> raw;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) raw[i] = (T)v[j * CH + i];
+        store_chunk<TAIL, T, CH>(to, t.at[j], raw);
+    }
+}
+
+// Sum of the squares of what this lane owns.
+template <bool TAIL, int CH, int NC, bool MULTI>
+__device__ __forceinline__ float squares(const float (&v)[NC * CH], const Team<CH, NC, MULTI> &t) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        float c = 0.f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const float x = TAIL && i < t.at[j].skip ? 0.f : v[j * CH + i];
+            c = fmaf(x, x, c);
+        }
+        s += t.at[j].skip < CH ? c : 0.f;
+    }
+    return s;
+}
+
+// A lane's weights: kw = k w1 (the two meet in every use of them in a row) and
+// w2, 1 where none is given.  The loads do not wait for one another: a weight
+// that is not given is read from another's place.  OWNED: 0 for an element that
+// the lane does not own.
+template <bool OWNED, int CH, int NC, bool MULTI>
+__device__ __forceinline__ void load_weights(float (&kw)[NC * CH], float (&w2)[NC * CH], const NormArgs &p,
+                                             const Team<CH, NC, MULTI> &t) {
+    const float *any = p.w1 ? p.w1 : p.k ? p.k : p.w2;
+    Chunk<float, CH> a[NC], b[NC], c[NC];
+    if (any) {
+        const float *pa = p.w1 ? p.w1 : any, *pb = p.k ? p.k : any, *pc = p.w2 ? p.w2 : any;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            a[j] = load_chunk<float, CH>(pa, t.at[j]);
+            b[j] = load_chunk<float, CH>(pb, t.at[j]);
+            c[j] = load_chunk<float, CH>(pc, t.at[j]);
+        }
     }
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
-        for (int i = 0; i < CH; ++i) v[j * CH + i] = (float)raw[j][i];
-}
-
-template <typename T, int CH, int NC, bool MULTI>
-__device__ __forceinline__ void store_row(const float (&v)[NC * CH], void *p, int64_t ld,
-                                          const Team<CH, NC, MULTI> &t, int D) {
-    T *to = static_cast<T *>(p) + t.row * ld;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        const int c = t.start + j * t.step;
-        Chunk<T, CH> raw;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) raw[i] = (T)v[j * CH + i];
-        store_chunk<T, CH>(to + c, D - c, raw);
-    }
-}
-
-template <int CH, int NC, bool MULTI>
-__device__ __forceinline__ void load_weights(float (&v)[NC * CH], const float *w, const Team<CH, NC, MULTI> &t,
-                                             int D) {
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        const int c = t.start + j * t.step;
-        Chunk<float, CH> raw;
-        if (w) raw = load_chunk<float, CH>(w + c, D - c);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) v[j * CH + i] = w ? raw[i] : 1.f;
-    }
-}
-
-// k w1: the two weights of a column meet in every use of them in a row
-template <int CH, int NC, bool MULTI>
-__device__ __forceinline__ void load_product(float (&v)[NC * CH], const float *k, const float *w1,
-                                             const Team<CH, NC, MULTI> &t, int D) {
-    float w[NC * CH];
-    load_weights(v, k, t, D);
-    load_weights(w, w1, t, D);
-#pragma unroll
-    for (int i = 0; i < NC * CH; ++i) v[i] *= w[i];
+        for (int i = 0; i < CH; ++i) {
+            const bool own = !OWNED || i >= t.at[j].skip;
+            kw[j * CH + i] = own ? (p.w1 ? a[j][i] : 1.f) * (p.k ? b[j][i] : 1.f) : 0.f;
+            w2[j * CH + i] = own ? (p.w2 ? c[j][i] : 1.f) : 0.f;
+        }
 }
 
 __device__ __forceinline__ float rnorm(float squares, const NormArgs &p) {
     return 1.f / sqrtf(squares / (float)p.D + p.eps);
 }
 
-// Forward: HBM-bound, every tensor once.
-template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
+// Forward: HBM-bound, every tensor once.  A team of several waves reads its next
+// row before it works on this one: a barrier a row holds all its waves, and few
+// such teams fit a CU.  ALL: o, gate and res are there.
+template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
     constexpr int N = CH * NC;
+    constexpr bool AHEAD = MULTI && THREADS <= 512;
     __shared__ float slots[2][16];
-    Team<CH, NC, MULTI> t;
+    Team<CH, NC, MULTI> t(p.D);
+    Raw<ALL, V, CH, NC> raw_o, raw_g;
+    Raw<ALL, W, CH, NC> raw_r;
+    const auto fetch = [&](int64_t row) {
+        raw_o.load(p.o, p.ldo, row, t);
+        raw_g.load(p.gate, p.ldg, row, t);
+        raw_r.load(p.res, p.ldres, row, t);
+    };
+    if (AHEAD && t.row < p.rows) fetch(t.row);
     float kw[N], w2[N];
-    load_product(kw, p.k, p.w1, t, p.D);
-    load_weights(w2, p.w2, t, p.D);
+    load_weights<false>(kw, w2, p, t);
     for (; t.row < p.rows; t.row += t.rows_step) {
         float o[N], g[N], r[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = 0.f, g[i] = 0.f, r[i] = 0.f;
-        if (p.o) load_row<V>(o, p.o, p.ldo, t, p.D);
-        if (p.gate) load_row<V>(g, p.gate, p.ldg, t, p.D);
-        if (p.res) load_row<W>(r, p.res, p.ldres, t, p.D);
-        float q = 1.f;
-        if (p.post) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) s = fmaf(o[i], o[i], s);
-            q = rnorm(t.sum(s, slots), p);
-        }
-        float s = 0.f;
+        if (!AHEAD) fetch(t.row);
+        raw_o.get(o);
+        raw_g.get(g);
+        raw_r.get(r);
+        if (AHEAD && t.row + t.rows_step < p.rows) fetch(t.row + t.rows_step);
+        const float q = p.post ? rnorm(t.sum(squares<TAIL>(o, t), slots), p) : 1.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float m = o[i] * q;
-            if (p.gate) {
+            if (ALL || p.gate) {
                 float slope;
                 m *= act_of(p.act, g[i], slope);
             }
             r[i] = fmaf(kw[i], m, r[i]);
-            s = fmaf(r[i], r[i], s);
         }
-        const float n = rnorm(t.sum(s, slots), p);
-        if (p.r) store_row<W>(r, p.r, p.ldr, t, p.D);
+        const float n = rnorm(t.sum(squares<TAIL>(r, t), slots), p);
+        if (p.r) store_row<TAIL, W>(r, p.r, p.ldr, t);
         if (p.a) {
 #pragma unroll
             for (int i = 0; i < N; ++i) r[i] = r[i] * n * w2[i];
-            store_row<V>(r, p.a, p.lda, t, p.D);
+            store_row<TAIL, V>(r, p.a, p.lda, t);
         }
-        if (p.saved && (t.start == 0)) {
+        if (p.saved && t.first) {
             p.saved[t.row] = q;
             p.saved[p.rows + t.row] = n;
         }
@@ -203,27 +230,38 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
 
 // Backward: every tensor of the row once, two row means, one after the other;
 // the column sums of a team's rows in registers, its workgroup's joined in LDS
-// (team after team, so the order is fixed) and written once.
-template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_norm_back(NormArgs p) {
+// (team after team, so the order is fixed) and written once.  Elements that a
+// lane does not own have weights of zero, so both means pass them by.
+template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) k_norm_back(NormArgs p) {
     constexpr int N = CH * NC;
+    constexpr bool AHEAD = MULTI && THREADS <= 512 && sizeof(W) == 2;   // with fp32 rows it would spill
     __shared__ float slots[2][16];
     __shared__ float join[MULTI ? 1 : 2 * 64 * N];
-    Team<CH, NC, MULTI> t;
+    Team<CH, NC, MULTI> t(p.D);
+    Raw<ALL, V, CH, NC> raw_o, raw_g, raw_da;
+    Raw<ALL, W, CH, NC> raw_r, raw_dr;
+    const auto fetch = [&](int64_t row) {
+        raw_o.load(p.o, p.ldo, row, t);
+        raw_g.load(p.gate, p.ldg, row, t);
+        raw_r.load(p.res, p.ldres, row, t);
+        raw_da.load(p.da, p.ldda, row, t);
+        raw_dr.load(p.dr, p.lddr, row, t);
+    };
+    if (AHEAD && t.row < p.rows) fetch(t.row);
     float kw[N], w2[N], c1[N], c2[N];
-    load_product(kw, p.k, p.w1, t, p.D);
-    load_weights(w2, p.w2, t, p.D);
+    load_weights<true>(kw, w2, p, t);
 #pragma unroll
     for (int i = 0; i < N; ++i) c1[i] = c2[i] = 0.f;
     for (; t.row < p.rows; t.row += t.rows_step) {
         float o[N], g[N], r[N], dr[N], da[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = g[i] = r[i] = dr[i] = da[i] = 0.f;
-        if (p.o) load_row<V>(o, p.o, p.ldo, t, p.D);
-        if (p.gate) load_row<V>(g, p.gate, p.ldg, t, p.D);
-        if (p.res) load_row<W>(r, p.res, p.ldres, t, p.D);
-        if (p.da) load_row<V>(da, p.da, p.ldda, t, p.D);
-        if (p.dr) load_row<W>(dr, p.dr, p.lddr, t, p.D);
+        if (!AHEAD) fetch(t.row);
+        raw_o.get(o);
+        raw_g.get(g);
+        raw_r.get(r);
+        raw_da.get(da);
+        raw_dr.get(dr);
+        if (AHEAD && t.row + t.rows_step < p.rows) fetch(t.row + t.rows_step);
         const float q = p.post ? p.saved[t.row] : 1.f, n = p.saved[p.rows + t.row];
         float act[N];
         float s = 0.f;
@@ -232,14 +270,14 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormArgs p) {
             o[i] *= q;                                   // unit o
             float slope = 0.f;
             act[i] = 1.f;
-            if (p.gate) act[i] = act_of(p.act, g[i], slope);
+            if (ALL || p.gate) act[i] = act_of(p.act, g[i], slope);
             g[i] = slope;
             r[i] = fmaf(kw[i], o[i] * act[i], r[i]) * n;   // unit r
             c2[i] = fmaf(da[i], r[i], c2[i]);
             da[i] *= w2[i];
             s = fmaf(da[i], r[i], s);
         }
-        const float mean2 = p.da ? t.sum(s, slots) / (float)p.D : 0.f;
+        const float mean2 = ALL || p.da ? t.sum(s, slots) / (float)p.D : 0.f;
         s = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -249,15 +287,15 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormArgs p) {
             act[i] = e * kw[i];
             s = fmaf(act[i], o[i], s);
         }
-        if (p.dres) store_row<W>(dr, p.dres, p.lddres, t, p.D);
+        if (p.dres) store_row<TAIL, W>(dr, p.dres, p.lddres, t);
         const float mean1 = p.post && p.d_o ? t.sum(s, slots) / (float)p.D : 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             g[i] *= dr[i] * kw[i] * o[i];
             o[i] = p.post ? q * fmaf(-o[i], mean1, act[i]) : act[i];
         }
-        if (p.dgate) store_row<V>(g, p.dgate, p.lddg, t, p.D);
-        if (p.d_o) store_row<V>(o, p.d_o, p.lddo, t, p.D);
+        if (p.dgate) store_row<TAIL, V>(g, p.dgate, p.lddg, t);
+        if (p.d_o) store_row<TAIL, V>(o, p.d_o, p.lddo, t);
     }
     if (!p.columns) return;
     float *part = p.part + (size_t)blockIdx.x * 2 * p.D;
@@ -277,30 +315,32 @@ __global__ void __launch_bounds__(THREADS) k_norm_back(NormArgs p) {
     }
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        const int c = t.start + j * t.step;
+        Chunk<float, CH> s1, s2;
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (c + i < p.D) {
-                part[c + i] = c1[j * CH + i];
-                part[p.D + c + i] = c2[j * CH + i];
-            }
+        for (int i = 0; i < CH; ++i) s1[i] = c1[j * CH + i], s2[i] = c2[j * CH + i];
+        store_chunk<TAIL, float, CH>(part, t.at[j], s1);
+        store_chunk<TAIL, float, CH>(part + p.D, t.at[j], s2);
     }
 }
 
-// The workgroups' column sums: 64 columns a workgroup, its four waves take
-// every fourth group and are added in their order.  dw1 and dk are the one sum
-// of dR act o q times k and w1.
-__global__ void __launch_bounds__(256) k_norm_columns(NormArgs p, int groups, float *dw1, float *dk, float *dw2) {
-    __shared__ float join[4][64];
+// The workgroups' column sums: 64 columns a workgroup, its sixteen waves take
+// every sixteenth group and are added in their order.  dw1 and dk are the one
+// sum of dR act o q times k and w1.  A wave's loads do not wait for each other.
+__global__ void __launch_bounds__(1024) k_norm_columns(NormArgs p, int groups, float *dw1, float *dk, float *dw2) {
+    __shared__ float join[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i = blockIdx.x * 64 + lane;
     float s = 0.f;
-    if (i < 2 * p.D)
-        for (int g = wave; g < groups; g += 4) s += p.part[(size_t)g * 2 * p.D + i];
+    if (i < 2 * p.D) {
+#pragma unroll 8
+        for (int g = wave; g < groups; g += 16) s += p.part[(size_t)g * 2 * p.D + i];
+    }
     join[wave][lane] = s;
     __syncthreads();
     if (wave || i >= 2 * p.D) return;
-    s = (join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]);
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += join[w][lane];
     if (i >= p.D) {
         if (dw2) dw2[i - p.D] = s;
         return;
@@ -355,19 +395,35 @@ void norm_args(const fi_norm_desc *q, NormArgs &a) {
     a.lddres = pitch_or(q->ld_dres, a.D);
 }
 
-template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
+template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS, bool TAIL, bool ALL>
 void launch(const NormArgs &a, bool backward, unsigned groups, unsigned threads, hipStream_t st) {
     if (backward)
-        hipLaunchKernelGGL((k_norm_back<V, W, CH, NC, MULTI, THREADS>), dim3(groups), dim3(threads), 0, st, a);
+        hipLaunchKernelGGL((k_norm_back<V, W, CH, NC, MULTI, TAIL, ALL, THREADS>), dim3(groups), dim3(threads), 0, st,
+                           a);
     else
-        hipLaunchKernelGGL((k_norm<V, W, CH, NC, MULTI, THREADS>), dim3(groups), dim3(threads), 0, st, a);
+        hipLaunchKernelGGL((k_norm<V, W, CH, NC, MULTI, TAIL, ALL, THREADS>), dim3(groups), dim3(threads), 0, st, a);
+}
+
+// With every tensor of a row given, without (and always at the smallest and
+// widest rows) the kernels that check for each.
+template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
+void launch(const NormArgs &a, bool backward, unsigned groups, unsigned threads, hipStream_t st) {
+    const bool all = a.o && a.gate && a.res && (!backward || (a.dr && a.da));
+    if constexpr (CH > 1 && THREADS <= 512) {
+        if (all && a.D % CH == 0)
+            return launch<V, W, CH, NC, MULTI, THREADS, false, true>(a, backward, groups, threads, st);
+        if (all) return launch<V, W, CH, NC, MULTI, THREADS, true, true>(a, backward, groups, threads, st);
+    }
+    launch<V, W, CH, NC, MULTI, THREADS, true, false>(a, backward, groups, threads, st);
 }
 
 template <typename V, typename W>
 void launch(const NormArgs &a, bool backward, unsigned groups, hipStream_t st) {
     constexpr int CH = sizeof(W) == 2 ? 8 : 4;
     const int waves = team_waves(a.D);
-    if (a.D <= 64 * CH)
+    if (a.D < CH)
+        launch<V, W, 1, 1, false, 256>(a, backward, groups, 256, st);
+    else if (a.D <= 64 * CH)
         launch<V, W, CH, 1, false, 256>(a, backward, groups, 256, st);
     else if (a.D <= 128 * CH)
         launch<V, W, CH, 2, false, 256>(a, backward, groups, 256, st);
@@ -470,7 +526,7 @@ fi_status fi_norm_backward(const fi_norm_desc *desc, const void *o, const void *
     const unsigned groups = n.rows > 0 ? norm_groups(n.rows, n.D, kNormGroups) : 0;
     if (groups) launch(desc, n, true, groups, st);
     if (n.columns)
-        hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)((2 * D + 63) / 64)), dim3(256), 0, st, n, (int)groups, dpost, dscale, dpre);
+        hipLaunchKernelGGL(k_norm_columns, dim3((unsigned)((2 * D + 63) / 64)), dim3(1024), 0, st, n, (int)groups, dpost, dscale, dpre);
     return op_launched(call);
 }
 
