@@ -2,22 +2,40 @@
 //
 // With d_t = 1 - sigmoid(z_t) and b_t = e(d_t) x_t a position is the map
 // s -> s - d_t s + b_t, affine in the state, and so is a run of positions:
-// s -> A s + S.  The length is cut into chunks; the maps of all chunks are
-// formed at once, the states at the chunks' ends follow one from the other,
-// and every chunk then runs from its own start state.  The gradients are the
-// same recurrence from the end: D_t = dy_t + c, c <- D_t - d_t D_t.
+// s -> A s + S.  The gradients are the same recurrence from the end:
+// D_t = dy_t + c, c <- D_t - d_t D_t.
 //
 // The state is updated as s - d s, never as a s with a = 1 - d rounded to
 // fp32: for decays near one (a memory of thousands of positions) the rounding
 // of a alone is a relative error of 2^-25 / d in the memory's length.
+//
+// One pass over the data (k_scan_tile, k_scan_back).  A workgroup holds a tile
+// of kTile positions x kCols columns in registers: a lane has kStep positions of
+// CH neighbouring columns (a "segment"), 16 lanes cover the tile's columns, the
+// other lanes and the waves go on in time.  Every lane forms its segment's map;
+// the first wave (one column a lane now) joins the segments' maps to the tile's
+// map, publishes it, and finds the state before the tile from the tiles before:
+// the nearest one that has published its end state, and the maps in between.
+// Tiles are numbered by a counter as workgroups begin, all columns of a time
+// before the next time: a tile only waits for tiles with lower numbers, which
+// are running or done, so every wait ends.
+//
+// The join is the same chain of fmas whichever tile the state was found at
+// (s <- A s + S, tile after tile), so results do not depend on timing.
 #include "fi_ops.h"
 
 namespace fi {
 
 namespace {
 
-constexpr int kScanChunk = 256;   // positions per chunk, and per state that is kept for the backward pass
-constexpr int kScanSub = 16;      // states held in registers at a time by the backward pass
+constexpr int kStep = 8;                        // positions of a lane
+constexpr int kRow = 16;                        // lanes along a row
+constexpr int kWaves = 8;                       // waves of a tile at most
+constexpr int kSeg = kWaves * 64 / kRow;        // segments of a tile in time
+constexpr int kTile = kSeg * kStep;             // positions of a tile
+constexpr int kWindow = 8;                      // tiles looked back at together
+constexpr int kSerial = 16;                     // lengths up to this run one position after the other
+constexpr int kPolls = 1 << 20;                 // looks at unfinished tiles before a wait gives up
 
 struct ScanArgs {
     const void *x, *gate, *dy;
@@ -25,13 +43,17 @@ struct ScanArgs {
     const float *bias, *state, *dfinal;
     float *final, *dstate;
     const int32_t *lengths;
-    float *saved;              // [chunks][R] state after each chunk
-    float *mul, *add;          // [chunks][R] maps of the chunks
-    float *pbias;              // [chunks][R] partial sums of the bias gradient
+    float *saved;              // [tiles][R] state after each tile
+    unsigned long long *link;  // [tiles][R] a tile's map, then its end state (see Link)
+    unsigned *ticket;          // tiles begun
+    float *pbias;              // [tiles][R] partial sums of the bias gradient
     int64_t T;
     int64_t ldx, ldg, ldy, lddy, lddx, lddg;
     int B, D;
-    int chunks;
+    int tiles;                 // along T
+    int lanes_row;             // lanes that cover one row of D columns
+    int lanes_all;             // and all B rows
+    int col_tiles;
 };
 
 __device__ __forceinline__ float sigmoid_neg(float z) {   // 1 - sigmoid(z) = 1 / (1 + e^z)
@@ -54,183 +76,424 @@ __device__ __forceinline__ float gate_slope(float d, float x, float before) {
     return a * (d * before - a * __builtin_amdgcn_sqrtf(d * __builtin_amdgcn_rcpf(2.f - d)) * x);
 }
 
-struct Column {                 // one (b, c) column of one chunk
-    int64_t t0, t1, end;        // the chunk's positions, and where the row's own positions end
-    int r, b, c;
-    float bias;
+// ---- what passes between tiles -------------------------------------------------
+//
+// One 64-bit word per tile and column, written and read whole (relaxed atomics
+// of device scope: the value is its own flag): all ones = nothing yet; else
+// {A, S}, the tile's map; then {kDone, state}, the state at the tile's end.
+
+constexpr unsigned long long kNothing = ~0ull;
+constexpr unsigned kDone = 0xfffffffeu;         // a NaN that no sum or product gives
+
+__device__ __forceinline__ void link_put(unsigned long long *at, unsigned a, float s) {
+    unsigned v = __float_as_uint(s);
+    if (v == 0xffffffffu) v = 0x7fc00000u;      // a NaN's payload must not read as kNothing
+    __hip_atomic_store(at, (unsigned long long)a << 32 | v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void link_put_map(unsigned long long *at, float A, float S) {
+    unsigned a = __float_as_uint(A);
+    if (a >= kDone) a = 0x7fc00000u;
+    link_put(at, a, S);
+}
+
+// The state at the end of the tile before, for one column.  `at` is this tile's
+// word, `step` the words between tiles (negative: the tiles come from the end),
+// `have` the number of tiles before it (>= 1).  A wait that gives up leaves NaN.
+__device__ float link_state(const unsigned long long *at, int64_t step, int have) {
+    const int n = have < kWindow ? have : kWindow;
+    for (int polls = 0; polls < kPolls; ++polls) {
+        unsigned long long v[kWindow];
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i)
+            v[i] = i < n ? __hip_atomic_load(at - (i + 1) * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : kNothing;
+        // the nearest tile with its state, if every nearer one has its map
+        int found = -1;
+        bool open = true;
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i) {
+            open = open && v[i] != kNothing;
+            if (open && (unsigned)(v[i] >> 32) == kDone) {
+                found = i;
+                open = false;
+            }
+        }
+        if (found >= 0) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = kWindow - 1; i >= 0; --i) {
+                const float lo = __uint_as_float((unsigned)v[i]);
+                if (i == found) s = lo;
+                if (i < found) s = fmaf(__uint_as_float((unsigned)(v[i] >> 32)), s, lo);
+            }
+            return s;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return __uint_as_float(0x7fc00000u);
+}
+
+__global__ void __launch_bounds__(256) k_scan_clear(unsigned long long *link, size_t n, unsigned *ticket) {
+    for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += gridDim.x * (size_t)256) link[i] = kNothing;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+}
+
+// ---- a lane's part of a tile ------------------------------------------------------
+
+template <int CH>
+struct Lane {
+    Place<CH> w;
+    int b;             // batch row
+    int64_t t0;        // first position
+    int live, inside;  // of its kStep positions: before the row's length, before T
+
+    // column group g of the tile's column tile, positions from t0 on
+    __device__ __forceinline__ Lane(const ScanArgs &p, int g, int64_t t0_) {
+        const int in = g < p.lanes_all ? g : p.lanes_all - 1;
+        b = in / p.lanes_row;
+        w = Place<CH>((in - b * p.lanes_row) * CH, p.D);
+        if (in != g) w.skip = CH;
+        t0 = t0_;
+        int64_t len = p.T;
+        if (p.lengths) {
+            const int64_t n = p.lengths[b];
+            len = n < 0 ? 0 : n < p.T ? n : p.T;
+        }
+        live = clip(len - t0);
+        inside = clip(p.T - t0);
+    }
+    static __device__ __forceinline__ int clip(int64_t n) { return n < 0 ? 0 : n < kStep ? (int)n : kStep; }
 };
 
-__device__ __forceinline__ bool column(const ScanArgs &p, Column &k) {
-    k.r = blockIdx.x * blockDim.x + threadIdx.x;
-    if (k.r >= p.B * p.D) return false;
-    k.b = k.r / p.D;
-    k.c = k.r - k.b * p.D;
-    k.t0 = (int64_t)blockIdx.y * kScanChunk;
-    k.t1 = k.t0 + kScanChunk < p.T ? k.t0 + kScanChunk : p.T;
+// kStep rows of a lane; positions at T or later read the row T - 1 (unused).
+template <typename V, int CH>
+__device__ __forceinline__ void load_steps(Chunk<V, CH> (&v)[kStep], const void *p, int64_t ld, const ScanArgs &q,
+                                           const Lane<CH> &l, bool whole) {
+    const int64_t step = ld * q.B;
+    const V *row = static_cast<const V *>(p) + l.b * ld + l.w.at;
+    if (whole) {
+        row += l.t0 * step;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) v[k] = *reinterpret_cast<const Chunk<V, CH> *>(row + k * step);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+            const int64_t t = l.t0 + k < q.T ? l.t0 + k : q.T - 1;
+            v[k] = *reinterpret_cast<const Chunk<V, CH> *>(row + t * step);
+        }
+    }
+}
+
+// kStep rows of a lane, up to T; zeros past the row's length.
+template <typename V, int CH>
+__device__ __forceinline__ void store_steps(const float (&v)[kStep][CH], void *p, int64_t ld, const ScanArgs &q,
+                                            const Lane<CH> &l) {
+    const int64_t step = ld * q.B;
+    V *row = static_cast<V *>(p) + l.b * ld + l.t0 * step;
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+        if (k >= l.inside) break;
+        Chunk<V, CH> c;
+#pragma unroll
+        for (int e = 0; e < CH; ++e) c[e] = (V)(k < l.live ? v[k][e] : 0.f);
+        store_chunk<true, V, CH>(row + k * step, l.w, c);
+    }
+}
+
+// This workgroup's tile: along T, and along the columns.
+struct Tile {
+    int j, c;
+    __device__ __forceinline__ Tile(const ScanArgs &p, int *slot) {
+        int n = blockIdx.x;
+        if (p.tiles > 1) {
+            if (threadIdx.x == 0) *slot = (int)atomicAdd(p.ticket, 1u);
+            __syncthreads();
+            n = __builtin_amdgcn_readfirstlane(*slot);
+        }
+        j = n / p.col_tiles;
+        c = n - j * p.col_tiles;
+    }
+};
+
+// One column of a tile for the first wave: lane i has element i % CH of lane
+// group i / CH.
+template <int CH>
+struct Column {
+    int64_t r;      // b * D + column
+    bool own;
+    __device__ __forceinline__ Column(const ScanArgs &p, int c, int lane) {
+        const Lane<CH> l(p, c * kRow + (lane / CH) % kRow, 0);
+        const int e = lane % CH;
+        own = lane < kRow * CH && e >= l.w.skip;
+        r = (int64_t)l.b * p.D + l.w.at + e;
+    }
+};
+
+template <typename V, int IN, int CH>
+__global__ void __launch_bounds__(kWaves * 64) k_scan_tile(ScanArgs p) {
+    constexpr int COLS = kRow * CH;
+    __shared__ float2 seg[kSeg][COLS];           // the segments' maps
+    __shared__ float from[kSeg][COLS];           // states before the segments
+    __shared__ int slot;
+    const Tile tile(p, &slot);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6, segs = waves * (64 / kRow);
+    const int g = lane % kRow, u = wave * (64 / kRow) + lane / kRow;
+    const Lane<CH> l(p, tile.c * kRow + g, (int64_t)tile.j * kTile + u * kStep);
+    const bool whole = (int64_t)(tile.j + 1) * kTile <= p.T;
+
+    float A[kStep][CH], S[kStep][CH];
+    {
+        Chunk<V, CH> xg[kStep], xx[kStep];
+        load_steps<V, CH>(xg, p.gate, p.ldg, p, l, whole);
+        load_steps<V, CH>(xx, p.x, p.ldx, p, l, whole);
+        Chunk<float, CH> bias = (Chunk<float, CH>)0.f;
+        if (p.bias) bias = load_chunk<float, CH>(p.bias, l.w);
+#pragma unroll
+        for (int k = 0; k < kStep; ++k)
+#pragma unroll
+            for (int e = 0; e < CH; ++e) {
+                float d = sigmoid_neg((float)xg[k][e] + bias[e]);
+                float b = input_factor<IN>(d) * (float)xx[k][e];
+                if (k >= l.live) d = 0.f, b = 0.f;
+                const float a0 = k ? A[k ? k - 1 : 0][e] : 1.f, s0 = k ? S[k ? k - 1 : 0][e] : 0.f;
+                A[k][e] = fmaf(-d, a0, a0);
+                S[k][e] = s0 + fmaf(-d, s0, b);
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e) seg[u][g * CH + e] = make_float2(A[kStep - 1][e], S[kStep - 1][e]);
+    __syncthreads();
+
+    if (wave == 0) {
+        const Column<CH> c(p, tile.c, lane);
+        if (c.own) {
+            const int64_t R = (int64_t)p.B * p.D;
+            float At = 1.f, St = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < segs; ++i) {
+                const float2 m = seg[i][lane];
+                St = fmaf(m.x, St, m.y);
+                At *= m.x;
+            }
+            float s;
+            if (tile.j == 0) {
+                s = p.state ? p.state[c.r] : 0.f;
+            } else {
+                unsigned long long *at = p.link + tile.j * R + c.r;
+                if (tile.j + 1 < p.tiles) link_put_map(at, At, St);
+                s = link_state(at, R, tile.j);
+            }
+            const float end = fmaf(At, s, St);
+            if (tile.j + 1 < p.tiles) link_put(p.link + tile.j * R + c.r, kDone, end);
+            if (p.saved) p.saved[tile.j * R + c.r] = end;
+            if (p.final && tile.j + 1 == p.tiles) p.final[c.r] = end;
+#pragma unroll 8
+            for (int i = 0; i < segs; ++i) {
+                from[i][lane] = s;
+                const float2 m = seg[i][lane];
+                s = fmaf(m.x, s, m.y);
+            }
+        }
+    }
+    __syncthreads();
+
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+        const float s = from[u][g * CH + e];
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) S[k][e] = fmaf(A[k][e], s, S[k][e]);
+    }
+    store_steps<V, CH>(S, p.y, p.ldy, p, l);
+}
+
+// Backwards.  The states before the segments come from the saved state before
+// the tile; the gradients' chain from the tiles after it.  Both kinds of maps
+// are formed in one go (they share A).
+template <typename V, int IN, int CH>
+__global__ void __launch_bounds__(kWaves * 64) k_scan_back(ScanArgs p) {
+    constexpr int COLS = kRow * CH;
+    __shared__ float mul[kSeg][COLS];            // A; then the segments' sums of dz
+    __shared__ float fwd[kSeg][COLS];            // S; then the states before the segments
+    __shared__ float rev[kSeg][COLS];            // S from the end; then c behind the segments
+    __shared__ int slot;
+    Tile tile(p, &slot);
+    tile.j = p.tiles - 1 - tile.j;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6, segs = waves * (64 / kRow);
+    const int g = lane % kRow, u = wave * (64 / kRow) + lane / kRow;
+    const Lane<CH> l(p, tile.c * kRow + g, (int64_t)tile.j * kTile + u * kStep);
+    const bool whole = (int64_t)(tile.j + 1) * kTile <= p.T;
+    const int64_t R = (int64_t)p.B * p.D;
+
+    float d[kStep][CH];
+    Chunk<V, CH> xx[kStep], dy[kStep];
+    {
+        Chunk<V, CH> xg[kStep];
+        load_steps<V, CH>(xg, p.gate, p.ldg, p, l, whole);
+        load_steps<V, CH>(xx, p.x, p.ldx, p, l, whole);
+        load_steps<V, CH>(dy, p.dy, p.lddy, p, l, whole);
+        Chunk<float, CH> bias = (Chunk<float, CH>)0.f;
+        if (p.bias) bias = load_chunk<float, CH>(p.bias, l.w);
+#pragma unroll
+        for (int k = 0; k < kStep; ++k)
+#pragma unroll
+            for (int e = 0; e < CH; ++e) {
+                d[k][e] = sigmoid_neg((float)xg[k][e] + bias[e]);
+                if (k >= l.live) d[k][e] = 0.f, xx[k][e] = (V)0.f, dy[k][e] = (V)0.f;
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+        float A = 1.f, S = 0.f, Z = 0.f;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+            A = fmaf(-d[k][e], A, A);
+            S = S + fmaf(-d[k][e], S, input_factor<IN>(d[k][e]) * (float)xx[k][e]);
+        }
+#pragma unroll
+        for (int k = kStep - 1; k >= 0; --k) {
+            const float G = (float)dy[k][e] + Z;
+            Z = fmaf(-d[k][e], G, G);
+        }
+        mul[u][g * CH + e] = A;
+        fwd[u][g * CH + e] = S;
+        rev[u][g * CH + e] = Z;
+    }
+    __syncthreads();
+
+    const Column<CH> c(p, tile.c, lane);
+    float At = 1.f, Zt = 0.f;
+    if (wave == 0 && c.own) {
+        float s = tile.j ? p.saved[(tile.j - 1) * R + c.r] : p.state ? p.state[c.r] : 0.f;
+#pragma unroll 8
+        for (int i = segs - 1; i >= 0; --i) {
+            Zt = fmaf(mul[i][lane], Zt, rev[i][lane]);
+            At *= mul[i][lane];
+        }
+        if (tile.j > 0 && tile.j + 1 < p.tiles) link_put_map(p.link + tile.j * R + c.r, At, Zt);
+#pragma unroll 8
+        for (int i = 0; i < segs; ++i) {
+            const float S = fwd[i][lane];
+            fwd[i][lane] = s;
+            s = fmaf(mul[i][lane], s, S);
+        }
+    }
+    __syncthreads();
+
+    if (wave == 0 && c.own) {
+        unsigned long long *at = p.link + tile.j * R + c.r;
+        float z = tile.j + 1 == p.tiles ? (p.dfinal ? p.dfinal[c.r] : 0.f)
+                                        : link_state(at, -R, p.tiles - 1 - tile.j);
+        const float end = fmaf(At, z, Zt);
+        if (tile.j > 0) link_put(at, kDone, end);
+        else if (p.dstate) p.dstate[c.r] = end;
+#pragma unroll 8
+        for (int i = segs - 1; i >= 0; --i) {
+            const float Z = rev[i][lane];
+            rev[i][lane] = z;
+            z = fmaf(mul[i][lane], z, Z);
+        }
+    }
+    float slope[kStep][CH];
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+        float s = fwd[u][g * CH + e];
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+            const float x = (float)xx[k][e];
+            slope[k][e] = gate_slope<IN>(d[k][e], x, s);
+            s = s + fmaf(-d[k][e], s, input_factor<IN>(d[k][e]) * x);
+        }
+    }
+    __syncthreads();
+
+    float sum[CH];
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+        float z = rev[u][g * CH + e];
+        sum[e] = 0.f;
+#pragma unroll
+        for (int k = kStep - 1; k >= 0; --k) {
+            const float G = (float)dy[k][e] + z;
+            z = fmaf(-d[k][e], G, G);
+            slope[k][e] *= G;
+            sum[e] += k < l.live ? slope[k][e] : 0.f;
+            d[k][e] = G * input_factor<IN>(d[k][e]);
+        }
+    }
+    store_steps<V, CH>(d, p.dx, p.lddx, p, l);
+    store_steps<V, CH>(slope, p.dgate, p.lddg, p, l);
+    if (!p.pbias) return;
+#pragma unroll
+    for (int e = 0; e < CH; ++e) mul[u][g * CH + e] = sum[e];
+    __syncthreads();
+    if (wave == 0 && c.own) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < segs; ++i) s += mul[i][lane];
+        p.pbias[tile.j * R + c.r] = s;
+    }
+}
+
+// Short lengths: a lane runs its columns from the first position to the last,
+// reading ahead; nothing passes between lanes.
+template <typename V, int IN, int CH>
+__global__ void __launch_bounds__(64) k_scan_serial(ScanArgs p) {
+    const int g = blockIdx.x * 64 + threadIdx.x;
+    if (g >= p.lanes_all) return;
+    const Lane<CH> l(p, g, 0);
     int64_t len = p.T;
     if (p.lengths) {
-        const int64_t n = p.lengths[k.b];
+        const int64_t n = p.lengths[l.b];
         len = n < 0 ? 0 : n < p.T ? n : p.T;
     }
-    k.end = len < k.t1 ? (len < k.t0 ? k.t0 : len) : k.t1;
-    k.bias = p.bias ? p.bias[k.c] : 0.f;
-    return true;
-}
-
-template <typename V>
-__device__ __forceinline__ float at(const void *p, int64_t row, int64_t ld, int c) {
-    return (float)static_cast<const V *>(p)[row * ld + c];
-}
-
-// The map of one chunk of one column.
-template <typename V, int IN>
-__global__ void __launch_bounds__(64) k_scan_map(ScanArgs p) {
-    Column k;
-    if (!column(p, k)) return;
-    float A = 1.f, S = 0.f;
-    for (int64_t t = k.t0; t < k.end; ++t) {
-        const int64_t row = t * p.B + k.b;
-        const float d = sigmoid_neg(at<V>(p.gate, row, p.ldg, k.c) + k.bias);
-        const float x = at<V>(p.x, row, p.ldx, k.c);
-        S = S + fmaf(-d, S, input_factor<IN>(d) * x);
-        A = fmaf(-d, A, A);
-    }
-    const size_t i = (size_t)blockIdx.y * (p.B * (size_t)p.D) + k.r;
-    p.mul[i] = A;
-    p.add[i] = S;
-}
-
-// States at the chunks' ends, one column per thread.
-__global__ void __launch_bounds__(64) k_scan_carry(ScanArgs p, float *ends) {
-    const size_t R = p.B * (size_t)p.D, r = blockIdx.x * (size_t)64 + threadIdx.x;
-    if (r >= R) return;
-    float s = p.state ? p.state[r] : 0.f;
-    for (int j = 0; j < p.chunks; ++j) {
-        const float A = p.mul[j * R + r], S = p.add[j * R + r];
-        if (j == 0) p.mul[r] = s;     // final may be state: the last chunk writes it while the first one runs
-        s = fmaf(A, s, S);
-        ends[j * R + r] = s;
-    }
-}
-
-template <typename V, int IN>
-__global__ void __launch_bounds__(64) k_scan_apply(ScanArgs p, const float *ends) {
-    Column k;
-    if (!column(p, k)) return;
-    const size_t R = p.B * (size_t)p.D;
-    float s = blockIdx.y ? ends[(blockIdx.y - 1) * R + k.r]
-                         : p.chunks > 1 ? p.mul[k.r] : p.state ? p.state[k.r] : 0.f;
-    V *y = static_cast<V *>(p.y);
-    for (int64_t t = k.t0; t < k.end; ++t) {
-        const int64_t row = t * p.B + k.b;
-        const float d = sigmoid_neg(at<V>(p.gate, row, p.ldg, k.c) + k.bias);
-        const float x = at<V>(p.x, row, p.ldx, k.c);
-        s = s + fmaf(-d, s, input_factor<IN>(d) * x);
-        y[row * p.ldy + k.c] = (V)s;
-    }
-    for (int64_t t = k.end; t < k.t1; ++t) y[(t * p.B + k.b) * p.ldy + k.c] = (V)0.f;
-    if (p.saved && p.chunks == 1) p.saved[k.r] = s;
-    if (p.final && (int)blockIdx.y == p.chunks - 1) p.final[k.r] = s;
-}
-
-// The backward maps: c at a chunk's end -> c before its start, c = (1 - d) D.
-template <typename V>
-__global__ void __launch_bounds__(64) k_scan_bmap(ScanArgs p) {
-    Column k;
-    if (!column(p, k)) return;
-    float A = 1.f, S = 0.f;
-    for (int64_t t = k.end - 1; t >= k.t0; --t) {
-        const int64_t row = t * p.B + k.b;
-        const float d = sigmoid_neg(at<V>(p.gate, row, p.ldg, k.c) + k.bias);
-        const float g = at<V>(p.dy, row, p.lddy, k.c) + S;
-        S = fmaf(-d, g, g);
-        A = fmaf(-d, A, A);
-    }
-    const size_t i = (size_t)blockIdx.y * (p.B * (size_t)p.D) + k.r;
-    p.mul[i] = A;
-    p.add[i] = S;
-}
-
-// c arriving at each chunk's end (into mul), one column per thread, from the last chunk.
-__global__ void __launch_bounds__(64) k_scan_bcarry(ScanArgs p) {
-    const size_t R = p.B * (size_t)p.D, r = blockIdx.x * (size_t)64 + threadIdx.x;
-    if (r >= R) return;
-    float c = p.dfinal ? p.dfinal[r] : 0.f;
-    for (int j = p.chunks - 1; j >= 0; --j) {
-        const float A = p.mul[j * R + r], S = p.add[j * R + r];
-        p.mul[j * R + r] = c;
-        c = fmaf(A, c, S);
-    }
-}
-
-template <typename V, int IN>
-__global__ void __launch_bounds__(64) k_scan_bapply(ScanArgs p) {
-    Column k;
-    if (!column(p, k)) return;
-    const size_t R = p.B * (size_t)p.D;
-    const int j = blockIdx.y;
-    V *dx = static_cast<V *>(p.dx), *dg = static_cast<V *>(p.dgate);
-    for (int64_t t = k.end; t < k.t1; ++t) {
-        dx[(t * p.B + k.b) * p.lddx + k.c] = (V)0.f;
-        dg[(t * p.B + k.b) * p.lddg + k.c] = (V)0.f;
-    }
-    // states before each sub-run of kScanSub positions
-    float start[kScanChunk / kScanSub];
-    float s = j ? p.saved[(j - 1) * R + k.r] : p.state ? p.state[k.r] : 0.f;
-#pragma unroll
-    for (int u = 0; u < kScanChunk / kScanSub; ++u) {
-        start[u] = s;
-        for (int i = 0; i < kScanSub; ++i) {
-            const int64_t t = k.t0 + u * kScanSub + i;
-            if (t >= k.end) break;
-            const int64_t row = t * p.B + k.b;
-            const float d = sigmoid_neg(at<V>(p.gate, row, p.ldg, k.c) + k.bias);
-            s = s + fmaf(-d, s, input_factor<IN>(d) * at<V>(p.x, row, p.ldx, k.c));
+    const size_t r = (size_t)l.b * p.D;
+    const V *gate = static_cast<const V *>(p.gate) + l.b * p.ldg + l.w.at;
+    const V *x = static_cast<const V *>(p.x) + l.b * p.ldx + l.w.at;
+    V *y = static_cast<V *>(p.y) + l.b * p.ldy;
+    Chunk<float, CH> bias = (Chunk<float, CH>)0.f, s = (Chunk<float, CH>)0.f;
+    Chunk<V, CH> ng = *reinterpret_cast<const Chunk<V, CH> *>(gate), nx = *reinterpret_cast<const Chunk<V, CH> *>(x);
+    if (p.bias) bias = load_chunk<float, CH>(p.bias, l.w);
+    if (p.state) s = load_chunk<float, CH>(p.state + r, l.w);
+    for (int64_t t = 0; t < p.T; ++t) {
+        const Chunk<V, CH> cg = ng, cx = nx;
+        if (t + 1 < p.T) {
+            ng = *reinterpret_cast<const Chunk<V, CH> *>(gate + (t + 1) * p.B * p.ldg);
+            nx = *reinterpret_cast<const Chunk<V, CH> *>(x + (t + 1) * p.B * p.ldx);
         }
-    }
-    float c = p.chunks > 1 ? p.mul[j * R + k.r] : p.dfinal ? p.dfinal[k.r] : 0.f;
-    float sum = 0.f;
+        Chunk<V, CH> out = (Chunk<V, CH>)(V)0.f;
+        if (t < len) {
 #pragma unroll
-    for (int u = kScanChunk / kScanSub - 1; u >= 0; --u) {
-        float before[kScanSub], dv[kScanSub], xv[kScanSub];
-        s = start[u];
-#pragma unroll
-        for (int i = 0; i < kScanSub; ++i) {
-            const int64_t t = k.t0 + u * kScanSub + i;
-            before[i] = s;
-            dv[i] = xv[i] = 0.f;
-            if (t < k.end) {
-                const int64_t row = t * p.B + k.b;
-                dv[i] = sigmoid_neg(at<V>(p.gate, row, p.ldg, k.c) + k.bias);
-                xv[i] = at<V>(p.x, row, p.ldx, k.c);
-                s = s + fmaf(-dv[i], s, input_factor<IN>(dv[i]) * xv[i]);
+            for (int e = 0; e < CH; ++e) {
+                const float d = sigmoid_neg((float)cg[e] + bias[e]);
+                s[e] = s[e] + fmaf(-d, s[e], input_factor<IN>(d) * (float)cx[e]);
+                out[e] = (V)s[e];
             }
         }
-#pragma unroll
-        for (int i = kScanSub - 1; i >= 0; --i) {
-            const int64_t t = k.t0 + u * kScanSub + i;
-            if (t < k.end) {
-                const int64_t row = t * p.B + k.b;
-                const float g = at<V>(p.dy, row, p.lddy, k.c) + c;
-                const float dz = g * gate_slope<IN>(dv[i], xv[i], before[i]);
-                dx[row * p.lddx + k.c] = (V)(g * input_factor<IN>(dv[i]));
-                dg[row * p.lddg + k.c] = (V)dz;
-                sum += dz;
-                c = fmaf(-dv[i], g, g);
-            }
-        }
+        store_chunk<true, V, CH>(y + t * p.B * p.ldy, l.w, out);
     }
-    if (p.pbias) p.pbias[j * R + k.r] = sum;
-    if (p.dstate && j == 0) p.dstate[k.r] = c;
+    if (p.saved) store_chunk<true, float, CH>(p.saved + r, l.w, s);
+    if (p.final) store_chunk<true, float, CH>(p.final + r, l.w, s);
 }
 
-// dbias: the chunks' and rows' partial sums of one channel, in a fixed order.
-__global__ void __launch_bounds__(64) k_scan_dbias(ScanArgs p, float *dbias) {
-    const int c = blockIdx.x * 64 + threadIdx.x;
-    if (c >= p.D) return;
-    float sum = 0.f;
-    for (int64_t i = 0; i < (int64_t)p.chunks * p.B; ++i) sum += p.pbias[i * p.D + c];
-    dbias[c] = sum;
+// dbias: the tiles' and rows' partial sums of 64 channels a workgroup; its
+// sixteen waves take every sixteenth row and are added in their order.
+__global__ void __launch_bounds__(1024) k_scan_dbias(ScanArgs p, float *dbias) {
+    __shared__ float join[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < p.D) {
+#pragma unroll 8
+        for (int64_t i = wave; i < (int64_t)p.tiles * p.B; i += 16) s += p.pbias[i * p.D + c];
+    }
+    join[wave][lane] = s;
+    __syncthreads();
+    if (wave || c >= p.D) return;
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += join[w][lane];
+    dbias[c] = s;
 }
 
 // T = 0: the state passes through.
@@ -241,8 +504,9 @@ __global__ void __launch_bounds__(64) k_scan_pass(const float *from, float *to, 
 
 struct Plan {
     size_t R;
-    int64_t chunks;
-    size_t part;       // bytes of one [chunks][R] array
+    int64_t tiles;
+    size_t part;       // bytes of one fp32 [tiles][R] array
+    size_t link;       // bytes of the words between tiles and their counter, 0 for one tile
 };
 
 const char *scan_plan(const fi_scan_desc *q, Plan &p) {
@@ -258,21 +522,29 @@ const char *scan_plan(const fi_scan_desc *q, Plan &p) {
     p.R = (size_t)q->batch * q->channels;
     if (p.R > (size_t(1) << 24)) return "batch * channels is over 2^24";
     if (q->T > (int64_t(1) << 23)) return "T is over 2^23";
-    p.chunks = (q->T + kScanChunk - 1) / kScanChunk;
-    if (p.chunks > 65535) return "too many chunks";
-    p.part = up256((size_t)p.chunks * p.R * sizeof(float));
+    p.tiles = (q->T + kTile - 1) / kTile;
+    p.part = up256((size_t)p.tiles * p.R * sizeof(float));
+    p.link = p.tiles > 1 ? up256((size_t)p.tiles * p.R * sizeof(unsigned long long)) + 256 : 0;
+    if (p.tiles * (int64_t)p.R > (int64_t(1) << 31)) return "batch * channels * T is too large";
     return nullptr;
 }
 
 size_t scan_workspace(const Plan &p, bool backward) {
-    return std::max<size_t>(backward ? p.part * 3 : p.chunks > 1 ? p.part * 2 : 0, 256);
+    return std::max<size_t>(p.link + (backward ? p.part : 0), 256);
+}
+
+// The counter, then the words between tiles (a backward pass keeps its sums behind them).
+void scan_links(const Plan &pl, void *workspace, ScanArgs &a) {
+    if (!pl.link) return;
+    a.ticket = (unsigned *)workspace;
+    a.link = (unsigned long long *)((char *)workspace + 256);
 }
 
 void scan_args(const fi_scan_desc *q, const Plan &pl, ScanArgs &a) {
     a.T = q->T;
     a.B = q->batch;
     a.D = q->channels;
-    a.chunks = (int)pl.chunks;
+    a.tiles = (int)pl.tiles;
     a.ldx = pitch_or(q->ld_x, a.D);
     a.ldg = pitch_or(q->ld_gate, a.D);
     a.ldy = pitch_or(q->ld_y, a.D);
@@ -281,26 +553,40 @@ void scan_args(const fi_scan_desc *q, const Plan &pl, ScanArgs &a) {
     a.lddg = pitch_or(q->ld_dgate, a.D);
 }
 
+template <typename V, int IN, int CH>
+void scan_launch(ScanArgs a, bool backward, hipStream_t st) {
+    a.lanes_row = (a.D + CH - 1) / CH;
+    a.lanes_all = a.lanes_row * a.B;
+    a.col_tiles = (a.lanes_all + kRow - 1) / kRow;
+    if (!backward && a.T <= kSerial) {
+        hipLaunchKernelGGL((k_scan_serial<V, IN, CH>), dim3((a.lanes_all + 63) / 64), dim3(64), 0, st, a);
+        return;
+    }
+    const unsigned per_wave = 64 / kRow * kStep;
+    const unsigned waves = a.tiles > 1 ? kWaves : (unsigned)((a.T + per_wave - 1) / per_wave);
+    if (a.tiles > 1) {
+        const size_t n = (size_t)a.tiles * a.B * a.D;
+        hipLaunchKernelGGL(k_scan_clear, dim3((unsigned)std::min<size_t>((n + 1023) / 1024, 4096)), dim3(256), 0, st,
+                           a.link, n, a.ticket);
+    }
+    const dim3 grid((unsigned)a.tiles * a.col_tiles), wg(waves * 64);
+    if (backward)
+        hipLaunchKernelGGL((k_scan_back<V, IN, CH>), grid, wg, 0, st, a);
+    else
+        hipLaunchKernelGGL((k_scan_tile<V, IN, CH>), grid, wg, 0, st, a);
+}
+
+// Lanes take four neighbouring columns, or one where a row has fewer.
 template <typename V, int IN>
 void scan_forward(const ScanArgs &a, hipStream_t st) {
-    const dim3 cols((unsigned)((a.B * (size_t)a.D + 63) / 64)), grid(cols.x, (unsigned)a.chunks);
-    float *ends = a.saved;
-    if (a.chunks > 1) {
-        hipLaunchKernelGGL((k_scan_map<V, IN>), grid, dim3(64), 0, st, a);
-        if (!ends) ends = a.add;
-        hipLaunchKernelGGL(k_scan_carry, cols, dim3(64), 0, st, a, ends);
-    }
-    hipLaunchKernelGGL((k_scan_apply<V, IN>), grid, dim3(64), 0, st, a, (const float *)ends);
+    if (a.D < 4) scan_launch<V, IN, 1>(a, false, st);
+    else scan_launch<V, IN, 4>(a, false, st);
 }
 
 template <typename V, int IN>
 void scan_backward(const ScanArgs &a, hipStream_t st) {
-    const dim3 cols((unsigned)((a.B * (size_t)a.D + 63) / 64)), grid(cols.x, (unsigned)a.chunks);
-    if (a.chunks > 1) {
-        hipLaunchKernelGGL((k_scan_bmap<V>), grid, dim3(64), 0, st, a);
-        hipLaunchKernelGGL(k_scan_bcarry, cols, dim3(64), 0, st, a);
-    }
-    hipLaunchKernelGGL((k_scan_bapply<V, IN>), grid, dim3(64), 0, st, a);
+    if (a.D < 4) scan_launch<V, IN, 1>(a, true, st);
+    else scan_launch<V, IN, 4>(a, true, st);
 }
 
 using ScanLaunch = void (*)(const ScanArgs &, hipStream_t);
@@ -367,8 +653,7 @@ fi_status fi_scan_forward(const fi_scan_desc *desc, const void *x, const void *g
             hipLaunchKernelGGL(k_scan_pass, dim3((unsigned)((pl.R + 63) / 64)), dim3(64), 0, st, state, final, pl.R);
         return op_launched(call);
     }
-    a.mul = (float *)workspace;
-    a.add = (float *)((char *)workspace + pl.part);
+    scan_links(pl, workspace, a);
     pick(desc->dtype, desc->input, false)(a, st);
     return op_launched(call);
 }
@@ -402,12 +687,11 @@ fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *
     if (rows == 0) {
         if (dstate) hipLaunchKernelGGL(k_scan_pass, dim3(cols), dim3(64), 0, st, dfinal, dstate, pl.R);
     } else {
-        a.mul = (float *)workspace;
-        a.add = (float *)((char *)workspace + pl.part);
-        a.pbias = dbias ? (float *)((char *)workspace + 2 * pl.part) : nullptr;
+        scan_links(pl, workspace, a);
+        a.pbias = dbias ? (float *)((char *)workspace + pl.link) : nullptr;
         pick(desc->dtype, desc->input, true)(a, st);
     }
-    if (dbias) hipLaunchKernelGGL(k_scan_dbias, dim3((unsigned)((a.D + 63) / 64)), dim3(64), 0, st, a, dbias);
+    if (dbias) hipLaunchKernelGGL(k_scan_dbias, dim3((unsigned)((a.D + 63) / 64)), dim3(1024), 0, st, a, dbias);
     return op_launched(call);
 }
 
