@@ -25,6 +25,11 @@ FLAGS = [
     # packed fp32 instructions are kept out of every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
+# flags of single files
+FILE_FLAGS = {
+    # paired across columns, the scan's phases hold their values twice and no longer fit two tiles on a CU
+    "fi_ops_scan.hip": ["-fno-slp-vectorize"],
+}
 
 
 def sources():
@@ -39,7 +44,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
 
     def compile_one(src):
         obj = os.path.join(OBJ, os.path.basename(src)[:-4] + "." + tag + ".o")
-        cmd = [HIPCC, *FLAGS, "-c", src, "-o", obj]
+        cmd = [HIPCC, *FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError("hipcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)

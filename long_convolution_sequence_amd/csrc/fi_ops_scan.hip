@@ -10,8 +10,8 @@
 // of a alone is a relative error of 2^-25 / d in the memory's length.
 //
 // One pass over the data (k_scan_tile, k_scan_back).  A workgroup holds a tile
-// of kTile positions x kCols columns in registers: a lane has kStep positions of
-// CH neighbouring columns (a "segment"), 16 lanes cover the tile's columns, the
+// of kTile positions x 64 columns in registers: a lane has kStep positions of
+// four neighbouring columns (a "segment"), 16 lanes cover the tile's columns, the
 // other lanes and the waves go on in time.  Every lane forms its segment's map;
 // the first wave (one column a lane now) joins the segments' maps to the tile's
 // map, publishes it, and finds the state before the tile from the tiles before:
@@ -22,6 +22,8 @@
 //
 // The join is the same chain of fmas whichever tile the state was found at
 // (s <- A s + S, tile after tile), so results do not depend on timing.
+#include <type_traits>
+
 #include "fi_ops.h"
 
 namespace fi {
@@ -31,9 +33,8 @@ namespace {
 constexpr int kStep = 8;                        // positions of a lane
 constexpr int kRow = 16;                        // lanes along a row
 constexpr int kWaves = 8;                       // waves of a tile at most
-constexpr int kSeg = kWaves * 64 / kRow;        // segments of a tile in time
-constexpr int kTile = kSeg * kStep;             // positions of a tile
-constexpr int kWindow = 8;                      // tiles looked back at together
+constexpr int kTile = kWaves * 64 / kRow * kStep;   // positions of a tile
+constexpr int kWindow = 6;                      // tiles looked back at together; eight no longer fit two tiles on a CU
 constexpr int kSerial = 16;                     // lengths up to this run one position after the other
 constexpr int kPolls = 1 << 20;                 // looks at unfinished tiles before a wait gives up
 
@@ -96,23 +97,29 @@ __device__ __forceinline__ void link_put_map(unsigned long long *at, float A, fl
     link_put(at, a, S);
 }
 
-// The state at the end of the tile before, for one column.  `at` is this tile's
-// word, `step` the words between tiles (negative: the tiles come from the end),
+__device__ __forceinline__ unsigned long long link_get(const unsigned long long *at) {
+    return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool link_done(unsigned long long v) { return (unsigned)(v >> 32) == kDone; }
+
+// The state at the end of the tile before, for one column r.  `row` is this tile's
+// row of words, `step` the words between tiles (negative: the tiles come from the end),
 // `have` the number of tiles before it (>= 1).  A wait that gives up leaves NaN.
-__device__ float link_state(const unsigned long long *at, int64_t step, int have) {
-    const int n = have < kWindow ? have : kWindow;
+// (All waves of the workgroup looking at 32 tiles together shortens the chain of
+// one narrow sequence from 75 to 67 us, and takes the memory from everybody else:
+// 170 -> 210 us at 131072 x 864.)
+__device__ __forceinline__ float link_state(const unsigned long long *row, unsigned r, int64_t step, int have) {
     for (int polls = 0; polls < kPolls; ++polls) {
         unsigned long long v[kWindow];
 #pragma unroll
-        for (int i = 0; i < kWindow; ++i)
-            v[i] = i < n ? __hip_atomic_load(at - (i + 1) * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : kNothing;
+        for (int i = 0; i < kWindow; ++i) v[i] = i < have ? link_get(in_row(row - (i + 1) * step, r)) : kNothing;
         // the nearest tile with its state, if every nearer one has its map
         int found = -1;
         bool open = true;
 #pragma unroll
         for (int i = 0; i < kWindow; ++i) {
             open = open && v[i] != kNothing;
-            if (open && (unsigned)(v[i] >> 32) == kDone) {
+            if (open && link_done(v[i])) {
                 found = i;
                 open = false;
             }
@@ -143,7 +150,7 @@ template <int CH>
 struct Lane {
     Place<CH> w;
     int b;             // batch row
-    int64_t t0;        // first position
+    int64_t t0, last;  // first position; the row's last position (0 if it has none)
     int live, inside;  // of its kStep positions: before the row's length, before T
 
     // column group g of the tile's column tile, positions from t0 on
@@ -160,46 +167,49 @@ struct Lane {
         }
         live = clip(len - t0);
         inside = clip(p.T - t0);
+        last = len > 0 ? len - 1 : 0;
     }
+    // whether every lane of the wave has all its positions
+    __device__ __forceinline__ bool full() const { return __builtin_amdgcn_ballot_w64(live < kStep) == 0; }
     static __device__ __forceinline__ int clip(int64_t n) { return n < 0 ? 0 : n < kStep ? (int)n : kStep; }
 };
 
-// kStep rows of a lane; positions at T or later read the row T - 1 (unused).
-template <typename V, int CH>
+// kStep rows of a lane.  FULL: all of them are live; else a row past the length
+// reads the last one before it (row 0 of an empty sequence), unused.
+template <bool FULL, typename V, int CH>
 __device__ __forceinline__ void load_steps(Chunk<V, CH> (&v)[kStep], const void *p, int64_t ld, const ScanArgs &q,
-                                           const Lane<CH> &l, bool whole) {
+                                           const Lane<CH> &l) {
     const int64_t step = ld * q.B;
     const V *row = static_cast<const V *>(p) + l.b * ld + l.w.at;
-    if (whole) {
-        row += l.t0 * step;
+    const int64_t t0 = FULL ? l.t0 : l.t0 < l.last ? l.t0 : l.last;
+    row += t0 * step;
+    const int most = l.live - 1;
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) v[k] = *reinterpret_cast<const Chunk<V, CH> *>(row + k * step);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-            const int64_t t = l.t0 + k < q.T ? l.t0 + k : q.T - 1;
-            v[k] = *reinterpret_cast<const Chunk<V, CH> *>(row + t * step);
-        }
+    for (int k = 0; k < kStep; ++k) {
+        const int64_t i = FULL ? k : k <= most ? k : most > 0 ? most : 0;
+        v[k] = *reinterpret_cast<const Chunk<V, CH> *>(row + i * step);
     }
 }
 
 // kStep rows of a lane, up to T; zeros past the row's length.
-template <typename V, int CH>
+template <bool FULL, typename V, int CH>
 __device__ __forceinline__ void store_steps(const float (&v)[kStep][CH], void *p, int64_t ld, const ScanArgs &q,
                                             const Lane<CH> &l) {
     const int64_t step = ld * q.B;
     V *row = static_cast<V *>(p) + l.b * ld + l.t0 * step;
 #pragma unroll
     for (int k = 0; k < kStep; ++k) {
-        if (k >= l.inside) break;
+        if (!FULL && k >= l.inside) break;
         Chunk<V, CH> c;
 #pragma unroll
-        for (int e = 0; e < CH; ++e) c[e] = (V)(k < l.live ? v[k][e] : 0.f);
+        for (int e = 0; e < CH; ++e) c[e] = (V)(FULL || k < l.live ? v[k][e] : 0.f);
         store_chunk<true, V, CH>(row + k * step, l.w, c);
     }
 }
 
-// This workgroup's tile: along T, and along the columns.
+// This workgroup's tile: along T (from either end), and along the columns.  One
+// tile a workgroup: with several, a tile's first loads wait in order behind the
+// stores of the one before (228 us where this takes 135).
 struct Tile {
     int j, c;
     __device__ __forceinline__ Tile(const ScanArgs &p, int *slot) {
@@ -214,38 +224,55 @@ struct Tile {
     }
 };
 
-// One column of a tile for the first wave: lane i has element i % CH of lane
-// group i / CH.
+// The other row of 16 lanes of a pair of rows, and the other half of a wave:
+// `lo` and `hi` are the values of the earlier and the later one, in both.
+__device__ __forceinline__ void rows_pair(float x, float &lo, float &hi) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    lo = __uint_as_float(r[0]);
+    hi = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void halves_pair(float x, float &lo, float &hi) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    lo = __uint_as_float(r[0]);
+    hi = __uint_as_float(r[1]);
+}
+
+// The tile's columns, one a lane: lane i has element i % CH of the lane group i / CH.
 template <int CH>
 struct Column {
-    int64_t r;      // b * D + column
+    unsigned r;     // b * D + column
     bool own;
-    __device__ __forceinline__ Column(const ScanArgs &p, int c, int lane) {
-        const Lane<CH> l(p, c * kRow + (lane / CH) % kRow, 0);
-        const int e = lane % CH;
-        own = lane < kRow * CH && e >= l.w.skip;
-        r = (int64_t)l.b * p.D + l.w.at + e;
+    __device__ __forceinline__ Column(const ScanArgs &p, int c) {
+        const int i = threadIdx.x & 63;
+        const Lane<CH> l(p, c * kRow + (i / CH) % kRow, 0);
+        const int e = i % CH;
+        own = i < kRow * CH && e >= l.w.skip;
+        r = (unsigned)l.b * (unsigned)p.D + l.w.at + e;
+        asm("" : "+v"(r));
     }
 };
 
 template <typename V, int IN, int CH>
-__global__ void __launch_bounds__(kWaves * 64) k_scan_tile(ScanArgs p) {
+__global__ void __launch_bounds__(kWaves * 64, 4) k_scan_tile(ScanArgs p) {
     constexpr int COLS = kRow * CH;
-    __shared__ float2 seg[kSeg][COLS];           // the segments' maps
-    __shared__ float from[kSeg][COLS];           // states before the segments
+    __shared__ float2 maps[kWaves][COLS];        // the waves' maps
+    __shared__ float from[kWaves][COLS];         // states before the waves' positions
     __shared__ int slot;
-    const Tile tile(p, &slot);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6, segs = waves * (64 / kRow);
-    const int g = lane % kRow, u = wave * (64 / kRow) + lane / kRow;
-    const Lane<CH> l(p, tile.c * kRow + g, (int64_t)tile.j * kTile + u * kStep);
-    const bool whole = (int64_t)(tile.j + 1) * kTile <= p.T;
-
+    const int waves = blockDim.x >> 6;
+    const int g = lane % kRow, row = lane / kRow;
+    const int64_t R = (int64_t)p.B * p.D;
+    const Tile tile(p, &slot);
+    const int j = tile.j, jc = tile.c;
+    const Lane<CH> l(p, jc * kRow + g, (int64_t)j * kTile + (wave * (64 / kRow) + row) * kStep);
+    const Column<CH> c(p, jc);
+    const bool full = l.full();
     float A[kStep][CH], S[kStep][CH];
-    {
+    const auto segment = [&](auto whole) {
+        constexpr bool FULL = decltype(whole)::value;
         Chunk<V, CH> xg[kStep], xx[kStep];
-        load_steps<V, CH>(xg, p.gate, p.ldg, p, l, whole);
-        load_steps<V, CH>(xx, p.x, p.ldx, p, l, whole);
+        load_steps<FULL, V, CH>(xg, p.gate, p.ldg, p, l);
+        load_steps<FULL, V, CH>(xx, p.x, p.ldx, p, l);
         Chunk<float, CH> bias = (Chunk<float, CH>)0.f;
         if (p.bias) bias = load_chunk<float, CH>(p.bias, l.w);
 #pragma unroll
@@ -254,94 +281,142 @@ __global__ void __launch_bounds__(kWaves * 64) k_scan_tile(ScanArgs p) {
             for (int e = 0; e < CH; ++e) {
                 float d = sigmoid_neg((float)xg[k][e] + bias[e]);
                 float b = input_factor<IN>(d) * (float)xx[k][e];
-                if (k >= l.live) d = 0.f, b = 0.f;
+                if (!FULL && k >= l.live) d = 0.f, b = 0.f;
                 const float a0 = k ? A[k ? k - 1 : 0][e] : 1.f, s0 = k ? S[k ? k - 1 : 0][e] : 0.f;
                 A[k][e] = fmaf(-d, a0, a0);
                 S[k][e] = s0 + fmaf(-d, s0, b);
             }
-    }
+    };
+    if (full) segment(std::true_type());
+    else segment(std::false_type());
+
+    // the wave's map, and the map of what lies before this row of lanes
+    float Ab[CH], Sb[CH];
 #pragma unroll
-    for (int e = 0; e < CH; ++e) seg[u][g * CH + e] = make_float2(A[kStep - 1][e], S[kStep - 1][e]);
+    for (int e = 0; e < CH; ++e) {
+        float a0, a1, s0, s1, pa0, pa1, ps0, ps1;
+        rows_pair(A[kStep - 1][e], a0, a1);
+        rows_pair(S[kStep - 1][e], s0, s1);
+        halves_pair(a0 * a1, pa0, pa1);
+        halves_pair(fmaf(a1, s0, s1), ps0, ps1);
+        if (lane < kRow) maps[wave][g * CH + e] = make_float2(pa0 * pa1, fmaf(pa1, ps0, ps1));
+        const float ea = row & 1 ? a0 : 1.f, es = row & 1 ? s0 : 0.f;
+        Ab[e] = row & 2 ? ea * pa0 : ea;
+        Sb[e] = row & 2 ? fmaf(ea, ps0, es) : es;
+    }
     __syncthreads();
 
-    if (wave == 0) {
-        const Column<CH> c(p, tile.c, lane);
-        if (c.own) {
-            const int64_t R = (int64_t)p.B * p.D;
-            float At = 1.f, St = 0.f;
+    if (wave == 0 && c.own) {
+        unsigned long long *row = p.link + j * R;
+        float At = 1.f, St = 0.f, s = 0.f;
 #pragma unroll 8
-            for (int i = 0; i < segs; ++i) {
-                const float2 m = seg[i][lane];
-                St = fmaf(m.x, St, m.y);
-                At *= m.x;
-            }
-            float s;
-            if (tile.j == 0) {
-                s = p.state ? p.state[c.r] : 0.f;
-            } else {
-                unsigned long long *at = p.link + tile.j * R + c.r;
-                if (tile.j + 1 < p.tiles) link_put_map(at, At, St);
-                s = link_state(at, R, tile.j);
-            }
-            const float end = fmaf(At, s, St);
-            if (tile.j + 1 < p.tiles) link_put(p.link + tile.j * R + c.r, kDone, end);
-            if (p.saved) p.saved[tile.j * R + c.r] = end;
-            if (p.final && tile.j + 1 == p.tiles) p.final[c.r] = end;
+        for (int i = 0; i < waves; ++i) {
+            const float2 m = maps[i][lane];
+            St = fmaf(m.x, St, m.y);
+            At *= m.x;
+        }
+        if (j > 0) {
+            if (j + 1 < p.tiles) link_put_map(in_row(row, c.r), At, St);
+            s = link_state(row, c.r, R, j);
+        } else if (p.state) {
+            s = *in_row(p.state, c.r);
+        }
+        const float end = fmaf(At, s, St);
+        if (j + 1 < p.tiles) link_put(in_row(row, c.r), kDone, end);
+        if (p.saved) *in_row(p.saved + j * R, c.r) = end;
+        if (p.final && j + 1 == p.tiles) *in_row(p.final, c.r) = end;
 #pragma unroll 8
-            for (int i = 0; i < segs; ++i) {
-                from[i][lane] = s;
-                const float2 m = seg[i][lane];
-                s = fmaf(m.x, s, m.y);
-            }
+        for (int i = 0; i < waves; ++i) {
+            from[i][lane] = s;
+            const float2 m = maps[i][lane];
+            s = fmaf(m.x, s, m.y);
         }
     }
     __syncthreads();
 
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
-        const float s = from[u][g * CH + e];
+        const float b = fmaf(Ab[e], from[wave][g * CH + e], Sb[e]);
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) S[k][e] = fmaf(A[k][e], s, S[k][e]);
+        for (int k = 0; k < kStep; ++k) S[k][e] = fmaf(A[k][e], b, S[k][e]);
     }
-    store_steps<V, CH>(S, p.y, p.ldy, p, l);
+    if (full) store_steps<true, V, CH>(S, p.y, p.ldy, p, l);
+    else store_steps<false, V, CH>(S, p.y, p.ldy, p, l);
+}
+
+// Makes the compiler forget what it knows of a lane's values, and so form what
+// follows from them again where it is needed instead of keeping it in registers
+// from phase to phase (x and its products as floats: 185 to 249 registers, one
+// tile a CU).
+template <typename V, int CH>
+__device__ __forceinline__ void forget(Chunk<V, CH> (&v)[kStep]) {
+    using Bits __attribute__((ext_vector_type(CH * sizeof(V) / 4 > 1 ? CH * sizeof(V) / 4 : 2))) = unsigned;
+    if constexpr (CH * sizeof(V) >= 8) {
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+            Bits b = __builtin_bit_cast(Bits, v[k]);
+            asm("" : "+v"(b));
+            v[k] = __builtin_bit_cast(Chunk<V, CH>, b);
+        }
+    }
+}
+template <int CH>
+__device__ __forceinline__ void forget(float (&v)[kStep][CH]) {
+#pragma unroll
+    for (int k = 0; k < kStep; ++k)
+#pragma unroll
+        for (int e = 0; e < CH; ++e) asm("" : "+v"(v[k][e]));
 }
 
 // Backwards.  The states before the segments come from the saved state before
 // the tile; the gradients' chain from the tiles after it.  Both kinds of maps
 // are formed in one go (they share A).
 template <typename V, int IN, int CH>
-__global__ void __launch_bounds__(kWaves * 64) k_scan_back(ScanArgs p) {
+__global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_back(ScanArgs p) {
     constexpr int COLS = kRow * CH;
-    __shared__ float mul[kSeg][COLS];            // A; then the segments' sums of dz
-    __shared__ float fwd[kSeg][COLS];            // S; then the states before the segments
-    __shared__ float rev[kSeg][COLS];            // S from the end; then c behind the segments
+    __shared__ float mul[kWaves][COLS];          // the waves' A; then their sums of dz
+    __shared__ float fwd[kWaves][COLS];          // S; then the states before the waves' positions
+    __shared__ float rev[kWaves][COLS];          // S from the end; then c behind the waves' positions
+    __shared__ Chunk<float, CH> behind[2][kWaves * 64];   // the lanes' maps of what lies behind them in their wave
     __shared__ int slot;
-    Tile tile(p, &slot);
-    tile.j = p.tiles - 1 - tile.j;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6, segs = waves * (64 / kRow);
-    const int g = lane % kRow, u = wave * (64 / kRow) + lane / kRow;
-    const Lane<CH> l(p, tile.c * kRow + g, (int64_t)tile.j * kTile + u * kStep);
-    const bool whole = (int64_t)(tile.j + 1) * kTile <= p.T;
+    const int waves = blockDim.x >> 6;
+    const int g = lane % kRow, row = lane / kRow;
     const int64_t R = (int64_t)p.B * p.D;
+    const Tile tile(p, &slot);
+    const int j = p.tiles - 1 - tile.j, jc = tile.c;
+    const Lane<CH> l(p, jc * kRow + g, (int64_t)j * kTile + (wave * (64 / kRow) + row) * kStep);
+    const Column<CH> c(p, jc);
+    const bool full = l.full();
+    const bool link = wave == 0 && c.own;
+    float s = 0.f;
+    if (link) s = j ? p.saved[(j - 1) * R + c.r] : p.state ? p.state[c.r] : 0.f;
 
     float d[kStep][CH];
     Chunk<V, CH> xx[kStep], dy[kStep];
-    {
+    const auto read = [&](auto whole) {
+        constexpr bool FULL = decltype(whole)::value;
         Chunk<V, CH> xg[kStep];
-        load_steps<V, CH>(xg, p.gate, p.ldg, p, l, whole);
-        load_steps<V, CH>(xx, p.x, p.ldx, p, l, whole);
-        load_steps<V, CH>(dy, p.dy, p.lddy, p, l, whole);
+        load_steps<FULL, V, CH>(xg, p.gate, p.ldg, p, l);
+        load_steps<FULL, V, CH>(xx, p.x, p.ldx, p, l);
+        load_steps<FULL, V, CH>(dy, p.dy, p.lddy, p, l);
         Chunk<float, CH> bias = (Chunk<float, CH>)0.f;
         if (p.bias) bias = load_chunk<float, CH>(p.bias, l.w);
 #pragma unroll
-        for (int k = 0; k < kStep; ++k)
+        for (int k = 0; k < kStep; ++k) {
+            if (!FULL && k >= l.live) xx[k] = dy[k] = (Chunk<V, CH>)(V)0.f;
 #pragma unroll
             for (int e = 0; e < CH; ++e) {
                 d[k][e] = sigmoid_neg((float)xg[k][e] + bias[e]);
-                if (k >= l.live) d[k][e] = 0.f, xx[k][e] = (V)0.f, dy[k][e] = (V)0.f;
+                if (!FULL && k >= l.live) d[k][e] = 0.f;
             }
-    }
+        }
+    };
+    if (full) read(std::true_type());
+    else read(std::false_type());
+    // maps of what lies before this row of lanes in its wave, and behind it
+    float Ab[CH], Sb[CH];
+    Chunk<float, CH> Az, Zz;
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
         float A = 1.f, S = 0.f, Z = 0.f;
@@ -355,24 +430,41 @@ __global__ void __launch_bounds__(kWaves * 64) k_scan_back(ScanArgs p) {
             const float G = (float)dy[k][e] + Z;
             Z = fmaf(-d[k][e], G, G);
         }
-        mul[u][g * CH + e] = A;
-        fwd[u][g * CH + e] = S;
-        rev[u][g * CH + e] = Z;
+        float a0, a1, s0, s1, z0, z1, pa0, pa1, ps0, ps1, pz0, pz1;
+        rows_pair(A, a0, a1);
+        rows_pair(S, s0, s1);
+        rows_pair(Z, z0, z1);
+        halves_pair(a0 * a1, pa0, pa1);
+        halves_pair(fmaf(a1, s0, s1), ps0, ps1);
+        halves_pair(fmaf(a0, z1, z0), pz0, pz1);
+        if (lane < kRow) {
+            mul[wave][g * CH + e] = pa0 * pa1;
+            fwd[wave][g * CH + e] = fmaf(pa1, ps0, ps1);
+            rev[wave][g * CH + e] = fmaf(pa0, pz1, pz0);
+        }
+        const float ea = row & 1 ? a0 : 1.f, es = row & 1 ? s0 : 0.f;
+        Ab[e] = row & 2 ? ea * pa0 : ea;
+        Sb[e] = row & 2 ? fmaf(ea, ps0, es) : es;
+        const float ha = row & 1 ? 1.f : a1, hz = row & 1 ? 0.f : z1;
+        Az[e] = row & 2 ? ha : ha * pa1;
+        Zz[e] = row & 2 ? hz : fmaf(ha, pz1, hz);
+        __builtin_amdgcn_sched_barrier(0);   // column after column: interleaved, all four would not fit the registers
     }
+    behind[0][threadIdx.x] = Az;
+    behind[1][threadIdx.x] = Zz;
     __syncthreads();
 
-    const Column<CH> c(p, tile.c, lane);
     float At = 1.f, Zt = 0.f;
-    if (wave == 0 && c.own) {
-        float s = tile.j ? p.saved[(tile.j - 1) * R + c.r] : p.state ? p.state[c.r] : 0.f;
+    unsigned long long *links = p.link + j * R;
+    if (link) {
 #pragma unroll 8
-        for (int i = segs - 1; i >= 0; --i) {
+        for (int i = waves - 1; i >= 0; --i) {
             Zt = fmaf(mul[i][lane], Zt, rev[i][lane]);
             At *= mul[i][lane];
         }
-        if (tile.j > 0 && tile.j + 1 < p.tiles) link_put_map(p.link + tile.j * R + c.r, At, Zt);
+        if (j > 0 && j + 1 < p.tiles) link_put_map(in_row(links, c.r), At, Zt);
 #pragma unroll 8
-        for (int i = 0; i < segs; ++i) {
+        for (int i = 0; i < waves; ++i) {
             const float S = fwd[i][lane];
             fwd[i][lane] = s;
             s = fmaf(mul[i][lane], s, S);
@@ -380,58 +472,78 @@ __global__ void __launch_bounds__(kWaves * 64) k_scan_back(ScanArgs p) {
     }
     __syncthreads();
 
-    if (wave == 0 && c.own) {
-        unsigned long long *at = p.link + tile.j * R + c.r;
-        float z = tile.j + 1 == p.tiles ? (p.dfinal ? p.dfinal[c.r] : 0.f)
-                                        : link_state(at, -R, p.tiles - 1 - tile.j);
+    if (link) {
+        float z = 0.f;
+        if (j + 1 < p.tiles) z = link_state(links, c.r, -R, p.tiles - 1 - j);
+        else if (p.dfinal) z = p.dfinal[c.r];
         const float end = fmaf(At, z, Zt);
-        if (tile.j > 0) link_put(at, kDone, end);
+        if (j > 0) link_put(in_row(links, c.r), kDone, end);
         else if (p.dstate) p.dstate[c.r] = end;
 #pragma unroll 8
-        for (int i = segs - 1; i >= 0; --i) {
+        for (int i = waves - 1; i >= 0; --i) {
             const float Z = rev[i][lane];
             rev[i][lane] = z;
             z = fmaf(mul[i][lane], z, Z);
         }
     }
+    // ds/dz of every position (the other waves while the first one looks)
+    forget(xx);
+    forget(dy);
+    forget(d);
     float slope[kStep][CH];
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
-        float s = fwd[u][g * CH + e];
+        float b = fmaf(Ab[e], fwd[wave][g * CH + e], Sb[e]);
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
             const float x = (float)xx[k][e];
-            slope[k][e] = gate_slope<IN>(d[k][e], x, s);
-            s = s + fmaf(-d[k][e], s, input_factor<IN>(d[k][e]) * x);
+            slope[k][e] = gate_slope<IN>(d[k][e], x, b);
+            b = b + fmaf(-d[k][e], b, input_factor<IN>(d[k][e]) * x);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
 
+    forget(d);
+    Az = behind[0][threadIdx.x];
+    Zz = behind[1][threadIdx.x];
     float sum[CH];
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
-        float z = rev[u][g * CH + e];
+        float b = fmaf(Az[e], rev[wave][g * CH + e], Zz[e]);
         sum[e] = 0.f;
 #pragma unroll
         for (int k = kStep - 1; k >= 0; --k) {
-            const float G = (float)dy[k][e] + z;
-            z = fmaf(-d[k][e], G, G);
+            const float G = (float)dy[k][e] + b;
+            b = fmaf(-d[k][e], G, G);
             slope[k][e] *= G;
-            sum[e] += k < l.live ? slope[k][e] : 0.f;
+            sum[e] += slope[k][e];     // 0 past the row's length: d = x = 0 there
             d[k][e] = G * input_factor<IN>(d[k][e]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
-    store_steps<V, CH>(d, p.dx, p.lddx, p, l);
-    store_steps<V, CH>(slope, p.dgate, p.lddg, p, l);
-    if (!p.pbias) return;
+    if (full) {
+        store_steps<true, V, CH>(d, p.dx, p.lddx, p, l);
+        store_steps<true, V, CH>(slope, p.dgate, p.lddg, p, l);
+    } else {
+        store_steps<false, V, CH>(d, p.dx, p.lddx, p, l);
+        store_steps<false, V, CH>(slope, p.dgate, p.lddg, p, l);
+    }
+    if (p.pbias) {
 #pragma unroll
-    for (int e = 0; e < CH; ++e) mul[u][g * CH + e] = sum[e];
-    __syncthreads();
-    if (wave == 0 && c.own) {
-        float s = 0.f;
+        for (int e = 0; e < CH; ++e) {
+            float s0, s1;
+            rows_pair(sum[e], s0, s1);
+            halves_pair(s0 + s1, s0, s1);
+            if (lane < kRow) mul[wave][g * CH + e] = s0 + s1;
+        }
+        __syncthreads();
+        if (link) {
+            float t = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < segs; ++i) s += mul[i][lane];
-        p.pbias[tile.j * R + c.r] = s;
+            for (int i = 0; i < waves; ++i) t += mul[i][lane];
+            p.pbias[j * R + c.r] = t;
+        }
     }
 }
 
