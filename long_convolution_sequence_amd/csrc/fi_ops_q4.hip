@@ -1,20 +1,27 @@
 // Matrix-vector products with 4-bit weights and group scales (fi_q4_*).
 //
 // On the matrix units: a wave takes 16 outputs and steps of 32 inputs
-// (v_mfma_f32_16x16x32_bf16, weights as A, the rows of x as columns of B).  A
-// code becomes bf16 without arithmetic: its four bits go to the top of the
-// significand of 16.0, which gives 16 + code exactly; the group's sum then
-// loses (16 + zero) times the group's sum of x.  x in bf16 is one column; fp16
-// and fp32 are cut into two and three bf16 terms (8 significand bits each, by
-// truncation, so the terms add up to x exactly), each a column of its own.
+// (v_mfma_f32_16x16x32, weights as A, the rows of x as columns of B).  A code
+// becomes a 16-bit float without arithmetic: its four bits go to the top of the
+// significand of 16.0, which gives 16 + code exactly; a group's sum then loses
+// (16 + zero) times the group's sum of x, which a second product with A = 1
+// gives in the same layout.  bf16 and fp16 inputs multiply as they are; fp32
+// inputs are cut into three bf16 terms (8 significand bits each, by truncation,
+// so the terms add up to x exactly), each a column of its own.
 //
-// Layout of the packed weights, tiles of 16 outputs x 128 inputs of 1 KB:
+// What bounds it: the bytes of the codes.  A workgroup takes 16 outputs, its
+// waves split K (128 inputs a step, every WK-th step), four steps' loads under
+// way at a time; x lies in LDS in the order of the product's operand, a stretch
+// of K at a time.  The waves' sums meet in LDS, in their order.
+//
+// Layout of the packed weights, tiles of 16 outputs x 128 inputs:
 //   codes  [N/16][K/128][64 lanes][4 words]   lane l: output l & 15; word s holds
 //          the inputs 32 s + 8 (l >> 4) + 0..7: value 2p in bits 4p..4p+3, value
 //          2p + 1 in bits 16 + 4p..
-//   scales [N/16][groups][16], zeros [N/16][groups][16] in 4 bits
-// with N and K rounded up (codes 0, scales 0); a lane of the product holds four
-// outputs (l >> 4) * 4 + 0..3 and so reads four scales side by side.
+//   scales [N/16][K/128][4][groups][4], zeros [N/16][K/128][4][groups][4 x 4 bits]:
+//          a lane of the product holds the outputs (l >> 4) * 4 + 0..3, and reads
+//          their scales of all the step's groups (128 / group) side by side
+// with N and K rounded up (codes 0, scales 0).
 #include "fi_ops.h"
 
 namespace fi {
@@ -25,6 +32,7 @@ constexpr int kQ4MaxRows = 16;
 constexpr int kQ4Max = 1 << 20;
 
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
+using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
 using u32x4 = __attribute__((ext_vector_type(4))) unsigned;
 
@@ -72,25 +80,36 @@ __global__ void __launch_bounds__(256) k_q4_codes(int N, int K, int kt, const ui
     out[i] = w;
 }
 
+// Where value i of the scales' layout comes from: its output and its group.
+struct Q4Where {
+    int n, g;
+    __device__ __forceinline__ Q4Where(int64_t i, int kt, int per) {
+        const int row = (int)(i & 3), in = (int)(i >> 2) % per, kq = (int)((i >> 2) / per & 3);
+        const int64_t step = i / (16 * per);
+        n = (int)(step / kt) * 16 + kq * 4 + row;
+        g = (int)(step % kt) * per + in;
+    }
+};
+
 template <typename V>
-__global__ void __launch_bounds__(256) k_q4_scales(int N, int have, int groups, const V *scales, V *out, int64_t n) {
+__global__ void __launch_bounds__(256) k_q4_scales(int N, int have, int kt, int per, const V *scales, V *out,
+                                                   int64_t n) {
     const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
     if (i >= n) return;
-    const int64_t tg = i >> 4;
-    const int row = (int)(tg / groups) * 16 + (int)(i & 15), g = (int)(tg % groups);
-    out[i] = row < N && g < have ? scales[(size_t)row * have + g] : (V)0.f;
+    const Q4Where w(i, kt, per);
+    out[i] = w.n < N && w.g < have ? scales[(size_t)w.n * have + w.g] : (V)0.f;
 }
 
-__global__ void __launch_bounds__(256) k_q4_zeros(int N, int have, int groups, const uint8_t *zeros, uint16_t *out,
-                                                  int64_t n) {
+__global__ void __launch_bounds__(256) k_q4_zeros(int N, int have, int kt, int per, const uint8_t *zeros,
+                                                  uint16_t *out, int64_t n) {
     const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
     if (i >= n) return;
-    const int64_t tg = i >> 2;
-    const int row0 = (int)(tg / groups) * 16 + (int)(i & 3) * 4, g = (int)(tg % groups);
-    unsigned w = 0;
-    for (int j = 0; j < 4; ++j)
-        if (row0 + j < N && g < have) w |= (zeros[(size_t)(row0 + j) * have + g] & 15u) << (4 * j);
-    out[i] = (uint16_t)w;
+    unsigned v = 0;
+    for (int j = 0; j < 4; ++j) {
+        const Q4Where w(i * 4 + j, kt, per);
+        if (w.n < N && w.g < have) v |= (zeros[(size_t)w.n * have + w.g] & 15u) << (4 * j);
+    }
+    out[i] = (uint16_t)v;
 }
 
 // One group of one row per wave.
@@ -120,22 +139,38 @@ struct Q4Args {
     const void *x;
     void *y;
     int64_t ldx, ldy;
-    int N, K, kt, groups, rows;
+    int N, K, kt, rows;
+    int cols;                  // columns of the product: rows x terms
+    int stretch;               // steps of K whose x is in LDS at a time
 };
 
-// The bf16 terms of a value: TERMS = 1 for bf16, 2 for fp16, 3 for fp32.
-template <typename V> struct Terms;
-template <> struct Terms<bf16_t> { static constexpr int n = 1; };
-template <> struct Terms<f16_t> { static constexpr int n = 2; };
-template <> struct Terms<float> { static constexpr int n = 3; };
+// What x of a type becomes in the product: its terms, and the operands' type.
+template <typename V> struct Operand;
+template <> struct Operand<bf16_t> {
+    static constexpr int terms = 1;
+    using T = bf16_t;
+    using X8 = bf16x8;
+};
+template <> struct Operand<f16_t> {
+    static constexpr int terms = 1;
+    using T = f16_t;
+    using X8 = f16x8;
+};
+template <> struct Operand<float> {
+    static constexpr int terms = 3;
+    using T = bf16_t;
+    using X8 = bf16x8;
+};
 
-__device__ __forceinline__ float cut(float &rest) {     // the leading 8 significand bits; rest keeps the others
-    const float hi = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-    rest -= hi;
-    return hi;
+__device__ __forceinline__ f32x4 product(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 product(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ bf16x8 weights(unsigned w) {
+// 16 + code of a word's eight codes.
+__device__ __forceinline__ void weights(unsigned w, bf16x8 &out) {
     union {
         unsigned u[4];
         bf16x8 v;
@@ -144,99 +179,197 @@ __device__ __forceinline__ bf16x8 weights(unsigned w) {
     r.u[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
     r.u[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
     r.u[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
-    return r.v;
+    out = r.v;
+}
+__device__ __forceinline__ void weights(unsigned w, f16x8 &out) {
+    union {
+        unsigned u[4];
+        f16x8 v;
+    } r;
+    r.u[0] = ((w << 6) & 0x03c003c0u) | 0x4c004c00u;
+    r.u[1] = ((w << 2) & 0x03c003c0u) | 0x4c004c00u;
+    r.u[2] = ((w >> 2) & 0x03c003c0u) | 0x4c004c00u;
+    r.u[3] = ((w >> 6) & 0x03c003c0u) | 0x4c004c00u;
+    out = r.v;
 }
 
-// A workgroup of four waves takes 16 outputs; the waves take every fourth
-// 128-wide step, and their sums meet in LDS.  CT column tiles of 16.
+// Eight inputs k.. of a row of x, zeros from K on.
+template <typename V>
+__device__ __forceinline__ Chunk<V, 8> inputs(const V *row, int k, int K) {
+    if (k + 8 <= K) return *reinterpret_cast<const Chunk<V, 8> *>(row + k);
+    Chunk<V, 8> v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? row[k + i] : (V)0.f;
+    return v;
+}
+
+// x of `steps` 128-wide steps from step t0 on, into LDS: [32-wide step][4][column]
+// chunks of eight inputs, as the lanes of the product read them.
+template <typename V, typename X8>
+__device__ __forceinline__ void stage(X8 *lds, const Q4Args &p, int t0, int steps) {
+    constexpr int TERMS = Operand<V>::terms;
+    const int chunks = steps * 16;
+    for (int i = threadIdx.x; i < chunks * p.rows; i += blockDim.x) {
+        const int r = i / chunks, c = i - r * chunks;
+        const Chunk<V, 8> v = inputs<V>(static_cast<const V *>(p.x) + r * p.ldx, t0 * 128 + c * 8, p.K);
+        X8 *to = lds + c * p.cols + r * TERMS;
+        if constexpr (TERMS == 1) {
+            X8 o;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = v[j];
+            to[0] = o;
+        } else {
+            // three terms of eight bits; the last one needs no cut
+            X8 o[3];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float rest = v[j];
+                const float hi = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+                rest -= hi;
+                const float mid = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+                o[0][j] = (bf16_t)hi;
+                o[1][j] = (bf16_t)mid;
+                o[2][j] = (bf16_t)(rest - mid);
+            }
+            to[0] = o[0], to[1] = o[1], to[2] = o[2];
+        }
+    }
+}
+
+constexpr int kQ4Ahead = 4;            // steps whose loads are under way together
+constexpr int kQ4Waves = 16;           // waves of a workgroup at most
+constexpr int kQ4Lds = 64 * 1024;      // bytes of x in LDS at most
+
+// CT column tiles of 16.
 template <typename V, typename S, int GROUP, int CT>
-__global__ void __launch_bounds__(256) k_q4(Q4Args p) {
-    constexpr int TERMS = Terms<V>::n;
-    __shared__ float part[4][CT][16][17];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__global__ void __launch_bounds__(kQ4Waves * 64) k_q4(Q4Args p) {
+    using Op = Operand<V>;
+    using X8 = typename Op::X8;
+    constexpr int TERMS = Op::terms, PER = 128 / GROUP;
+    extern __shared__ __align__(16) char lds[];
+    X8 *xs = reinterpret_cast<X8 *>(lds);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
     const int col = lane & 15, kq = lane >> 4;
     const int64_t tile = blockIdx.x;
+    const u32x4 *codes = p.codes + tile * p.kt * 64 + lane;
+    const Chunk<S, 4> *scales = reinterpret_cast<const Chunk<S, 4> *>(p.scales) + (tile * p.kt * 4 + kq) * PER;
+    const uint16_t *zeros = p.zeros ? p.zeros + (tile * p.kt * 4 + kq) * PER : nullptr;
+    int at[CT];                        // this lane's column of each tile (one without a column reads another's)
+#pragma unroll
+    for (int c = 0; c < CT; ++c) at[c] = kq * p.cols + (c * 16 + col < p.cols ? c * 16 + col : 0);
+    X8 ones;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ones[j] = (typename Op::T)1.f;
     f32x4 y[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) y[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int t = wave; t < p.kt; t += 4) {
-        const u32x4 w = p.codes[(tile * p.kt + t) * 64 + lane];
-        f32x4 acc[CT];
-        float sum[CT];
+
+    for (int t0 = 0; t0 < p.kt; t0 += p.stretch) {
+        const int t1 = t0 + p.stretch < p.kt ? t0 + p.stretch : p.kt;
+        bool staged = false;
+        for (int t = t0 + wave; t < t1 || !staged; t += waves * kQ4Ahead) {
+            u32x4 w[kQ4Ahead];
+            Chunk<S, 4> sc[kQ4Ahead][PER];
+            uint16_t ze[kQ4Ahead][PER];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if ((s * 32) % GROUP == 0)
+            for (int a = 0; a < kQ4Ahead; ++a) {
+                const int u = t + a * waves < t1 ? t + a * waves : t1 - 1;
+                w[a] = codes[(int64_t)u * 64];
 #pragma unroll
-                for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f}, sum[c] = 0.f;
-            const bf16x8 a = weights(w[s]);
-            const int k0 = t * 128 + s * 32 + kq * 8;
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const int xr = (c * 16 + col) / TERMS, term = (c * 16 + col) % TERMS;
-                bf16x8 b;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v = xr < p.rows && k0 + j < p.K
-                                  ? (float)static_cast<const V *>(p.x)[xr * p.ldx + k0 + j] : 0.f;
-                    float hi = v;
-#pragma unroll
-                    for (int i = 0; i < TERMS; ++i) {
-                        const float h = cut(v);
-                        if (i == term) hi = h;
-                    }
-                    b[j] = (__bf16)hi;
-                    sum[c] += hi;
+                for (int g = 0; g < PER; ++g) {
+                    sc[a][g] = scales[(int64_t)u * 4 * PER + g];
+                    ze[a][g] = zeros ? zeros[(int64_t)u * 4 * PER + g] : (uint16_t)0x8888u;
                 }
-                acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc[c], 0, 0, 0);
             }
-            if ((s + 1) * 32 % GROUP == 0) {
-                const int g = (t * 128 + s * 32) / GROUP;
-                const int64_t at = (tile * p.groups + g) * 16 + kq * 4;
-                const unsigned z = p.zeros ? p.zeros[at >> 2] : 0x8888u;
+            if (!staged) {             // under the first loads
+                if (t0) __syncthreads();
+                stage<V>(xs, p, t0, t1 - t0);
+                __syncthreads();
+                staged = true;
+            }
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    float x = sum[c];
-                    x += __shfl_xor(x, 16, 64);
-                    x += __shfl_xor(x, 32, 64);
+            for (int a = 0; a < kQ4Ahead; ++a) {
+                const int u = t + a * waves;
+                if (u >= t1) break;
+                const X8 *x = xs + (u - t0) * 16 * p.cols;
+#pragma unroll
+                for (int g = 0; g < PER; ++g) {
+                    f32x4 acc[CT], sum[CT];
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[c] = sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < GROUP / 32; ++s) {
+                        X8 q;
+                        weights(w[a][g * (GROUP / 32) + s], q);
+#pragma unroll
+                        for (int c = 0; c < CT; ++c) {
+                            const X8 b = x[(g * (GROUP / 32) + s) * 4 * p.cols + at[c]];
+                            acc[c] = product(q, b, acc[c]);
+                            sum[c] = product(ones, b, sum[c]);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float zero = (float)(16 + ((z >> (4 * i)) & 15u));
-                        const float scale = (float)static_cast<const S *>(p.scales)[at + i];
-                        y[c][i] = fmaf(scale, fmaf(-zero, x, acc[c][i]), y[c][i]);
+                        const float zero = (float)(16 + (((unsigned)ze[a][g] >> (4 * i)) & 15u));
+                        const float scale = (float)sc[a][g][i];
+#pragma unroll
+                        for (int c = 0; c < CT; ++c)
+                            y[c][i] = fmaf(scale, fmaf(-zero, sum[c][i], acc[c][i]), y[c][i]);
                     }
                 }
             }
         }
     }
+    // the waves' sums, in their order; then an input's terms, the smallest first
+    float *part = reinterpret_cast<float *>(lds);
+    __syncthreads();
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][c][kq * 4 + i][col] = y[c][i];
+        for (int i = 0; i < 4; ++i) part[((wave * CT + c) * 16 + kq * 4 + i) * 17 + col] = y[c][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * p.rows; i += 256) {
+    for (int i = threadIdx.x; i < 16 * p.rows; i += blockDim.x) {
         const int n = i & 15, r = i >> 4;
         float v = 0.f;
 #pragma unroll
         for (int j = TERMS - 1; j >= 0; --j) {
             const int k = r * TERMS + j;
             float q = 0.f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) q += part[u][k >> 4][n][k & 15];
+            for (int u = 0; u < waves; ++u) q += part[((u * CT + (k >> 4)) * 16 + n) * 17 + (k & 15)];
             v += q;
         }
         if (tile * 16 + n < p.N) static_cast<V *>(p.y)[r * p.ldy + tile * 16 + n] = (V)v;
     }
 }
 
+// Waves that split K: enough that the whole device has sixteen a CU, four at
+// least, no more than there are steps.
+int q4_waves(int tiles, int kt) {
+    const int want = (4096 + tiles - 1) / tiles;
+    return std::min(std::min(std::max(want, 4), kQ4Waves), kt);
+}
+
+template <typename V, typename S, int GROUP, int CT>
+void q4_launch(Q4Args a, hipStream_t st) {
+    const int tiles = (a.N + 15) / 16, waves = q4_waves(tiles, a.kt);
+    const int step = a.cols * 256;                       // bytes of x in LDS of one step
+    a.stretch = std::min(std::max(kQ4Lds / step, 1), a.kt);
+    if (a.stretch < a.kt) a.stretch = std::max(a.stretch / waves * waves, 1);
+    const size_t part = (size_t)waves * CT * 16 * 17 * sizeof(float);
+    const size_t bytes = std::max((size_t)a.stretch * step, part);
+    hipLaunchKernelGGL((k_q4<V, S, GROUP, CT>), dim3((unsigned)tiles), dim3(waves * 64), bytes, st, a);
+}
+
 template <typename V, typename S, int GROUP>
-void q4_launch(const Q4Args &a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.N + 15) / 16)), wg(256);
-    const int tiles = (a.rows * Terms<V>::n + 15) / 16;
-    if (tiles == 1) hipLaunchKernelGGL((k_q4<V, S, GROUP, 1>), grid, wg, 0, st, a);
-    if constexpr (Terms<V>::n > 1)
-        if (tiles == 2) hipLaunchKernelGGL((k_q4<V, S, GROUP, 2>), grid, wg, 0, st, a);
-    if constexpr (Terms<V>::n > 2)
-        if (tiles == 3) hipLaunchKernelGGL((k_q4<V, S, GROUP, 3>), grid, wg, 0, st, a);
+void q4_launch(Q4Args a, hipStream_t st) {
+    a.cols = a.rows * Operand<V>::terms;
+    const int tiles = (a.cols + 15) / 16;
+    if (tiles == 1) q4_launch<V, S, GROUP, 1>(a, st);
+    if constexpr (Operand<V>::terms == 3) {
+        if (tiles == 2) q4_launch<V, S, GROUP, 2>(a, st);
+        if (tiles == 3) q4_launch<V, S, GROUP, 3>(a, st);
+    }
 }
 
 template <typename V, typename S>
@@ -304,13 +437,14 @@ fi_status fi_q4_pack(const fi_q4_desc *desc, const uint8_t *codes, const void *s
     hipLaunchKernelGGL(k_q4_codes, dim3(blocks(words)), dim3(256), 0, st, desc->N, desc->K, l.kt, codes,
                        (unsigned *)(to + l.codes), words);
     if (desc->scale_dtype == FI_F32)
-        hipLaunchKernelGGL((k_q4_scales<float>), dim3(blocks(sc)), dim3(256), 0, st, desc->N, have, l.groups,
+        hipLaunchKernelGGL((k_q4_scales<float>), dim3(blocks(sc)), dim3(256), 0, st, desc->N, have, l.kt, 128 / desc->group,
                            (const float *)scales, (float *)(to + l.scales), sc);
     else    // both 16-bit types are copied as they are
-        hipLaunchKernelGGL((k_q4_scales<bf16_t>), dim3(blocks(sc)), dim3(256), 0, st, desc->N, have, l.groups,
+        hipLaunchKernelGGL((k_q4_scales<bf16_t>), dim3(blocks(sc)), dim3(256), 0, st, desc->N, have, l.kt, 128 / desc->group,
                            (const bf16_t *)scales, (bf16_t *)(to + l.scales), sc);
     if (zeros)
-        hipLaunchKernelGGL(k_q4_zeros, dim3(blocks(sc / 4)), dim3(256), 0, st, desc->N, have, l.groups, zeros,
+        hipLaunchKernelGGL(k_q4_zeros, dim3(blocks(sc / 4)), dim3(256), 0, st, desc->N, have, l.kt,
+                           128 / desc->group, zeros,
                            (uint16_t *)(to + l.zeros), sc / 4);
     return op_launched(call);
 }
@@ -360,7 +494,7 @@ fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int
     a.codes = (const u32x4 *)((const char *)packed + l.codes);
     a.scales = (const char *)packed + l.scales;
     a.zeros = desc->has_zeros ? (const uint16_t *)((const char *)packed + l.zeros) : nullptr;
-    a.x = x, a.y = y, a.N = desc->N, a.K = desc->K, a.kt = l.kt, a.groups = l.groups, a.rows = rows;
+    a.x = x, a.y = y, a.N = desc->N, a.K = desc->K, a.kt = l.kt, a.rows = rows;
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == FI_F32) q4_launch<float>(a, desc->group, desc->scale_dtype, st);
     else if (dtype == FI_BF16) q4_launch<bf16_t>(a, desc->group, desc->scale_dtype, st);
