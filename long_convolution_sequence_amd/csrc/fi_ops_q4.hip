@@ -10,9 +10,10 @@
 // so the terms add up to x exactly), each a column of its own.
 //
 // What bounds it: the bytes of the codes.  A workgroup takes 16 outputs, its
-// waves split K (128 inputs a step, every WK-th step), four steps' loads under
-// way at a time; x lies in LDS in the order of the product's operand, a stretch
-// of K at a time.  The waves' sums meet in LDS, in their order.
+// waves split K (128 inputs a step, a step a wave in turn).  A wave brings x of
+// its step through LDS into the order of the product's operand; with many
+// outputs it takes four row tiles for each operand.  The waves' sums meet in
+// LDS, in their order.
 //
 // Layout of the packed weights, tiles of 16 outputs x 128 inputs:
 //   codes  [N/16][K/128][64 lanes][4 words]   lane l: output l & 15; word s holds
@@ -22,6 +23,8 @@
 //          a lane of the product holds the outputs (l >> 4) * 4 + 0..3, and reads
 //          their scales of all the step's groups (128 / group) side by side
 // with N and K rounded up (codes 0, scales 0).
+#include <type_traits>
+
 #include "fi_ops.h"
 
 namespace fi {
@@ -141,7 +144,6 @@ struct Q4Args {
     int64_t ldx, ldy;
     int N, K, kt, rows;
     int cols;                  // columns of the product: rows x terms
-    int stretch;               // steps of K whose x is in LDS at a time
 };
 
 // What x of a type becomes in the product: its terms, and the operands' type.
@@ -203,162 +205,192 @@ __device__ __forceinline__ Chunk<V, 8> inputs(const V *row, int k, int K) {
     return v;
 }
 
-// x of `steps` 128-wide steps from step t0 on, into LDS: [32-wide step][4][column]
-// chunks of eight inputs, as the lanes of the product read them.
+// The three bf16 terms of fp32 values: eight significand bits each, by
+// truncation; the last one needs no cut.
+__device__ __forceinline__ void cut(float v, bf16_t &hi, bf16_t &mid, bf16_t &lo) {
+    const float h = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+    v -= h;
+    const float m = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+    hi = (bf16_t)h;
+    mid = (bf16_t)m;
+    lo = (bf16_t)(v - m);
+}
+
+// Eight inputs of a row into LDS, at its columns of a chunk's [column].
 template <typename V, typename X8>
-__device__ __forceinline__ void stage(X8 *lds, const Q4Args &p, int t0, int steps) {
-    constexpr int TERMS = Operand<V>::terms;
-    const int chunks = steps * 16;
-    for (int i = threadIdx.x; i < chunks * p.rows; i += blockDim.x) {
-        const int r = i / chunks, c = i - r * chunks;
-        const Chunk<V, 8> v = inputs<V>(static_cast<const V *>(p.x) + r * p.ldx, t0 * 128 + c * 8, p.K);
-        X8 *to = lds + c * p.cols + r * TERMS;
-        if constexpr (TERMS == 1) {
-            X8 o;
+__device__ __forceinline__ void put(X8 *to, const Chunk<V, 8> &v) {
+    if constexpr (Operand<V>::terms == 1) {
+        X8 o;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = v[j];
-            to[0] = o;
-        } else {
-            // three terms of eight bits; the last one needs no cut
-            X8 o[3];
+        for (int j = 0; j < 8; ++j) o[j] = v[j];
+        to[0] = o;
+    } else {
+        X8 o[3];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float rest = v[j];
-                const float hi = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-                rest -= hi;
-                const float mid = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-                o[0][j] = (bf16_t)hi;
-                o[1][j] = (bf16_t)mid;
-                o[2][j] = (bf16_t)(rest - mid);
-            }
-            to[0] = o[0], to[1] = o[1], to[2] = o[2];
+        for (int j = 0; j < 8; ++j) {
+            bf16_t t[3];
+            cut(v[j], t[0], t[1], t[2]);
+            o[0][j] = t[0], o[1][j] = t[1], o[2][j] = t[2];
         }
+        to[0] = o[0], to[1] = o[1], to[2] = o[2];
     }
 }
 
-constexpr int kQ4Ahead = 4;            // steps whose loads are under way together
 constexpr int kQ4Waves = 16;           // waves of a workgroup at most
-constexpr int kQ4Lds = 64 * 1024;      // bytes of x in LDS at most
+constexpr int kQ4Lds = 64 * 1024;      // bytes of LDS at most
+constexpr int kQ4Tall = 4;             // row tiles of a wave where there are many
+constexpr int kQ4TallFrom = 1024;
 
-// CT column tiles of 16.
-template <typename V, typename S, int GROUP, int CT>
-__global__ void __launch_bounds__(kQ4Waves * 64) k_q4(Q4Args p) {
+// RT row tiles and CT column tiles of 16.  Every wave brings x of its step into
+// a part of LDS of its own, so nothing waits at a barrier before the end.
+template <typename V, typename S, int GROUP, int CT, int RT>
+__global__ void __launch_bounds__(RT > 1 ? 512 : kQ4Waves * 64) k_q4(Q4Args p) {
     using Op = Operand<V>;
     using X8 = typename Op::X8;
     constexpr int TERMS = Op::terms, PER = 128 / GROUP;
+    constexpr int ROWS = TERMS == 1 ? 16 : CT * 16 / TERMS;      // rows of x at most
+    constexpr int LOADS = (ROWS + 3) / 4;                        // 16 lanes read a row's step
+    using Scales = S __attribute__((ext_vector_type(4 * PER)));
+    using Zeros = std::conditional_t<PER == 4, uint64_t, std::conditional_t<PER == 2, uint32_t, uint16_t>>;
+    const Scales *scales = static_cast<const Scales *>(p.scales);
+    const Zeros *zeros = reinterpret_cast<const Zeros *>(p.zeros);
     extern __shared__ __align__(16) char lds[];
-    X8 *xs = reinterpret_cast<X8 *>(lds);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
     const int col = lane & 15, kq = lane >> 4;
-    const int64_t tile = blockIdx.x;
-    const u32x4 *codes = p.codes + tile * p.kt * 64 + lane;
-    const Chunk<S, 4> *scales = reinterpret_cast<const Chunk<S, 4> *>(p.scales) + (tile * p.kt * 4 + kq) * PER;
-    const uint16_t *zeros = p.zeros ? p.zeros + (tile * p.kt * 4 + kq) * PER : nullptr;
-    int at[CT];                        // this lane's column of each tile (one without a column reads another's)
+    const int64_t tile = blockIdx.x * (int64_t)RT;
+    const int last = (p.N + 15) / 16 - 1;
+    // an odd number of 16-byte places between chunks: at an even one the writes of
+    // x (a row's chunks from 16 lanes) would meet in few banks
+    const int pitch = p.cols | 1;
+    X8 *xs = reinterpret_cast<X8 *>(lds) + wave * 16 * pitch;
+    // this lane's column of each column tile (one without a column reads another's)
+    int at[CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) at[c] = kq * p.cols + (c * 16 + col < p.cols ? c * 16 + col : 0);
+    for (int c = 0; c < CT; ++c) at[c] = kq * pitch + (c * 16 + col < p.cols ? c * 16 + col : 0);
     X8 ones;
 #pragma unroll
     for (int j = 0; j < 8; ++j) ones[j] = (typename Op::T)1.f;
-    f32x4 y[CT];
+    f32x4 y[RT][CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) y[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) y[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int t0 = 0; t0 < p.kt; t0 += p.stretch) {
-        const int t1 = t0 + p.stretch < p.kt ? t0 + p.stretch : p.kt;
-        bool staged = false;
-        for (int t = t0 + wave; t < t1 || !staged; t += waves * kQ4Ahead) {
-            u32x4 w[kQ4Ahead];
-            Chunk<S, 4> sc[kQ4Ahead][PER];
-            uint16_t ze[kQ4Ahead][PER];
+    for (int u = wave; u < p.kt; u += waves) {
+        u32x4 w[RT];
+        Scales sc[RT];
+        Zeros ze[RT];
+        Chunk<V, 8> raw[LOADS];
 #pragma unroll
-            for (int a = 0; a < kQ4Ahead; ++a) {
-                const int u = t + a * waves < t1 ? t + a * waves : t1 - 1;
-                w[a] = codes[(int64_t)u * 64];
-#pragma unroll
-                for (int g = 0; g < PER; ++g) {
-                    sc[a][g] = scales[(int64_t)u * 4 * PER + g];
-                    ze[a][g] = zeros ? zeros[(int64_t)u * 4 * PER + g] : (uint16_t)0x8888u;
-                }
-            }
-            if (!staged) {             // under the first loads
-                if (t0) __syncthreads();
-                stage<V>(xs, p, t0, t1 - t0);
-                __syncthreads();
-                staged = true;
-            }
-#pragma unroll
-            for (int a = 0; a < kQ4Ahead; ++a) {
-                const int u = t + a * waves;
-                if (u >= t1) break;
-                const X8 *x = xs + (u - t0) * 16 * p.cols;
-#pragma unroll
-                for (int g = 0; g < PER; ++g) {
-                    f32x4 acc[CT], sum[CT];
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) acc[c] = sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < GROUP / 32; ++s) {
-                        X8 q;
-                        weights(w[a][g * (GROUP / 32) + s], q);
-#pragma unroll
-                        for (int c = 0; c < CT; ++c) {
-                            const X8 b = x[(g * (GROUP / 32) + s) * 4 * p.cols + at[c]];
-                            acc[c] = product(q, b, acc[c]);
-                            sum[c] = product(ones, b, sum[c]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float zero = (float)(16 + (((unsigned)ze[a][g] >> (4 * i)) & 15u));
-                        const float scale = (float)sc[a][g][i];
-#pragma unroll
-                        for (int c = 0; c < CT; ++c)
-                            y[c][i] = fmaf(scale, fmaf(-zero, sum[c][i], acc[c][i]), y[c][i]);
-                    }
-                }
-            }
+        for (int m = 0; m < LOADS; ++m) {
+            if (m * 4 >= p.rows) break;
+            const int r = m * 4 + kq < p.rows ? m * 4 + kq : p.rows - 1;
+            const V *x = static_cast<const V *>(p.x) + r * p.ldx;
+            if (u * 128 + 128 <= p.K)
+                raw[m] = *reinterpret_cast<const Chunk<V, 8> *>(x + u * 128 + col * 8);
+            else
+                raw[m] = inputs<V>(x, u * 128 + col * 8, p.K);
         }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            // a row tile past the last one reads that one, and is not stored
+            const int64_t at = (tile + r < last ? tile + r : last) * p.kt + u;
+            w[r] = p.codes[at * 64 + lane];
+            sc[r] = scales[at * 4 + kq];
+            ze[r] = zeros ? zeros[at * 4 + kq] : (Zeros)0x8888888888888888ull;
+        }
+        // [32-wide step][4][column]; a wave's LDS accesses are done in order, so the
+        // reads of the step before come first
+#pragma unroll
+        for (int m = 0; m < LOADS; ++m)
+            if (m * 4 + kq < p.rows) put<V>(xs + col * pitch + (m * 4 + kq) * TERMS, raw[m]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int g = 0; g < PER; ++g) {
+            f32x4 acc[RT][CT], sum[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int r = 0; r < RT; ++r) acc[r][c] = sum[c];
+            }
+#pragma unroll
+            for (int s = 0; s < GROUP / 32; ++s) {
+                const int s32 = g * (GROUP / 32) + s;
+                X8 b[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    b[c] = xs[s32 * 4 * pitch + at[c]];
+                    sum[c] = product(ones, b[c], sum[c]);
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    X8 q;
+                    weights(w[r][s32], q);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[r][c] = product(q, b[c], acc[r][c]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float zero = (float)(16 + ((unsigned)(ze[r] >> (16 * g + 4 * i)) & 15u));
+                    const float scale = (float)sc[r][4 * g + i];
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        y[r][c][i] = fmaf(scale, fmaf(-zero, sum[c][i], acc[r][c][i]), y[r][c][i]);
+                }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     // the waves' sums, in their order; then an input's terms, the smallest first
     float *part = reinterpret_cast<float *>(lds);
-    __syncthreads();
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+    for (int r = 0; r < RT; ++r) {
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[((wave * CT + c) * 16 + kq * 4 + i) * 17 + col] = y[c][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * p.rows; i += blockDim.x) {
-        const int n = i & 15, r = i >> 4;
-        float v = 0.f;
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int j = TERMS - 1; j >= 0; --j) {
-            const int k = r * TERMS + j;
-            float q = 0.f;
-            for (int u = 0; u < waves; ++u) q += part[((u * CT + (k >> 4)) * 16 + n) * 17 + (k & 15)];
-            v += q;
+            for (int i = 0; i < 4; ++i) part[((wave * CT + c) * 16 + kq * 4 + i) * 17 + col] = y[r][c][i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 16 * p.rows; i += blockDim.x) {
+            const int n = i & 15, b = i >> 4;
+            float v = 0.f;
+#pragma unroll
+            for (int j = TERMS - 1; j >= 0; --j) {
+                const int k = b * TERMS + j;
+                float q = 0.f;
+                for (int u = 0; u < waves; ++u) q += part[((u * CT + (k >> 4)) * 16 + n) * 17 + (k & 15)];
+                v += q;
+            }
+            if ((tile + r) * 16 + n < p.N) static_cast<V *>(p.y)[b * p.ldy + (tile + r) * 16 + n] = (V)v;
         }
-        if (tile * 16 + n < p.N) static_cast<V *>(p.y)[r * p.ldy + tile * 16 + n] = (V)v;
     }
 }
 
 // Waves that split K: enough that the whole device has sixteen a CU, four at
 // least, no more than there are steps.
-int q4_waves(int tiles, int kt) {
-    const int want = (4096 + tiles - 1) / tiles;
-    return std::min(std::min(std::max(want, 4), kQ4Waves), kt);
+int q4_waves(int groups, int kt, int most) {
+    const int want = (4096 + groups - 1) / groups;
+    return std::min(std::min(std::max(want, 4), most), kt);
+}
+
+template <typename V, typename S, int GROUP, int CT, int RT>
+void q4_launch(const Q4Args &a, hipStream_t st) {
+    const int tiles = (a.N + 15) / 16, groups = (tiles + RT - 1) / RT;
+    const size_t step = (size_t)(a.cols | 1) * 256;      // bytes of x of one step in LDS
+    const int waves = std::min(q4_waves(groups, a.kt, RT > 1 ? 8 : kQ4Waves), kQ4Lds / (int)step);
+    const size_t part = (size_t)waves * CT * 16 * 17 * sizeof(float);
+    hipLaunchKernelGGL((k_q4<V, S, GROUP, CT, RT>), dim3((unsigned)groups), dim3(waves * 64),
+                       std::max(waves * step, part), st, a);
 }
 
 template <typename V, typename S, int GROUP, int CT>
-void q4_launch(Q4Args a, hipStream_t st) {
-    const int tiles = (a.N + 15) / 16, waves = q4_waves(tiles, a.kt);
-    const int step = a.cols * 256;                       // bytes of x in LDS of one step
-    a.stretch = std::min(std::max(kQ4Lds / step, 1), a.kt);
-    if (a.stretch < a.kt) a.stretch = std::max(a.stretch / waves * waves, 1);
-    const size_t part = (size_t)waves * CT * 16 * 17 * sizeof(float);
-    const size_t bytes = std::max((size_t)a.stretch * step, part);
-    hipLaunchKernelGGL((k_q4<V, S, GROUP, CT>), dim3((unsigned)tiles), dim3(waves * 64), bytes, st, a);
+void q4_launch(const Q4Args &a, hipStream_t st) {
+    if ((a.N + 15) / 16 >= kQ4TallFrom) q4_launch<V, S, GROUP, CT, kQ4Tall>(a, st);
+    else q4_launch<V, S, GROUP, CT, 1>(a, st);
 }
 
 template <typename V, typename S, int GROUP>
