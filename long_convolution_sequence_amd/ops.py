@@ -15,12 +15,13 @@ is fine); states, weights and ``lengths`` are densely packed.  Sequences are
 """
 from __future__ import annotations
 
-import ctypes
+import functools
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
-from .fi import FI_EDEVICE, FI_EINVAL, FI_OK, FiError, load_library
+from .fi import FI_EINVAL, FI_OK, FiError, load_library
 
 F32, BF16, F16 = 0, 1, 2
 SCAN_PLAIN, SCAN_CONVEX, SCAN_ENERGY = 0, 1, 2
@@ -30,24 +31,10 @@ GATE_LINEAR, GATE_SIGMOID, GATE_SILU = 0, 1, 2
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
-class ScanDesc(ctypes.Structure):
-    _fields_ = [("T", ctypes.c_int64), ("batch", ctypes.c_int), ("channels", ctypes.c_int), ("dtype", ctypes.c_int),
-                ("input", ctypes.c_int), ("ld_x", ctypes.c_int64), ("ld_gate", ctypes.c_int64),
-                ("ld_y", ctypes.c_int64), ("ld_dy", ctypes.c_int64), ("ld_dx", ctypes.c_int64),
-                ("ld_dgate", ctypes.c_int64), ("reserved", ctypes.c_int * 4)]
-
-
-class NormDesc(ctypes.Structure):
-    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int), ("dtype", ctypes.c_int),
-                ("res_dtype", ctypes.c_int), ("post_norm", ctypes.c_int), ("act", ctypes.c_int),
-                ("eps", ctypes.c_float)] + \
-        [(n, ctypes.c_int64) for n in ("ld_o", "ld_gate", "ld_res", "ld_r", "ld_a", "ld_dr", "ld_da", "ld_do",
-                                       "ld_dgate", "ld_dres")] + [("reserved", ctypes.c_int * 4)]
-
-
-class Q4Desc(ctypes.Structure):
-    _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("group", ctypes.c_int), ("scale_dtype", ctypes.c_int),
-                ("has_zeros", ctypes.c_int), ("reserved", ctypes.c_int * 3)]
+# The descriptors of include/fi.h, packed (reserved fields zero).
+_SCAN_DESC = struct.Struct("=q4i6q16x")       # T batch channels dtype input ld_x ld_gate ld_y ld_dy ld_dx ld_dgate
+_NORM_DESC = struct.Struct("=q5if10q16x")     # rows channels dtype res_dtype post_norm act eps ld_o .. ld_dres
+_Q4_DESC = struct.Struct("=5i12x")            # N K group scale_dtype has_zeros
 
 
 def _bad(what):
@@ -61,12 +48,13 @@ def _check(status):
 
 
 def _device(t, name):
-    """The device every tensor of a call has to be on: that of its first one."""
+    """Index of the device that every tensor of a call has to be on: that of its first one."""
     if not isinstance(t, torch.Tensor):
         _bad(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         _bad(f"{name}: not a device tensor")
-    return t.device
+    return index
 
 
 def _type(t, name):
@@ -76,21 +64,31 @@ def _type(t, name):
     return d
 
 
-def _rows(t, shape, dtype, device, name):
-    """(pointer, row pitch) of a tensor of that exact shape, dtype and device
-    with contiguous rows at one pitch; (None, 0) for None."""
-    if t is None:
-        return None, 0
+def _fits(t, shape, dtype, device, name):
+    """Check a tensor's shape, dtype and device (an index, -1 the host)."""
     if not isinstance(t, torch.Tensor):
         _bad(f"{name}: expected a torch tensor, got {type(t).__name__}")
     if t.shape != shape:
         _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         _bad(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        _bad(f"{name}: on {t.device}, expected {device}")
-    if t.is_contiguous():
+    if t.get_device() != device:
+        _bad(f"{name}: on {t.device}, expected the call's device {device}")
+
+
+def _packed(t, shape, dtype, device):
+    return (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == device and
+            t.is_contiguous())
+
+
+def _rows(t, shape, dtype, device, name):
+    """(pointer, row pitch) of a tensor of that exact shape, dtype and device
+    with contiguous rows at one pitch (0: densely packed); (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if _packed(t, shape, dtype, device):
         return t.data_ptr(), 0
+    _fits(t, shape, dtype, device, name)
     if t.stride(-1) != 1 and shape[-1] != 1:
         _bad(f"{name}: its rows are not contiguous")
     pitch, step = None, 0
@@ -111,46 +109,59 @@ def _dense(t, shape, dtype, device, name):
     """Pointer of a densely packed tensor, or None."""
     if t is None:
         return None
-    p, _ = _rows(t, shape, dtype, device, name)
-    if not t.is_contiguous():
-        _bad(f"{name}: not contiguous")
-    return p
+    if _packed(t, shape, dtype, device):
+        return t.data_ptr()
+    _fits(t, shape, dtype, device, name)
+    _bad(f"{name}: not contiguous")
+
+
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream      # the hipStream_t of a device's current stream
 
 
 def _call(device, fn, *args):
     """Run one C call on the device's current stream (its last argument)."""
-    if device.index != torch.cuda.current_device():
+    if device != _current_device():
         with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            status = fn(*args, _current_stream(device))
     else:
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        status = fn(*args, _current_stream(device))
+    if status != FI_OK:
+        _check(status)
 
 
-def _bytes(n, device):
-    return torch.empty(n, dtype=torch.uint8, device=device)
+def _bytes(n, like):
+    return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
 # ---- gated linear recurrence ---------------------------------------------------
 
-def _scan_desc(x, input):
+@functools.lru_cache(maxsize=256)
+def _scan_sizes(T, B, D, dtype, input):
+    """Bytes of the forward pass's workspace, the backward pass's, and the saved states."""
+    lib = load_library()
+    d = _SCAN_DESC.pack(T, B, D, dtype, input, 0, 0, 0, 0, 0, 0)
+    return lib.fi_scan_workspace_bytes(d, 0), lib.fi_scan_workspace_bytes(d, 1), lib.fi_scan_saved_bytes(d)
+
+
+def _scan_inputs(x, gate, bias, state, lengths, input):
     device = _device(x, "x")
-    if x.dim() != 3 or x.shape[1] < 1 or x.shape[2] < 1:
-        _bad(f"x: shape {tuple(x.shape)}, expected [T][B][D]")
-    q = ScanDesc()
-    q.T, q.batch, q.channels = x.shape
-    q.dtype, q.input = _type(x, "x"), input
-    return q, device
-
-
-def _scan_inputs(q, x, gate, bias, state, lengths, device):
-    B, D = q.batch, q.channels
-    px, q.ld_x = _rows(x, x.shape, x.dtype, device, "x")
+    shape = x.shape
+    if len(shape) != 3 or shape[1] < 1 or shape[2] < 1:
+        _bad(f"x: shape {tuple(shape)}, expected [T][B][D]")
+    if input not in (SCAN_PLAIN, SCAN_CONVEX, SCAN_ENERGY):
+        _bad(f"input: {input!r}, expected SCAN_PLAIN, SCAN_CONVEX or SCAN_ENERGY")
+    T, B, D = shape
+    dtype = x.dtype
+    head = (T, B, D, _type(x, "x"), input)
+    px, ldx = _rows(x, shape, dtype, device, "x")
     if gate is None:
         _bad("gate: required")
-    pg, q.ld_gate = _rows(gate, x.shape, x.dtype, device, "gate")
-    return (px, pg, _dense(bias, (D,), torch.float32, device, "bias"),
-            _dense(state, (B, D), torch.float32, device, "state"),
-            _dense(lengths, (B,), torch.int32, device, "lengths"))
+    pg, ldg = _rows(gate, shape, dtype, device, "gate")
+    return (device, shape, dtype, head, (ldx, ldg),
+            (px, pg, _dense(bias, (D,), torch.float32, device, "bias"),
+             _dense(state, (B, D), torch.float32, device, "state"),
+             _dense(lengths, (B,), torch.int32, device, "lengths")))
 
 
 def gated_scan(x, gate, bias=None, state=None, lengths=None, *, input=SCAN_CONVEX, save=False, y=None, final=None):
@@ -160,24 +171,25 @@ def gated_scan(x, gate, bias=None, state=None, lengths=None, *, input=SCAN_CONVE
     (SCAN_PLAIN), d (SCAN_CONVEX) or sqrt(d (2 - d)) (SCAN_ENERGY).
 
     x, gate [T][B][D] of one type; bias [D], state [B][D] fp32 (the state before the first position)
-    or None for zeros; lengths [B] int32 or None: rows past a sequence's length are not read, give
+    or None for zeros; lengths [B] int32 or None: rows past a sequence's length count for nothing, give
     y = 0 and leave the state.  Returns (y, final [B][D] fp32), with save=True also what
     gated_scan_backward needs.  final may be given as the state itself."""
-    q, device = _scan_desc(x, input)
-    args = _scan_inputs(q, x, gate, bias, state, lengths, device)
+    device, shape, dtype, head, ld, args = _scan_inputs(x, gate, bias, state, lengths, input)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=device)
-    py, q.ld_y = _rows(y, x.shape, x.dtype, device, "y")
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+        py, ldy = y.data_ptr(), 0
+    else:
+        py, ldy = _rows(y, shape, dtype, device, "y")
     if final is None:
-        final = torch.empty((q.batch, q.channels), dtype=torch.float32, device=device)
-    pf = _dense(final, (q.batch, q.channels), torch.float32, device, "final")
-    lib = load_library()
-    desc = ctypes.addressof(q)
-    n = lib.fi_scan_workspace_bytes(desc, 0)
-    work = _bytes(n, device) if n > 256 else None
-    saved = _bytes(lib.fi_scan_saved_bytes(desc), device) if save else None
-    _call(device, lib.fi_scan_forward, desc, *args, py, pf, saved.data_ptr() if save else None,
-          work.data_ptr() if work is not None else None)
+        final = torch.empty(shape[1:], dtype=torch.float32, device=x.device)
+        pf = final.data_ptr()
+    else:
+        pf = _dense(final, shape[1:], torch.float32, device, "final")
+    work, _, kept = _scan_sizes(*head)
+    work = _bytes(work, x) if work > 256 else None
+    saved = _bytes(kept, x) if save else None
+    _call(device, load_library().fi_scan_forward, _SCAN_DESC.pack(*head, *ld, ldy, 0, 0, 0), *args, py, pf,
+          saved.data_ptr() if save else None, work.data_ptr() if work is not None else None)
     return (y, final, saved) if save else (y, final)
 
 
@@ -200,29 +212,23 @@ def gated_scan_backward(dy, x, gate, saved, bias=None, state=None, lengths=None,
     """Gradients of gated_scan (fi_scan_backward): the forward call's arguments, its `saved`, and the
     gradients dy [T][B][D] and dfinal [B][D] fp32 (or None) of its outputs.  Returns (dx, dgate,
     dbias, dstate); dbias and dstate are None where bias and state are."""
-    q, device = _scan_desc(x, input)
-    px, pg, pb, ps, pl = _scan_inputs(q, x, gate, bias, state, lengths, device)
-    if dy is None:
-        _bad("dy: required")
-    pdy, q.ld_dy = _rows(dy, x.shape, x.dtype, device, "dy")
-    B, D = q.batch, q.channels
-    pdf = _dense(dfinal, (B, D), torch.float32, device, "dfinal")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=device) if dx is None else dx
-    dgate = torch.empty(x.shape, dtype=x.dtype, device=device) if dgate is None else dgate
-    pdx, q.ld_dx = _rows(dx, x.shape, x.dtype, device, "dx")
-    pdg, q.ld_dgate = _rows(dgate, x.shape, x.dtype, device, "dgate")
-    dbias = torch.empty((D,), dtype=torch.float32, device=device) if bias is not None else None
-    dstate = torch.empty((B, D), dtype=torch.float32, device=device) if state is not None else None
-    lib = load_library()
-    desc = ctypes.addressof(q)
-    n = lib.fi_scan_saved_bytes(desc)
-    psv = _dense(saved, (n,), torch.uint8, device, "saved")
-    if psv is None:
-        _bad("saved: required")
-    work = _bytes(lib.fi_scan_workspace_bytes(desc, 1), device)
-    _call(device, lib.fi_scan_backward, desc, px, pg, pb, ps, pl, psv, pdy, pdf, pdx, pdg,
-          dbias.data_ptr() if dbias is not None else None, dstate.data_ptr() if dstate is not None else None,
-          work.data_ptr())
+    device, shape, dtype, head, ld, args = _scan_inputs(x, gate, bias, state, lengths, input)
+    if dy is None or saved is None:
+        _bad("dy and saved are required")
+    pdy, lddy = _rows(dy, shape, dtype, device, "dy")
+    pdf = _dense(dfinal, shape[1:], torch.float32, device, "dfinal")
+    dx = torch.empty(shape, dtype=dtype, device=x.device) if dx is None else dx
+    dgate = torch.empty(shape, dtype=dtype, device=x.device) if dgate is None else dgate
+    pdx, lddx = _rows(dx, shape, dtype, device, "dx")
+    pdg, lddg = _rows(dgate, shape, dtype, device, "dgate")
+    dbias = torch.empty(shape[2:], dtype=torch.float32, device=x.device) if bias is not None else None
+    dstate = torch.empty(shape[1:], dtype=torch.float32, device=x.device) if state is not None else None
+    _, work, kept = _scan_sizes(*head)
+    psv = _dense(saved, (kept,), torch.uint8, device, "saved")
+    work = _bytes(work, x)
+    _call(device, load_library().fi_scan_backward, _SCAN_DESC.pack(*head, *ld, 0, lddy, lddx, lddg), *args, psv, pdy,
+          pdf, pdx, pdg, dbias.data_ptr() if dbias is not None else None,
+          dstate.data_ptr() if dstate is not None else None, work.data_ptr())
     return dx, dgate, dbias, dstate
 
 
@@ -237,33 +243,29 @@ class NormGradients(NamedTuple):
     pre_weight: Optional[torch.Tensor]
 
 
-def _norm_desc(o, res, post_norm, act, eps):
+def _norm_inputs(o, res, gate, post_weight, scale, pre_weight, post_norm, act, eps):
     first = o if o is not None else res
     if first is None:
         _bad("o or res is required")
     device = _device(first, "o" if o is not None else "res")
-    if first.dim() < 1 or first.shape[-1] < 1:
-        _bad(f"o: shape {tuple(first.shape)}, expected [..., D]")
-    q = NormDesc()
-    q.channels = first.shape[-1]
-    q.rows = first.numel() // q.channels
-    q.dtype = _type(first, "o")
-    q.post_norm, q.act, q.eps = int(bool(post_norm)), act, eps
-    return q, device, first.shape, first.dtype
-
-
-def _norm_inputs(q, o, res, gate, post_weight, scale, pre_weight, device, shape, dtype):
+    shape, dtype = first.shape, first.dtype
+    if len(shape) < 1 or shape[-1] < 1:
+        _bad(f"o: shape {tuple(shape)}, expected [..., D]")
+    if act not in (GATE_LINEAR, GATE_SIGMOID, GATE_SILU):
+        _bad(f"act: {act!r}, expected GATE_LINEAR, GATE_SIGMOID or GATE_SILU")
+    D = shape[-1]
+    rows = first.numel() // D
     rt = res.dtype if isinstance(res, torch.Tensor) else dtype
-    if rt != dtype and rt != torch.float32:
+    if rt is not dtype and rt is not torch.float32:
         _bad(f"res: dtype {rt}, expected {dtype} or torch.float32")
-    q.res_dtype = _TYPES[rt]
-    D = (q.channels,)
-    po, q.ld_o = _rows(o, shape, dtype, device, "o")
-    pg, q.ld_gate = _rows(gate, shape, dtype, device, "gate")
-    pr, q.ld_res = _rows(res, shape, rt, device, "res")
-    return rt, (po, pg, pr, _dense(post_weight, D, torch.float32, device, "post_weight"),
-                _dense(scale, D, torch.float32, device, "scale"),
-                _dense(pre_weight, D, torch.float32, device, "pre_weight"))
+    po, ldo = _rows(o, shape, dtype, device, "o")
+    pg, ldg = _rows(gate, shape, dtype, device, "gate")
+    pr, ldr = _rows(res, shape, rt, device, "res")
+    head = (rows, D, _type(first, "o"), _TYPES[rt], int(bool(post_norm)), act, eps, ldo, ldg, ldr)
+    return (first, device, shape, dtype, rt, rows, head,
+            (po, pg, pr, _dense(post_weight, (D,), torch.float32, device, "post_weight"),
+             _dense(scale, (D,), torch.float32, device, "scale"),
+             _dense(pre_weight, (D,), torch.float32, device, "pre_weight")))
 
 
 def block_norm(o, res=None, gate=None, *, post_weight=None, scale=None, pre_weight=None, post_norm=False,
@@ -275,16 +277,27 @@ def block_norm(o, res=None, gate=None, *, post_weight=None, scale=None, pre_weig
     (r = res; then a has res's type).  o, gate, a [..., D] of one type; res, r of that type or
     fp32; weights and scale fp32 [D].  r may be given as res itself.  Returns (r, a), with
     save=True also what block_norm_backward needs."""
-    q, device, shape, dtype = _norm_desc(o, res, post_norm, act, eps)
-    rt, args = _norm_inputs(q, o, res, gate, post_weight, scale, pre_weight, device, shape, dtype)
-    r = torch.empty(shape, dtype=rt, device=device) if r is None else r
-    a = torch.empty(shape, dtype=dtype, device=device) if a is None else a
-    pr, q.ld_r = _rows(r, shape, rt, device, "r")
-    pa, q.ld_a = _rows(a, shape, dtype, device, "a")
-    saved = torch.empty((2, q.rows), dtype=torch.float32, device=device) if save else None
-    _call(device, load_library().fi_norm_forward, ctypes.addressof(q), *args, pr, pa,
+    first, device, shape, dtype, rt, rows, head, args = _norm_inputs(o, res, gate, post_weight, scale, pre_weight,
+                                                                     post_norm, act, eps)
+    if r is None:
+        r = torch.empty(shape, dtype=rt, device=first.device)
+        pr, ldr = r.data_ptr(), 0
+    else:
+        pr, ldr = _rows(r, shape, rt, device, "r")
+    if a is None:
+        a = torch.empty(shape, dtype=dtype, device=first.device)
+        pa, lda = a.data_ptr(), 0
+    else:
+        pa, lda = _rows(a, shape, dtype, device, "a")
+    saved = torch.empty((2, rows), dtype=torch.float32, device=first.device) if save else None
+    _call(device, load_library().fi_norm_forward, _NORM_DESC.pack(*head, ldr, lda, 0, 0, 0, 0, 0), *args, pr, pa,
           saved.data_ptr() if save else None)
     return (r, a, saved) if save else (r, a)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(rows, D, dtype, res_dtype):
+    return load_library().fi_norm_workspace_bytes(_NORM_DESC.pack(rows, D, dtype, res_dtype, 0, 0, 0.0, *([0] * 10)))
 
 
 def block_norm_backward(dr, da, o, res, gate, saved, *, post_weight=None, scale=None, pre_weight=None,
@@ -292,32 +305,30 @@ def block_norm_backward(dr, da, o, res, gate, saved, *, post_weight=None, scale=
     """Gradients of block_norm (fi_norm_backward) from those of r and a (either may be None): the
     forward call's arguments and its `saved`.  Returns NormGradients, None where the input is None.
     dres may be given as dr itself."""
-    q, device, shape, dtype = _norm_desc(o, res, post_norm, act, eps)
-    rt, args = _norm_inputs(q, o, res, gate, post_weight, scale, pre_weight, device, shape, dtype)
-    psv = _dense(saved, (2, q.rows), torch.float32, device, "saved")
-    if psv is None:
+    first, device, shape, dtype, rt, rows, head, args = _norm_inputs(o, res, gate, post_weight, scale, pre_weight,
+                                                                     post_norm, act, eps)
+    if saved is None:
         _bad("saved: required")
-    pdr, q.ld_dr = _rows(dr, shape, rt, device, "dr")
-    pda, q.ld_da = _rows(da, shape, dtype, device, "da")
+    psv = _dense(saved, (2, rows), torch.float32, device, "saved")
+    pdr, lddr = _rows(dr, shape, rt, device, "dr")
+    pda, ldda = _rows(da, shape, dtype, device, "da")
 
     def like(given, want, dt):
-        return torch.empty(shape, dtype=dt, device=device) if want is not None and given is None else given
+        return torch.empty(shape, dtype=dt, device=first.device) if want is not None and given is None else given
     do, dres, dgate = like(do, o, dtype), like(dres, res, rt), like(dgate, gate, dtype)
-    pdo, q.ld_do = _rows(do, shape, dtype, device, "do")
-    pdres, q.ld_dres = _rows(dres, shape, rt, device, "dres")
-    pdg, q.ld_dgate = _rows(dgate, shape, dtype, device, "dgate")
-    if pre_weight is not None and da is None:
-        cols = torch.zeros((3, q.channels), dtype=torch.float32, device=device)
-    else:
-        cols = torch.empty((3, q.channels), dtype=torch.float32, device=device)
+    pdo, lddo = _rows(do, shape, dtype, device, "do")
+    pdres, lddres = _rows(dres, shape, rt, device, "dres")
+    pdg, lddg = _rows(dgate, shape, dtype, device, "dgate")
+    D = shape[-1]
+    cols = torch.empty((3, D), dtype=torch.float32, device=first.device)
     w = [cols[i] if t is not None else None for i, t in enumerate((post_weight, scale, pre_weight))]
     ptr = [t.data_ptr() if t is not None else None for t in w]
-    if da is None:
+    if da is None and w[2] is not None:
+        w[2].zero_()
         ptr[2] = None
-    lib = load_library()
-    desc = ctypes.addressof(q)
-    work = _bytes(lib.fi_norm_workspace_bytes(desc), device)
-    _call(device, lib.fi_norm_backward, desc, *args, psv, pdr, pda, pdo, pdg, pdres, *ptr, work.data_ptr())
+    work = _bytes(_norm_workspace(rows, D, head[2], head[3]), first)
+    _call(device, load_library().fi_norm_backward, _NORM_DESC.pack(*head, 0, 0, lddr, ldda, lddo, lddg, lddres), *args,
+          psv, pdr, pda, pdo, pdg, pdres, *ptr, work.data_ptr())
     return NormGradients(do, dres, dgate, *w)
 
 
@@ -337,21 +348,19 @@ class Q4Weight:
             _bad(f"codes: shape {tuple(codes.shape)}, expected [N][K]")
         if not isinstance(scales, torch.Tensor):
             _bad(f"scales: expected a torch tensor, got {type(scales).__name__}")
-        q = Q4Desc()
-        q.N, q.K = codes.shape
-        q.group, q.scale_dtype, q.has_zeros = group, _type(scales, "scales"), int(zeros is not None)
-        self.N, self.K, self.group, self.device = q.N, q.K, group, device
+        self.N, self.K = codes.shape
+        self.group, self.device, self._index = group, codes.device, device
+        self._desc = _Q4_DESC.pack(self.N, self.K, group, _type(scales, "scales"), int(zeros is not None))
         lib = load_library()
-        self._desc = q
-        n = lib.fi_q4_packed_bytes(ctypes.addressof(q))
+        n = lib.fi_q4_packed_bytes(self._desc)
         if n == 0:
-            _bad(f"unsupported N={q.N} K={q.K} group={group}")
-        shape = (q.N, -(-q.K // group))
+            _bad(f"unsupported N={self.N} K={self.K} group={group}")
+        shape = (self.N, -(-self.K // group))
         pc = _dense(codes, codes.shape, torch.uint8, device, "codes")
         ps = _dense(scales, shape, scales.dtype, device, "scales")
         pz = _dense(zeros, shape, torch.uint8, device, "zeros")
-        self.packed = _bytes(n, device)
-        _call(device, lib.fi_q4_pack, ctypes.addressof(q), pc, ps, pz, self.packed.data_ptr())
+        self.packed = _bytes(n, codes)
+        _call(device, lib.fi_q4_pack, self._desc, pc, ps, pz, self.packed.data_ptr())
 
     @classmethod
     def quantize(cls, w, *, group=128, scale_dtype=torch.bfloat16):
@@ -364,15 +373,13 @@ class Q4Weight:
             _bad(f"scale_dtype: {scale_dtype}, expected float32, bfloat16 or float16")
         if group not in (32, 64, 128):
             _bad(f"group: {group}, expected 32, 64 or 128")
-        q = Q4Desc()
-        q.N, q.K = w.shape
-        q.group, q.scale_dtype = group, _TYPES[scale_dtype]
+        N, K = w.shape
         wt = _type(w, "w")
         pw, ld = _rows(w, w.shape, w.dtype, device, "w")
-        codes = torch.empty(w.shape, dtype=torch.uint8, device=device)
-        scales = torch.empty((q.N, -(-q.K // group)), dtype=scale_dtype, device=device)
-        _call(device, load_library().fi_q4_quantize, ctypes.addressof(q), wt, pw, ld, codes.data_ptr(),
-              scales.data_ptr())
+        codes = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((N, -(-K // group)), dtype=scale_dtype, device=w.device)
+        _call(device, load_library().fi_q4_quantize, _Q4_DESC.pack(N, K, group, _TYPES[scale_dtype], 0), wt, pw, ld,
+              codes.data_ptr(), scales.data_ptr())
         out = cls(codes, scales, group=group)
         out.codes, out.scales = codes, scales
         return out
@@ -383,16 +390,18 @@ def q4_matvec(w, x, y=None):
     if not isinstance(w, Q4Weight):
         _bad(f"w: expected a Q4Weight, got {type(w).__name__}")
     device = _device(x, "x")
-    if device != w.device:
-        _bad(f"x: on {device}, expected {w.device}")
+    if device != w._index:
+        _bad(f"x: on {x.device}, expected {w.device}")
     if x.dim() != 2:
         _bad(f"x: shape {tuple(x.shape)}, expected [B][{w.K}]")
+    dtype = x.dtype
     dt = _type(x, "x")
     rows = x.shape[0]
-    px, ldx = _rows(x, (rows, w.K), x.dtype, device, "x")
+    px, ldx = _rows(x, (rows, w.K), dtype, device, "x")
     if y is None:
-        y = torch.empty((rows, w.N), dtype=x.dtype, device=device)
-    py, ldy = _rows(y, (rows, w.N), x.dtype, device, "y")
-    _call(device, load_library().fi_q4_matvec, ctypes.addressof(w._desc), w.packed.data_ptr(), rows, dt, px, ldx, py,
-          ldy)
+        y = torch.empty((rows, w.N), dtype=dtype, device=x.device)
+        py, ldy = y.data_ptr(), 0
+    else:
+        py, ldy = _rows(y, (rows, w.N), dtype, device, "y")
+    _call(device, load_library().fi_q4_matvec, w._desc, w.packed.data_ptr(), rows, dt, px, ldx, py, ldy)
     return y

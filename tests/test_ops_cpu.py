@@ -7,6 +7,26 @@ import torch
 
 from long_convolution_sequence_amd import fi, ops
 
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("batch", ctypes.c_int), ("channels", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("input", ctypes.c_int), ("ld_x", ctypes.c_int64), ("ld_gate", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("ld_dy", ctypes.c_int64), ("ld_dx", ctypes.c_int64),
+                ("ld_dgate", ctypes.c_int64), ("reserved", ctypes.c_int * 4)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("res_dtype", ctypes.c_int), ("post_norm", ctypes.c_int), ("act", ctypes.c_int),
+                ("eps", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("ld_o", "ld_gate", "ld_res", "ld_r", "ld_a", "ld_dr", "ld_da", "ld_do",
+                                       "ld_dgate", "ld_dres")] + [("reserved", ctypes.c_int * 4)]
+
+
+class Q4Desc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("group", ctypes.c_int), ("scale_dtype", ctypes.c_int),
+                ("has_zeros", ctypes.c_int), ("reserved", ctypes.c_int * 3)]
+
+
 P = 0x100000          # made-up device addresses: nothing below reaches a launch
 STEP = 0x1000000
 
@@ -21,7 +41,7 @@ def _ptrs(n):
 
 
 def _scan(T=300, B=2, D=5, dtype=ops.F32, input=ops.SCAN_CONVEX, **kw):
-    q = ops.ScanDesc()
+    q = ScanDesc()
     q.T, q.batch, q.channels, q.dtype, q.input = T, B, D, dtype, input
     for k, v in kw.items():
         setattr(q, k, v)
@@ -110,7 +130,7 @@ def test_scan_backward_outputs_may_not_overlap(lib, kw):
 
 
 def _norm(rows=7, D=9, dtype=ops.BF16, res_dtype=ops.F32, post_norm=1, act=ops.GATE_SILU, eps=1e-6, **kw):
-    q = ops.NormDesc()
+    q = NormDesc()
     q.rows, q.channels, q.dtype, q.res_dtype, q.post_norm, q.act, q.eps = rows, D, dtype, res_dtype, post_norm, act, eps
     for k, v in kw.items():
         setattr(q, k, v)
@@ -185,7 +205,7 @@ def test_norm_backward_outputs_may_not_overlap(lib, kw):
 
 
 def _q4(N=20, K=70, group=32, scale_dtype=ops.BF16, has_zeros=0):
-    q = ops.Q4Desc()
+    q = Q4Desc()
     q.N, q.K, q.group, q.scale_dtype, q.has_zeros = N, K, group, scale_dtype, has_zeros
     return q
 
@@ -249,7 +269,7 @@ def test_binding_refuses_host_tensors_and_wrong_types():
 
 def test_row_pitches():
     """What the binding takes as rows at one pitch, and what it refuses."""
-    cpu = torch.device("cpu")
+    cpu = -1
     wide = torch.zeros(6, 2, 24)
     assert ops._rows(wide, wide.shape, torch.float32, cpu, "t")[1] == 0
     assert ops._rows(wide[..., 8:16], (6, 2, 8), torch.float32, cpu, "t")[1] == 24
