@@ -462,6 +462,8 @@ fi_status fi_dd_destroy(fi_dd *ctx);
  *    unless stated (FI_EINVAL); column slices of one tensor are separate.
  *  - A workspace (256-byte aligned) belongs to one call until its work on the
  *    stream is done; its contents need no initialisation and do not survive.
+ *  - Pointers are aligned to their values, workspaces, saved states and packed
+ *    weights to 256 bytes.
  *  - FI_EINVAL for a bad argument, FI_EDEVICE for a failed launch; nothing is
  *    launched when FI_EINVAL is returned.  fi_op_last_error() describes the
  *    calling thread's last failure.
@@ -481,8 +483,8 @@ const char *fi_op_last_error(void);
 enum { FI_SCAN_PLAIN = 0, FI_SCAN_CONVEX = 1, FI_SCAN_ENERGY = 2 };
 
 typedef struct fi_scan_desc {
-    int64_t T;             /* positions, >= 0 */
-    int batch, channels;   /* B, D >= 1 */
+    int64_t T;             /* positions, 0 .. 2^23 */
+    int batch, channels;   /* B, D >= 1, B * D <= 2^24, ceil(T / 256) * B * D <= 2^31 */
     int dtype;             /* of x, gate, y and their gradients */
     int input;             /* FI_SCAN_* */
     int64_t ld_x, ld_gate, ld_y;            /* row pitches, elements; 0 = channels */
@@ -500,8 +502,8 @@ size_t fi_scan_workspace_bytes(const fi_scan_desc *desc, int backward);
  * position) and saved (for fi_scan_backward).  bias [D] fp32 or NULL (zeros);
  * state [B][D] fp32, the state before the first position, or NULL (zeros);
  * lengths [B] int32 (device) or NULL: row b has positions t < lengths[b] (taken
- * into [0, T]); later rows are not read, give y = 0 and leave the state as it
- * is.  final may be state.  T = 1 is the form for one token: one launch. */
+ * into [0, T]); what later rows hold counts for nothing, they give y = 0 and
+ * leave the state as it is.  final may be state.  T = 1 is the form for one token: one launch. */
 fi_status fi_scan_forward(const fi_scan_desc *desc, const void *x, const void *gate, const float *bias,
                           const float *state, const int32_t *lengths, void *y, float *final, void *saved,
                           void *workspace, void *stream);

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <initializer_list>
 
 #include "../../include/fi.h"
 
@@ -44,9 +45,10 @@ struct View {
 // views of different pitch whose extents meet are taken to overlap.
 inline bool views_meet(const View &a, const View &b) {
     if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+    using Wide = unsigned __int128;
     const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
-    const uintptr_t ea = pa + (size_t)(a.rows - 1) * a.pitch + a.width;
-    const uintptr_t eb = pb + (size_t)(b.rows - 1) * b.pitch + b.width;
+    const Wide ea = (Wide)pa + (Wide)(a.rows - 1) * a.pitch + a.width;
+    const Wide eb = (Wide)pb + (Wide)(b.rows - 1) * b.pitch + b.width;
     if (ea <= pb || eb <= pa) return false;
     if (a.pitch != b.pitch) return true;
     const size_t delta = pb >= pa ? (pb - pa) % a.pitch : (a.pitch - (pa - pb) % a.pitch) % a.pitch;
@@ -64,6 +66,13 @@ inline bool outputs_meet(const View *out, int nout, const View *in, int nin) {
             if (views_meet(out[i], in[j])) return true;
     }
     return false;
+}
+
+// Whether every pointer (null ones too) is aligned to `bytes`.
+inline bool aligned(size_t bytes, std::initializer_list<const void *> pointers) {
+    for (const void *p : pointers)
+        if ((uintptr_t)p % bytes) return false;
+    return true;
 }
 
 inline int64_t pitch_or(int64_t ld, int64_t width) { return ld ? ld : width; }

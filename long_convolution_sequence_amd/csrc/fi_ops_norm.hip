@@ -486,6 +486,8 @@ fi_status fi_norm_forward(const fi_norm_desc *desc, const void *o, const void *g
     NormArgs n = {};
     norm_args(desc, n);
     const size_t es = value_bytes(desc->dtype), rs = value_bytes(desc->res_dtype), D = n.D;
+    if (!aligned(es, {o, gate, a}) || !aligned(rs, {res, r}) || !aligned(4, {post_weight, scale, pre_weight, saved}))
+        return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
     const View vr = {r, n.rows, D * rs, n.ldr * rs}, vres = {res, n.rows, D * rs, n.ldres * rs};
     const View out[] = {vr, {a, n.rows, D * es, n.lda * es}, {saved, 1, (size_t)n.rows * 8, (size_t)n.rows * 8}};
     const View in[] = {{o, n.rows, D * es, n.ldo * es}, {gate, n.rows, D * es, n.ldg * es},
@@ -515,6 +517,9 @@ fi_status fi_norm_backward(const fi_norm_desc *desc, const void *o, const void *
             return op_fail(FI_EINVAL, call, "a gradient is asked for whose input is not given");
     }
     const size_t es = value_bytes(desc->dtype), rs = value_bytes(desc->res_dtype), D = n.D;
+    if (!aligned(es, {o, gate, da, d_o, dgate}) || !aligned(rs, {res, dr, dres}) ||
+        !aligned(4, {post_weight, scale, pre_weight, saved, dpost, dscale, dpre}))
+        return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
     const size_t ws = fi_norm_workspace_bytes(desc);
     const View vdr = {dr, n.rows, D * rs, n.lddr * rs}, vdres = {dres, n.rows, D * rs, n.lddres * rs};
     const View out[] = {vdres, {d_o, n.rows, D * es, n.lddo * es}, {dgate, n.rows, D * es, n.lddg * es},

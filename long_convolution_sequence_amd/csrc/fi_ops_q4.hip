@@ -454,6 +454,7 @@ fi_status fi_q4_pack(const fi_q4_desc *desc, const uint8_t *codes, const void *s
     if (const char *why = q4_check(desc)) return op_fail(FI_EINVAL, call, why);
     if (!codes || !scales || !packed || (uintptr_t)packed % 256)
         return op_fail(FI_EINVAL, call, "codes, scales and packed (aligned to 256 bytes) are required");
+    if (!aligned(value_bytes(desc->scale_dtype), {scales})) return op_fail(FI_EINVAL, call, "scales is not aligned to its values");
     if ((zeros != nullptr) != (desc->has_zeros != 0)) return op_fail(FI_EINVAL, call, "zeros do not go with has_zeros");
     Q4Layout l;
     q4_layout(desc, l);
@@ -495,6 +496,8 @@ fi_status fi_q4_quantize(const fi_q4_desc *desc, int w_dtype, const void *w, int
     const size_t nk = (size_t)desc->N * desc->K, sb = (size_t)desc->N * have * value_bytes(desc->scale_dtype);
     const View out[] = {{codes, 1, nk, nk}, {scales, 1, sb, sb}};
     const size_t ws = value_bytes(w_dtype);
+    if (!aligned(ws, {w}) || !aligned(value_bytes(desc->scale_dtype), {scales}))
+        return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
     const View in = {w, desc->N, desc->K * ws, ldw * ws};
     if (outputs_meet(out, 2, &in, 1)) return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
     const hipStream_t st = (hipStream_t)stream;
@@ -520,6 +523,7 @@ fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int
     Q4Layout l;
     q4_layout(desc, l);
     const size_t es = value_bytes(dtype);
+    if (!aligned(es, {x, y})) return op_fail(FI_EINVAL, call, "x or y is not aligned to its values");
     const View out = {y, rows, desc->N * es, a.ldy * es};
     const View in[] = {{x, rows, desc->K * es, a.ldx * es}, {packed, 1, l.total, l.total}};
     if (outputs_meet(&out, 1, in, 2)) return op_fail(FI_EINVAL, call, "y shares memory with another argument");

@@ -752,6 +752,8 @@ fi_status fi_scan_forward(const fi_scan_desc *desc, const void *x, const void *g
         return op_fail(FI_EINVAL, call, "x, gate, y and workspace are required");
     if ((uintptr_t)workspace % 256 || (uintptr_t)saved % 256)
         return op_fail(FI_EINVAL, call, "workspace and saved need an alignment of 256 bytes");
+    if (!aligned(es, {x, gate, y}) || !aligned(4, {bias, state, lengths, final}))
+        return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
     const View out[] = {{y, rows, w, a.ldy * es}, {final, 1, fr, fr}, {saved, 1, pl.part, pl.part},
                         {workspace, 1, ws, ws}};
     const View in[] = {{x, rows, w, a.ldx * es}, {gate, rows, w, a.ldg * es}, {bias, 1, a.D * 4u, a.D * 4u},
@@ -786,6 +788,8 @@ fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *
         return op_fail(FI_EINVAL, call, "x, gate, saved, dy, dx, dgate and workspace are required");
     if ((uintptr_t)workspace % 256 || (uintptr_t)saved % 256)
         return op_fail(FI_EINVAL, call, "workspace and saved need an alignment of 256 bytes");
+    if (!aligned(es, {x, gate, dy, dx, dgate}) || !aligned(4, {bias, state, lengths, dfinal, dbias, dstate}))
+        return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
     const size_t ws = scan_workspace(pl, true);
     const View out[] = {{dx, rows, w, a.lddx * es}, {dgate, rows, w, a.lddg * es}, {dbias, 1, a.D * 4u, a.D * 4u},
                         {dstate, 1, fr, fr}, {workspace, 1, ws, ws}};

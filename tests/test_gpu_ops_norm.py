@@ -125,7 +125,7 @@ def test_column_slices(D, dtype, rt):
 
 def test_in_place_residual_and_gradient():
     say("case norm in place")
-    for D, rt in ((130, F32), (864, BF16), (2000, F32), (9000, F32)):
+    for D, rt in ((130, F32), (864, BF16), (2000, F32), (9000, F32), (7, BF16), (1037, BF16), (2001, F32), (8195, BF16)):
         v = _inputs(21, D, BF16, rt, seed=5)
         c = _cuda(v)
         want = _run(c, True, ops.GATE_SILU)

@@ -255,6 +255,36 @@ def test_q4_arguments_are_checked(lib):
     _refused(lib, mv(q, P, 2, 0, P + STEP, 0, P + STEP + 4, 0, None), "shares memory")
 
 
+def test_misaligned_pointers_are_refused(lib):
+    q = _scan(T=2000)
+    for name in ("x", "gate", "y", "bias", "state", "lengths", "final"):
+        a = dict(zip(["x", "gate", "bias", "state", "lengths", "y", "final", "saved", "workspace"], _ptrs(9)))
+        _refused(lib, lib.fi_scan_forward(ctypes.byref(q), *_scan_args(**{name: a[name] + 2})), "aligned")
+    names = ["x", "gate", "bias", "state", "lengths", "saved", "dy", "dfinal", "dx", "dgate", "dbias", "dstate", "workspace"]
+    a = dict(zip(names, _ptrs(13)))
+    for name in ("x", "dy", "dfinal", "dx", "dgate", "dbias", "dstate"):
+        _refused(lib, lib.fi_scan_backward(ctypes.byref(q), *_back_args(**{name: a[name] + 2})), "aligned")
+    n = _norm(rows=50)
+    names = ["o", "gate", "res", "w1", "k", "w2", "r", "a", "saved"]
+    for name, off in zip(names, (1, 1, 2, 2, 2, 2, 2, 1, 2)):
+        at = dict(zip(names, _ptrs(9)))[name] + off
+        _refused(lib, lib.fi_norm_forward(ctypes.byref(n), *_norm_args(**{name: at})), "aligned")
+    names = ["o", "gate", "res", "w1", "k", "w2", "saved", "dr", "da", "do", "dgate", "dres", "dpost", "dscale", "dpre"]
+    for name in ("dr", "da", "do", "dgate", "dres", "dpost", "dscale", "dpre"):
+        at = dict(zip(names, _ptrs(15)))[name] + 1
+        _refused(lib, lib.fi_norm_backward(ctypes.byref(n), *_norm_back_args(**{name: at})), "aligned")
+    w = _q4()
+    _refused(lib, lib.fi_q4_pack(ctypes.byref(w), P, P + STEP + 1, None, P + 2 * STEP, None), "aligned")
+    _refused(lib, lib.fi_q4_quantize(ctypes.byref(w), 0, P + 2, 0, P + STEP, P + 2 * STEP, None), "aligned")
+    _refused(lib, lib.fi_q4_matvec(ctypes.byref(w), P, 1, 0, P + STEP + 2, 0, P + 2 * STEP, 0, None), "aligned")
+
+
+def test_huge_pitches_do_not_wrap_the_overlap_check(lib):
+    """2^40 rows at 2^40 elements: the extents pass 64 bits, and still overlap."""
+    n = _norm(rows=1 << 40, ld_o=1 << 40, ld_a=(1 << 40) - 64)
+    _refused(lib, lib.fi_norm_forward(ctypes.byref(n), *_norm_args()), "shares memory")
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     x = torch.zeros(4, 2, 8)
     for call in (lambda: ops.gated_scan(x, x), lambda: ops.gated_scan_step(x[0], x[0], x[0]),
