@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kNormMaxD = 16384;
 constexpr int kNormLane = 16;          // values of a row per lane at most
+constexpr int64_t kNormCache = 256 << 20;   // bytes of the last-level cache
 constexpr int kNormCUs = 256;          // compute units that the workgroups are spread over
 
 struct NormArgs {
@@ -92,7 +93,7 @@ struct Team {
 
 // A row's values as they are loaded.  ALL: the tensor is there; else a null one
 // reads as zeros.
-template <bool ALL, typename T, int CH, int NC>
+template <bool ALL, bool STREAM, typename T, int CH, int NC>
 struct Raw {
     Chunk<T, CH> v[NC];
 
@@ -105,7 +106,7 @@ struct Raw {
         }
         const T *from = static_cast<const T *>(p) + row * ld;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) v[j] = load_chunk<T, CH>(from, t.at[j]);
+        for (int j = 0; j < NC; ++j) v[j] = load_chunk<T, CH, STREAM>(from, t.at[j]);
     }
     __device__ __forceinline__ void get(float (&f)[NC * CH]) const {
 #pragma unroll
@@ -179,15 +180,16 @@ __device__ __forceinline__ float rnorm(float squares, const NormArgs &p) {
 
 // Forward: HBM-bound, every tensor once.  A team of several waves reads its next
 // row before it works on this one: a barrier a row holds all its waves, and few
-// such teams fit a CU.  ALL: o, gate and res are there.
-template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, int THREADS>
+// such teams fit a CU.  ALL: o, gate and res are there.  STREAM: the inputs are
+// larger than the last-level cache (see launch).
+template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, bool STREAM, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
     constexpr int N = CH * NC;
     constexpr bool AHEAD = MULTI && THREADS <= 512;
     __shared__ float slots[2][16];
     Team<CH, NC, MULTI> t(p.D);
-    Raw<ALL, V, CH, NC> raw_o, raw_g;
-    Raw<ALL, W, CH, NC> raw_r;
+    Raw<ALL, STREAM, V, CH, NC> raw_o, raw_g;
+    Raw<ALL, STREAM, W, CH, NC> raw_r;
     const auto fetch = [&](int64_t row) {
         raw_o.load(p.o, p.ldo, row, t);
         raw_g.load(p.gate, p.ldg, row, t);
@@ -231,15 +233,15 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
 // the column sums of a team's rows in registers, its workgroup's joined in LDS
 // (team after team, so the order is fixed) and written once.  Elements that a
 // lane does not own have weights of zero, so both means pass them by.
-template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, int THREADS>
+template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, bool STREAM, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) k_norm_back(NormArgs p) {
     constexpr int N = CH * NC;
     constexpr bool AHEAD = MULTI && THREADS <= 512 && sizeof(W) == 2;   // with fp32 rows it would spill
     __shared__ float slots[2][16];
     __shared__ float join[MULTI ? 1 : 2 * 64 * N];
     Team<CH, NC, MULTI> t(p.D);
-    Raw<ALL, V, CH, NC> raw_o, raw_g, raw_da;
-    Raw<ALL, W, CH, NC> raw_r, raw_dr;
+    Raw<ALL, STREAM, V, CH, NC> raw_o, raw_g, raw_da;
+    Raw<ALL, STREAM, W, CH, NC> raw_r, raw_dr;
     const auto fetch = [&](int64_t row) {
         raw_o.load(p.o, p.ldo, row, t);
         raw_g.load(p.gate, p.ldg, row, t);
@@ -403,26 +405,38 @@ void norm_args(const fi_norm_desc *q, NormArgs &a) {
     a.lddres = pitch_or(q->ld_dres, a.D);
 }
 
-template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS, bool TAIL, bool ALL>
+template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS, bool TAIL, bool ALL, bool STREAM>
 void launch(const NormArgs &a, bool backward, unsigned groups, unsigned threads, hipStream_t st) {
     if (backward)
-        hipLaunchKernelGGL((k_norm_back<V, W, CH, NC, MULTI, TAIL, ALL, THREADS>), dim3(groups), dim3(threads), 0, st,
-                           a);
+        hipLaunchKernelGGL((k_norm_back<V, W, CH, NC, MULTI, TAIL, ALL, STREAM, THREADS>), dim3(groups), dim3(threads), 0,
+                           st, a);
     else
-        hipLaunchKernelGGL((k_norm<V, W, CH, NC, MULTI, TAIL, ALL, THREADS>), dim3(groups), dim3(threads), 0, st, a);
+        hipLaunchKernelGGL((k_norm<V, W, CH, NC, MULTI, TAIL, ALL, STREAM, THREADS>), dim3(groups), dim3(threads), 0, st,
+                           a);
 }
 
 // With every tensor of a row given, without (and always at the smallest and
-// widest rows) the kernels that check for each.
+// widest rows) the kernels that check for each.  Inputs of more than the
+// last-level cache are read as streams: 131072 x 864 rows 302 -> 293 us, a
+// training pass 695 -> 666; below that a producer's output may still be cached,
+// and reading it so costs (a chain of scan, norm, scan over 4096 x 864 38.4
+// against 35.6 us).
 template <typename V, typename W, int CH, int NC, bool MULTI, int THREADS>
 void launch(const NormArgs &a, bool backward, unsigned groups, unsigned threads, hipStream_t st) {
     const bool all = a.o && a.gate && a.res && (!backward || (a.dr && a.da));
+    const int64_t values = a.rows * a.D;
+    const bool stream = values * (int64_t)((backward ? 3 : 2) * sizeof(V) + (backward ? 2 : 1) * sizeof(W)) > kNormCache;
     if constexpr (CH > 1 && THREADS <= 512) {
-        if (all && a.D % CH == 0)
-            return launch<V, W, CH, NC, MULTI, THREADS, false, true>(a, backward, groups, threads, st);
-        if (all) return launch<V, W, CH, NC, MULTI, THREADS, true, true>(a, backward, groups, threads, st);
+        if (all && a.D % CH == 0) {
+            if (stream) return launch<V, W, CH, NC, MULTI, THREADS, false, true, true>(a, backward, groups, threads, st);
+            return launch<V, W, CH, NC, MULTI, THREADS, false, true, false>(a, backward, groups, threads, st);
+        }
+        if (all) {
+            if (stream) return launch<V, W, CH, NC, MULTI, THREADS, true, true, true>(a, backward, groups, threads, st);
+            return launch<V, W, CH, NC, MULTI, THREADS, true, true, false>(a, backward, groups, threads, st);
+        }
     }
-    launch<V, W, CH, NC, MULTI, THREADS, true, false>(a, backward, groups, threads, st);
+    launch<V, W, CH, NC, MULTI, THREADS, true, false, false>(a, backward, groups, threads, st);
 }
 
 template <typename V, typename W>
