@@ -484,7 +484,7 @@ enum { FI_SCAN_PLAIN = 0, FI_SCAN_CONVEX = 1, FI_SCAN_ENERGY = 2 };
 
 typedef struct fi_scan_desc {
     int64_t T;             /* positions, 0 .. 2^23 */
-    int batch, channels;   /* B, D >= 1, B * D <= 2^24, ceil(T / 256) * B * D <= 2^31 */
+    int batch, channels;   /* B, D >= 1, B * D <= 2^24, ceil(T / 256) * B * D <= 2^28 (D < 4: 2^26) */
     int dtype;             /* of x, gate, y and their gradients */
     int input;             /* FI_SCAN_* */
     int64_t ld_x, ld_gate, ld_y;            /* row pitches, elements; 0 = channels */
@@ -503,7 +503,10 @@ size_t fi_scan_workspace_bytes(const fi_scan_desc *desc, int backward);
  * state [B][D] fp32, the state before the first position, or NULL (zeros);
  * lengths [B] int32 (device) or NULL: row b has positions t < lengths[b] (taken
  * into [0, T]); what later rows hold counts for nothing, they give y = 0 and
- * leave the state as it is.  final may be state.  T = 1 is the form for one token: one launch. */
+ * leave the state as it is.  final may be state.  T = 1 is the form for one token:
+ * one launch.  Of the positions that count, an infinity or NaN in x, gate or the
+ * state makes its channel's later values non-finite (from an infinity, NaN may
+ * come one position on). */
 fi_status fi_scan_forward(const fi_scan_desc *desc, const void *x, const void *gate, const float *bias,
                           const float *state, const int32_t *lengths, void *y, float *final, void *saved,
                           void *workspace, void *stream);
@@ -590,7 +593,8 @@ fi_status fi_q4_pack(const fi_q4_desc *desc, const uint8_t *codes, const void *s
 /* Codes and scales of a weight matrix w [N][K] of w_dtype (row pitch ld_w
  * elements, 0 = K), zeros all 8: scale = max|w| of the group / 7 rounded to
  * scale_dtype, code = 8 + w / scale rounded to nearest even, in 1..15.  A
- * group of zeros, or one whose scale rounds to zero, gets scale 0 and codes 8. */
+ * group of zeros, or one whose scale rounds to zero, gets scale 0 and codes 8.
+ * w is finite, and max|w| / 7 in the range of scale_dtype. */
 fi_status fi_q4_quantize(const fi_q4_desc *desc, int w_dtype, const void *w, int64_t ld_w, uint8_t *codes,
                          void *scales, void *stream);
 

@@ -66,28 +66,30 @@ const char *q4_check(const fi_q4_desc *q) {
     return nullptr;
 }
 
-// One word of codes per thread.
+// The laying out and the quantizing run once a weight; their threads go through
+// the whole of it in strides (a launch has less than 2^32 threads).
+// One word of codes per thread and turn.
 __global__ void __launch_bounds__(256) k_q4_codes(int N, int K, int kt, const uint8_t *codes, unsigned *out,
                                                   int64_t words) {
-    const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (i >= words) return;
-    const int s = i & 3, lane = (i >> 2) & 63;
-    const int64_t tile = i >> 8;
-    const int n = (int)(tile / kt) * 16 + (lane & 15);
-    const int k0 = (int)(tile % kt) * 128 + s * 32 + (lane >> 4) * 8;
-    unsigned w = 0;
-    for (int j = 0; j < 8; ++j) {
-        const unsigned q = n < N && k0 + j < K ? codes[(size_t)n * K + k0 + j] & 15u : 0u;
-        w |= q << ((j >> 1) * 4 + (j & 1) * 16);
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < words; i += gridDim.x * (int64_t)256) {
+        const int s = i & 3, lane = (i >> 2) & 63;
+        const int64_t tile = i >> 8;
+        const int n = (int)(tile / kt) * 16 + (lane & 15);
+        const int k0 = (int)(tile % kt) * 128 + s * 32 + (lane >> 4) * 8;
+        unsigned w = 0;
+        for (int j = 0; j < 8; ++j) {
+            const unsigned q = n < N && k0 + j < K ? codes[(size_t)n * K + k0 + j] & 15u : 0u;
+            w |= q << ((j >> 1) * 4 + (j & 1) * 16);
+        }
+        out[i] = w;
     }
-    out[i] = w;
 }
 
 // Where value i of the scales' layout comes from: its output and its group.
 struct Q4Where {
     int n, g;
     __device__ __forceinline__ Q4Where(int64_t i, int kt, int per) {
-        const int row = (int)(i & 3), in = (int)(i >> 2) % per, kq = (int)((i >> 2) / per & 3);
+        const int row = (int)(i & 3), in = (int)((i >> 2) % per), kq = (int)((i >> 2) / per & 3);
         const int64_t step = i / (16 * per);
         n = (int)(step / kt) * 16 + kq * 4 + row;
         g = (int)(step % kt) * per + in;
@@ -97,42 +99,46 @@ struct Q4Where {
 template <typename V>
 __global__ void __launch_bounds__(256) k_q4_scales(int N, int have, int kt, int per, const V *scales, V *out,
                                                    int64_t n) {
-    const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (i >= n) return;
-    const Q4Where w(i, kt, per);
-    out[i] = w.n < N && w.g < have ? scales[(size_t)w.n * have + w.g] : (V)0.f;
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += gridDim.x * (int64_t)256) {
+        const Q4Where w(i, kt, per);
+        out[i] = w.n < N && w.g < have ? scales[(size_t)w.n * have + w.g] : (V)0.f;
+    }
 }
 
 __global__ void __launch_bounds__(256) k_q4_zeros(int N, int have, int kt, int per, const uint8_t *zeros,
                                                   uint16_t *out, int64_t n) {
-    const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (i >= n) return;
-    unsigned v = 0;
-    for (int j = 0; j < 4; ++j) {
-        const Q4Where w(i * 4 + j, kt, per);
-        if (w.n < N && w.g < have) v |= (zeros[(size_t)w.n * have + w.g] & 15u) << (4 * j);
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += gridDim.x * (int64_t)256) {
+        unsigned v = 0;
+        for (int j = 0; j < 4; ++j) {
+            const Q4Where w(i * 4 + j, kt, per);
+            if (w.n < N && w.g < have) v |= (zeros[(size_t)w.n * have + w.g] & 15u) << (4 * j);
+        }
+        out[i] = (uint16_t)v;
     }
-    out[i] = (uint16_t)v;
 }
 
-// One group of one row per wave.
+// One group of one row per wave and turn.
 template <typename W, typename S>
-__global__ void __launch_bounds__(64) k_q4_quantize(int K, int group, int have, const W *w, int64_t ldw,
-                                                    uint8_t *codes, S *scales) {
-    const int n = blockIdx.x / have, g = blockIdx.x - n * have, lane = threadIdx.x;
-    const int k0 = g * group, k1 = k0 + group < K ? k0 + group : K;
-    float m = 0.f;
-    for (int k = k0 + lane; k < k1; k += 64) m = fmaxf(m, fabsf((float)w[n * ldw + k]));
+__global__ void __launch_bounds__(256) k_q4_quantize(int N, int K, int group, int have, const W *w, int64_t ldw,
+                                                     uint8_t *codes, S *scales) {
+    const int lane = threadIdx.x & 63;
+    const int64_t groups = (int64_t)N * have;
+    for (int64_t i = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6); i < groups; i += gridDim.x * (int64_t)4) {
+        const int n = (int)(i / have), g = (int)(i - (int64_t)n * have);
+        const int k0 = g * group, k1 = k0 + group < K ? k0 + group : K;
+        float m = 0.f;
+        for (int k = k0 + lane; k < k1; k += 64) m = fmaxf(m, fabsf((float)w[n * ldw + k]));
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    const S s = (S)(m / 7.f);
-    const float f = (float)s;
-    for (int k = k0 + lane; k < k1; k += 64) {
-        float q = 0.f;
-        if (f > 0.f) q = fminf(fmaxf(rintf((float)w[n * ldw + k] / f), -7.f), 7.f);
-        codes[(size_t)n * K + k] = (uint8_t)(8 + (int)q);
+        for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+        const S s = (S)(m / 7.f);
+        const float f = (float)s;
+        for (int k = k0 + lane; k < k1; k += 64) {
+            float q = 0.f;
+            if (f > 0.f) q = fminf(fmaxf(rintf((float)w[n * ldw + k] / f), -7.f), 7.f);
+            codes[(size_t)n * K + k] = (uint8_t)(8 + (int)q);
+        }
+        if (lane == 0) scales[i] = s;
     }
-    if (lane == 0) scales[(size_t)n * have + g] = s;
 }
 
 struct Q4Args {
@@ -418,22 +424,23 @@ void q4_launch(const Q4Args &a, int group, int sdt, hipStream_t st) {
     else q4_launch<V, f16_t>(a, group, st);
 }
 
+// Workgroups of four waves for n pieces of work, `per` in one: eight a CU at most.
+unsigned blocks(int64_t n, int per) { return (unsigned)std::min<int64_t>((n + per - 1) / per, 2048); }
+
 template <typename W>
 void quantize(const fi_q4_desc *q, int have, const void *w, int64_t ldw, uint8_t *codes, void *scales,
               hipStream_t st) {
-    const dim3 grid((unsigned)((size_t)q->N * have)), wg(64);
+    const dim3 grid(blocks((int64_t)q->N * have, 4)), wg(256);
     if (q->scale_dtype == FI_F32)
-        hipLaunchKernelGGL((k_q4_quantize<W, float>), grid, wg, 0, st, q->K, q->group, have, (const W *)w, ldw, codes,
-                           (float *)scales);
+        hipLaunchKernelGGL((k_q4_quantize<W, float>), grid, wg, 0, st, q->N, q->K, q->group, have, (const W *)w,
+                           ldw, codes, (float *)scales);
     else if (q->scale_dtype == FI_BF16)
-        hipLaunchKernelGGL((k_q4_quantize<W, bf16_t>), grid, wg, 0, st, q->K, q->group, have, (const W *)w, ldw,
-                           codes, (bf16_t *)scales);
+        hipLaunchKernelGGL((k_q4_quantize<W, bf16_t>), grid, wg, 0, st, q->N, q->K, q->group, have, (const W *)w,
+                           ldw, codes, (bf16_t *)scales);
     else
-        hipLaunchKernelGGL((k_q4_quantize<W, f16_t>), grid, wg, 0, st, q->K, q->group, have, (const W *)w, ldw, codes,
-                           (f16_t *)scales);
+        hipLaunchKernelGGL((k_q4_quantize<W, f16_t>), grid, wg, 0, st, q->N, q->K, q->group, have, (const W *)w,
+                           ldw, codes, (f16_t *)scales);
 }
-
-unsigned blocks(int64_t n) { return (unsigned)((n + 255) / 256); }
 
 }  // namespace
 
@@ -467,16 +474,16 @@ fi_status fi_q4_pack(const fi_q4_desc *desc, const uint8_t *codes, const void *s
     const hipStream_t st = (hipStream_t)stream;
     char *to = (char *)packed;
     const int64_t words = (int64_t)l.tiles * l.kt * 256, sc = (int64_t)l.tiles * l.groups * 16;
-    hipLaunchKernelGGL(k_q4_codes, dim3(blocks(words)), dim3(256), 0, st, desc->N, desc->K, l.kt, codes,
+    hipLaunchKernelGGL(k_q4_codes, dim3(blocks(words, 256)), dim3(256), 0, st, desc->N, desc->K, l.kt, codes,
                        (unsigned *)(to + l.codes), words);
     if (desc->scale_dtype == FI_F32)
-        hipLaunchKernelGGL((k_q4_scales<float>), dim3(blocks(sc)), dim3(256), 0, st, desc->N, have, l.kt, 128 / desc->group,
+        hipLaunchKernelGGL((k_q4_scales<float>), dim3(blocks(sc, 256)), dim3(256), 0, st, desc->N, have, l.kt, 128 / desc->group,
                            (const float *)scales, (float *)(to + l.scales), sc);
     else    // both 16-bit types are copied as they are
-        hipLaunchKernelGGL((k_q4_scales<bf16_t>), dim3(blocks(sc)), dim3(256), 0, st, desc->N, have, l.kt, 128 / desc->group,
+        hipLaunchKernelGGL((k_q4_scales<bf16_t>), dim3(blocks(sc, 256)), dim3(256), 0, st, desc->N, have, l.kt, 128 / desc->group,
                            (const bf16_t *)scales, (bf16_t *)(to + l.scales), sc);
     if (zeros)
-        hipLaunchKernelGGL(k_q4_zeros, dim3(blocks(sc / 4)), dim3(256), 0, st, desc->N, have, l.kt,
+        hipLaunchKernelGGL(k_q4_zeros, dim3(blocks(sc / 4, 256)), dim3(256), 0, st, desc->N, have, l.kt,
                            128 / desc->group, zeros,
                            (uint16_t *)(to + l.zeros), sc / 4);
     return op_launched(call);
@@ -492,7 +499,6 @@ fi_status fi_q4_quantize(const fi_q4_desc *desc, int w_dtype, const void *w, int
     const int64_t ldw = ld_w ? ld_w : desc->K;
     if (ldw < desc->K || ldw > (int64_t(1) << 40)) return op_fail(FI_EINVAL, call, "the row pitch is less than K");
     const int have = (desc->K + desc->group - 1) / desc->group;
-    if ((size_t)desc->N * have > 0x7fffffffu) return op_fail(FI_EINVAL, call, "too many groups");
     const size_t nk = (size_t)desc->N * desc->K, sb = (size_t)desc->N * have * value_bytes(desc->scale_dtype);
     const View out[] = {{codes, 1, nk, nk}, {scales, 1, sb, sb}};
     const size_t ws = value_bytes(w_dtype);

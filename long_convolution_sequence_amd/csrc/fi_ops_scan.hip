@@ -637,7 +637,11 @@ const char *scan_plan(const fi_scan_desc *q, Plan &p) {
     p.tiles = (q->T + kTile - 1) / kTile;
     p.part = up256((size_t)p.tiles * p.R * sizeof(float));
     p.link = p.tiles > 1 ? up256((size_t)p.tiles * p.R * sizeof(unsigned long long)) + 256 : 0;
-    if (p.tiles * (int64_t)p.R > (int64_t(1) << 31)) return "batch * channels * T is too large";
+    // a launch has less than 2^32 threads, so less than 2^23 workgroups of 512; a
+    // workgroup has 64 columns (no less than 40: rows of 5 are two groups of 4), or
+    // 16 where rows have less than 4
+    if (p.tiles * (int64_t)p.R > (int64_t(1) << (q->channels < 4 ? 26 : 28)))
+        return "batch * channels * T is too large";
     return nullptr;
 }
 

@@ -41,6 +41,13 @@ def _bad(what):
     raise FiError(FI_EINVAL, what)
 
 
+def _pack(desc, *values):
+    try:
+        return desc.pack(*values)
+    except (struct.error, TypeError, OverflowError) as e:      # a size past its field, an eps that is no number
+        raise FiError(FI_EINVAL, str(e)) from None
+
+
 def _check(status):
     if status != FI_OK:
         msg = load_library().fi_op_last_error()
@@ -140,7 +147,7 @@ def _bytes(n, like):
 def _scan_sizes(T, B, D, dtype, input):
     """Bytes of the forward pass's workspace, the backward pass's, and the saved states."""
     lib = load_library()
-    d = _SCAN_DESC.pack(T, B, D, dtype, input, 0, 0, 0, 0, 0, 0)
+    d = _pack(_SCAN_DESC, T, B, D, dtype, input, 0, 0, 0, 0, 0, 0)
     return lib.fi_scan_workspace_bytes(d, 0), lib.fi_scan_workspace_bytes(d, 1), lib.fi_scan_saved_bytes(d)
 
 
@@ -188,7 +195,7 @@ def gated_scan(x, gate, bias=None, state=None, lengths=None, *, input=SCAN_CONVE
     work, _, kept = _scan_sizes(*head)
     work = _bytes(work, x) if work > 256 else None
     saved = _bytes(kept, x) if save else None
-    _call(device, load_library().fi_scan_forward, _SCAN_DESC.pack(*head, *ld, ldy, 0, 0, 0), *args, py, pf,
+    _call(device, load_library().fi_scan_forward, _pack(_SCAN_DESC, *head, *ld, ldy, 0, 0, 0), *args, py, pf,
           saved.data_ptr() if save else None, work.data_ptr() if work is not None else None)
     return (y, final, saved) if save else (y, final)
 
@@ -226,7 +233,7 @@ def gated_scan_backward(dy, x, gate, saved, bias=None, state=None, lengths=None,
     _, work, kept = _scan_sizes(*head)
     psv = _dense(saved, (kept,), torch.uint8, device, "saved")
     work = _bytes(work, x)
-    _call(device, load_library().fi_scan_backward, _SCAN_DESC.pack(*head, *ld, 0, lddy, lddx, lddg), *args, psv, pdy,
+    _call(device, load_library().fi_scan_backward, _pack(_SCAN_DESC, *head, *ld, 0, lddy, lddx, lddg), *args, psv, pdy,
           pdf, pdx, pdg, dbias.data_ptr() if dbias is not None else None,
           dstate.data_ptr() if dstate is not None else None, work.data_ptr())
     return dx, dgate, dbias, dstate
@@ -290,14 +297,14 @@ def block_norm(o, res=None, gate=None, *, post_weight=None, scale=None, pre_weig
     else:
         pa, lda = _rows(a, shape, dtype, device, "a")
     saved = torch.empty((2, rows), dtype=torch.float32, device=first.device) if save else None
-    _call(device, load_library().fi_norm_forward, _NORM_DESC.pack(*head, ldr, lda, 0, 0, 0, 0, 0), *args, pr, pa,
+    _call(device, load_library().fi_norm_forward, _pack(_NORM_DESC, *head, ldr, lda, 0, 0, 0, 0, 0), *args, pr, pa,
           saved.data_ptr() if save else None)
     return (r, a, saved) if save else (r, a)
 
 
 @functools.lru_cache(maxsize=256)
 def _norm_workspace(rows, D, dtype, res_dtype):
-    return load_library().fi_norm_workspace_bytes(_NORM_DESC.pack(rows, D, dtype, res_dtype, 0, 0, 0.0, *([0] * 10)))
+    return load_library().fi_norm_workspace_bytes(_pack(_NORM_DESC, rows, D, dtype, res_dtype, 0, 0, 0.0, *([0] * 10)))
 
 
 def block_norm_backward(dr, da, o, res, gate, saved, *, post_weight=None, scale=None, pre_weight=None,
@@ -327,7 +334,7 @@ def block_norm_backward(dr, da, o, res, gate, saved, *, post_weight=None, scale=
         w[2].zero_()
         ptr[2] = None
     work = _bytes(_norm_workspace(rows, D, head[2], head[3]), first)
-    _call(device, load_library().fi_norm_backward, _NORM_DESC.pack(*head, 0, 0, lddr, ldda, lddo, lddg, lddres), *args,
+    _call(device, load_library().fi_norm_backward, _pack(_NORM_DESC, *head, 0, 0, lddr, ldda, lddo, lddg, lddres), *args,
           psv, pdr, pda, pdo, pdg, pdres, *ptr, work.data_ptr())
     return NormGradients(do, dres, dgate, *w)
 
@@ -350,7 +357,7 @@ class Q4Weight:
             _bad(f"scales: expected a torch tensor, got {type(scales).__name__}")
         self.N, self.K = codes.shape
         self.group, self.device, self._index = group, codes.device, device
-        self._desc = _Q4_DESC.pack(self.N, self.K, group, _type(scales, "scales"), int(zeros is not None))
+        self._desc = _pack(_Q4_DESC, self.N, self.K, group, _type(scales, "scales"), int(zeros is not None))
         lib = load_library()
         n = lib.fi_q4_packed_bytes(self._desc)
         if n == 0:
@@ -378,7 +385,7 @@ class Q4Weight:
         pw, ld = _rows(w, w.shape, w.dtype, device, "w")
         codes = torch.empty((N, K), dtype=torch.uint8, device=w.device)
         scales = torch.empty((N, -(-K // group)), dtype=scale_dtype, device=w.device)
-        _call(device, load_library().fi_q4_quantize, _Q4_DESC.pack(N, K, group, _TYPES[scale_dtype], 0), wt, pw, ld,
+        _call(device, load_library().fi_q4_quantize, _pack(_Q4_DESC, N, K, group, _TYPES[scale_dtype], 0), wt, pw, ld,
               codes.data_ptr(), scales.data_ptr())
         out = cls(codes, scales, group=group)
         out.codes, out.scales = codes, scales

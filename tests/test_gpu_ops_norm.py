@@ -204,6 +204,46 @@ def test_many_rows():
     _check(_run(_cuda(v), True, ops.GATE_SILU), v, True, ops.GATE_SILU, F32, F32)
 
 
+@pytest.mark.parametrize("D,dtype,rt", [(864, BF16, F32), (1001, F16, F16), (256, F32, F32), (5000, BF16, BF16),
+                                        (5001, F16, F32)])
+def test_more_than_the_caches_hold(D, dtype, rt):
+    """Inputs past the size from which they are read as streams: the rows as in slices of it (each of
+    which is below that size), the column sums against 64-bit ones of the rows' terms."""
+    N = (1 << 28) // (D * (4 if dtype is F32 else 2) * 2) + 77
+    say(f"case norm streamed N={N} D={D} {dtype}/{rt}")
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")        # noqa: E731
+    c = {"o": r(N, D).to(dtype), "gate": r(N, D).to(dtype), "res": r(N, D).to(rt), "w1": 1 + r(D) / 8,
+         "k": 0.5 + r(D) / 8, "w2": 1 + r(D) / 8, "dr": r(N, D).to(rt), "da": r(N, D).to(dtype)}
+    got = _run(c, True, ops.GATE_SILU)
+    sums = {k: torch.zeros(D, dtype=torch.float64, device="cuda") for k in ("dpost", "dscale", "dpre")}
+    size = {k: torch.zeros(D, dtype=torch.float64, device="cuda") for k in sums}
+    step = -(-N // 8)
+    for i in range(0, N, step):
+        part = {k: t[i:i + step] if t.dim() == 2 else t for k, t in c.items()}
+        one = _run(part, True, ops.GATE_SILU)
+        for k in ("r", "a", "do", "dres", "dgate"):
+            assert torch.equal(got[k][i:i + step], one[k]), f"{k} rows {i}.."
+        o, g, res, dr, da = (part[k].double() for k in ("o", "gate", "res", "dr", "da"))
+        u = o * (o.pow(2).mean(-1, keepdim=True) + EPS).rsqrt()
+        act = g * torch.sigmoid(g)
+        R = res + c["k"].double() * c["w1"].double() * u * act
+        n = (R.pow(2).mean(-1, keepdim=True) + EPS).rsqrt()
+        R *= n
+        da_w = da * c["w2"].double()
+        dR = dr + n * (da_w - R * (da_w * R).mean(-1, keepdim=True))
+        terms = {"dpre": da * R, "dscale": dR * act * u * c["w1"].double(), "dpost": dR * act * u * c["k"].double()}
+        # a term's error: at most D / 4 roundings in a mean's chain, 60 elsewhere, relative to
+        # the parts that it is made of
+        near = (da.abs() + (dr.abs() + n * (da_w.abs() + R.abs() * (da_w * R).abs().mean(-1, keepdim=True))) *
+                (u.abs() * (g.abs() + 1)) * 2)
+        for k, t in terms.items():
+            sums[k] += t.sum(0)
+            size[k] += (t.abs() * N + near * (1 + R.abs()) * (D / 4 + 60)).sum(0) * ref.U
+    for k in sums:
+        assert ((got[k].double() - sums[k]).abs() <= size[k]).all(), k
+
+
 def test_binding_refuses_mismatches():
     say("case norm refusals")
     o = torch.zeros(4, 8, device="cuda")
@@ -214,6 +254,7 @@ def test_binding_refuses_mismatches():
                  lambda: ops.block_norm(o, pre_weight=w[:7]), lambda: ops.block_norm(o, pre_weight=w.half()),
                  lambda: ops.block_norm(o, post_weight=w), lambda: ops.block_norm(None, o, o),
                  lambda: ops.block_norm(o, act=9), lambda: ops.block_norm(o, eps=-1.0), lambda: ops.block_norm(o, a=o),
+                 lambda: ops.block_norm(o, eps="1"), lambda: ops.block_norm(o, eps=1e300),
                  lambda: ops.block_norm(torch.zeros(2, 16385, device="cuda")),
                  lambda: ops.block_norm(o[:, ::2]), lambda: ops.block_norm_backward(o, o, o, None, None, None),
                  lambda: ops.block_norm_backward(o, o, o, None, None, saved[:, :3]),

@@ -73,6 +73,30 @@ def test_full_precision_of_the_inputs():
     assert float((y - x).abs().max()) < 2.0 ** -14                    # bf16 alone would be off by 2^-8
 
 
+def test_tiny_inputs_are_not_dropped():
+    """fp16 inputs below the normal numbers, whole scales: exact.  In units of 2^-24 no sum passes
+    7 groups x 32 x 200 x 15 x 8 < 2^23, and within a group 32 x 200 x 31 < 2^18."""
+    say("case q4 tiny inputs")
+    v = _inputs(40, 200, 3, 32, F16, F32, True, seed=6)
+    gen = torch.Generator().manual_seed(11)
+    v["x"] = (torch.randint(-200, 201, (3, 200), generator=gen).double() * 2.0 ** -24).to(F16)
+    v["scales"] = (2.0 ** torch.randint(0, 4, v["scales"].shape, generator=gen)).float()
+    y = ops.q4_matvec(_weight(v, 32), v["x"].cuda())
+    want, _ = ref.q4(v["x"], v["codes"], v["scales"], v["zeros"], 32)
+    assert torch.equal(y.cpu(), want.to(F16))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_outputs_and_a_large_weight(dtype):
+    """More weights than the layout's kernels take in one turn, and row tiles enough for four a wave."""
+    say(f"case q4 large {dtype}")
+    N, K, B = 16900, 1100, 3
+    v = _inputs(N, K, B, 32, dtype, F32, True, seed=7)
+    y = ops.q4_matvec(_weight(v, 32), v["x"].cuda())
+    want, tol = ref.q4(v["x"], v["codes"], v["scales"], v["zeros"], 32)
+    assert ref.worst(y, want, ref.stored(want, tol, dtype)) <= 1.0
+
+
 def test_bad_rows_stay_alone():
     say("case q4 bad rows")
     v = _inputs(50, 260, 6, 32, F32, BF16, True, seed=2)
@@ -106,7 +130,7 @@ def test_column_slices(dtype):
 
 @pytest.mark.parametrize("wt", [F32, BF16, F16])
 @pytest.mark.parametrize("st", [F32, BF16, F16])
-@pytest.mark.parametrize("N,K,group", [(3, 40, 32), (20, 300, 64), (7, 256, 128)])
+@pytest.mark.parametrize("N,K,group", [(3, 40, 32), (20, 300, 64), (7, 256, 128), (900, 1300, 32)])
 def test_quantize(wt, st, N, K, group):
     """Scales are max|w| / 7 rounded to their type; codes are the nearest, at most half a scale off
     (more only where the rounded scale cannot reach the largest value)."""

@@ -72,7 +72,9 @@ def _refused(lib, status, why):
     (dict(T=-1), "T >= 0"), (dict(B=0), "batch >= 1"), (dict(D=0), "channels >= 1"), (dict(dtype=3), "dtype"),
     (dict(dtype=-1), "dtype"), (dict(input=3), "input"), (dict(input=-1), "input"), (dict(ld_x=4), "pitch"),
     (dict(ld_gate=-5), "pitch"), (dict(ld_y=4), "pitch"), (dict(ld_dy=1), "pitch"), (dict(ld_dx=1), "pitch"),
-    (dict(ld_dgate=1), "pitch"), (dict(B=1 << 13, D=1 << 12), "2^24"), (dict(T=(1 << 23) + 1), "2^23")])
+    (dict(ld_dgate=1), "pitch"), (dict(B=1 << 13, D=1 << 12), "2^24"), (dict(T=(1 << 23) + 1), "2^23"),
+    (dict(T=1 << 23, B=1, D=8193), "too large"), (dict(T=1 << 23, B=2049, D=1), "too large"),
+    (dict(T=1 << 23, B=683, D=3), "too large")])
 def test_scan_descriptors_are_checked(lib, kw, why):
     q = _scan(**kw)
     assert lib.fi_scan_saved_bytes(ctypes.byref(q)) == 0
@@ -295,6 +297,23 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         with pytest.raises(fi.FiError) as e:
             call()
         assert e.value.status == fi.FI_EINVAL
+
+
+def test_binding_refuses_values_past_a_descriptors_fields():
+    for values in ((1 << 70, 1, 1, 0, 0), (1, 1 << 40, 1, 0, 0), (1, 1, 1, 0, 0.5), (1, 1, None, 0, 0)):
+        with pytest.raises(fi.FiError) as e:
+            ops._scan_sizes(*values)
+        assert e.value.status == fi.FI_EINVAL
+
+
+def test_largest_scans_fit_a_launch(lib):
+    """The largest sizes that are taken: less than 2^23 workgroups, so less than 2^32 threads."""
+    for T, B, D in ((1 << 23, 1, 8192), (1 << 23, 1638, 5), (1 << 23, 2048, 1), (1 << 23, 682, 3), (257, 1 << 24, 1),
+                    (1 << 20, 1 << 14, 1)):
+        assert lib.fi_scan_workspace_bytes(ctypes.byref(_scan(T=T, B=B, D=D)), 0) > 0
+        c = 4 if D >= 4 else 1
+        groups = (B * -(-D // c) + 15) // 16
+        assert -(-T // 256) * groups < 1 << 23
 
 
 def test_row_pitches():
