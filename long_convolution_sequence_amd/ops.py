@@ -151,14 +151,14 @@ def _scan_sizes(T, B, D, dtype, input):
     return lib.fi_scan_workspace_bytes(d, 0), lib.fi_scan_workspace_bytes(d, 1), lib.fi_scan_saved_bytes(d)
 
 
-def _scan_inputs(x, gate, bias, state, lengths, input):
+def _scan_inputs(x, gate, bias, state, lengths, input, positions=True):
     device = _device(x, "x")
     shape = x.shape
-    if len(shape) != 3 or shape[1] < 1 or shape[2] < 1:
-        _bad(f"x: shape {tuple(shape)}, expected [T][B][D]")
+    T, B, D = shape if positions and len(shape) == 3 else (1, *shape) if not positions and len(shape) == 2 else (0, 0, 0)
+    if B < 1 or D < 1:
+        _bad(f"x: shape {tuple(shape)}, expected {'[T]' if positions else ''}[B][D]")
     if input not in (SCAN_PLAIN, SCAN_CONVEX, SCAN_ENERGY):
         _bad(f"input: {input!r}, expected SCAN_PLAIN, SCAN_CONVEX or SCAN_ENERGY")
-    T, B, D = shape
     dtype = x.dtype
     head = (T, B, D, _type(x, "x"), input)
     px, ldx = _rows(x, shape, dtype, device, "x")
@@ -203,14 +203,16 @@ def gated_scan(x, gate, bias=None, state=None, lengths=None, *, input=SCAN_CONVE
 def gated_scan_step(x, gate, state, bias=None, lengths=None, *, input=SCAN_CONVEX, y=None):
     """One position: x, gate [B][D]; state [B][D] fp32 is updated in place.  lengths [B] int32 or None:
     a row with 0 is an empty slot (y = 0, its state stays).  Returns y."""
-    _device(x, "x")
-    if x.dim() != 2 or not isinstance(gate, torch.Tensor) or state is None:
-        _bad("x and gate [B][D] and state [B][D] are required")
+    device, shape, dtype, head, ld, args = _scan_inputs(x, gate, bias, state, lengths, input, positions=False)
+    if state is None:
+        _bad("state: required")
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif not isinstance(y, torch.Tensor):
-        _bad(f"y: expected a torch tensor, got {type(y).__name__}")
-    gated_scan(x.unsqueeze(0), gate.unsqueeze(0), bias, state, lengths, input=input, y=y.unsqueeze(0), final=state)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+        py, ldy = y.data_ptr(), 0
+    else:
+        py, ldy = _rows(y, shape, dtype, device, "y")
+    _call(device, load_library().fi_scan_forward, _pack(_SCAN_DESC, *head, *ld, ldy, 0, 0, 0), *args, py, args[3], None,
+          None)
     return y
 
 
