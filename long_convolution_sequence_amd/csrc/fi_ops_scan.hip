@@ -34,7 +34,14 @@ constexpr int kStep = 8;                        // positions of a lane
 constexpr int kRow = 16;                        // lanes along a row
 constexpr int kWaves = 8;                       // waves of a tile at most
 constexpr int kTile = kWaves * 64 / kRow * kStep;   // positions of a tile
-constexpr int kWindow = 6;                      // tiles looked back at together; eight no longer fit two tiles on a CU
+// Tiles looked back at together.  A step along the chain of tiles takes about 1 us
+// (a state out to memory and in again), so few columns, with many times under way,
+// want it long: kFar where there are no more than kNarrow column tiles, 128525 x 81
+// fp32 86 -> 59 us, x 384 bf16 92 -> 77, x 512 (eight) 100 -> 96 but its fp32
+// training pass 387 -> 407.  With many columns the words cost more than the steps
+// (131072 x 864 bf16 166 -> 183 us; kNear = 4 178, 5 174).
+constexpr int kNear = 6, kFar = 16;
+constexpr int kNarrow = 7;
 constexpr int kSerial = 16;                     // lengths up to this run one position after the other
 constexpr int kPolls = 1 << 20;                 // looks at unfinished tiles before a wait gives up
 
@@ -102,41 +109,43 @@ __device__ __forceinline__ unsigned long long link_get(const unsigned long long 
 }
 __device__ __forceinline__ bool link_done(unsigned long long v) { return (unsigned)(v >> 32) == kDone; }
 
-// The state at the end of the tile before, for one column r.  `row` is this tile's
-// row of words, `step` the words between tiles (negative: the tiles come from the end),
-// `have` the number of tiles before it (>= 1).  A wait that gives up leaves NaN.
-// (All waves of the workgroup looking at 32 tiles together shortens the chain of
-// one narrow sequence from 75 to 67 us, and takes the memory from everybody else:
-// 170 -> 210 us at 131072 x 864.)
-__device__ __forceinline__ float link_state(const unsigned long long *row, unsigned r, int64_t step, int have) {
-    for (int polls = 0; polls < kPolls; ++polls) {
-        unsigned long long v[kWindow];
+// The state at the end of the tile before, for one column r, from the WINDOW tiles
+// before.  `row` is this tile's row of words, `step` the words between tiles
+// (negative: the tiles come from the end), `have` the number of tiles before it
+// (>= 1).
+template <int WINDOW>
+__device__ __forceinline__ bool link_look(const unsigned long long *row, unsigned r, int64_t step, int have, float &s) {
+    unsigned long long v[WINDOW];
 #pragma unroll
-        for (int i = 0; i < kWindow; ++i) v[i] = i < have ? link_get(in_row(row - (i + 1) * step, r)) : kNothing;
-        // the nearest tile with its state, if every nearer one has its map
-        int found = -1;
-        bool open = true;
+    for (int i = 0; i < WINDOW; ++i) v[i] = i < have ? link_get(in_row(row - (i + 1) * step, r)) : kNothing;
+    // the nearest tile with its state, if every nearer one has its map
+    int found = -1;
+    bool open = true;
 #pragma unroll
-        for (int i = 0; i < kWindow; ++i) {
-            open = open && v[i] != kNothing;
-            if (open && link_done(v[i])) {
-                found = i;
-                open = false;
-            }
+    for (int i = 0; i < WINDOW; ++i) {
+        open = open && v[i] != kNothing;
+        if (open && link_done(v[i])) {
+            found = i;
+            open = false;
         }
-        if (found >= 0) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = kWindow - 1; i >= 0; --i) {
-                const float lo = __uint_as_float((unsigned)v[i]);
-                if (i == found) s = lo;
-                if (i < found) s = fmaf(__uint_as_float((unsigned)(v[i] >> 32)), s, lo);
-            }
-            return s;
-        }
-        __builtin_amdgcn_s_sleep(1);
     }
-    return __uint_as_float(0x7fc00000u);
+    if (found < 0) return false;
+#pragma unroll
+    for (int i = WINDOW - 1; i >= 0; --i) {
+        const float lo = __uint_as_float((unsigned)v[i]);
+        if (i == found) s = lo;
+        if (i < found) s = fmaf(__uint_as_float((unsigned)(v[i] >> 32)), s, lo);
+    }
+    return true;
+}
+
+// Looks until it is found.  A wait that gives up leaves NaN.
+template <int WINDOW>
+__device__ __forceinline__ float link_state(const unsigned long long *row, unsigned r, int64_t step, int have) {
+    float s = __uint_as_float(0x7fc00000u);
+    for (int polls = 0; polls < kPolls && !link_look<WINDOW>(row, r, step, have, s); ++polls)
+        __builtin_amdgcn_s_sleep(1);
+    return s;
 }
 
 __global__ void __launch_bounds__(256) k_scan_clear(unsigned long long *link, size_t n, unsigned *ticket) {
@@ -252,11 +261,32 @@ struct Column {
     }
 };
 
-template <typename V, int IN, int CH>
+// A wave's values of its positions put aside in LDS, and taken back: kFar words a
+// lane and the values together are more registers than two tiles a CU leave.
+template <typename T, int CH>
+using Parked = T __attribute__((ext_vector_type(CH)))[kStep][64];
+
+template <typename T, int CH, typename Values>
+__device__ __forceinline__ void park(Parked<T, CH> &to, const Values &v) {
+#pragma unroll
+    for (int k = 0; k < kStep; ++k)
+#pragma unroll
+        for (int e = 0; e < CH; ++e) to[k][threadIdx.x & 63][e] = v[k][e];
+}
+template <typename T, int CH, typename Values>
+__device__ __forceinline__ void unpark(const Parked<T, CH> &from, Values &v) {
+#pragma unroll
+    for (int k = 0; k < kStep; ++k)
+#pragma unroll
+        for (int e = 0; e < CH; ++e) v[k][e] = from[k][threadIdx.x & 63][e];
+}
+
+template <typename V, int IN, int CH, bool FAR>
 __global__ void __launch_bounds__(kWaves * 64, 4) k_scan_tile(ScanArgs p) {
     constexpr int COLS = kRow * CH;
     __shared__ float2 maps[kWaves][COLS];        // the waves' maps
     __shared__ float from[kWaves][COLS];         // states before the waves' positions
+    __shared__ Parked<float, CH> parkA, parkS;   // FAR: the first wave's maps while it looks back
     __shared__ int slot;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
@@ -306,30 +336,40 @@ __global__ void __launch_bounds__(kWaves * 64, 4) k_scan_tile(ScanArgs p) {
     }
     __syncthreads();
 
-    if (wave == 0 && c.own) {
-        unsigned long long *row = p.link + j * R;
-        float At = 1.f, St = 0.f, s = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < waves; ++i) {
-            const float2 m = maps[i][lane];
-            St = fmaf(m.x, St, m.y);
-            At *= m.x;
+    if (wave == 0) {
+        if constexpr (FAR) {
+            park<float, CH>(parkA, A);
+            park<float, CH>(parkS, S);
         }
-        if (j > 0) {
-            if (j + 1 < p.tiles) link_put_map(in_row(row, c.r), At, St);
-            s = link_state(row, c.r, R, j);
-        } else if (p.state) {
-            s = *in_row(p.state, c.r);
-        }
-        const float end = fmaf(At, s, St);
-        if (j + 1 < p.tiles) link_put(in_row(row, c.r), kDone, end);
-        if (p.saved) *in_row(p.saved + j * R, c.r) = end;
-        if (p.final && j + 1 == p.tiles) *in_row(p.final, c.r) = end;
+        if (c.own) {
+            unsigned long long *row = p.link + j * R;
+            float At = 1.f, St = 0.f, s = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < waves; ++i) {
-            from[i][lane] = s;
-            const float2 m = maps[i][lane];
-            s = fmaf(m.x, s, m.y);
+            for (int i = 0; i < waves; ++i) {
+                const float2 m = maps[i][lane];
+                St = fmaf(m.x, St, m.y);
+                At *= m.x;
+            }
+            if (j > 0) {
+                if (j + 1 < p.tiles) link_put_map(in_row(row, c.r), At, St);
+                s = link_state<FAR ? kFar : kNear>(row, c.r, R, j);
+            } else if (p.state) {
+                s = *in_row(p.state, c.r);
+            }
+            const float end = fmaf(At, s, St);
+            if (j + 1 < p.tiles) link_put(in_row(row, c.r), kDone, end);
+            if (p.saved) *in_row(p.saved + j * R, c.r) = end;
+            if (p.final && j + 1 == p.tiles) *in_row(p.final, c.r) = end;
+#pragma unroll 8
+            for (int i = 0; i < waves; ++i) {
+                from[i][lane] = s;
+                const float2 m = maps[i][lane];
+                s = fmaf(m.x, s, m.y);
+            }
+        }
+        if constexpr (FAR) {
+            unpark<float, CH>(parkA, A);
+            unpark<float, CH>(parkS, S);
         }
     }
     __syncthreads();
@@ -371,13 +411,15 @@ __device__ __forceinline__ void forget(float (&v)[kStep][CH]) {
 // Backwards.  The states before the segments come from the saved state before
 // the tile; the gradients' chain from the tiles after it.  Both kinds of maps
 // are formed in one go (they share A).
-template <typename V, int IN, int CH>
+template <typename V, int IN, int CH, bool FAR>
 __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_back(ScanArgs p) {
     constexpr int COLS = kRow * CH;
     __shared__ float mul[kWaves][COLS];          // the waves' A; then their sums of dz
     __shared__ float fwd[kWaves][COLS];          // S; then the states before the waves' positions
     __shared__ float rev[kWaves][COLS];          // S from the end; then c behind the waves' positions
     __shared__ Chunk<float, CH> behind[2][kWaves * 64];   // the lanes' maps of what lies behind them in their wave
+    __shared__ Parked<V, CH> parkx, parkdy;      // FAR: the first wave's values while it looks back
+    __shared__ Parked<float, CH> parkd;
     __shared__ int slot;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
@@ -472,18 +514,30 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
     }
     __syncthreads();
 
-    if (link) {
-        float z = 0.f;
-        if (j + 1 < p.tiles) z = link_state(links, c.r, -R, p.tiles - 1 - j);
-        else if (p.dfinal) z = p.dfinal[c.r];
-        const float end = fmaf(At, z, Zt);
-        if (j > 0) link_put(in_row(links, c.r), kDone, end);
-        else if (p.dstate) p.dstate[c.r] = end;
+    if (wave == 0) {
+        if constexpr (FAR) {
+            park<V, CH>(parkx, xx);
+            park<V, CH>(parkdy, dy);
+            park<float, CH>(parkd, d);
+        }
+        if (link) {
+            float z = 0.f;
+            if (j + 1 < p.tiles) z = link_state<FAR ? kFar : kNear>(links, c.r, -R, p.tiles - 1 - j);
+            else if (p.dfinal) z = p.dfinal[c.r];
+            const float end = fmaf(At, z, Zt);
+            if (j > 0) link_put(in_row(links, c.r), kDone, end);
+            else if (p.dstate) p.dstate[c.r] = end;
 #pragma unroll 8
-        for (int i = waves - 1; i >= 0; --i) {
-            const float Z = rev[i][lane];
-            rev[i][lane] = z;
-            z = fmaf(mul[i][lane], z, Z);
+            for (int i = waves - 1; i >= 0; --i) {
+                const float Z = rev[i][lane];
+                rev[i][lane] = z;
+                z = fmaf(mul[i][lane], z, Z);
+            }
+        }
+        if constexpr (FAR) {
+            unpark<V, CH>(parkx, xx);
+            unpark<V, CH>(parkdy, dy);
+            unpark<float, CH>(parkd, d);
         }
     }
     // ds/dz of every position (the other waves while the first one looks)
@@ -686,10 +740,14 @@ void scan_launch(ScanArgs a, bool backward, hipStream_t st) {
                            a.link, n, a.ticket);
     }
     const dim3 grid((unsigned)a.tiles * a.col_tiles), wg(waves * 64);
-    if (backward)
-        hipLaunchKernelGGL((k_scan_back<V, IN, CH>), grid, wg, 0, st, a);
-    else
-        hipLaunchKernelGGL((k_scan_tile<V, IN, CH>), grid, wg, 0, st, a);
+    if (a.tiles > 1 && a.col_tiles <= kNarrow) {
+        if (backward) hipLaunchKernelGGL((k_scan_back<V, IN, CH, true>), grid, wg, 0, st, a);
+        else hipLaunchKernelGGL((k_scan_tile<V, IN, CH, true>), grid, wg, 0, st, a);
+    } else if (backward) {
+        hipLaunchKernelGGL((k_scan_back<V, IN, CH, false>), grid, wg, 0, st, a);
+    } else {
+        hipLaunchKernelGGL((k_scan_tile<V, IN, CH, false>), grid, wg, 0, st, a);
+    }
 }
 
 // Lanes take four neighbouring columns, or one where a row has fewer.

@@ -52,7 +52,8 @@ def _check(got, v, kind, dtype):
 CASES = [(1, 1, 1, F32, 1), (1, 8, 864, BF16, 1), (2, 3, 5, F16, 2), (7, 1, 64, F32, 0), (31, 2, 33, BF16, 2),
          (64, 4, 8, F16, 1), (65, 1, 257, F32, 2), (127, 2, 100, BF16, 0), (128, 1, 66, F32, 1), (129, 3, 12, F16, 0),
          (255, 2, 7, F32, 2), (256, 1, 130, BF16, 1), (257, 1, 3, F32, 1), (511, 3, 20, F32, 0), (513, 2, 65, F16, 2),
-         (1025, 1, 16, BF16, 2), (3001, 2, 9, F32, 1), (5000, 1, 65, F32, 2)]
+         (1025, 1, 16, BF16, 2), (3001, 2, 9, F32, 1), (5000, 1, 65, F32, 2), (2600, 3, 200, BF16, 2),
+         (4000, 1, 516, F16, 0), (4500, 1, 40, BF16, 0), (2100, 8, 70, F32, 1), (4300, 1, 30, F16, 1), (4200, 1, 2, BF16, 1)]
 
 
 @pytest.mark.parametrize("T,B,D,dtype,kind", CASES)
