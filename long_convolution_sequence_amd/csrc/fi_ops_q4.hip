@@ -3,11 +3,11 @@
 // On the matrix units: a wave takes 16 outputs and steps of 32 inputs
 // (v_mfma_f32_16x16x32, weights as A, the rows of x as columns of B).  A code
 // becomes a 16-bit float without arithmetic: its four bits go to the top of the
-// significand of 16.0, which gives 16 + code exactly; a group's sum then loses
-// (16 + zero) times the group's sum of x, which a second product with A = 1
-// gives in the same layout.  bf16 and fp16 inputs multiply as they are; fp32
-// inputs are cut into three bf16 terms (8 significand bits each, by truncation,
-// so the terms add up to x exactly), each a column of its own.
+// significand of 16.0, which gives 16 + code exactly; a second product into the
+// same sum, with -(16 + zero) made in the same way along the whole row of A, takes
+// the zeros away.  bf16 and fp16 inputs multiply as they are; fp32 inputs are cut
+// into three bf16 terms (8 significand bits each, by truncation, so the terms add
+// up to x exactly), each a column of its own.
 //
 // What bounds it: the bytes of the codes.  A workgroup takes 16 outputs, its
 // waves split K (128 inputs a step, a step a wave in turn).  A wave brings x of
@@ -19,9 +19,10 @@
 //   codes  [N/16][K/128][64 lanes][4 words]   lane l: output l & 15; word s holds
 //          the inputs 32 s + 8 (l >> 4) + 0..7: value 2p in bits 4p..4p+3, value
 //          2p + 1 in bits 16 + 4p..
-//   scales [N/16][K/128][4][groups][4], zeros [N/16][K/128][4][groups][4 x 4 bits]:
-//          a lane of the product holds the outputs (l >> 4) * 4 + 0..3, and reads
-//          their scales of all the step's groups (128 / group) side by side
+//   scales [N/16][K/128][4][groups][4]: a lane of the product holds the outputs
+//          (l >> 4) * 4 + 0..3, and reads their scales of all the step's groups
+//          (128 / group) side by side
+//   zeros  [N/16][K/128][16 outputs][groups] of 4 bits, as the lanes of A need them
 // with N and K rounded up (codes 0, scales 0).
 #include <type_traits>
 
@@ -105,13 +106,15 @@ __global__ void __launch_bounds__(256) k_q4_scales(int N, int have, int kt, int 
     }
 }
 
+// Four zeros per value: outputs in order, the groups of a step inside an output.
 __global__ void __launch_bounds__(256) k_q4_zeros(int N, int have, int kt, int per, const uint8_t *zeros,
                                                   uint16_t *out, int64_t n) {
     for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += gridDim.x * (int64_t)256) {
         unsigned v = 0;
         for (int j = 0; j < 4; ++j) {
-            const Q4Where w(i * 4 + j, kt, per);
-            if (w.n < N && w.g < have) v |= (zeros[(size_t)w.n * have + w.g] & 15u) << (4 * j);
+            const int64_t at = (i * 4 + j) / per, step = at / 16;
+            const int w = (int)(step / kt) * 16 + (int)(at % 16), g = (int)(step % kt) * per + j % per;
+            if (w < N && g < have) v |= (zeros[(size_t)w * have + g] & 15u) << (4 * j);
         }
         out[i] = (uint16_t)v;
     }
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(256) k_q4_quantize(int N, int K, int group, in
 struct Q4Args {
     const u32x4 *codes;
     const void *scales;
-    const uint16_t *zeros;     // four outputs' zeros per value, or NULL
+    const uint8_t *zeros;      // or NULL
     const void *x;
     void *y;
     int64_t ldx, ldy;
@@ -199,6 +202,18 @@ __device__ __forceinline__ void weights(unsigned w, f16x8 &out) {
     r.u[2] = ((w >> 2) & 0x03c003c0u) | 0x4c004c00u;
     r.u[3] = ((w >> 6) & 0x03c003c0u) | 0x4c004c00u;
     out = r.v;
+}
+
+// -(16 + zero) eight times; -24 where no zeros are given.
+__device__ __forceinline__ void minus(unsigned zero, bf16x8 &out) {
+    const unsigned z = zero << 19 | zero << 3 | 0xc180c180u;
+    const u32x4 v = {z, z, z, z};
+    out = __builtin_bit_cast(bf16x8, v);
+}
+__device__ __forceinline__ void minus(unsigned zero, f16x8 &out) {
+    const unsigned z = zero << 22 | zero << 6 | 0xcc00cc00u;
+    const u32x4 v = {z, z, z, z};
+    out = __builtin_bit_cast(f16x8, v);
 }
 
 // Eight inputs k.. of a row of x, zeros from K on.
@@ -257,13 +272,14 @@ __global__ void __launch_bounds__(RT > 1 ? 512 : kQ4Waves * 64) k_q4(Q4Args p) {
     constexpr int ROWS = TERMS == 1 ? 16 : CT * 16 / TERMS;      // rows of x at most
     constexpr int LOADS = (ROWS + 3) / 4;                        // 16 lanes read a row's step
     using Scales = S __attribute__((ext_vector_type(4 * PER)));
-    using Zeros = std::conditional_t<PER == 4, uint64_t, std::conditional_t<PER == 2, uint32_t, uint16_t>>;
+    using Zeros = std::conditional_t<PER == 4, uint16_t, uint8_t>;     // an output's, or two outputs'
     const Scales *scales = static_cast<const Scales *>(p.scales);
     const Zeros *zeros = reinterpret_cast<const Zeros *>(p.zeros);
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
     const int col = lane & 15, kq = lane >> 4;
+    const int nibble = PER == 1 ? lane % 2 * 4 : 0;
     const int64_t tile = blockIdx.x * (int64_t)RT;
     const int last = (p.N + 15) / 16 - 1;
     // an odd number of 16-byte places between chunks: at an even one the writes of
@@ -274,9 +290,6 @@ __global__ void __launch_bounds__(RT > 1 ? 512 : kQ4Waves * 64) k_q4(Q4Args p) {
     int at[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) at[c] = kq * pitch + (c * 16 + col < p.cols ? c * 16 + col : 0);
-    X8 ones;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ones[j] = (typename Op::T)1.f;
     f32x4 y[RT][CT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -304,7 +317,7 @@ __global__ void __launch_bounds__(RT > 1 ? 512 : kQ4Waves * 64) k_q4(Q4Args p) {
             const int64_t at = (tile + r < last ? tile + r : last) * p.kt + u;
             w[r] = p.codes[at * 64 + lane];
             sc[r] = scales[at * 4 + kq];
-            ze[r] = zeros ? zeros[at * 4 + kq] : (Zeros)0x8888888888888888ull;
+            ze[r] = zeros ? zeros[PER == 1 ? at * 8 + col / 2 : at * 16 + col] : (Zeros)0x8888;
         }
         // [32-wide step][4][column]; a wave's LDS accesses are done in order, so the
         // reads of the step before come first
@@ -314,26 +327,26 @@ __global__ void __launch_bounds__(RT > 1 ? 512 : kQ4Waves * 64) k_q4(Q4Args p) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
         for (int g = 0; g < PER; ++g) {
-            f32x4 acc[RT][CT], sum[CT];
+            f32x4 acc[RT][CT];
+            X8 less[RT];
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < RT; ++r) {
+                minus(ze[r] >> (4 * g + nibble) & 15u, less[r]);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][c] = sum[c];
+                for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
 #pragma unroll
             for (int s = 0; s < GROUP / 32; ++s) {
                 const int s32 = g * (GROUP / 32) + s;
                 X8 b[CT];
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    b[c] = xs[s32 * 4 * pitch + at[c]];
-                    sum[c] = product(ones, b[c], sum[c]);
-                }
+                for (int c = 0; c < CT; ++c) b[c] = xs[s32 * 4 * pitch + at[c]];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     X8 q;
                     weights(w[r][s32], q);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[r][c] = product(less[r], b[c], acc[r][c]);
 #pragma unroll
                     for (int c = 0; c < CT; ++c) acc[r][c] = product(q, b[c], acc[r][c]);
                 }
@@ -342,11 +355,9 @@ __global__ void __launch_bounds__(RT > 1 ? 512 : kQ4Waves * 64) k_q4(Q4Args p) {
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float zero = (float)(16 + ((unsigned)(ze[r] >> (16 * g + 4 * i)) & 15u));
                     const float scale = (float)sc[r][4 * g + i];
 #pragma unroll
-                    for (int c = 0; c < CT; ++c)
-                        y[r][c][i] = fmaf(scale, fmaf(-zero, sum[c][i], acc[r][c][i]), y[r][c][i]);
+                    for (int c = 0; c < CT; ++c) y[r][c][i] = fmaf(scale, acc[r][c][i], y[r][c][i]);
                 }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -535,7 +546,7 @@ fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int
     if (outputs_meet(&out, 1, in, 2)) return op_fail(FI_EINVAL, call, "y shares memory with another argument");
     a.codes = (const u32x4 *)((const char *)packed + l.codes);
     a.scales = (const char *)packed + l.scales;
-    a.zeros = desc->has_zeros ? (const uint16_t *)((const char *)packed + l.zeros) : nullptr;
+    a.zeros = desc->has_zeros ? (const uint8_t *)packed + l.zeros : nullptr;
     a.x = x, a.y = y, a.N = desc->N, a.K = desc->K, a.kt = l.kt, a.rows = rows;
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == FI_F32) q4_launch<float>(a, desc->group, desc->scale_dtype, st);
