@@ -259,8 +259,13 @@ __device__ __forceinline__ void put(X8 *to, const Chunk<V, 8> &v) {
 
 constexpr int kQ4Waves = 16;           // waves of a workgroup at most
 constexpr int kQ4Lds = 64 * 1024;      // bytes of LDS at most
-constexpr int kQ4Tall = 4;             // row tiles of a wave where there are many
-constexpr int kQ4TallFrom = 1024;
+// Row tiles of a wave where there are kQ4TallFrom of them.  Four save more of x's
+// way through LDS, two leave registers for more waves, which the groups' scales
+// want: 28672 x 8192 bf16 in groups of 128 28.6 us with four, 29.6 with two; in
+// groups of 32 41 and 36.5; 13757 x 14352 (860 row tiles) in groups of 32 41 with
+// one, 32 with two; 9258 x 13611 fp32 (579) 30 with one, 34.5 with two.
+constexpr int kQ4TallFrom = 768;
+template <int GROUP> constexpr int kQ4Tall = GROUP == 128 ? 4 : 2;
 
 // RT row tiles and CT column tiles of 16.  Every wave brings x of its step into
 // a part of LDS of its own, so nothing waits at a barrier before the end.
@@ -387,10 +392,11 @@ __global__ void __launch_bounds__(RT > 1 ? 512 : kQ4Waves * 64) k_q4(Q4Args p) {
     }
 }
 
-// Waves that split K: enough that the whole device has sixteen a CU, four at
-// least, no more than there are steps.
-int q4_waves(int groups, int kt, int most) {
-    const int want = (4096 + groups - 1) / groups;
+// Waves that split K: enough that the whole device has sixteen a CU (twice that
+// with two row tiles a wave: 36.5 us against 55 at 28672 x 8192 in groups of 32; with
+// one, 50 against 57 at 13757 x 14352), four at least, no more than there are steps.
+int q4_waves(int groups, int kt, int rt, int most) {
+    const int want = ((rt == 2 ? 8192 : 4096) + groups - 1) / groups;
     return std::min(std::min(std::max(want, 4), most), kt);
 }
 
@@ -398,7 +404,7 @@ template <typename V, typename S, int GROUP, int CT, int RT>
 void q4_launch(const Q4Args &a, hipStream_t st) {
     const int tiles = (a.N + 15) / 16, groups = (tiles + RT - 1) / RT;
     const size_t step = (size_t)(a.cols | 1) * 256;      // bytes of x of one step in LDS
-    const int waves = std::min(q4_waves(groups, a.kt, RT > 1 ? 8 : kQ4Waves), kQ4Lds / (int)step);
+    const int waves = std::min(q4_waves(groups, a.kt, RT, RT > 1 ? 8 : kQ4Waves), kQ4Lds / (int)step);
     const size_t part = (size_t)waves * CT * 16 * 17 * sizeof(float);
     hipLaunchKernelGGL((k_q4<V, S, GROUP, CT, RT>), dim3((unsigned)groups), dim3(waves * 64),
                        std::max(waves * step, part), st, a);
@@ -406,7 +412,7 @@ void q4_launch(const Q4Args &a, hipStream_t st) {
 
 template <typename V, typename S, int GROUP, int CT>
 void q4_launch(const Q4Args &a, hipStream_t st) {
-    if ((a.N + 15) / 16 >= kQ4TallFrom) q4_launch<V, S, GROUP, CT, kQ4Tall>(a, st);
+    if ((a.N + 15) / 16 >= kQ4TallFrom) q4_launch<V, S, GROUP, CT, kQ4Tall<GROUP>>(a, st);
     else q4_launch<V, S, GROUP, CT, 1>(a, st);
 }
 
