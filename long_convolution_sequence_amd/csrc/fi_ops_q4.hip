@@ -77,11 +77,15 @@ __global__ void __launch_bounds__(256) k_q4_codes(int N, int K, int kt, const ui
         const int64_t tile = i >> 8;
         const int n = (int)(tile / kt) * 16 + (lane & 15);
         const int k0 = (int)(tile % kt) * 128 + s * 32 + (lane >> 4) * 8;
+        const uint8_t *from = codes + (size_t)n * K + k0;
+        Chunk<uint8_t, 8> q = (Chunk<uint8_t, 8>)(uint8_t)0;
+        if (n < N && k0 + 8 <= K)
+            q = *reinterpret_cast<const Chunk<uint8_t, 8> *>(from);
+        else if (n < N)
+            for (int j = 0; j < 8; ++j) q[j] = k0 + j < K ? from[j] : 0;
         unsigned w = 0;
-        for (int j = 0; j < 8; ++j) {
-            const unsigned q = n < N && k0 + j < K ? codes[(size_t)n * K + k0 + j] & 15u : 0u;
-            w |= q << ((j >> 1) * 4 + (j & 1) * 16);
-        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w |= (q[j] & 15u) << ((j >> 1) * 4 + (j & 1) * 16);
         out[i] = w;
     }
 }
