@@ -22,6 +22,20 @@
 //
 // The join is the same chain of fmas whichever tile the state was found at
 // (s <- A s + S, tile after tile), so results do not depend on timing.
+//
+// What bounds it: the memory's bytes where there are many columns.  Forward
+// 32768 x 4 x 768 bf16 129 us (4.7 TB/s of the 5.0 that a copy reaches, x and gate
+// read, y written, all once), 8192 x 8 x 768 fp32 padded 85 us (4.8); 131072 x 864
+// bf16 158 us (4.3): rows of 1728 bytes begin in the middle of a 128-byte line
+// every other time, and two tiles fetch it (1.37 times the bytes through the L2).
+// Backward, 32768 x 4 x 768 bf16, 228 us (4.4).  Few columns: the chain of tiles
+// (see kNear).  One time step after the other, four columns a lane, took 315 us
+// where this takes 85 (padded), 514 for 158.
+//
+// A tile of 256 x 64: 128-byte pieces of 16-bit rows, two tiles of eight waves on a
+// CU at 128 registers.  128 columns took 186 us where this took 170, 256 columns
+// 274; four waves 206, twelve 177, sixteen 200.  All waves looking back at 32
+// tiles together: 210.
 #include <type_traits>
 
 #include "fi_ops.h"
@@ -42,7 +56,10 @@ constexpr int kTile = kWaves * 64 / kRow * kStep;   // positions of a tile
 // (131072 x 864 bf16 166 -> 183 us; kNear = 4 178, 5 174).
 constexpr int kNear = 6, kFar = 16;
 constexpr int kNarrow = 7;
-constexpr int kSerial = 16;                     // lengths up to this run one position after the other
+// Lengths up to this run one position after the other, a lane its columns: a single
+// token is one short kernel (2.8 us at 8 x 864).  At T = 16 the tile takes 229 us
+// and this 172 with 4096 x 2048 columns, 5.3 and 6.5 with 8 x 864; at T = 8 209 and 90.
+constexpr int kSerial = 16;
 constexpr int kPolls = 1 << 20;                 // looks at unfinished tiles before a wait gives up
 
 struct ScanArgs {
