@@ -137,6 +137,11 @@ def _call(device, fn, *args):
         _check(status)
 
 
+def _like(t):
+    """A new packed tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _bytes(n, like):
     return torch.empty(n, dtype=torch.uint8, device=like.device)
 
@@ -183,12 +188,12 @@ def gated_scan(x, gate, bias=None, state=None, lengths=None, *, input=SCAN_CONVE
     gated_scan_backward needs.  final may be given as the state itself."""
     device, shape, dtype, head, ld, args = _scan_inputs(x, gate, bias, state, lengths, input)
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
+        y = _like(x)
         py, ldy = y.data_ptr(), 0
     else:
         py, ldy = _rows(y, shape, dtype, device, "y")
     if final is None:
-        final = torch.empty(shape[1:], dtype=torch.float32, device=x.device)
+        final = _like(state) if state is not None else x.new_empty(shape[1:], dtype=torch.float32)
         pf = final.data_ptr()
     else:
         pf = _dense(final, shape[1:], torch.float32, device, "final")
@@ -207,7 +212,7 @@ def gated_scan_step(x, gate, state, bias=None, lengths=None, *, input=SCAN_CONVE
     if state is None:
         _bad("state: required")
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
+        y = _like(x)
         py, ldy = y.data_ptr(), 0
     else:
         py, ldy = _rows(y, shape, dtype, device, "y")
@@ -226,12 +231,12 @@ def gated_scan_backward(dy, x, gate, saved, bias=None, state=None, lengths=None,
         _bad("dy and saved are required")
     pdy, lddy = _rows(dy, shape, dtype, device, "dy")
     pdf = _dense(dfinal, shape[1:], torch.float32, device, "dfinal")
-    dx = torch.empty(shape, dtype=dtype, device=x.device) if dx is None else dx
-    dgate = torch.empty(shape, dtype=dtype, device=x.device) if dgate is None else dgate
+    dx = _like(x) if dx is None else dx
+    dgate = _like(gate) if dgate is None else dgate
     pdx, lddx = _rows(dx, shape, dtype, device, "dx")
     pdg, lddg = _rows(dgate, shape, dtype, device, "dgate")
-    dbias = torch.empty(shape[2:], dtype=torch.float32, device=x.device) if bias is not None else None
-    dstate = torch.empty(shape[1:], dtype=torch.float32, device=x.device) if state is not None else None
+    dbias = _like(bias) if bias is not None else None
+    dstate = _like(state) if state is not None else None
     _, work, kept = _scan_sizes(*head)
     psv = _dense(saved, (kept,), torch.uint8, device, "saved")
     work = _bytes(work, x)
@@ -289,12 +294,12 @@ def block_norm(o, res=None, gate=None, *, post_weight=None, scale=None, pre_weig
     first, device, shape, dtype, rt, rows, head, args = _norm_inputs(o, res, gate, post_weight, scale, pre_weight,
                                                                      post_norm, act, eps)
     if r is None:
-        r = torch.empty(shape, dtype=rt, device=first.device)
+        r = _like(res) if res is not None else _like(o)
         pr, ldr = r.data_ptr(), 0
     else:
         pr, ldr = _rows(r, shape, rt, device, "r")
     if a is None:
-        a = torch.empty(shape, dtype=dtype, device=first.device)
+        a = _like(first)
         pa, lda = a.data_ptr(), 0
     else:
         pa, lda = _rows(a, shape, dtype, device, "a")
@@ -322,9 +327,8 @@ def block_norm_backward(dr, da, o, res, gate, saved, *, post_weight=None, scale=
     pdr, lddr = _rows(dr, shape, rt, device, "dr")
     pda, ldda = _rows(da, shape, dtype, device, "da")
 
-    def like(given, want, dt):
-        return torch.empty(shape, dtype=dt, device=first.device) if want is not None and given is None else given
-    do, dres, dgate = like(do, o, dtype), like(dres, res, rt), like(dgate, gate, dtype)
+    do, dres, dgate = [_like(t) if t is not None and given is None else given
+                       for given, t in ((do, o), (dres, res), (dgate, gate))]
     pdo, lddo = _rows(do, shape, dtype, device, "do")
     pdres, lddres = _rows(dres, shape, rt, device, "dres")
     pdg, lddg = _rows(dgate, shape, dtype, device, "dgate")
@@ -408,7 +412,7 @@ def q4_matvec(w, x, y=None):
     rows = x.shape[0]
     px, ldx = _rows(x, (rows, w.K), dtype, device, "x")
     if y is None:
-        y = torch.empty((rows, w.N), dtype=dtype, device=x.device)
+        y = x.new_empty((rows, w.N))
         py, ldy = y.data_ptr(), 0
     else:
         py, ldy = _rows(y, (rows, w.N), dtype, device, "y")
