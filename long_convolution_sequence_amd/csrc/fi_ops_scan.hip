@@ -883,8 +883,11 @@ fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *
         if (dstate) hipLaunchKernelGGL(k_scan_pass, dim3(cols), dim3(64), 0, st, dfinal, dstate, pl.R);
     } else {
         scan_links(pl, workspace, a);
-        a.pbias = dbias ? (float *)((char *)workspace + pl.link) : nullptr;
+        // one tile of one row: its sums are the gradient
+        const bool alone = pl.tiles == 1 && a.B == 1;
+        a.pbias = dbias ? alone ? dbias : (float *)((char *)workspace + pl.link) : nullptr;
         pick(desc->dtype, desc->input, true)(a, st);
+        if (alone) return op_launched(call);
     }
     if (dbias) hipLaunchKernelGGL(k_scan_dbias, dim3((unsigned)((a.D + 63) / 64)), dim3(1024), 0, st, a, dbias);
     return op_launched(call);

@@ -86,14 +86,16 @@ def test_tiny_inputs_are_not_dropped():
     assert torch.equal(y.cpu(), want.to(F16))
 
 
-@pytest.mark.parametrize("dtype", [F32, BF16])
-def test_many_outputs_and_a_large_weight(dtype):
-    """More weights than the layout's kernels take in one turn, and row tiles enough for four a wave."""
-    say(f"case q4 large {dtype}")
-    N, K, B = 16900, 1100, 3
-    v = _inputs(N, K, B, 32, dtype, F32, True, seed=7)
-    y = ops.q4_matvec(_weight(v, 32), v["x"].cuda())
-    want, tol = ref.q4(v["x"], v["codes"], v["scales"], v["zeros"], 32)
+@pytest.mark.parametrize("dtype,B,group", [(F32, 3, 32), (BF16, 3, 128), (F32, 8, 128), (F32, 16, 64), (F32, 11, 128),
+                                           (F16, 16, 32)])
+def test_many_outputs_and_a_large_weight(dtype, B, group):
+    """More weights than the layout's kernels take in one turn, and row tiles enough for several a
+    wave (1057: the last wave's are not all there)."""
+    say(f"case q4 large {dtype} B={B} group={group}")
+    N, K = 16900, 1100
+    v = _inputs(N, K, B, group, dtype, F32, True, seed=7)
+    y = ops.q4_matvec(_weight(v, group), v["x"].cuda())
+    want, tol = ref.q4(v["x"], v["codes"], v["scales"], v["zeros"], group)
     assert ref.worst(y, want, ref.stored(want, tol, dtype)) <= 1.0
 
 
