@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kNormMaxD = 16384;
 constexpr int kNormLane = 16;          // values of a row per lane at most
+constexpr int kNormHalf = 768;         // threads of the backward workgroups with half of that (see half_lanes)
 constexpr int64_t kNormCache = 256 << 20;   // bytes of the last-level cache
 constexpr int kNormCUs = 256;          // compute units that the workgroups are spread over
 
@@ -236,9 +237,10 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
 // (team after team, so the order is fixed) and written once.  Elements that a
 // lane does not own have weights of zero, so both means pass them by.
 template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, bool STREAM, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) k_norm_back(NormArgs p) {
+__global__ void __launch_bounds__(THREADS, THREADS == kNormHalf ? 3 : THREADS <= 512 ? 2 : 1) k_norm_back(NormArgs p) {
     constexpr int N = CH * NC;
-    constexpr bool AHEAD = MULTI && THREADS <= 512 && sizeof(W) == 2;   // with fp32 rows it would spill
+    // the next row's values on their way; with fp32 rows and 16 values a lane they would spill
+    constexpr bool AHEAD = MULTI && (THREADS == kNormHalf || (THREADS <= 512 && sizeof(W) == 2));
     __shared__ float slots[2][16];
     __shared__ float join[MULTI ? 1 : 2 * 64 * N];
     Team<CH, NC, MULTI> t(p.D);
@@ -372,6 +374,13 @@ const char *norm_check(const fi_norm_desc *q) {
 
 int team_waves(int D) { return (D + 64 * kNormLane - 1) / (64 * kNormLane); }
 
+// Backwards, rows of five or six waves at 16 values a lane leave a CU's eight
+// places partly empty and its four SIMDs unevenly loaded: 8 values a lane then, and
+// nine to twelve waves of the twelve that their registers allow.  1999 x 5001 fp16
+// training 82 -> 75 us, 8888 x 4500 bf16 with fp32 rows 328 -> 291, 6510 x 6144 fp16
+// 217 -> 206; below, 13333 x 3000 fp16 195 -> 251, 20000 x 4096 bf16 387 -> 427.
+bool half_lanes(int D) { return D > 4096 && D <= 6144; }
+
 // Workgroups: as many as are resident together (their registers allow 16 waves a
 // CU forwards, and backwards 8, 16 or 24 with 16, 8 or 4 values a lane), so that
 // a team runs through its rows without a second round of workgroups, and the
@@ -381,8 +390,9 @@ int team_waves(int D) { return (D + 64 * kNormLane - 1) / (64 * kNormLane); }
 // against 316).
 unsigned norm_groups(const fi_norm_desc *q, bool backward) {
     const int ch = value_bytes(q->res_dtype) == 2 ? 8 : 4, D = q->channels, waves = team_waves(D);
-    const int group = waves > 1 ? waves : 4;
-    const int resident = !backward ? 16 : D <= 64 * 4 && ch == 4 ? 24 : D <= 64 * 8 ? 16 : 8;
+    const bool half = backward && half_lanes(D);
+    const int group = half ? (D + 511) / 512 : waves > 1 ? waves : 4;
+    const int resident = half ? 12 : !backward ? 16 : D <= 64 * 4 && ch == 4 ? 24 : D <= 64 * 8 ? 16 : 8;
     const int64_t most = kNormCUs * std::max(1, resident / group) * (!backward && waves == 1 ? 2 : 1);
     const int64_t need = std::max<int64_t>(1, waves > 1 ? q->rows : (q->rows + 3) / 4);
     const int64_t turns = (need + most - 1) / most;
@@ -412,7 +422,7 @@ void launch(const NormArgs &a, bool backward, unsigned groups, unsigned threads,
     if (backward)
         hipLaunchKernelGGL((k_norm_back<V, W, CH, NC, MULTI, TAIL, ALL, STREAM, THREADS>), dim3(groups), dim3(threads), 0,
                            st, a);
-    else
+    else if constexpr (THREADS != kNormHalf)
         hipLaunchKernelGGL((k_norm<V, W, CH, NC, MULTI, TAIL, ALL, STREAM, THREADS>), dim3(groups), dim3(threads), 0, st,
                            a);
 }
@@ -428,7 +438,7 @@ void launch(const NormArgs &a, bool backward, unsigned groups, unsigned threads,
     const bool all = a.o && a.gate && a.res && (!backward || (a.dr && a.da));
     const int64_t values = a.rows * a.D;
     const bool stream = values * (int64_t)((backward ? 3 : 2) * sizeof(V) + (backward ? 2 : 1) * sizeof(W)) > kNormCache;
-    if constexpr (CH > 1 && THREADS <= 512) {
+    if constexpr (CH > 1 && THREADS <= kNormHalf) {
         if (all && a.D % CH == 0) {
             if (stream) return launch<V, W, CH, NC, MULTI, THREADS, false, true, true>(a, backward, groups, threads, st);
             return launch<V, W, CH, NC, MULTI, THREADS, false, true, false>(a, backward, groups, threads, st);
@@ -445,7 +455,9 @@ template <typename V, typename W>
 void launch(const NormArgs &a, bool backward, unsigned groups, hipStream_t st) {
     constexpr int CH = sizeof(W) == 2 ? 8 : 4;
     const int waves = team_waves(a.D);
-    if (a.D < CH)
+    if (backward && half_lanes(a.D))
+        launch<V, W, CH, kNormLane / 2 / CH, true, kNormHalf>(a, backward, groups, (a.D + 511) / 512 * 64, st);
+    else if (a.D < CH)
         launch<V, W, 1, 1, false, 256>(a, backward, groups, 256, st);
     else if (a.D <= 64 * CH)
         launch<V, W, CH, 1, false, 256>(a, backward, groups, 256, st);

@@ -51,7 +51,9 @@ CASES = [(1, 1, F32, F32, True, 2), (1, 864, BF16, F32, True, 2), (8, 864, BF16,
          (70, 256, F32, F32, True, 2), (9, 257, BF16, BF16, True, 2), (4, 1000, F16, F32, True, 0),
          (3, 1024, F32, F32, True, 1), (6, 1025, BF16, F32, False, 0), (2, 2050, F32, F32, True, 2),
          (3, 4100, F16, F16, True, 2), (2, 8191, BF16, F32, True, 2), (2, 16384, F32, F32, True, 2),
-         (3, 16383, F16, F32, True, 1), (2500, 40, F32, F32, True, 2), (1300, 96, BF16, F32, True, 2)]
+         (3, 16383, F16, F32, True, 1), (2500, 40, F32, F32, True, 2), (1300, 96, BF16, F32, True, 2),
+         (5, 4097, BF16, F32, True, 2), (4, 4608, F32, F32, True, 1), (600, 5001, F16, F16, True, 2), (3, 6144, BF16, BF16, True, 2),
+         (3, 6145, F16, F32, True, 0)]
 
 
 @pytest.mark.parametrize("N,D,dtype,rt,post,act", CASES)
@@ -204,7 +206,7 @@ def test_many_rows():
     _check(_run(_cuda(v), True, ops.GATE_SILU), v, True, ops.GATE_SILU, F32, F32)
 
 
-@pytest.mark.parametrize("D,dtype,rt", [(864, BF16, F32), (1001, F16, F16), (256, F32, F32), (5000, BF16, BF16),
+@pytest.mark.parametrize("D,dtype,rt", [(864, BF16, F32), (1001, F16, F16), (256, F32, F32), (5000, BF16, BF16), (3000, BF16, BF16),
                                         (5001, F16, F32)])
 def test_more_than_the_caches_hold(D, dtype, rt):
     """Inputs past the size from which they are read as streams: the rows as in slices of it (each of
