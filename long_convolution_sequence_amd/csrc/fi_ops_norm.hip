@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
 }
 
 // Backward: every tensor of the row once (131072 x 768 bf16 with fp32 rows 400 us, 5.5
-// TB/s; 1999 x 5001 fp16 48 us), two row means, one after the other;
+// TB/s; 1999 x 5001 fp16 43 us), two row means, one after the other;
 // the column sums of a team's rows in registers, its workgroup's joined in LDS
 // (team after team, so the order is fixed) and written once.  Elements that a
 // lane does not own have weights of zero, so both means pass them by.
