@@ -382,10 +382,11 @@ int team_waves(int D) { return (D + 64 * kNormLane - 1) / (64 * kNormLane); }
 bool half_lanes(int D) { return D > 4096 && D <= 6144; }
 
 // Workgroups: as many as are resident together (their registers allow 16 waves a
-// CU forwards, and backwards 8, 16 or 24 with 16, 8 or 4 values a lane), so that
-// a team runs through its rows without a second round of workgroups, and the
-// backward pass has few column sums; the rows are spread evenly.  Rows of 5001
-// in 512 workgroups instead of 256: 99 us against 90; of 256 in 512 instead of
+// CU forwards, and backwards 8, 16 or 24 with 16, 8 or 4 values a lane, 12 with
+// half_lanes), so that a team runs through its rows without a second round of
+// workgroups, and the backward pass has few column sums; the rows are spread
+// evenly.  Training over rows of 5001 at 16 values a lane in 512 workgroups instead
+// of 256: 99 us against 90; of 256 in 512 instead of
 // 1024: 200 against 185.  Forwards one wave a row takes twice as many (310 us
 // against 316).
 unsigned norm_groups(const fi_norm_desc *q, bool backward) {
