@@ -599,8 +599,8 @@ fi_status fi_q4_quantize(const fi_q4_desc *desc, int w_dtype, const void *w, int
                          void *scales, void *stream);
 
 /* y [rows][N] = x [rows][K] times the packed weights; rows 1 .. 16, x and y of
- * `dtype`.  fp32 inputs are multiplied in full (as three bf16 terms), 16-bit
- * ones exactly too; sums are fp32.  A row of x with an infinity or NaN gives
+ * `dtype`.  fp32 inputs are multiplied in full (as three bf16 terms; below 2^-110
+ * in size the last bits may be lost), 16-bit ones exactly too; sums are fp32.  A row of x with an infinity or NaN gives
  * non-finite values in its row of y only.  |x| stays below 2^120. */
 fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int dtype, const void *x, int64_t ld_x,
                        void *y, int64_t ld_y, void *stream);
