@@ -408,11 +408,24 @@ int q4_waves(int groups, int kt, int rt, int most) {
     return std::min(std::min(std::max(want, 4), most), kt);
 }
 
+// With several column tiles a CU has registers for sixteen waves and LDS for few: a
+// count that leaves part of either unused, and workgroups for a second round, goes
+// down to the multiple of four with which more of them fit (7357 x 15788 of 8 fp32
+// rows nine waves 43 us, eight 33; 9000 x 9000 of 16 five 54, four 44).
+int q4_fitting(int waves, int groups, int step) {
+    const auto on_cu = [&](int w) { return std::min(16 / w, 160 * 1024 / (w * step)); };
+    if (groups <= 256 * on_cu(waves)) return waves;
+    for (int w = waves / 4 * 4; w >= 4 && w < waves; w -= 4)
+        if (on_cu(w) > on_cu(waves)) return w;
+    return waves;
+}
+
 template <typename V, typename S, int GROUP, int CT, int RT>
 void q4_launch(const Q4Args &a, hipStream_t st) {
     const int tiles = (a.N + 15) / 16, groups = (tiles + RT - 1) / RT;
     const size_t step = (size_t)(a.cols | 1) * 256;      // bytes of x of one step in LDS
-    const int waves = std::min(q4_waves(groups, a.kt, RT, RT > 1 ? 8 : kQ4Waves), kQ4Lds / (int)step);
+    int waves = std::min(q4_waves(groups, a.kt, RT, RT > 1 ? 8 : kQ4Waves), kQ4Lds / (int)step);
+    if (CT > 1 && RT == 1 && waves % 4) waves = q4_fitting(waves, groups, (int)step);
     const size_t part = (size_t)waves * CT * 16 * 17 * sizeof(float);
     hipLaunchKernelGGL((k_q4<V, S, GROUP, CT, RT>), dim3((unsigned)groups), dim3(waves * 64),
                        std::max(waves * step, part), st, a);
