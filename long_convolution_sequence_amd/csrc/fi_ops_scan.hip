@@ -5,9 +5,14 @@
 // s -> A s + S.  The gradients are the same recurrence from the end:
 // D_t = dy_t + c, c <- D_t - d_t D_t.
 //
-// The state is updated as s - d s, never as a s with a = 1 - d rounded to
-// fp32: for decays near one (a memory of thousands of positions) the rounding
-// of a alone is a relative error of 2^-25 / d in the memory's length.
+// Where the gate is open (z >= 0) the state is updated as s - d s, never as a s
+// with a = 1 - d rounded to fp32: for decays near one (a memory of thousands of
+// positions) the rounding of a alone is a relative error of 2^-25 / d in the
+// memory's length.  Where it is shut (z < 0) the same rounding would be the whole
+// of a (from z = -17 on 1 - d is 0, and with it every gradient through the gate):
+// there a = e^z d, and the update is a s.  A position keeps the smaller of the two
+// (see Decay).  It costs selects: a training pass over 32768 x 4 x 768 bf16 takes 368 us
+// where 1 - d alone took 349, 131072 x 864 bf16 forwards 161 for 157.
 //
 // One pass over the data (k_scan_tile, k_scan_back).  A workgroup holds a tile
 // of kTile positions x 64 columns in registers: a lane has kStep positions of
@@ -81,8 +86,27 @@ struct ScanArgs {
     int col_tiles;
 };
 
-__device__ __forceinline__ float sigmoid_neg(float z) {   // 1 - sigmoid(z) = 1 / (1 + e^z)
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * 1.44269504088896f));
+// A position's decay, to the last digits whichever way its gate lies.  `w` is what
+// is kept of it: -d = -1 / (1 + e^z) where the gate is open (z >= 0, or NaN), a = e^z d
+// where it is shut.  Its sign bit tells which (d = 0 is -0, a = 0 is +0).
+struct Decay {
+    float w, d;
+    bool open;
+    __device__ __forceinline__ Decay(float z) {
+        const float ez = __builtin_amdgcn_exp2f(z * 1.44269504088896f);
+        d = __builtin_amdgcn_rcpf(1.f + ez);
+        open = !(z < 0.f);
+        w = open ? -d : ez * d;
+    }
+    // of a position past its row's length: it leaves the state
+    __device__ __forceinline__ void none() { d = 0.f, w = -0.f, open = true; }
+};
+__device__ __forceinline__ bool is_open(float w) { return (int)__float_as_uint(w) < 0; }
+
+// (1 - d) s, as s - d s or a s; and one position, (1 - d) s + b.
+__device__ __forceinline__ float decayed(bool open, float w, float s) { return fmaf(w, s, open ? s : 0.f); }
+__device__ __forceinline__ float moved(bool open, float w, float s, float b) {
+    return (open ? s : 0.f) + fmaf(w, s, b);
 }
 
 template <int IN>
@@ -92,13 +116,31 @@ __device__ __forceinline__ float input_factor(float d) {
     return __builtin_amdgcn_sqrtf(d * (2.f - d));
 }
 
-// ds/dz of one position: the decay's part d(1-d) s_{t-1} and the input factor's.
+// The same from what is kept: d (2 - d) as 2d - d^2 or 1 - a^2, d x as d x or x - a x.
+__device__ __forceinline__ float energy(bool open, float w) { return fmaf(-w, w, open ? -2.f * w : 1.f); }
 template <int IN>
-__device__ __forceinline__ float gate_slope(float d, float x, float before) {
-    const float a = 1.f - d;
-    if (IN == FI_SCAN_PLAIN) return a * d * before;
-    if (IN == FI_SCAN_CONVEX) return a * d * (before - x);
-    return a * (d * before - a * __builtin_amdgcn_sqrtf(d * __builtin_amdgcn_rcpf(2.f - d)) * x);
+__device__ __forceinline__ float input_of(bool open, float w, float x) {
+    if (IN == FI_SCAN_PLAIN) return x;
+    if (IN == FI_SCAN_CONVEX) return fmaf(-w, x, open ? 0.f : x);
+    return __builtin_amdgcn_sqrtf(energy(open, w)) * x;
+}
+
+// The state behind one position, and ds/dz there: the decay's part a d s_{t-1},
+// with a d = |w| - w^2 whichever w is, and the input factor's.  One reciprocal root
+// of d (2 - d) gives the energy factor and its slope -a^2 d / e (at d = 0 it is a
+// finite number, and both are 0).
+template <int IN>
+__device__ __forceinline__ float slope_and_move(float w, float x, float &s) {
+    const bool open = is_open(w);
+    const float ad = fmaf(-fabsf(w), fabsf(w), fabsf(w)), before = s;
+    if (IN != FI_SCAN_ENERGY) {
+        s = moved(open, w, s, input_of<IN>(open, w, x));
+        return ad * (IN == FI_SCAN_PLAIN ? before : before - x);
+    }
+    const float sq = energy(open, w), inv = __builtin_amdgcn_rsqf(fmaxf(sq, 0x1p-126f));
+    const float a = (open ? 1.f : 0.f) + w;
+    s = moved(open, w, s, sq * inv * x);
+    return fmaf(ad, before, -(a * inv * ad) * x);
 }
 
 // ---- what passes between tiles -------------------------------------------------
@@ -326,12 +368,12 @@ __global__ void __launch_bounds__(kWaves * 64, 4) k_scan_tile(ScanArgs p) {
         for (int k = 0; k < kStep; ++k)
 #pragma unroll
             for (int e = 0; e < CH; ++e) {
-                float d = sigmoid_neg((float)xg[k][e] + bias[e]);
-                float b = input_factor<IN>(d) * (float)xx[k][e];
-                if (!FULL && k >= l.live) d = 0.f, b = 0.f;
+                Decay q((float)xg[k][e] + bias[e]);
+                float b = input_factor<IN>(q.d) * (float)xx[k][e];
+                if (!FULL && k >= l.live) q.none(), b = 0.f;
                 const float a0 = k ? A[k ? k - 1 : 0][e] : 1.f, s0 = k ? S[k ? k - 1 : 0][e] : 0.f;
-                A[k][e] = fmaf(-d, a0, a0);
-                S[k][e] = s0 + fmaf(-d, s0, b);
+                A[k][e] = decayed(q.open, q.w, a0);
+                S[k][e] = moved(q.open, q.w, s0, b);
             }
     };
     if (full) segment(std::true_type());
@@ -436,7 +478,7 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
     __shared__ float rev[kWaves][COLS];          // S from the end; then c behind the waves' positions
     __shared__ Chunk<float, CH> behind[2][kWaves * 64];   // the lanes' maps of what lies behind them in their wave
     __shared__ Parked<V, CH> parkx, parkdy;      // FAR: the first wave's values while it looks back
-    __shared__ Parked<float, CH> parkd;
+    __shared__ Parked<float, CH> parkw;
     __shared__ int slot;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
@@ -451,7 +493,10 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
     float s = 0.f;
     if (link) s = j ? p.saved[(j - 1) * R + c.r] : p.state ? p.state[c.r] : 0.f;
 
-    float d[kStep][CH];
+    float w[kStep][CH];                          // decays; in the end dx
+    // this lane's maps: s -> A s + S, and from the end c -> A c + Z, Z the sum of
+    // dy_k times the decays up to k
+    float A[CH], S[CH], Z[CH];
     Chunk<V, CH> xx[kStep], dy[kStep];
     const auto read = [&](auto whole) {
         constexpr bool FULL = decltype(whole)::value;
@@ -462,13 +507,22 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
         Chunk<float, CH> bias = (Chunk<float, CH>)0.f;
         if (p.bias) bias = load_chunk<float, CH>(p.bias, l.w);
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) {
+        for (int k = 0; k < kStep; ++k)
             if (!FULL && k >= l.live) xx[k] = dy[k] = (Chunk<V, CH>)(V)0.f;
 #pragma unroll
-            for (int e = 0; e < CH; ++e) {
-                d[k][e] = sigmoid_neg((float)xg[k][e] + bias[e]);
-                if (!FULL && k >= l.live) d[k][e] = 0.f;
+        for (int e = 0; e < CH; ++e) {
+            float a = 1.f, s = 0.f, z = 0.f;
+#pragma unroll
+            for (int k = 0; k < kStep; ++k) {
+                Decay q((float)xg[k][e] + bias[e]);
+                if (!FULL && k >= l.live) q.none();
+                w[k][e] = q.w;
+                a = decayed(q.open, q.w, a);
+                s = moved(q.open, q.w, s, input_factor<IN>(q.d) * (float)xx[k][e]);
+                z = fmaf(a, (float)dy[k][e], z);
             }
+            A[e] = a, S[e] = s, Z[e] = z;
+            __builtin_amdgcn_sched_barrier(0);   // column after column: interleaved, all four would not fit the registers
         }
     };
     if (full) read(std::true_type());
@@ -478,21 +532,10 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
     Chunk<float, CH> Az, Zz;
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
-        float A = 1.f, S = 0.f, Z = 0.f;
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-            A = fmaf(-d[k][e], A, A);
-            S = S + fmaf(-d[k][e], S, input_factor<IN>(d[k][e]) * (float)xx[k][e]);
-        }
-#pragma unroll
-        for (int k = kStep - 1; k >= 0; --k) {
-            const float G = (float)dy[k][e] + Z;
-            Z = fmaf(-d[k][e], G, G);
-        }
         float a0, a1, s0, s1, z0, z1, pa0, pa1, ps0, ps1, pz0, pz1;
-        rows_pair(A, a0, a1);
-        rows_pair(S, s0, s1);
-        rows_pair(Z, z0, z1);
+        rows_pair(A[e], a0, a1);
+        rows_pair(S[e], s0, s1);
+        rows_pair(Z[e], z0, z1);
         halves_pair(a0 * a1, pa0, pa1);
         halves_pair(fmaf(a1, s0, s1), ps0, ps1);
         halves_pair(fmaf(a0, z1, z0), pz0, pz1);
@@ -507,7 +550,6 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
         const float ha = row & 1 ? 1.f : a1, hz = row & 1 ? 0.f : z1;
         Az[e] = row & 2 ? ha : ha * pa1;
         Zz[e] = row & 2 ? hz : fmaf(ha, pz1, hz);
-        __builtin_amdgcn_sched_barrier(0);   // column after column: interleaved, all four would not fit the registers
     }
     behind[0][threadIdx.x] = Az;
     behind[1][threadIdx.x] = Zz;
@@ -535,7 +577,7 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
         if constexpr (FAR) {
             park<V, CH>(parkx, xx);
             park<V, CH>(parkdy, dy);
-            park<float, CH>(parkd, d);
+            park<float, CH>(parkw, w);
         }
         if (link) {
             float z = 0.f;
@@ -554,28 +596,24 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
         if constexpr (FAR) {
             unpark<V, CH>(parkx, xx);
             unpark<V, CH>(parkdy, dy);
-            unpark<float, CH>(parkd, d);
+            unpark<float, CH>(parkw, w);
         }
     }
     // ds/dz of every position (the other waves while the first one looks)
     forget(xx);
     forget(dy);
-    forget(d);
+    forget(w);
     float slope[kStep][CH];
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
         float b = fmaf(Ab[e], fwd[wave][g * CH + e], Sb[e]);
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-            const float x = (float)xx[k][e];
-            slope[k][e] = gate_slope<IN>(d[k][e], x, b);
-            b = b + fmaf(-d[k][e], b, input_factor<IN>(d[k][e]) * x);
-        }
+        for (int k = 0; k < kStep; ++k) slope[k][e] = slope_and_move<IN>(w[k][e], (float)xx[k][e], b);
         __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
 
-    forget(d);
+    forget(w);
     Az = behind[0][threadIdx.x];
     Zz = behind[1][threadIdx.x];
     float sum[CH];
@@ -586,18 +624,19 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
 #pragma unroll
         for (int k = kStep - 1; k >= 0; --k) {
             const float G = (float)dy[k][e] + b;
-            b = fmaf(-d[k][e], G, G);
+            const bool open = is_open(w[k][e]);
+            b = decayed(open, w[k][e], G);
             slope[k][e] *= G;
             sum[e] += slope[k][e];     // 0 past the row's length: d = x = 0 there
-            d[k][e] = G * input_factor<IN>(d[k][e]);
+            w[k][e] = input_of<IN>(open, w[k][e], G);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
     if (full) {
-        store_steps<true, V, CH>(d, p.dx, p.lddx, p, l);
+        store_steps<true, V, CH>(w, p.dx, p.lddx, p, l);
         store_steps<true, V, CH>(slope, p.dgate, p.lddg, p, l);
     } else {
-        store_steps<false, V, CH>(d, p.dx, p.lddx, p, l);
+        store_steps<false, V, CH>(w, p.dx, p.lddx, p, l);
         store_steps<false, V, CH>(slope, p.dgate, p.lddg, p, l);
     }
     if (p.pbias) {
@@ -648,8 +687,8 @@ __global__ void __launch_bounds__(64) k_scan_serial(ScanArgs p) {
         if (t < len) {
 #pragma unroll
             for (int e = 0; e < CH; ++e) {
-                const float d = sigmoid_neg((float)cg[e] + bias[e]);
-                s[e] = s[e] + fmaf(-d, s[e], input_factor<IN>(d) * (float)cx[e]);
+                const Decay q((float)cg[e] + bias[e]);
+                s[e] = moved(q.open, q.w, s[e], input_factor<IN>(q.d) * (float)cx[e]);
                 out[e] = (V)s[e];
             }
         }

@@ -34,10 +34,13 @@ def factor(kind, d, a):
     return torch.sqrt(d * (1 + a)), -a * a * torch.sqrt(d / (1 + a))
 
 
-def scan(x, gate, bias, state, lengths, kind, dy=None, dfinal=None):
+def scan(x, gate, bias, state, lengths, kind, dy=None, dfinal=None, digits=False):
     """The recurrence and (with dy) its gradients in fp64 on the CPU, by the definition,
     each with the bound of an fp32 evaluation.  Returns {name: (value, bound)}; bounds do
-    not hold the rounding of what is stored."""
+    not hold the rounding of what is stored.
+
+    digits: of an evaluation that keeps the digits of a = 1 - d however small it is (the
+    bounds without it allow a an absolute error)."""
     x, gate = x.double().cpu(), gate.double().cpu()
     T, B, D = x.shape
     z = gate + (bias.double().cpu() if bias is not None else 0.0)
@@ -51,16 +54,21 @@ def scan(x, gate, bias, state, lengths, kind, dy=None, dfinal=None):
     # from there on d may be 0, a relative error of 1 of a d below 2^-126 (and of its root in e);
     # d / (2 - d), under the root in the slope of e, passes it at d = 2^-125 already
     rel = torch.where(d < 2.0 ** -124.9, torch.ones_like(rel), rel)
+    # of a: e^z d where z < 0, off by e^z's and d's errors and a rounding (from 2^-126 on it may be 0);
+    # 1 - d where z >= 0, so d (rel + U) of at least 1/2, and d is no more than 1/2
+    ra = torch.where(z < 0, 2 * rel + U, rel + 2 * U)
+    ra = torch.where(a < 2.0 ** -124.9, torch.ones_like(ra), ra)
     e, slope = factor(kind, d, a)
     zero = torch.zeros_like(x)
     # masked places may hold anything: nothing of theirs is used
-    x, d, rel, slope, e = (torch.where(live, v, zero) for v in (x, d, rel, slope, e))
+    x, d, rel, ra, slope, e = (torch.where(live, v, zero) for v in (x, d, rel, ra, slope, e))
     a = torch.where(live, a, zero + 1)
     s, m, tol = s0.clone(), s0.abs(), torch.zeros_like(s0)
     S, M, E = [s0], [m], [tol]
     for t in range(T):
         b = e[t] * x[t]
-        tol = a[t] * tol + (rel[t] + U) * d[t] * m + (rel[t] + 6 * U) * b.abs()
+        step = (ra[t] + U) * a[t] if digits else (rel[t] + U) * d[t]
+        tol = a[t] * tol + step * m + (rel[t] + 6 * U) * b.abs()
         s, m = a[t] * s + b, a[t] * m + b.abs()
         tol = tol + 3 * U * torch.where(live[t], m, zero[t])
         S.append(s), M.append(m), E.append(tol)
@@ -82,10 +90,13 @@ def scan(x, gate, bias, state, lengths, kind, dy=None, dfinal=None):
         mk = a[t] * d[t] * M[t] + slope[t].abs() * x[t].abs()
         q = torch.sqrt(d[t] / (2 - d[t])) if kind == 2 else zero[t]
         dk = d[t] * (rel[t] + 4 * U) * (M[t] + x[t].abs()) + a[t] * d[t] * E[t] + 3 * x[t].abs() * q * (rel[t] + 6 * U)
+        if digits:        # the factors' errors, each of its term
+            dk = (2 * ra[t] + rel[t] + 10 * U) * mk + a[t] * d[t] * E[t]
         dk = torch.where(live[t], dk, zero[t])
         dz[t], bz[t], mz[t] = G * k, mg * dk + mk * tg10 + 3 * U * mg * mk, mg * mk
         c, mc = a[t] * G, a[t] * mg
-        tc = a[t] * tg + torch.where(live[t], (rel[t] + U) * d[t] * mg + U * mc, zero[t])
+        step = (ra[t] + U) * a[t] if digits else (rel[t] + U) * d[t]
+        tc = a[t] * tg + torch.where(live[t], step * mg + U * mc, zero[t])
     dx, dz, bx, bz = (torch.where(live, v, zero) for v in (dx, dz, bx, bz))
     out.update(dx=(dx, bx), dgate=(dz, bz), dstate=(c, tc + 10 * U * mc))
     terms = 300 + (T // 64 + 2) * B             # roundings on a term's way into the sum

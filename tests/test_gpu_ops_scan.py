@@ -124,6 +124,40 @@ def test_gates_at_the_ends(kind, T):
         assert w <= 1.0, f"{name}: {w:.3g} of its bound"
 
 
+@pytest.mark.parametrize("T,B,D,dtype", [(5, 2, 12, F32), (40, 1, 7, F32), (300, 2, 12, F32), (900, 1, 3, F32),
+                                         (700, 1, 520, F32), (600, 2, 12, BF16), (530, 1, 600, F16)])
+@pytest.mark.parametrize("kind", [0, 1, 2])
+def test_shut_gates_keep_their_digits(T, B, D, dtype, kind):
+    """Gates from -4 down to -40: what passes through them (the state, and every gradient) is a
+    number of e^z, right to its last digits, not the rounding of 1 - d.  Channels differ by their
+    gate; rows 0 mod 3 have x = 0, where what is left of the state is all there is."""
+    say(f"case scan shut gates T={T} B={B} D={D} {dtype} input={kind}")
+    v = _inputs(T, B, D, dtype, seed=14)
+    v["bias"] = -torch.tensor([4.0, 8.0, 12.0, 14.0, 16.0, 18.0, 25.0, 40.0]).repeat(D // 8 + 1)[:D]
+    v["gate"] = v["gate"] / 4
+    v["x"][::3] = 0.0
+    got = _run(_cuda(v), kind)
+    want = ref.scan(v["x"], v["gate"], v["bias"], v["state"], None, kind, v["dy"], v["dfinal"], digits=True)
+    for name, g in got.items():
+        value, tol = want[name]
+        w = ref.worst(g, value, ref.stored(value, tol, dtype if name in ("y", "dx", "dgate") else F32))
+        assert w <= 1.0, f"{name}: {w:.3g} of its bound"
+
+
+def test_open_and_shut_gates_by_turns():
+    """Gates of both signs and of every size by turns, with the bounds that hold a's digits."""
+    say("case scan open and shut gates")
+    for T, dtype in ((9, F32), (200, F32), (1500, F32), (400, BF16)):
+        v = _inputs(T, 2, 20, dtype, seed=15, bias=False)
+        v["gate"] *= 12
+        got = _run(_cuda(v), ops.SCAN_ENERGY)
+        want = ref.scan(v["x"], v["gate"], None, v["state"], None, ops.SCAN_ENERGY, v["dy"], v["dfinal"], digits=True)
+        for name in ("y", "final", "dx", "dgate", "dstate"):
+            value, tol = want[name]
+            w = ref.worst(got[name], value, ref.stored(value, tol, dtype if name in ("y", "dx", "dgate") else F32))
+            assert w <= 1.0, f"T={T} {dtype} {name}: {w:.3g} of its bound"
+
+
 @pytest.mark.parametrize("T,B,D,dtype", [(37, 2, 24, BF16), (600, 1, 20, F32), (300, 3, 17, F16), (700, 2, 64, BF16)])
 def test_column_slices(T, B, D, dtype):
     """x, gate and y as column slices of one tensor, the gradients of another: the same values as
