@@ -33,19 +33,17 @@ struct NormArgs {
     bool columns;            // column sums wanted
 };
 
-__device__ __forceinline__ float sigmoid(float z) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896f));
-}
-
 // act(g) and its derivative
 __device__ __forceinline__ float act_of(int act, float g, float &slope) {
     if (act == FI_GATE_LINEAR) {
         slope = 1.f;
         return g;
     }
-    const float s = sigmoid(g);
+    const float t = __builtin_amdgcn_exp2f(g * -1.44269504088896f);     // e^-g
+    const float s = __builtin_amdgcn_rcpf(1.f + t);
     if (act == FI_GATE_SIGMOID) {
-        slope = s * (1.f - s);
+        // 1 - s would lose the digits of what is left of an open gate's slope
+        slope = s * (g > 0.f ? t * s : 1.f - s);
         return s;
     }
     slope = s * fmaf(g, 1.f - s, 1.f);

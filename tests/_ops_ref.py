@@ -109,10 +109,10 @@ def act(kind, g):
     """act(g) and its derivative."""
     if kind == 0:
         return g, torch.ones_like(g)
-    s = torch.sigmoid(g)
+    s, rest = torch.sigmoid(g), torch.sigmoid(-g)      # 1 - s would be 0 from g = 37 on, also in fp64
     if kind == 1:
-        return s, s * (1 - s)
-    return g * s, s * (1 + g * (1 - s))
+        return s, s * rest
+    return g * s, s * (1 + g * rest)
 
 
 def norm(o, res, gate, w1, k, w2, post, kind, eps, dr=None, da=None, back=False):

@@ -92,6 +92,15 @@ def test_zero_rows_and_no_rows():
     assert all((got[k] == 0).all() for k in ("dpost", "dscale", "dpre"))
 
 
+def test_slopes_of_open_gates():
+    """Sigmoid gates from -40 to 40: their slope s (1 - s) is right to its last digits on both sides."""
+    say("case norm wide sigmoid gates")
+    for D, dtype in ((300, F32), (2000, F32), (864, F16)):
+        v = _inputs(9, D, dtype, F32, seed=12)
+        v["gate"] = (torch.arange(9 * D).reshape(9, D) % 81 - 40.0).to(dtype)
+        _check(_run(_cuda(v), True, ops.GATE_SIGMOID), v, True, ops.GATE_SIGMOID, dtype, F32)
+
+
 def test_bad_values_stay_in_their_row():
     """A NaN or an infinity in one row leaves the others as they were."""
     say("case norm bad rows")
