@@ -600,8 +600,10 @@ fi_status fi_q4_quantize(const fi_q4_desc *desc, int w_dtype, const void *w, int
 
 /* y [rows][N] = x [rows][K] times the packed weights; rows 1 .. 16, x and y of
  * `dtype`.  fp32 inputs are multiplied in full (as three bf16 terms; below 2^-110
- * in size the last bits may be lost), 16-bit ones exactly too; sums are fp32.  A row of x with an infinity or NaN gives
- * non-finite values in its row of y only.  |x| stays below 2^120. */
+ * in size the last bits may be lost), 16-bit ones exactly too; sums are fp32.  A
+ * row of x with an infinity or NaN gives non-finite values in its row of y only.
+ * |x| stays below 2^116: then no sum within a group of 128 passes fp32's largest
+ * number, whatever the codes and zeros ((32 x 31 + 96 x 15) 2^116 < 2^128). */
 fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int dtype, const void *x, int64_t ld_x,
                        void *y, int64_t ld_y, void *stream);
 

@@ -399,7 +399,7 @@ class Q4Weight:
 
 
 def q4_matvec(w, x, y=None):
-    """y [B][N] = x [B][K] times a Q4Weight, 1 <= B <= 16 rows (fi_q4_matvec); y has x's type."""
+    """y [B][N] = x [B][K] times a Q4Weight, 1 <= B <= 16 rows (fi_q4_matvec); y has x's type, |x| < 2^116."""
     if not isinstance(w, Q4Weight):
         _bad(f"w: expected a Q4Weight, got {type(w).__name__}")
     device = _device(x, "x")

@@ -73,6 +73,29 @@ def test_full_precision_of_the_inputs():
     assert float((y - x).abs().max()) < 2.0 ** -14                    # bf16 alone would be off by 2^-8
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zero,code", [(15, 15), (15, 0), (0, 15), (None, 8), (None, 0), (8, "any")])
+def test_largest_inputs(dtype, group, zero, code):
+    """Inputs of one sign next to 2^116, the largest that are taken: within a group no partial sum
+    passes (32 x 31 + 96 x 15) 2^116 < 2^128, whatever the codes and zeros."""
+    say(f"case q4 largest inputs {dtype} group={group} zero={zero} code={code}")
+    N, K, B = 40, 300, 6
+    v = _inputs(N, K, B, group, dtype, F32, False, seed=12)
+    groups = -(-K // group)
+    v["x"] = torch.full((B, K), 2.0 ** 116 * (1 - 2.0 ** -23)).to(dtype)
+    if dtype is BF16:
+        v["x"] = torch.full((B, K), 2.0 ** 116 * (1 - 2.0 ** -8), dtype=BF16)
+    v["x"][1::2] *= -1
+    if code != "any":
+        v["codes"][:] = code
+    v["zeros"] = torch.full((N, groups), zero, dtype=torch.uint8) if zero is not None else None
+    v["scales"] = v["scales"] * 2.0 ** -30
+    want, tol = ref.q4(v["x"], v["codes"], v["scales"], v["zeros"], group)
+    y = ops.q4_matvec(_weight(v, group), v["x"].cuda())
+    assert ref.worst(y, want, ref.stored(want, tol, dtype)) <= 1.0
+
+
 def test_tiny_inputs_are_not_dropped():
     """fp16 inputs below the normal numbers, whole scales: exact.  In units of 2^-24 no sum passes
     7 groups x 32 x 200 x 15 x 8 < 2^23, and within a group 32 x 200 x 31 < 2^18."""
