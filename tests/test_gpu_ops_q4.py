@@ -73,6 +73,34 @@ def test_full_precision_of_the_inputs():
     assert float((y - x).abs().max()) < 2.0 ** -14                    # bf16 alone would be off by 2^-8
 
 
+@pytest.mark.parametrize("N,B,group", [(50, 1, 32), (70, 5, 64), (40, 9, 128), (33, 16, 32), (12400, 16, 128)])
+def test_every_bit_of_the_inputs(N, B, group):
+    """One input a group that is not zero, with all 24 significand bits, times a power of two: each of
+    its three terms is a product of at most 8 + 5 bits, so every sum is exact and y is the input, bit
+    for bit.  Two terms of 8 bits do not hold any of these inputs."""
+    say(f"case q4 every bit N={N} B={B} group={group}")
+    groups = 5
+    K = groups * group
+    gen = torch.Generator().manual_seed(N + B)
+    at = torch.arange(groups) * group + torch.randint(0, group, (groups,), generator=gen)
+    x = torch.zeros(B, K)
+    # 24 bits, the lowest of them set; sizes from 2^-20 to 2^20
+    bits = torch.randint(1 << 22, 1 << 23, (B, groups), generator=gen) * 2 + 1
+    x[:, at] = bits.float() * 2.0 ** torch.randint(-43, -3, (B, groups), generator=gen).float()
+    top = (x.view(torch.int32) & -65536).view(torch.float32)
+    rest = x - top
+    two = top + (rest.view(torch.int32) & -65536).view(torch.float32)
+    assert (two != x)[:, at].all()
+    mine = torch.arange(N) % groups
+    step = torch.tensor([1, -1, 2, -2, 4, -4, -8])[torch.arange(N) % 7]
+    codes = torch.full((N, K), 8, dtype=torch.uint8)
+    codes[torch.arange(N), at[mine]] = (8 + step).to(torch.uint8)
+    for zeros in (None, torch.full((N, groups), 8, dtype=torch.uint8)):
+        w = _weight({"codes": codes, "scales": torch.ones(N, groups), "zeros": zeros}, group)
+        y = ops.q4_matvec(w, x.cuda()).cpu()
+        assert torch.equal(y, x[:, at][:, mine] * step.float())
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("zero,code", [(15, 15), (15, 0), (0, 15), (None, 8), (None, 0), (8, "any")])
