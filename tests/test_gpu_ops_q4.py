@@ -124,6 +124,18 @@ def test_largest_inputs(dtype, group, zero, code):
     assert ref.worst(y, want, ref.stored(want, tol, dtype)) <= 1.0
 
 
+@pytest.mark.parametrize("N,K,B", [(5003, 1700, 8), (5003, 1750, 9), (9003, 1500, 16), (9003, 1500, 11), (4807, 1500, 16),
+                                   (9003, 1500, 8), (4803, 700, 6), (12270, 900, 10)])
+def test_several_rows_between_few_and_many_outputs(N, K, B):
+    """fp32 rows and 257 to 767 row tiles, where the number of waves goes down to a multiple of four
+    (ten and nine to eight, five to four) or stays as it is, by how many workgroups a CU holds."""
+    say(f"case q4 wave counts N={N} K={K} B={B}")
+    v = _inputs(N, K, B, 64, F32, BF16, B % 2 == 0, seed=13)
+    y = ops.q4_matvec(_weight(v, 64), v["x"].cuda())
+    want, tol = ref.q4(v["x"], v["codes"], v["scales"], v["zeros"], 64)
+    assert ref.worst(y, want, ref.stored(want, tol, F32)) <= 1.0
+
+
 def test_tiny_inputs_are_not_dropped():
     """fp16 inputs below the normal numbers, whole scales: exact.  In units of 2^-24 no sum passes
     7 groups x 32 x 200 x 15 x 8 < 2^23, and within a group 32 x 200 x 31 < 2^18."""
