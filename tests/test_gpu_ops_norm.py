@@ -255,6 +255,51 @@ def test_more_than_the_caches_hold(D, dtype, rt):
         assert ((got[k].double() - sums[k]).abs() <= size[k]).all(), k
 
 
+@pytest.mark.parametrize("D,dtype,rt", [(864, BF16, F32), (1001, F16, F16), (256, F32, F32), (5000, BF16, BF16),
+                                        (3000, BF16, BF16), (5001, F16, F32), (40, BF16, F32)])
+def test_no_part_of_the_column_sums_is_lost(D, dtype, rt):
+    """Column sums over many rows of terms of one sign, with the roundings of the sum's real chain:
+    no bound is wider than half of one workgroup's part, so a lost part would show in every column."""
+    N = (1 << 28) // (D * (4 if dtype is F32 else 2) * 2) + 77
+    say(f"case norm column parts N={N} D={D} {dtype}/{rt}")
+    gen = torch.Generator(device="cuda").manual_seed(D + 1)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").clamp_(-3, 3)        # noqa: E731
+    c = {"o": (1 + r(N, D) / 5).to(dtype), "gate": (1 + r(N, D) / 5).to(dtype), "res": (1 + r(N, D) / 5).to(rt),
+         "w1": 1 + r(D) / 8, "k": 0.5 + r(D) / 16, "w2": 1 + r(D) / 8, "dr": (2 + r(N, D) / 5).to(rt),
+         "da": (1 + r(N, D) / 5).to(dtype)}
+    got = _run(c, True, ops.GATE_SILU)
+    # the workspace holds two fp32 sums a column and workgroup
+    groups = ops._norm_workspace(N, D, ops._TYPES[dtype], ops._TYPES[rt]) // (8 * D)
+    # rows of a wave (or of a workgroup), its workgroup's waves, a sixteenth of the workgroups, sixteen sums
+    chain = -(-N // groups) + 4 + -(-groups // 16) + 16
+    sums = {k: torch.zeros(D, dtype=torch.float64, device="cuda") for k in ("dpost", "dscale", "dpre")}
+    size = {k: torch.zeros(D, dtype=torch.float64, device="cuda") for k in sums}
+    for i in range(0, N, -(-N // 8)):
+        part = {k: t[i:i + -(-N // 8)] if t.dim() == 2 else t for k, t in c.items()}
+        o, g, res, dr, da = (part[k].double() for k in ("o", "gate", "res", "dr", "da"))
+        w1, k1, w2 = (c[k].double() for k in ("w1", "k", "w2"))
+        mean = lambda v: v.mean(-1, keepdim=True)                       # noqa: E731
+        u = o * (mean(o * o) + EPS).rsqrt()
+        act = g * torch.sigmoid(g)
+        R = res + k1 * w1 * u * act
+        n = (mean(R * R) + EPS).rsqrt()
+        R *= n
+        big = n * (da * w2).abs() + n * R.abs() * mean((da * w2 * R).abs())
+        dR = dr + n * (da * w2 - R * mean(da * w2 * R))
+        terms = {"dpre": da * R, "dscale": dR * act * u * w1, "dpost": dR * act * u * k1}
+        # a term's factors: two reciprocal norms and a mean, each a sum of at most D / 64 values in a lane and
+        # 24 across the row, and no more than 60 + 3 |g| other roundings; dR counts for the parts it is made of
+        near = 3 * (D / 64 + 24) + 60 + 3 * g.abs()
+        parts = {"dpre": (da * R).abs(), "dscale": (dr.abs() + big) * (act * u * w1).abs(),
+                 "dpost": (dr.abs() + big) * (act * u * k1).abs()}
+        for k, t in terms.items():
+            sums[k] += t.sum(0)
+            size[k] += (t.abs() * chain + parts[k] * near).sum(0) * ref.U
+    for k in sums:
+        assert (size[k] < sums[k].abs() / (2 * groups)).all(), f"{k}: the bound says nothing"
+        assert ((got[k].double() - sums[k]).abs() <= size[k] + ref.U * sums[k].abs()).all(), k
+
+
 def test_binding_refuses_mismatches():
     say("case norm refusals")
     o = torch.zeros(4, 8, device="cuda")
