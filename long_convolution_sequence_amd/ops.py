@@ -7,7 +7,9 @@ CPU path; a mismatch raises ``FiError(FI_EINVAL)`` before anything is
 launched.  Every call runs on the current torch stream of its tensors' device,
 waits for nothing and can be captured into a graph; workspaces and outputs
 that are not given come from torch's allocator on that stream.  Gradients are
-explicit calls: nothing here records itself for autograd.
+explicit calls: nothing here records itself for autograd, and a forward call on
+tensors that require gradients warns, unless it saves what the backward call
+takes or stands under ``torch.no_grad()``.
 
 Tensors need contiguous rows at one pitch (a column slice of a wider tensor
 is fine); states, weights and ``lengths`` are densely packed.  Sequences are
@@ -17,6 +19,7 @@ from __future__ import annotations
 
 import functools
 import struct
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -122,6 +125,16 @@ def _dense(t, shape, dtype, device, name):
     _bad(f"{name}: not contiguous")
 
 
+_any_requires_grad = torch._C._any_requires_grad
+
+
+def _not_recorded(call):
+    """Warn where autograd would be expected to see a call: its outputs carry no graph."""
+    if torch.is_grad_enabled():
+        warnings.warn(f"{call}: autograd does not see this call, its outputs carry no gradients (the gradients are "
+                      f"calls of their own; torch.no_grad() silences this)", stacklevel=3)
+
+
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream      # the hipStream_t of a device's current stream
 
@@ -185,7 +198,9 @@ def gated_scan(x, gate, bias=None, state=None, lengths=None, *, input=SCAN_CONVE
     x, gate [T][B][D] of one type; bias [D], state [B][D] fp32 (the state before the first position)
     or None for zeros; lengths [B] int32 or None: rows past a sequence's length count for nothing, give
     y = 0 and leave the state.  Returns (y, final [B][D] fp32), with save=True also what
-    gated_scan_backward needs.  final may be given as the state itself."""
+    gated_scan_backward needs.  final may be given as the state itself.  Autograd does not see it."""
+    if not save and _any_requires_grad(x, gate, bias, state):
+        _not_recorded("gated_scan")
     device, shape, dtype, head, ld, args = _scan_inputs(x, gate, bias, state, lengths, input)
     if y is None:
         y = _like(x)
@@ -207,7 +222,9 @@ def gated_scan(x, gate, bias=None, state=None, lengths=None, *, input=SCAN_CONVE
 
 def gated_scan_step(x, gate, state, bias=None, lengths=None, *, input=SCAN_CONVEX, y=None):
     """One position: x, gate [B][D]; state [B][D] fp32 is updated in place.  lengths [B] int32 or None:
-    a row with 0 is an empty slot (y = 0, its state stays).  Returns y."""
+    a row with 0 is an empty slot (y = 0, its state stays).  Returns y.  Autograd does not see it."""
+    if _any_requires_grad(x, gate, state, bias):
+        _not_recorded("gated_scan_step")
     device, shape, dtype, head, ld, args = _scan_inputs(x, gate, bias, state, lengths, input, positions=False)
     if state is None:
         _bad("state: required")
@@ -290,7 +307,9 @@ def block_norm(o, res=None, gate=None, *, post_weight=None, scale=None, pre_weig
     a = r / rms(r) * pre_weight; what is None is left out.  o None: the norm before a first block
     (r = res; then a has res's type).  o, gate, a [..., D] of one type; res, r of that type or
     fp32; weights and scale fp32 [D].  r may be given as res itself.  Returns (r, a), with
-    save=True also what block_norm_backward needs."""
+    save=True also what block_norm_backward needs.  Autograd does not see it."""
+    if not save and _any_requires_grad(o, res, gate, post_weight, scale, pre_weight):
+        _not_recorded("block_norm")
     first, device, shape, dtype, rt, rows, head, args = _norm_inputs(o, res, gate, post_weight, scale, pre_weight,
                                                                      post_norm, act, eps)
     if r is None:
@@ -399,7 +418,10 @@ class Q4Weight:
 
 
 def q4_matvec(w, x, y=None):
-    """y [B][N] = x [B][K] times a Q4Weight, 1 <= B <= 16 rows (fi_q4_matvec); y has x's type, |x| < 2^116."""
+    """y [B][N] = x [B][K] times a Q4Weight, 1 <= B <= 16 rows (fi_q4_matvec); y has x's type, |x| < 2^116.
+    Autograd does not see it."""
+    if _any_requires_grad(x):
+        _not_recorded("q4_matvec")
     if not isinstance(w, Q4Weight):
         _bad(f"w: expected a Q4Weight, got {type(w).__name__}")
     device = _device(x, "x")

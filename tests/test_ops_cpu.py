@@ -1,6 +1,7 @@
 """Refusals of the recurrent-block operators, without a GPU: every bad argument
 is an error before anything is launched, at the C entries and in the binding."""
 import ctypes
+import warnings
 
 import pytest
 import torch
@@ -297,6 +298,31 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         with pytest.raises(fi.FiError) as e:
             call()
         assert e.value.status == fi.FI_EINVAL
+
+
+def test_binding_warns_where_autograd_would_be_expected():
+    """A forward call on a tensor that requires gradients says that it is not recorded (and then
+    refuses the host tensor); under no_grad, or without such a tensor, it does not."""
+    x = torch.zeros(4, 2, 8)
+    w = torch.ones(8, requires_grad=True)
+    q = object.__new__(ops.Q4Weight)
+    q._index = 0
+    calls = {"gated_scan": lambda: ops.gated_scan(x, x, w), "gated_scan_step": lambda: ops.gated_scan_step(x[0], x[0], x[0], w),
+             "block_norm": lambda: ops.block_norm(x, pre_weight=w),
+             "q4_matvec": lambda: ops.q4_matvec(q, x[0].requires_grad_())}
+    for name, call in calls.items():
+        with pytest.warns(UserWarning, match=f"{name}: autograd does not see"), pytest.raises(fi.FiError):
+            call()
+        with warnings.catch_warnings(), torch.no_grad(), pytest.raises(fi.FiError):
+            warnings.simplefilter("error")
+            call()
+    with warnings.catch_warnings(), pytest.raises(fi.FiError):
+        warnings.simplefilter("error")
+        ops.gated_scan(x, x, w.detach())
+    for call in (lambda: ops.gated_scan(x, x, w, save=True), lambda: ops.block_norm(x, pre_weight=w, save=True)):
+        with warnings.catch_warnings(), pytest.raises(fi.FiError):       # the gradients are asked for explicitly
+            warnings.simplefilter("error")
+            call()
 
 
 def test_binding_refuses_values_past_a_descriptors_fields():
