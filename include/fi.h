@@ -493,8 +493,9 @@ typedef struct fi_scan_desc {
 } fi_scan_desc;
 
 /* Bytes of the states the forward pass keeps for the backward pass (`saved`),
- * and of the workspace of either pass; 0 for a bad descriptor.  256 means that
- * the workspace is not used and may be NULL. */
+ * and of the workspace of either pass; 0 for a bad descriptor.  256 for the
+ * forward pass means that its workspace is not used and may be NULL; the
+ * backward pass needs one at every T > 0. */
 size_t fi_scan_saved_bytes(const fi_scan_desc *desc);
 size_t fi_scan_workspace_bytes(const fi_scan_desc *desc, int backward);
 
@@ -504,9 +505,12 @@ size_t fi_scan_workspace_bytes(const fi_scan_desc *desc, int backward);
  * lengths [B] int32 (device) or NULL: row b has positions t < lengths[b] (taken
  * into [0, T]); what later rows hold counts for nothing, they give y = 0 and
  * leave the state as it is.  final may be state.  T = 1 is the form for one token:
- * one launch.  Of the positions that count, an infinity or NaN in x, gate or the
- * state makes its channel's later values non-finite (from an infinity, NaN may
- * come one position on). */
+ * one launch.  Of the positions that count, an infinity or NaN in x or the state,
+ * or a NaN in gate, makes its channel's later values non-finite (from an infinity,
+ * NaN may come one position on); an infinite gate is a decay of exactly 0 or 1.
+ * A long sequence runs in tiles that hand the state on.  A tile that has waited
+ * for the one before it through 2^20 looks (about a second: the launch is not
+ * running as it should) goes on with NaN; the call has returned FI_OK by then. */
 fi_status fi_scan_forward(const fi_scan_desc *desc, const void *x, const void *gate, const float *bias,
                           const float *state, const int32_t *lengths, void *y, float *final, void *saved,
                           void *workspace, void *stream);
@@ -514,7 +518,8 @@ fi_status fi_scan_forward(const fi_scan_desc *desc, const void *x, const void *g
 /* Gradients of sum(y . dy) + sum(final . dfinal): dx, dgate [T][B][D] (0 past a
  * row's length), and where not NULL dbias [D] fp32 (summed over t and b in a
  * fixed order) and dstate [B][D] fp32.  The other arguments are those of the
- * forward call that wrote `saved`; dfinal may be NULL (zeros). */
+ * forward call that wrote `saved`; dfinal may be NULL (zeros).  Tiles wait as in
+ * the forward pass. */
 fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *gate, const float *bias,
                            const float *state, const int32_t *lengths, const void *saved, const void *dy,
                            const float *dfinal, void *dx, void *dgate, float *dbias, float *dstate,
@@ -529,8 +534,9 @@ fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *
  *     a = r / sqrt(mean(r^2) + eps) * pre_weight     the next block's input
  *
  * o NULL (then gate, scale and post_norm are too): r = res, the norm before a
- * first block.  post_weight needs post_norm.  The mean is over the row; a is formed from r before r is
- * rounded. */
+ * first block.  post_weight needs post_norm.  The mean is over the row; a
+ * row whose squares' sum passes fp32's largest number is normed to 0.  a is
+ * formed from r before r is rounded. */
 enum { FI_GATE_LINEAR = 0, FI_GATE_SIGMOID = 1, FI_GATE_SILU = 2 };
 
 typedef struct fi_norm_desc {

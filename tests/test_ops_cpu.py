@@ -106,6 +106,18 @@ def test_scan_backward_needs_its_tensors(lib, missing):
     _refused(lib, lib.fi_scan_backward(ctypes.byref(q), *_back_args(**{missing: None})), "required")
 
 
+@pytest.mark.parametrize("T,B,D", [(10, 2, 5), (200, 2, 32), (256, 1, 64), (300, 1, 1), (300, 2, 5)])
+def test_which_scans_need_a_workspace(lib, T, B, D):
+    """Forwards a workspace of 256 bytes may be left out (the call gets as far as the next check);
+    backwards none may, also where 256 bytes are all there is."""
+    q = _scan(T=T, B=B, D=D)
+    forward = lib.fi_scan_workspace_bytes(ctypes.byref(q), 0)
+    why = "aligned" if forward == 256 else "required"
+    assert (forward == 256) == (T <= 256)
+    _refused(lib, lib.fi_scan_forward(ctypes.byref(q), *_scan_args(workspace=None, bias=P + 2 * STEP + 1)), why)
+    _refused(lib, lib.fi_scan_backward(ctypes.byref(q), *_back_args(workspace=None, bias=P + 2 * STEP + 1)), "required")
+
+
 @pytest.mark.parametrize("kw", [dict(y=P + 4), dict(y=P + STEP), dict(final=P), dict(final=P + 3 * STEP + 4),
                                 dict(saved=P + 5 * STEP), dict(workspace=P + 256), dict(final=P + 5 * STEP),
                                 dict(state=P + 5 * STEP, final=P + 5 * STEP)])
