@@ -127,10 +127,10 @@ __device__ __forceinline__ float input_of(bool open, float w, float x) {
 
 // The state behind one position, and ds/dz there: the decay's part a d s_{t-1},
 // with a d = |w| - w^2 whichever w is, and the input factor's.  One reciprocal root
-// of d (2 - d) gives the energy factor and its slope -a^2 d / e (at d = 0 it is a
+// of d (2 - d) gives the energy factor (also left in e) and its slope -a^2 d / e (at d = 0 it is a
 // finite number, and both are 0).
 template <int IN>
-__device__ __forceinline__ float slope_and_move(float w, float x, float &s) {
+__device__ __forceinline__ float slope_and_move(float w, float x, float &s, float &e) {
     const bool open = is_open(w);
     const float ad = fmaf(-fabsf(w), fabsf(w), fabsf(w)), before = s;
     if (IN != FI_SCAN_ENERGY) {
@@ -139,7 +139,8 @@ __device__ __forceinline__ float slope_and_move(float w, float x, float &s) {
     }
     const float sq = energy(open, w), inv = __builtin_amdgcn_rsqf(fmaxf(sq, 0x1p-126f));
     const float a = (open ? 1.f : 0.f) + w;
-    s = moved(open, w, s, sq * inv * x);
+    e = sq * inv;
+    s = moved(open, w, s, e * x);
     return fmaf(ad, before, -(a * inv * ad) * x);
 }
 
@@ -473,6 +474,10 @@ __device__ __forceinline__ void forget(float (&v)[kStep][CH]) {
 template <typename V, int IN, int CH, bool FAR>
 __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_back(ScanArgs p) {
     constexpr int COLS = kRow * CH;
+    // the energy factors take the place of x, where they fit it and the last phase
+    // need not form them again (7390 x 3 x 768 training 100 -> 96 us; in registers of
+    // their own, with 16-bit values, they spill: 32768 x 4 x 768 bf16 368 -> 388)
+    constexpr bool FACTORS = IN == FI_SCAN_ENERGY && sizeof(V) == 4;
     __shared__ float mul[kWaves][COLS];          // the waves' A; then their sums of dz
     __shared__ float fwd[kWaves][COLS];          // S; then the states before the waves' positions
     __shared__ float rev[kWaves][COLS];          // S from the end; then c behind the waves' positions
@@ -608,7 +613,11 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
     for (int e = 0; e < CH; ++e) {
         float b = fmaf(Ab[e], fwd[wave][g * CH + e], Sb[e]);
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) slope[k][e] = slope_and_move<IN>(w[k][e], (float)xx[k][e], b);
+        for (int k = 0; k < kStep; ++k) {
+            float factor = 0.f;
+            slope[k][e] = slope_and_move<IN>(w[k][e], (float)xx[k][e], b, factor);
+            if constexpr (FACTORS) xx[k][e] = factor;
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
@@ -628,7 +637,7 @@ __global__ void __launch_bounds__(kWaves * 64, sizeof(V) == 2 ? 4 : 2) k_scan_ba
             b = decayed(open, w[k][e], G);
             slope[k][e] *= G;
             sum[e] += slope[k][e];     // 0 past the row's length: d = x = 0 there
-            w[k][e] = input_of<IN>(open, w[k][e], G);
+            w[k][e] = FACTORS ? (float)xx[k][e] * G : input_of<IN>(open, w[k][e], G);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
