@@ -178,7 +178,7 @@ __device__ __forceinline__ float rnorm(float squares, const NormArgs &p) {
 }
 
 // Forward: HBM-bound, every tensor once (131072 x 864 bf16 with fp32 rows 292 us, 5.4
-// TB/s; 1999 x 5001 fp16 31 us, 2.6: few rows, a barrier in each).  A team of several waves reads its next
+// TB/s; 1999 x 5001 fp16 29 us, 2.8: few rows, a barrier in each).  A team of several waves reads its next
 // row before it works on this one: a barrier a row holds all its waves, and few
 // such teams fit a CU.  ALL: o, gate and res are there.  STREAM: the inputs are
 // larger than the last-level cache (see launch).
@@ -230,10 +230,13 @@ __global__ void __launch_bounds__(THREADS) k_norm(NormArgs p) {
 }
 
 // Backward: every tensor of the row once (131072 x 768 bf16 with fp32 rows 400 us, 5.5
-// TB/s; 1999 x 5001 fp16 43 us), two row means, one after the other;
+// TB/s; 1999 x 5001 fp16 38 us), two row means, one after the other;
 // the column sums of a team's rows in registers, its workgroup's joined in LDS
 // (team after team, so the order is fixed) and written once.  Elements that a
-// lane does not own have weights of zero, so both means pass them by.
+// lane does not own have weights of zero, so both means pass them by.  Rows of more
+// than 8192 values: 16 waves leave a lane 128 registers, 105 to 124 values of it
+// spill, and that bounds it (2048 x 16384 bf16 with fp32 rows 409 us, 148 by its
+// bytes; 2048 x 12288 338 and 111).
 template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, bool STREAM, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == kNormHalf ? 3 : THREADS <= 512 ? 2 : 1) k_norm_back(NormArgs p) {
     constexpr int N = CH * NC;
@@ -379,11 +382,12 @@ int team_waves(int D) { return (D + 64 * kNormLane - 1) / (64 * kNormLane); }
 // 217 -> 206; below, 13333 x 3000 fp16 195 -> 251, 20000 x 4096 bf16 387 -> 427.
 bool half_lanes(int D) { return D > 4096 && D <= 6144; }
 
-// Workgroups: as many as are resident together (their registers allow 16 waves a
-// CU forwards, and backwards 8, 16 or 24 with 16, 8 or 4 values a lane, 12 with
-// half_lanes), so that a team runs through its rows without a second round of
-// workgroups, and the backward pass has few column sums; the rows are spread
-// evenly.  Training over rows of 5001 at 16 values a lane in 512 workgroups instead
+// Workgroups: as many as are resident together (16 waves a CU forwards, and
+// backwards 8, 16 or 24 with 16, 8 or 4 values a lane, 12 with half_lanes), so that
+// a team runs through its rows without a second round of workgroups, and the
+// backward pass has few column sums; the rows are spread evenly.  One kind is not
+// resident as counted: forwards over fp32 rows of 1025 to 8192 values the registers
+// (132 to 158) allow 12 waves, and what is left of the 16 begins as the others end.  Training over rows of 5001 at 16 values a lane in 512 workgroups instead
 // of 256: 99 us against 90; of 256 in 512 instead of
 // 1024: 200 against 185.  Forwards one wave a row takes twice as many (310 us
 // against 316).

@@ -411,7 +411,10 @@ int q4_waves(int groups, int kt, int rt, int most) {
 // With several column tiles a CU has registers for sixteen waves and LDS for few: a
 // count that leaves part of either unused, and workgroups for a second round, goes
 // down to the multiple of four with which more of them fit (7357 x 15788 of 8 fp32
-// rows nine waves 43 us, eight 33; 9000 x 9000 of 16 five 54, four 44).
+// rows nine waves 43 us, eight 33; 9000 x 9000 of 16 five 54, four 44).  What bounds
+// them then: the products, three terms' and the zeros' (13 and 9 us by the bytes);
+// with fp32 scales in groups of 32 or 64 and three column tiles 6 or 2 registers
+// spill besides.
 int q4_fitting(int waves, int groups, int step) {
     const auto on_cu = [&](int w) { return std::min(16 / w, 160 * 1024 / (w * step)); };
     if (groups <= 256 * on_cu(waves)) return waves;

@@ -29,18 +29,20 @@
 // (s <- A s + S, tile after tile), so results do not depend on timing.
 //
 // What bounds it: the memory's bytes where there are many columns.  Forward
-// 32768 x 4 x 768 bf16 129 us (4.7 TB/s of the 5.0 that a copy reaches, x and gate
-// read, y written, all once), 8192 x 8 x 768 fp32 padded 85 us (4.8); 131072 x 864
-// bf16 158 us (4.3): rows of 1728 bytes begin in the middle of a 128-byte line
-// every other time, and two tiles fetch it (1.37 times the bytes through the L2).
-// Backward, 32768 x 4 x 768 bf16, 228 us (4.4).  Few columns: the chain of tiles
-// (see kNear).  One time step after the other, four columns a lane, took 315 us
-// where this takes 85 (padded), 514 for 158.
+// 32768 x 4 x 768 bf16 128 us at least and 138 in the mean (4.7 and 4.4 TB/s of the
+// 5.0 that a copy reaches, x and gate read, y written, all once), 8192 x 8 x 768 fp32
+// padded 86 us; 131072 x 864 bf16 161 us (4.2): rows of 1728 bytes begin in the
+// middle of a 128-byte line every other time, and two tiles fetch it (1.39 times the
+// bytes through the L2).  Backward, 32768 x 4 x 768 bf16, 246 us at least and 261 in
+// the mean (4.1 and 3.9): the vector ALU, about 70 operations a value, some of
+// them roots and exponentials.  Few columns: the chain of tiles (see kNear).  One
+// time step after the other, four columns a lane, took 315 us where this took 85
+// (padded), 514 for 158.
 //
 // A tile of 256 x 64: 128-byte pieces of 16-bit rows, two tiles of eight waves on a
-// CU at 128 registers.  128 columns took 186 us where this took 170, 256 columns
-// 274; four waves 206, twelve 177, sixteen 200.  All waves looking back at 32
-// tiles together: 210.
+// CU at 128 registers (backwards over fp32 values one, at up to 159).  128 columns
+// took 186 us where this took 170, 256 columns 274; four waves 206, twelve 177,
+// sixteen 200.  All waves looking back at 32 tiles together: 210.
 #include <type_traits>
 
 #include "fi_ops.h"
