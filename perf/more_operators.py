@@ -348,7 +348,8 @@ def _plain_layer(s, c):
 
 def _plain_q8(s, c):
     x = s["x"].float()
-    scale = x.abs().amax(-1, keepdim=True) / 127
+    # a quotient by a tensor: by a number, torch multiplies by its rounded reciprocal
+    scale = x.abs().amax(-1, keepdim=True) / torch.full((), 127.0, device=x.device)
     codes = torch.round(torch.where(scale > 0, x / scale, 0.0))
     y = (codes @ s["codes"].float().t()) * scale * s["scales"]
     if s["bias"] is not None:
@@ -460,7 +461,8 @@ def _exact_layer(s, c):
 def _exact_q8(s, c):
     """Output by output in groups; scales and codes are by definition those of a quotient in 32 bits."""
     x = s["x"].float()
-    scale = x.abs().amax(-1, keepdim=True).div(127)
+    scale = x.abs().amax(-1, keepdim=True)
+    scale = scale.div(torch.full_like(scale, 127.0))
     codes = x.div(scale).nan_to_num(0.0).round().double()
     scale = scale.double()
     y = torch.empty((c["rows"], c["N"]), dtype=torch.float64, device=x.device)
