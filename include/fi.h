@@ -525,6 +525,60 @@ fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *
                            const float *dfinal, void *dx, void *dgate, float *dbias, float *dstate,
                            void *workspace, void *stream);
 
+/* The gated delta rule: a recurrence whose state is a matrix S [dk][dv], per batch
+ * row and head:
+ *
+ *     S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,  a_t = e^decay_t,
+ *     y_t = scale S_t^T q_t
+ *
+ * with the write strength b = beta (0 .. 1, or to 2 for a map with negative
+ * eigenvalues).  With `unit`, k and q are divided by their lengths first: k /
+ * sqrt(sum k^2 + 10^-6); without, keys of about length one are the caller's (a map
+ * of norm over one grows without end).  Groups of heads / key_heads heads share a
+ * query and key head: head h takes the key head h / (heads / key_heads). */
+typedef struct fi_delta_desc {
+    int64_t T;             /* positions, 0 .. 2^23 */
+    int batch;             /* B >= 1 */
+    int key_heads, heads;  /* HK, H >= 1, H a multiple of HK, B H <= 2^20 */
+    int dk, dv;            /* 1 .. 128, 1 .. 1024 */
+    int dtype;             /* of q, k, v, y and their gradients */
+    int unit;              /* 0 or 1 */
+    float scale;
+    int64_t ld_q, ld_k, ld_v, ld_decay, ld_beta, ld_y;   /* row pitches, elements; 0 = a row's own length */
+    int64_t ld_dy, ld_dq, ld_dk, ld_dv, ld_ddecay, ld_dbeta;
+    int reserved[4];       /* must be zero */
+} fi_delta_desc;
+
+/* Bytes of what the forward pass keeps for the backward pass (`saved`), and of the
+ * workspace of either pass; 0 for a bad descriptor.  A forward call of up to 8
+ * positions that saves nothing uses no workspace (it may be NULL). */
+size_t fi_delta_saved_bytes(const fi_delta_desc *desc);
+size_t fi_delta_workspace_bytes(const fi_delta_desc *desc, int backward);
+
+/* q, k [T][B][HK][dk], v [T][B][H][dv], decay and beta [T][B][H] fp32; state
+ * [B][H][dk][dv] fp32, the state before the first position, or NULL (zeros);
+ * lengths as in fi_scan_forward.  y [T][B][H][dv] (0 past a row's length) and,
+ * where not NULL, final [B][H][dk][dv] fp32 (it may be state) and saved.
+ * A decay of -infinity (any below -10^4) forgets everything before its position.
+ * Products of the state are of fp32 quality (three bf16 terms a factor), what only
+ * a 16-bit y is made of in two terms (2^-17 of it).  Values, sums of squares and
+ * products of keys and queries stay below 2^127.  An infinity or NaN at a position
+ * that counts makes its head's values non-finite from the start of its chunk on (64
+ * positions, 32 for FI_F16 and FI_F32); other heads and rows are as without it. */
+fi_status fi_delta_forward(const fi_delta_desc *desc, const void *q, const void *k, const void *v, const float *decay,
+                           const float *beta, const float *state, const int32_t *lengths, void *y, float *final,
+                           void *saved, void *workspace, void *stream);
+
+/* Gradients of sum(y . dy) + sum(final . dfinal): dq, dk, dv per row (dq and dk
+ * summed over the heads that share them), ddecay and dbeta [T][B][H] fp32, all 0
+ * past a row's length, and where not NULL dstate [B][H][dk][dv] fp32.  The other
+ * arguments are those of the forward call that wrote `saved`; dfinal may be NULL
+ * (zeros). */
+fi_status fi_delta_backward(const fi_delta_desc *desc, const void *q, const void *k, const void *v, const float *decay,
+                            const float *beta, const float *state, const int32_t *lengths, const void *saved,
+                            const void *dy, const float *dfinal, void *dq, void *dk, void *dv, float *ddecay,
+                            float *dbeta, float *dstate, void *workspace, void *stream);
+
 /* The norms around a block, with the block's gate, residual and residual scale,
  * per row of `channels` values (each factor that is NULL is left out):
  *
@@ -572,6 +626,46 @@ fi_status fi_norm_backward(const fi_norm_desc *desc, const void *o, const void *
                            const void *dr, const void *da, void *d_o, void *dgate, void *dres, float *dpost,
                            float *dscale, float *dpre, void *workspace, void *stream);
 
+/* The layer norm with a residual, per row of `channels` values:
+ *
+ *     r = res + x
+ *     a = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) * weight + bias
+ *
+ * x or res may be NULL (not both: r is the other; with x NULL, a is of dtype and
+ * res of res_dtype, so an fp32 stream is normed into 16 bits), weight and bias
+ * too (1 and 0).  The means are over the row.  A row whose deviations' squares
+ * pass fp32's largest number is normed to 0, one whose sum does gives NaN; the
+ * other rows are as they would be without it.  a is formed from r before r is
+ * rounded. */
+typedef struct fi_layer_desc {
+    int64_t rows;          /* >= 0 */
+    int channels;          /* 1 .. 16384 */
+    int dtype;             /* of x, a and their gradients */
+    int res_dtype;         /* of res, r and their gradients: dtype or FI_F32 */
+    float eps;             /* >= 0 */
+    int64_t ld_x, ld_res, ld_r, ld_a;            /* row pitches, elements; 0 = channels */
+    int64_t ld_dr, ld_da, ld_dx, ld_dres;
+    int reserved[4];       /* must be zero */
+} fi_layer_desc;
+
+/* Workspace of fi_layer_backward; 0 for a bad descriptor. */
+size_t fi_layer_workspace_bytes(const fi_layer_desc *desc);
+
+/* r and a (either may be NULL), and where not NULL saved [2][rows] fp32 (mean
+ * and reciprocal deviation, for the backward pass).  weight and bias are fp32
+ * [channels].  r may be res itself (same pointer and pitch). */
+fi_status fi_layer_forward(const fi_layer_desc *desc, const void *x, const void *res, const float *weight,
+                           const float *bias, void *r, void *a, float *saved, void *stream);
+
+/* Gradients of sum(r . dr) + sum(a . da) (dr or da may be NULL: zeros): where
+ * not NULL dx and dres per row (the same values, each in its type) and dweight,
+ * dbias fp32 [channels] (summed over the rows in a fixed order; they need da).
+ * The other arguments are those of the forward call that wrote `saved`.  dres may
+ * be dr itself. */
+fi_status fi_layer_backward(const fi_layer_desc *desc, const void *x, const void *res, const float *weight,
+                            const float *saved, const void *dr, const void *da, void *dx, void *dres, float *dweight,
+                            float *dbias, void *workspace, void *stream);
+
 /* Matrix-vector products with 4-bit weights and group scales, for the block's
  * projections on the few rows of one position:
  *
@@ -612,6 +706,36 @@ fi_status fi_q4_quantize(const fi_q4_desc *desc, int w_dtype, const void *w, int
  * number, whatever the codes and zeros ((32 x 31 + 96 x 15) 2^116 < 2^128). */
 fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int dtype, const void *x, int64_t ld_x,
                        void *y, int64_t ld_y, void *stream);
+
+/* Products in 8-bit integers with a scale a row and a scale an output, for the
+ * block's projections on any number of rows:
+ *
+ *     y[m][n] = sa[m] sw[n] sum_k a[m][k] w[n][k] + bias[n]
+ *
+ * Weights [N][K] and activations [rows][K] are kept alike: codes -128 .. 127 in
+ * the order of the matrix instructions and an fp32 scale a row, laid out from
+ * codes and scales (fi_q8_pack) or from values (fi_q8_quantize).  rows and N are
+ * up to 2^24, K up to 131071 (the sums are whole numbers of 32 bits and exact),
+ * rows * N up to 2^42. */
+
+/* Device bytes of a packed matrix (256-byte aligned); 0 for a bad size. */
+size_t fi_q8_bytes(int64_t rows, int K);
+
+/* codes [rows][K] int8 and scales [rows] fp32, device memory, densely packed. */
+fi_status fi_q8_pack(int64_t rows, int K, const int8_t *codes, const float *scales, void *packed, void *stream);
+
+/* From values x [rows][K] of dtype (row pitch ld_x elements, 0 = K): scale =
+ * max|x| of the row / 127 and code = x / scale rounded to nearest even, both
+ * quotients in fp32.  A row whose scale rounds to zero gets codes 0; one with an
+ * infinity or NaN gets a scale of NaN and gives NaN in its outputs only.  Below a
+ * largest |x| of 2^-119 the scale is no normal number and has lost digits. */
+fi_status fi_q8_quantize(int64_t rows, int K, int dtype, const void *x, int64_t ld_x, void *packed, void *stream);
+
+/* y [rows][N] of dtype (row pitch ld_y elements, 0 = N); bias [N] fp32 or NULL.
+ * The whole sum is rounded to fp32, multiplied by both scales and rounded once
+ * more when it is stored. */
+fi_status fi_q8_product(int64_t rows, int64_t N, int K, const void *a, const void *w, const float *bias, int dtype,
+                        void *y, int64_t ld_y, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,444 @@
+// The gated delta rule: what its kernels share.  Per head, with decays a = e^g:
+//   S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,  y_t = scale S_t^T q_t.
+// A chunk of C positions at once: with G the sum of g from the chunk's start,
+// E_ij = e^(G_i - G_j) and S the state before the chunk,
+//   (I + A) w = v - e^G K S,  A_ij = E_ij (k_i . k_j) b_j (i > j),
+//   y = scale (e^G Q S + (E o Q K^T)(b w)),  S' = e^(G_C) S + sum_j e^(G_C - G_j) k_j (b_j w_j)^T.
+// Only S passes from chunk to chunk, and its columns do not meet: a wave runs 32
+// columns of a head along the sequence, with S in the accumulators of the matrix
+// instruction v_mfma_f32_32x32x16_bf16.
+//
+// Operands.  The instruction's left operand is kept in LDS or memory as an image: a
+// piece of 32 rows x 16 values of the summed index is 1 KB, lane l's 16 bytes are the
+// values 8 (j / 4) + 4 (l / 32) + j % 4, j < 8, of row l % 32.  In that order of the
+// summed index an accumulator (lane l: rows 8 (r / 4) + 4 (l / 32) + r % 4 of column
+// l % 32) is a right operand as it stands, registers 8 s .. 8 s + 7 its step s: what
+// one product gives goes into the next without leaving the lane.
+//
+// Values in 32 bits are multiplied as terms of bf16 (x = t0 + t1 + t2, each the
+// rounding of what is left, exact to 2^-24): of two factors the products of terms i
+// and j with i + j <= 2 are taken (<= 1 where the result is rounded to 16 bits and
+// nothing else is made of it: 2^-17 there).  bf16 inputs are one term, fp16 two, fp32 three.
+#pragma once
+#include "fi_ops.h"
+
+namespace fi {
+
+namespace {
+
+constexpr int kDeltaMaxK = 128;        // channels of a key at most
+constexpr int kDeltaMaxV = 1024;       // of a value
+constexpr float kDeltaUnit = 1e-6f;    // k / sqrt(sum k^2 + this)
+constexpr int kPiece = 1024;           // bytes of an operand's piece
+constexpr float kLog2e = 1.44269504088896f;
+
+using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+using bf16x4 = __bf16 __attribute__((ext_vector_type(4)));
+using f32x16 = float __attribute__((ext_vector_type(16)));
+
+// Terms of an input, positions of a chunk and terms of what only y is made of.
+// Chunks of fp16 and fp32 are 32 long: the images of two and three terms of 64
+// positions leave a CU one workgroup or none.
+template <typename T>
+struct DeltaType;
+template <>
+struct DeltaType<bf16_t> {
+    static constexpr int terms = 1, chunk = 64, out = 2;
+};
+template <>
+struct DeltaType<f16_t> {
+    static constexpr int terms = 2, chunk = 32, out = 2;
+};
+template <>
+struct DeltaType<float> {
+    static constexpr int terms = 3, chunk = 32, out = 3;
+};
+inline int delta_chunk(int dtype) { return dtype == FI_BF16 ? 64 : 32; }
+
+struct DeltaArgs {
+    const void *q, *k, *v, *dy;
+    void *y, *dq, *dk_out, *dv_out;
+    const float *g, *beta, *state, *dfinal;
+    float *final, *dstate, *dg, *dbeta;
+    const int32_t *lengths;
+    int64_t T, chunks, per;                // positions, chunks, chunks of a segment
+    int64_t ldq, ldk, ldv, ldg, ldb, ldy, lddy, lddq, lddk, lddv, lddg, lddb;
+    int B, HK, H, dk, dv, segments;
+    int unit;
+    float scale;
+    // [chunk][B][H] of each
+    char *images;                          // M and P of a chunk (backwards N^T and P^T)
+    float *factors;                        // [5][C]
+    float *states;                         // [dk][dv] before each chunk, and [B][H] of them after the last
+    float *ends;                           // backwards [dk][dv] after each chunk
+    float *w, *x;                          // [C][dv]
+    // [segment][B][H]
+    float *local;                          // [dk][dv] what a segment makes of nothing
+    float *maps;                           // [dk][dk] what it makes of a state
+    float *starts;                         // [dk][dv] the state before it (backwards: the gradient behind it)
+};
+
+// ---- operands ------------------------------------------------------------------
+
+template <int N>
+struct Frag {
+    bf16x8 t[N];
+};
+
+// Terms of eight values.
+template <int N>
+__device__ __forceinline__ Frag<N> split(const float (&x)[8]) {
+    Frag<N> f;
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f.t[t][i] = (__bf16)r[i];
+        if (t + 1 < N) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] -= (float)f.t[t][i];
+        }
+    }
+    return f;
+}
+
+// Step `s` (16 rows) of an accumulator as a right operand.
+template <int N>
+__device__ __forceinline__ Frag<N> step_of(const f32x16 &v, int s) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[s * 8 + i];
+    return split<N>(x);
+}
+
+// acc += a b, the products of terms i and j with i + j <= ORDER.
+template <int ORDER, int NA, int NB>
+__device__ __forceinline__ void multiply(f32x16 &acc, const Frag<NA> &a, const Frag<NB> &b) {
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = NB - 1; j >= 0; --j)
+            if (i + j <= ORDER) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[i], b.t[j], acc, 0, 0, 0);
+}
+
+// An image's piece as an operand; terms are `stride` bytes apart.
+template <int N>
+__device__ __forceinline__ Frag<N> piece(const char *image, int at, int stride) {
+    Frag<N> f;
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+        f.t[t] = *reinterpret_cast<const bf16x8 *>(image + t * stride + at * kPiece + (threadIdx.x & 63) * 16);
+    return f;
+}
+
+// Byte of value `k` of row `row` in an image with `steps` pieces along the summed
+// index; four values from a multiple of four on are neighbours.
+__device__ __forceinline__ int image_at(int row, int k, int steps) {
+    return ((row >> 5) * steps + (k >> 4)) * kPiece + (((k >> 2) & 1) * 32 + (row & 31)) * 16 + ((k >> 3) & 1) * 8;
+}
+
+template <int N>
+__device__ __forceinline__ void put_terms(char *image, int at, int stride, const float (&x)[4]) {
+    float r[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        bf16x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (__bf16)r[i];
+        *reinterpret_cast<bf16x4 *>(image + t * stride + at) = v;
+        if (t + 1 < N) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] -= (float)v[i];
+        }
+    }
+}
+
+// Row of register r of an accumulator, for the lane's half.
+__device__ __forceinline__ int acc_row(int r) { return 8 * (r >> 2) + 4 * ((threadIdx.x >> 5) & 1) + (r & 3); }
+
+// Four values of a row from d on, zeros behind D and where the row does not count.
+template <typename T>
+__device__ __forceinline__ void load4(float (&x)[4], const T *row, int d, int D, bool live) {
+    if (live && d + 4 <= D) {
+        const Chunk<T, 4> v = *reinterpret_cast<const Chunk<T, 4> *>(row + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (float)v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = live && d + i < D ? (float)row[d + i] : 0.f;
+    }
+}
+
+// C rows of a tensor as images: `rows` with the channels as the summed index,
+// `cols` (the transpose) with the positions; either may be null.  Rows from `live`
+// on are zeros.  A thread takes four rows of four channels.
+template <typename T, int C>
+__device__ __forceinline__ void stage(const T *x, int64_t pitch, int D, int padded, int live, char *rows, char *cols) {
+    constexpr int N = DeltaType<T>::terms;
+    const int runs = padded / 4, rstep = padded / 16, image = C * padded * 2;
+    for (int u = threadIdx.x; u < C / 4 * runs; u += blockDim.x) {
+        const int i = u / runs * 4, d = (u - u / runs * runs) * 4;
+        float m[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) load4(m[r], x + (i + r) * pitch, d, D, i + r < live);
+        if (rows) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) put_terms<N>(rows, image_at(i + r, d, rstep), image, m[r]);
+        }
+        if (cols) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float t[4] = {m[0][c], m[1][c], m[2][c], m[3][c]};
+                put_terms<N>(cols, image_at(d + c, i, C / 16), image, t);
+            }
+        }
+    }
+}
+
+// Bytes from memory into LDS, 16 a thread and turn.
+__device__ __forceinline__ void copy_in(char *to, const char *from, int bytes) {
+    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+        *reinterpret_cast<float4 *>(to + i) = *reinterpret_cast<const float4 *>(from + i);
+}
+
+__device__ __forceinline__ int64_t delta_length(const DeltaArgs &p, int b) {
+    if (!p.lengths) return p.T;
+    const int64_t n = p.lengths[b];
+    return n < 0 ? 0 : n < p.T ? n : p.T;
+}
+
+__device__ __forceinline__ f32x16 zeros16() {
+    f32x16 v;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    return v;
+}
+
+// ---- a chunk's own matrices ----------------------------------------------------
+
+// Sum over a wave's lanes of the same half-position (lanes l and l ^ 32).
+__device__ __forceinline__ float both_halves(float v) { return v + __shfl_xor(v, 32, 64); }
+
+template <typename T, bool BACK>
+constexpr int image_bytes() {          // of a chunk: M in three terms and P
+    constexpr int C = DeltaType<T>::chunk;
+    return C * C * 2 * (3 + (BACK ? 3 : DeltaType<T>::out));
+}
+
+// A wave a chunk and head.  Forwards the images of M = (I + A)^-1 and of
+// P_ij = scale E_ij (q_i . k_j) b_j, and the factors e^G_i of k_i S, scale e^G_i of
+// q_i S, e^(G_C - G_i) b_i of k_i, e^(G_C).  Backwards those of N^T, N = (I + A')^-1
+// with A'_ij = b_i E_ij (k_i . k_j), and of P^T without the b_j, and e^(G_C - G_i),
+// scale e^G_i, e^G_i b_i, b_i, e^(G_C).  "unit" divides k and q by their lengths in
+// these factors, so the operands stay the inputs themselves.
+// The inverse: lane j solves for column j, row by row from registers, the rows of A
+// read from LDS for all lanes at once.
+template <typename T, int KT, bool BACK>
+__global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, MT = C / 32, CS = C / 16, KS = KT * 2, LD = C + 4;
+    constexpr int PT = BACK ? 3 : DeltaType<T>::out;
+    __shared__ __align__(16) float m[C * LD];
+    __shared__ double sum[C];
+    __shared__ float fb[C], fk[C], fq[C];
+    const int lane = threadIdx.x, half = lane >> 5, col = lane & 31;
+    const int64_t at = blockIdx.x;                       // [chunk][B][H]
+    const int h = (int)(at % p.H), b = (int)(at / p.H % p.B), hk = h / (p.H / p.HK);
+    const int64_t t0 = at / p.H / p.B * C, n = delta_length(p, b) - t0;
+    if (n <= 0) return;
+    const int live = n < C ? (int)n : C;
+
+    // decays, in 64 bits: differences of sums keep their digits next to a large one
+    if (lane < C) {
+        const int64_t row = (t0 + lane) * p.B + b;
+        float g = 0.f, beta = 0.f;
+        if (lane < live) {
+            g = p.g[row * p.ldg + h];
+            beta = p.beta[row * p.ldb + h];
+        }
+        g = g < -1e4f ? -1e4f : g;                       // e^-10^4 is 0 in any case, -inf would be NaN in differences
+        double s = (double)g * 1.4426950408889634;
+#pragma unroll
+        for (int d = 1; d < C; d *= 2) {
+            const double o = __shfl_up(s, d, 64);
+            if (lane >= d) s += o;
+        }
+        sum[lane] = s;
+        fb[lane] = beta;
+    }
+    // k and q as operands, straight from memory
+    Frag<N> fk_[MT][KS];
+    float ssk[MT], ssq[MT];
+    const T *k = static_cast<const T *>(p.k) + hk * p.dk, *q = static_cast<const T *>(p.q) + hk * p.dk;
+    const auto fetch = [&](const T *from, int64_t ld, int mt, int ks, float &ss) {
+        const int i = mt * 32 + col;
+        const T *row = from + ((t0 + i) * p.B + b) * ld;
+        float x[8], y[4], z[4];
+        load4(y, row, ks * 16 + 4 * half, p.dk, i < live);
+        load4(z, row, ks * 16 + 4 * half + 8, p.dk, i < live);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = y[j], x[4 + j] = z[j];
+            ss = fmaf(y[j], y[j], ss);
+            ss = fmaf(z[j], z[j], ss);
+        }
+        return split<N>(x);
+    };
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        ssk[mt] = ssq[mt] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) fk_[mt][ks] = fetch(k, p.ldk, mt, ks, ssk[mt]);
+    }
+    f32x16 kk[MT][MT], qk[MT][MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) kk[i][j] = qk[i][j] = zeros16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const Frag<N> fq_ = fetch(q, p.ldq, i, ks, ssq[i]);
+#pragma unroll
+            for (int j = 0; j <= i; ++j) {
+                multiply<2>(kk[i][j], fk_[i][ks], fk_[j][ks]);
+                multiply<2>(qk[i][j], fq_, fk_[j][ks]);
+            }
+        }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const float a = both_halves(ssk[mt]), c = both_halves(ssq[mt]);
+        if (half == 0) {
+            fk[mt * 32 + col] = p.unit ? 1.f / sqrtf(a + kDeltaUnit) : 1.f;
+            fq[mt * 32 + col] = p.scale * (p.unit ? 1.f / sqrtf(c + kDeltaUnit) : 1.f);
+        }
+    }
+    __syncthreads();
+
+    // A in rows
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = i * 32 + acc_row(r), c = j * 32 + col;
+                float a = 0.f, e = 0.f;
+                if (j <= i && row >= c) {
+                    e = exp2f((float)(sum[row] - sum[c])) * fk[c];
+                    if (row > c) a = e * fk[row] * fb[BACK ? row : c] * kk[i][j <= i ? j : 0][r];
+                    e *= fq[row] * (BACK ? 1.f : fb[c]);
+                }
+                m[row * LD + c] = a;
+                if (j <= i) qk[i][j <= i ? j : 0][r] *= e;       // P
+            }
+    __syncthreads();
+    float x[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        float s0 = lane == i ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int j = 0; j < i; j += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(m + i * LD + j);
+            s0 = fmaf(-a.x, x[j], s0);
+            if (j + 1 < i) s1 = fmaf(-a.y, x[j + 1], s1);
+            if (j + 2 < i) s2 = fmaf(-a.z, x[j + 2], s2);
+            if (j + 3 < i) s3 = fmaf(-a.w, x[j + 3], s3);
+        }
+        x[i] = (s0 + s1) + (s2 + s3);
+        asm volatile("" ::: "memory");                   // the rows' loads stay in order: ahead of it they would spill
+    }
+    __syncthreads();
+    const auto flush = [&](char *image, auto terms) {      // m (or its transpose) as an image
+        constexpr int NT = decltype(terms)::value;
+        for (int mt = 0; mt < MT; ++mt)
+            for (int cs = 0; cs < CS; ++cs) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = mt * 32 + col, c = cs * 16 + 8 * (j >> 2) + 4 * half + (j & 3);
+                    v[j] = BACK ? m[c * LD + r] : m[r * LD + c];
+                }
+                const Frag<NT> f = split<NT>(v);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    *reinterpret_cast<bf16x8 *>(image + t * C * C * 2 + (mt * CS + cs) * kPiece + lane * 16) = f.t[t];
+            }
+    };
+    char *image = p.images + at * image_bytes<T, BACK>();
+    if (lane < C) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) m[i * LD + lane] = x[i];
+    }
+    __syncthreads();
+    flush(image, std::integral_constant<int, 3>());
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) m[(i * 32 + acc_row(r)) * LD + j * 32 + col] = j <= i ? qk[i][j <= i ? j : 0][r] : 0.f;
+    __syncthreads();
+    flush(image + 3 * C * C * 2, std::integral_constant<int, PT>());
+    if (lane < C) {
+        float *f = p.factors + at * 5 * C;
+        const float rise = exp2f((float)sum[lane]), fall = exp2f((float)(sum[C - 1] - sum[lane]));
+        f[lane] = fk[lane] * (BACK ? fall : rise);
+        f[C + lane] = fq[lane] * rise;
+        f[2 * C + lane] = fk[lane] * (BACK ? rise : fall) * fb[lane];
+        f[3 * C + lane] = fb[lane];
+        f[4 * C + lane] = exp2f((float)sum[C - 1]);
+    }
+}
+
+// ---- host side -----------------------------------------------------------------
+
+constexpr int kDeltaSIMDs = 1024;      // waves that run side by side
+
+struct DeltaPlan {
+    int C, KT;
+    int64_t chunks, per;               // chunks of the sequence, of a segment
+    int segments;
+    size_t images, factors, states, ends, rows, local, maps;   // bytes, each a multiple of 256
+};
+
+// Segments: a wave runs 32 columns of a head along the sequence; where that leaves
+// most of the card idle, the sequence is cut into as many segments as fill it, each
+// run once from nothing (with the columns of the state's own map, dk of them, beside
+// it), joined, and run again from what is before it.  That is 2.4 times the work, so
+// it takes eight segments at least to be worth it, and eight chunks a segment.
+inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
+    DeltaPlan d = {};
+    d.C = delta_chunk(q->dtype);
+    d.KT = (q->dk + 31) / 32;
+    d.chunks = (q->T + d.C - 1) / d.C;
+    const int64_t heads = (int64_t)q->batch * q->heads, waves = heads * ((q->dv + 31) / 32);
+    int64_t want = std::min<int64_t>(kDeltaSIMDs / std::max<int64_t>(1, waves), d.chunks / 8);
+    if (want < 4) want = 1;
+    d.per = std::max<int64_t>(1, (d.chunks + want - 1) / want);
+    d.segments = (int)std::max<int64_t>(1, (d.chunks + d.per - 1) / d.per);
+    const size_t all = (size_t)d.chunks * heads, C = d.C, sk = (size_t)q->dk * q->dv * 4;
+    const size_t out = backward || q->dtype == FI_F32 ? 3 : 2;
+    d.images = up256(all * C * C * 2 * (3 + out));
+    d.factors = up256(all * 5 * C * 4);
+    d.states = up256(all * sk);
+    d.ends = up256(all * sk);
+    d.rows = up256(all * C * q->dv * 4);
+    const size_t parts = d.segments > 1 ? (size_t)d.segments * heads : 0;
+    d.local = up256(parts * sk);
+    d.maps = up256(parts * q->dk * q->dk * 4);
+    return d;
+}
+
+}  // namespace
+
+const char *delta_check(const fi_delta_desc *q);
+void delta_args(const fi_delta_desc *q, const DeltaPlan &plan, DeltaArgs &a);
+// Joins the segments: starts[0] = first (or zeros), starts[s + 1] = maps[s] starts[s] + local[s];
+// backwards from the last segment on, with the maps' transposes.
+void delta_join(const DeltaArgs &a, const float *first, bool backward, hipStream_t st);
+
+}  // namespace fi

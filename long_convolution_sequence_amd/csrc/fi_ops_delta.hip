@@ -1,0 +1,458 @@
+// The gated delta rule (fi_delta_*): the forward pass in chunks, and position by
+// position where there are few.
+#include "fi_delta.h"
+
+namespace fi {
+
+namespace {
+
+enum { CHAIN_LOCAL, CHAIN_FULL };
+
+// The sequence of a segment's chunks, 32 columns a wave (blockIdx.y: four waves'
+// columns).  FULL: from the state before the segment; y, the states before each chunk
+// and w where they are kept, the last state.  LOCAL: from nothing, only the state at
+// the end; the columns behind the state's are those of the map (v = 0, from a unit
+// column).
+template <typename T, int KT, int MODE>
+__global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
+    constexpr int MT = C / 32, CS = C / 16, KS = KT * 2, DK = KT * 32;
+    constexpr int KB = C * DK * 2, MB = C * C * 2;           // bytes of a term
+    constexpr bool FULL = MODE == CHAIN_FULL;
+    extern __shared__ __align__(16) char lds[];
+    char *const ik = lds, *const ikt = ik + N * KB, *const im = ikt + N * KB;
+    char *const ip = im + 3 * MB, *const iq = ip + NY * MB;   // FULL only
+    float *const f = reinterpret_cast<float *>(FULL ? iq + N * KB : ip);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int heads = p.B * p.H, seg = blockIdx.x / heads, bh = blockIdx.x % heads, b = bh / p.H, h = bh % p.H;
+    const int tiles = (p.dv + 31) / 32, tile = blockIdx.y * 4 + wave;
+    const bool map = !FULL && tile >= tiles;
+    const int column = (map ? tile - tiles : tile) * 32 + (lane & 31), width = map ? p.dk : p.dv;
+    const bool mine = column < width && (!map || tile - tiles < KT);
+    const int64_t length = delta_length(p, b);
+    const int hk = h / (p.H / p.HK);
+
+    f32x16 S[KT];
+    const float *from = FULL ? (p.segments > 1 ? p.starts + ((int64_t)seg * heads + bh) * p.dk * p.dv
+                                               : p.state ? p.state + (int64_t)bh * p.dk * p.dv : nullptr)
+                             : nullptr;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = t * 32 + acc_row(r);
+            S[t][r] = map ? (row == column ? 1.f : 0.f) : from && mine && row < p.dk ? from[(int64_t)row * p.dv + column] : 0.f;
+        }
+    const auto keep = [&](float *to, int w) {
+        if (!mine) return;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = t * 32 + acc_row(r);
+                if (row < p.dk) to[(int64_t)row * w + column] = S[t][r];
+            }
+    };
+    const T *const q = static_cast<const T *>(p.q) + hk * p.dk, *const k = static_cast<const T *>(p.k) + hk * p.dk;
+    const T *const v = static_cast<const T *>(p.v) + (int64_t)h * p.dv;
+    const int64_t first = seg * p.per, last = min(p.chunks, first + p.per);
+    for (int64_t c = first; c < last; ++c) {
+        const int64_t t0 = c * C, n = length - t0;
+        const int rows = (int)min<int64_t>(C, p.T - t0), live = n < 0 ? 0 : n < rows ? (int)n : rows;
+        T *const y = FULL ? static_cast<T *>(p.y) + (int64_t)h * p.dv : nullptr;
+        if (live == 0) {
+            if (!FULL) break;
+            if (p.states) keep(p.states + (c * heads + bh) * p.dk * p.dv, p.dv);
+            if (mine)
+                for (int i = lane >> 5; i < rows; i += 2) y[((t0 + i) * p.B + b) * p.ldy + column] = (T)0.f;
+            continue;
+        }
+        const int64_t at = c * heads + bh;
+        __syncthreads();
+        stage<T, C>(k + (t0 * p.B + b) * p.ldk, p.B * p.ldk, p.dk, DK, live, ik, ikt);
+        if (FULL) stage<T, C>(q + (t0 * p.B + b) * p.ldq, p.B * p.ldq, p.dk, DK, live, iq, nullptr);
+        copy_in(im, p.images + at * image_bytes<T, false>(), FULL ? (3 + NY) * MB : 3 * MB);
+        copy_in((char *)f, (const char *)(p.factors + at * 5 * C), 5 * C * 4);
+        __syncthreads();
+
+        if (FULL && p.states) keep(p.states + at * p.dk * p.dv, p.dv);
+        f32x16 R[MT], Y[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) R[i] = Y[i] = zeros16();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const Frag<3> s = step_of<3>(S[ks / 2], ks & 1);
+            Frag<NY> sy;
+#pragma unroll
+            for (int i = 0; i < NY; ++i) sy.t[i] = s.t[i];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                multiply<2>(R[i], piece<N>(ik, i * KS + ks, KB), s);
+                if (FULL) multiply<NY - 1>(Y[i], piece<N>(iq, i * KS + ks, KB), sy);
+            }
+        }
+        // v - e^G K S, and w = M of it
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = i * 32 + acc_row(r);
+                const float x = !map && mine && row < live ? (float)v[((t0 + row) * p.B + b) * p.ldv + column] : 0.f;
+                R[i][r] = fmaf(-f[row], R[i][r], x);
+            }
+        f32x16 W[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) W[i] = zeros16();
+#pragma unroll
+        for (int cs = 0; cs < CS; ++cs) {
+            const Frag<3> s = step_of<3>(R[cs / 2], cs & 1);
+#pragma unroll
+            for (int i = cs / 2; i < MT; ++i) multiply<2>(W[i], piece<3>(im, i * CS + cs, MB), s);
+        }
+        if (FULL) {
+            if (p.w && mine) {
+                float *to = p.w + at * C * p.dv + column;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) to[(i * 32 + acc_row(r)) * p.dv] = W[i][r];
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) Y[i][r] *= f[C + i * 32 + acc_row(r)];
+#pragma unroll
+            for (int cs = 0; cs < CS; ++cs) {
+                const Frag<NY> s = step_of<NY>(W[cs / 2], cs & 1);
+#pragma unroll
+                for (int i = cs / 2; i < MT; ++i) multiply<NY - 1>(Y[i], piece<NY>(ip, i * CS + cs, MB), s);
+            }
+            if (mine)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int row = i * 32 + acc_row(r);
+                        if (row < rows) y[((t0 + row) * p.B + b) * p.ldy + column] = (T)(row < live ? Y[i][r] : 0.f);
+                    }
+        }
+        const float decay = f[4 * C];
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[t][r] *= decay;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) W[i][r] *= f[2 * C + i * 32 + acc_row(r)];
+#pragma unroll
+        for (int cs = 0; cs < CS; ++cs) {
+            const Frag<3> s = step_of<3>(W[cs / 2], cs & 1);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) multiply<2>(S[t], piece<N>(ikt, t * CS + cs, KB), s);
+        }
+    }
+    if (!FULL) {
+        if (map) {
+            if (tile - tiles < KT) keep(p.maps + ((int64_t)seg * heads + bh) * p.dk * p.dk, p.dk);
+        } else
+            keep(p.local + ((int64_t)seg * heads + bh) * p.dk * p.dv, p.dv);
+        return;
+    }
+    if (seg == p.segments - 1) {
+        if (p.states) keep(p.states + (p.chunks * heads + bh) * p.dk * p.dv, p.dv);
+        if (p.final) keep(p.final + (int64_t)bh * p.dk * p.dv, p.dv);
+    }
+}
+
+// starts[s + 1] = maps[s] starts[s] + local[s] (backwards starts[s - 1] = maps[s]^T
+// starts[s] + local[s]), 32 columns a wave.
+template <int KT>
+__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs p, const float *first, bool back) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+    const int heads = p.B * p.H, bh = blockIdx.x, column = (blockIdx.y * 4 + wave) * 32 + (lane & 31);
+    const bool mine = column < p.dv;
+    const int64_t size = (int64_t)p.dk * p.dv;
+    f32x16 S[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = t * 32 + acc_row(r);
+            S[t][r] = first && mine && row < p.dk ? first[bh * size + (int64_t)row * p.dv + column] : 0.f;
+        }
+    for (int n = 0; n < p.segments; ++n) {
+        const int s = back ? p.segments - 1 - n : n;
+        const int64_t at = (int64_t)s * heads + bh;
+        if (mine)
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = t * 32 + acc_row(r);
+                    if (row < p.dk) p.starts[at * size + (int64_t)row * p.dv + column] = S[t][r];
+                }
+        if (n + 1 == p.segments) break;
+        f32x16 next[KT];
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = t * 32 + acc_row(r);
+                next[t][r] = mine && row < p.dk ? p.local[at * size + (int64_t)row * p.dv + column] : 0.f;
+            }
+        const float *map = p.maps + at * p.dk * p.dk;
+#pragma unroll
+        for (int ks = 0; ks < KT * 2; ++ks) {
+            const Frag<3> b = step_of<3>(S[ks / 2], ks & 1);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = t * 32 + (lane & 31), k = ks * 16 + 8 * (j >> 2) + 4 * half + (j & 3);
+                    x[j] = row < p.dk && k < p.dk ? map[back ? (int64_t)k * p.dk + row : (int64_t)row * p.dk + k] : 0.f;
+                }
+                multiply<2>(next[t], split<3>(x), b);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t] = next[t];
+    }
+}
+
+// Position by position, for a few of them: a workgroup 32 columns of a head, a thread
+// four columns of every 32nd row, held in registers.  Both sums over the rows, k . S
+// and q . S, are taken of the state before the position:
+// y = scale (a q.S + (k.q) u), u = b (v - a k.S).
+template <typename T>
+__global__ void __launch_bounds__(256) k_delta_steps(DeltaArgs p) {
+    constexpr int ROWS = kDeltaMaxK / 32;
+    __shared__ float ks[kDeltaMaxK], qs[kDeltaMaxK];
+    __shared__ float4 join[2][4][8];
+    __shared__ float dots[3][4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, cg = tid & 7, rg = tid >> 3;
+    const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.HK), column = blockIdx.y * 32 + cg * 4;
+    const int64_t length = delta_length(p, b);
+    float S[ROWS][4];
+    const float *from = p.state ? p.state + (int64_t)bh * p.dk * p.dv : nullptr;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = rg + i * 32;
+        if (from) load4(S[i], from + (int64_t)row * p.dv, column, p.dv, row < p.dk);
+        else S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
+    }
+    for (int64_t t = 0; t < p.T; ++t) {
+        const int64_t row = t * p.B + b;
+        T *const y = static_cast<T *>(p.y) + row * p.ldy + (int64_t)h * p.dv;
+        if (t >= length) {
+            if (rg == 0)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (column + j < p.dv) y[column + j] = (T)0.f;
+            continue;
+        }
+        __syncthreads();
+        float kk = 0.f, qq = 0.f, kq = 0.f;
+        if (tid < kDeltaMaxK) {
+            const bool in = tid < p.dk;
+            const float a = in ? (float)static_cast<const T *>(p.k)[row * p.ldk + hk * p.dk + tid] : 0.f;
+            const float c = in ? (float)static_cast<const T *>(p.q)[row * p.ldq + hk * p.dk + tid] : 0.f;
+            ks[tid] = a, qs[tid] = c;
+            kk = a * a, qq = c * c, kq = a * c;
+        }
+        kk = lanes_sum(kk), qq = lanes_sum(qq), kq = lanes_sum(kq);
+        if (lane == 0) dots[0][wave] = kk, dots[1][wave] = qq, dots[2][wave] = kq;
+        __syncthreads();
+        const float rk = p.unit ? 1.f / sqrtf(dots[0][0] + dots[0][1] + kDeltaUnit) : 1.f;
+        const float rq = p.scale * (p.unit ? 1.f / sqrtf(dots[1][0] + dots[1][1] + kDeltaUnit) : 1.f);
+        float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const float a = ks[rg + i * 32], c = qs[rg + i * 32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pk[j] = fmaf(a, S[i][j], pk[j]), pq[j] = fmaf(c, S[i][j], pq[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = 8; s < 64; s *= 2) pk[j] += __shfl_xor(pk[j], s, 64), pq[j] += __shfl_xor(pq[j], s, 64);
+        if (lane < 8) {
+            join[0][wave][cg] = make_float4(pk[0], pk[1], pk[2], pk[3]);
+            join[1][wave][cg] = make_float4(pq[0], pq[1], pq[2], pq[3]);
+        }
+        __syncthreads();
+        float v[4];
+        load4(v, static_cast<const T *>(p.v) + row * p.ldv + (int64_t)h * p.dv, column, p.dv, true);
+        const float g = p.g[row * p.ldg + h], beta = p.beta[row * p.ldb + h], a = exp2f(g * kLog2e);
+        const float cross = (dots[2][0] + dots[2][1]) * rk * rq;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float sk = 0.f, sq = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) sk += (&join[0][w][cg].x)[j], sq += (&join[1][w][cg].x)[j];
+            const float u = beta * fmaf(-a * rk, sk, v[j]);
+            if (rg == 0 && column + j < p.dv) y[column + j] = (T)fmaf(a * rq, sq, cross * u);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) S[i][j] = fmaf(ks[rg + i * 32] * rk, u, a * S[i][j]);
+        }
+    }
+    if (!p.final) return;
+    float *const to = p.final + (int64_t)bh * p.dk * p.dv;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = rg + i * 32;
+        if (row < p.dk)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (column + j < p.dv) to[(int64_t)row * p.dv + column + j] = S[i][j];
+    }
+}
+
+// Positions that run one by one: below, the chunk's launches cost more.
+constexpr int64_t kDeltaSteps = 8;
+
+template <typename T, int KT>
+void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
+    constexpr int KB = C * KT * 64, MB = C * C * 2;
+    const int heads = a.B * a.H, tiles = (a.dv + 31) / 32;
+    hipLaunchKernelGGL((k_delta_prep<T, KT, false>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
+    if (a.segments > 1) {
+        const int all = tiles + KT;
+        hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_LOCAL>), dim3((unsigned)((a.segments - 1) * heads), (all + 3) / 4),
+                           dim3(std::min(4, all) * 64), N * KB * 2 + 3 * MB + 5 * C * 4, st, a);
+        delta_join(a, a.state, false, st);
+    }
+    hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_FULL>), dim3((unsigned)(a.segments * heads), (tiles + 3) / 4),
+                       dim3(std::min(4, tiles) * 64), N * KB * 3 + (3 + NY) * MB + 5 * C * 4, st, a);
+}
+
+template <typename T>
+void forward(const DeltaArgs &a, const DeltaPlan &d, bool steps, hipStream_t st) {
+    if (steps)
+        hipLaunchKernelGGL((k_delta_steps<T>), dim3(a.B * a.H, (a.dv + 31) / 32), dim3(256), 0, st, a);
+    else if (d.KT == 1) forward<T, 1>(a, d, st);
+    else if (d.KT == 2) forward<T, 2>(a, d, st);
+    else if (d.KT == 3) forward<T, 3>(a, d, st);
+    else forward<T, 4>(a, d, st);
+}
+
+}  // namespace
+
+const char *delta_check(const fi_delta_desc *q) {
+    if (!q) return "null descriptor";
+    if (q->T < 0 || q->T > (int64_t(1) << 23)) return "T is not in 0 .. 2^23";
+    if (q->batch < 1 || q->key_heads < 1 || q->heads < 1) return "batch >= 1, key_heads >= 1 and heads >= 1 are required";
+    if (q->heads % q->key_heads) return "heads is no multiple of key_heads";
+    if (q->dk < 1 || q->dk > kDeltaMaxK) return "dk is not in 1 .. 128";
+    if (q->dv < 1 || q->dv > kDeltaMaxV) return "dv is not in 1 .. 1024";
+    if (!value_type(q->dtype)) return "dtype is none of FI_F32, FI_BF16, FI_F16";
+    if (q->unit != 0 && q->unit != 1) return "unit is not 0 or 1";
+    if (!(q->scale == q->scale)) return "scale is not a number";
+    if ((int64_t)q->batch * q->heads > int64_t(1) << 20) return "batch * heads is over 2^20";
+    const int C = delta_chunk(q->dtype);
+    if ((q->T + C - 1) / C * q->batch * q->heads > int64_t(1) << 24) return "too large: chunks * batch * heads is over 2^24";
+    const int64_t qk = (int64_t)q->key_heads * q->dk, v = (int64_t)q->heads * q->dv, h = q->heads;
+    const int64_t ld[][2] = {{q->ld_q, qk}, {q->ld_k, qk}, {q->ld_v, v}, {q->ld_decay, h}, {q->ld_beta, h}, {q->ld_y, v},
+                             {q->ld_dy, v}, {q->ld_dq, qk}, {q->ld_dk, qk}, {q->ld_dv, v}, {q->ld_ddecay, h},
+                             {q->ld_dbeta, h}};
+    for (auto &l : ld)
+        if (l[0] != 0 && (l[0] < l[1] || l[0] > (int64_t(1) << 40))) return "a row pitch is less than its row";
+    for (int v : q->reserved)
+        if (v) return "reserved is not zero";
+    return nullptr;
+}
+
+void delta_args(const fi_delta_desc *q, const DeltaPlan &d, DeltaArgs &a) {
+    a.T = q->T, a.chunks = d.chunks, a.per = d.per, a.segments = d.segments;
+    a.B = q->batch, a.HK = q->key_heads, a.H = q->heads, a.dk = q->dk, a.dv = q->dv, a.unit = q->unit, a.scale = q->scale;
+    const int64_t qk = (int64_t)a.HK * a.dk, v = (int64_t)a.H * a.dv;
+    a.ldq = pitch_or(q->ld_q, qk), a.ldk = pitch_or(q->ld_k, qk), a.ldv = pitch_or(q->ld_v, v);
+    a.ldg = pitch_or(q->ld_decay, a.H), a.ldb = pitch_or(q->ld_beta, a.H), a.ldy = pitch_or(q->ld_y, v);
+    a.lddy = pitch_or(q->ld_dy, v), a.lddq = pitch_or(q->ld_dq, qk), a.lddk = pitch_or(q->ld_dk, qk);
+    a.lddv = pitch_or(q->ld_dv, v), a.lddg = pitch_or(q->ld_ddecay, a.H), a.lddb = pitch_or(q->ld_dbeta, a.H);
+}
+
+void delta_join(const DeltaArgs &a, const float *first, bool back, hipStream_t st) {
+    const int tiles = (a.dv + 31) / 32;
+    const dim3 grid(a.B * a.H, (tiles + 3) / 4), block(std::min(4, tiles) * 64);
+    switch ((a.dk + 31) / 32) {
+        case 1: hipLaunchKernelGGL((k_delta_join<1>), grid, block, 0, st, a, first, back); break;
+        case 2: hipLaunchKernelGGL((k_delta_join<2>), grid, block, 0, st, a, first, back); break;
+        case 3: hipLaunchKernelGGL((k_delta_join<3>), grid, block, 0, st, a, first, back); break;
+        default: hipLaunchKernelGGL((k_delta_join<4>), grid, block, 0, st, a, first, back);
+    }
+}
+
+}  // namespace fi
+
+using namespace fi;
+
+extern "C" {
+
+size_t fi_delta_saved_bytes(const fi_delta_desc *desc) {
+    if (delta_check(desc)) return 0;
+    const DeltaPlan d = delta_plan(desc, false);
+    const size_t last = up256((size_t)desc->batch * desc->heads * desc->dk * desc->dv * 4);
+    return d.states + last + d.rows + d.maps + 256;
+}
+
+size_t fi_delta_workspace_bytes(const fi_delta_desc *desc, int backward) {
+    if (delta_check(desc)) return 0;
+    if (backward) {
+        const DeltaPlan d = delta_plan(desc, true);
+        return d.images + d.factors + d.ends + d.rows + 2 * d.local + 256;
+    }
+    const DeltaPlan d = delta_plan(desc, false);
+    return d.images + d.factors + 2 * d.local + d.maps + 256;
+}
+
+fi_status fi_delta_forward(const fi_delta_desc *desc, const void *q, const void *k, const void *v, const float *decay,
+                           const float *beta, const float *state, const int32_t *lengths, void *y, float *final,
+                           void *saved, void *workspace, void *stream) {
+    static const char *call = "fi_delta_forward";
+    if (const char *why = delta_check(desc)) return op_fail(FI_EINVAL, call, why);
+    const bool steps = desc->T == 0 || (desc->T <= kDeltaSteps && !saved);
+    const size_t es = value_bytes(desc->dtype);
+    if (desc->T > 0 && (!q || !k || !v || !decay || !beta || !y || (!steps && !workspace)))
+        return op_fail(FI_EINVAL, call, "q, k, v, decay, beta, y and the workspace are required");
+    if (!aligned(es, {q, k, v, y}) || !aligned(4, {decay, beta, state, lengths, final}) || !aligned(256, {saved, workspace}))
+        return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
+    const DeltaPlan d = delta_plan(desc, false);
+    DeltaArgs a = {};
+    delta_args(desc, d, a);
+    const int64_t rows = a.T * a.B;
+    const size_t qk = (size_t)a.HK * a.dk * es, vb = (size_t)a.H * a.dv * es, hb = (size_t)a.H * 4;
+    const size_t sb = (size_t)a.B * a.H * a.dk * a.dv * 4, lb = (size_t)a.B * 4;
+    const size_t sv = fi_delta_saved_bytes(desc), ws = fi_delta_workspace_bytes(desc, 0);
+    const View vstate = {state, 1, sb, sb}, vfinal = {final, 1, sb, sb};
+    const View out[] = {vfinal, {y, rows, vb, (size_t)a.ldy * es}, {saved, 1, sv, sv}, {steps ? nullptr : workspace, 1, ws, ws}};
+    const View in[] = {{q, rows, qk, (size_t)a.ldq * es}, {k, rows, qk, (size_t)a.ldk * es}, {v, rows, vb, (size_t)a.ldv * es},
+                       {decay, rows, hb, (size_t)a.ldg * 4}, {beta, rows, hb, (size_t)a.ldb * 4}, {lengths, 1, lb, lb}};
+    const bool inplace = final && state == final;
+    if (outputs_meet(out, 4, in, 6) || outputs_meet(out + 1, 3, &vstate, 1) || (!inplace && views_meet(vfinal, vstate)))
+        return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
+    a.q = q, a.k = k, a.v = v, a.g = decay, a.beta = beta, a.state = state, a.lengths = lengths, a.y = y, a.final = final;
+    char *w = (char *)workspace;
+    a.images = w, w += d.images;
+    a.factors = (float *)w, w += d.factors;
+    a.starts = (float *)w, w += d.local;
+    a.local = (float *)w, w += d.local;
+    a.maps = (float *)w;
+    if (saved) {
+        char *s = (char *)saved;
+        const size_t last = up256((size_t)a.B * a.H * a.dk * a.dv * 4);
+        a.states = (float *)s, s += d.states + last;
+        a.w = (float *)s, s += d.rows;
+        a.maps = (float *)s;
+    }
+    const hipStream_t st = (hipStream_t)stream;
+    if (a.T == 0 && !final && !saved) return FI_OK;
+    if (desc->dtype == FI_F32) forward<float>(a, d, steps, st);
+    else if (desc->dtype == FI_BF16) forward<bf16_t>(a, d, steps, st);
+    else forward<f16_t>(a, d, steps, st);
+    return op_launched(call);
+}
+
+}  // extern "C"

@@ -7,14 +7,13 @@
 //   dg = dm v act'(g),  do = q (dv w1 - o q mean(dv w1 o q)),
 //   dw1 = k P, dk = w1 P with P = sum dR act(g) o q,  dw2 = sum da r p   (over the rows).
 // r is formed again from o, g and res in fp32, not read back rounded.
-#include "fi_ops.h"
+#include "fi_rows.h"
 
 namespace fi {
 
 namespace {
 
 constexpr int kNormMaxD = 16384;
-constexpr int kNormLane = 16;          // values of a row per lane at most
 constexpr int kNormHalf = 768;         // threads of the backward workgroups with half of that (see half_lanes)
 constexpr int64_t kNormCache = 256 << 20;   // bytes of the last-level cache
 constexpr int kNormCUs = 256;          // compute units that the workgroups are spread over
@@ -48,101 +47,6 @@ __device__ __forceinline__ float act_of(int act, float g, float &slope) {
     }
     slope = s * fmaf(g, 1.f - s, 1.f);
     return g * s;
-}
-
-// A row is held in registers by a team: one wave up to 1024 values (four teams
-// to a workgroup, no barrier), else a workgroup of as many waves as the row
-// needs.  A lane holds NC chunks of CH neighbouring values, CH chosen so that
-// the widest tensor of the row is read 16 bytes at a time; a team's waves take
-// alternate stretches.  A team keeps its columns' weights (and, backwards,
-// their column sums) in registers over all its rows.
-template <int CH, int NC, bool MULTI>
-struct Team {
-    Place<CH> at[NC];      // this lane's chunks
-    bool first;            // the lane of column 0
-    int waves, wave, lane;
-    int64_t row, rows_step;
-    int turn;
-
-    __device__ __forceinline__ Team(int D) {
-        lane = threadIdx.x & 63;
-        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        waves = blockDim.x >> 6;
-        turn = 0;
-        const int start = ((MULTI ? wave * 64 : 0) + lane) * CH, step = (MULTI ? waves : 1) * 64 * CH;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) at[j] = Place<CH>(start + j * step, D);
-        first = start == 0;
-        row = MULTI ? blockIdx.x : blockIdx.x * (int64_t)waves + wave;
-        rows_step = MULTI ? gridDim.x : gridDim.x * (int64_t)waves;
-    }
-    // Sum over the team, in every lane.  Two sets of slots by turns: a wave that
-    // writes a set has passed the barrier after everybody's reads of that set.
-    __device__ __forceinline__ float sum(float v, float (*slots)[16]) {
-        v = lanes_sum(v);
-        if (!MULTI) return v;
-        if (lane == 0) slots[turn][wave] = v;
-        __syncthreads();
-        v = 0.f;
-        for (int i = 0; i < waves; ++i) v += slots[turn][i];
-        turn ^= 1;
-        return v;
-    }
-};
-
-// A row's values as they are loaded.  ALL: the tensor is there; else a null one
-// reads as zeros.
-template <bool ALL, bool STREAM, typename T, int CH, int NC>
-struct Raw {
-    Chunk<T, CH> v[NC];
-
-    template <bool MULTI>
-    __device__ __forceinline__ void load(const void *p, int64_t ld, int64_t row, const Team<CH, NC, MULTI> &t) {
-        if (!ALL && !p) {
-#pragma unroll
-            for (int j = 0; j < NC; ++j) v[j] = (Chunk<T, CH>)(T)0.f;
-            return;
-        }
-        const T *from = static_cast<const T *>(p) + row * ld;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) v[j] = load_chunk<T, CH, STREAM>(from, t.at[j]);
-    }
-    __device__ __forceinline__ void get(float (&f)[NC * CH]) const {
-#pragma unroll
-        for (int j = 0; j < NC; ++j)
-#pragma unroll
-            for (int i = 0; i < CH; ++i) f[j * CH + i] = (float)v[j][i];
-    }
-};
-
-template <bool TAIL, typename T, int CH, int NC, bool MULTI>
-__device__ __forceinline__ void store_row(const float (&v)[NC * CH], void *p, int64_t ld,
-                                          const Team<CH, NC, MULTI> &t) {
-    T *to = static_cast<T *>(p) + t.row * ld;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        Chunk<T, CH> raw;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) raw[i] = (T)v[j * CH + i];
-        store_chunk<TAIL, T, CH>(to, t.at[j], raw);
-    }
-}
-
-// Sum of the squares of what this lane owns.
-template <bool TAIL, int CH, int NC, bool MULTI>
-__device__ __forceinline__ float squares(const float (&v)[NC * CH], const Team<CH, NC, MULTI> &t) {
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        float c = 0.f;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const float x = TAIL && i < t.at[j].skip ? 0.f : v[j * CH + i];
-            c = fmaf(x, x, c);
-        }
-        s += t.at[j].skip < CH ? c : 0.f;
-    }
-    return s;
 }
 
 // A lane's weights: kw = k w1 (the two meet in every use of them in a row) and
@@ -329,24 +233,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormHalf ? 3 : THREADS <=
     }
 }
 
-// The workgroups' column sums: 64 columns a workgroup, its sixteen waves take
-// every sixteenth group and are added in their order.  dw1 and dk are the one
-// sum of dR act o q times k and w1.  A wave's loads do not wait for each other.
+// The workgroups' column sums; dw1 and dk are the one sum of dR act o q times k
+// and w1.
 __global__ void __launch_bounds__(1024) k_norm_columns(NormArgs p, int groups, float *dw1, float *dk, float *dw2) {
-    __shared__ float join[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int i = blockIdx.x * 64 + lane;
-    float s = 0.f;
-    if (i < 2 * p.D) {
-#pragma unroll 8
-        for (int g = wave; g < groups; g += 16) s += p.part[(size_t)g * 2 * p.D + i];
-    }
-    join[wave][lane] = s;
-    __syncthreads();
-    if (wave || i >= 2 * p.D) return;
-    s = 0.f;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) s += join[w][lane];
+    const int i = blockIdx.x * 64 + (threadIdx.x & 63);
+    float s;
+    if (!column_sum(p.part, p.D, groups, i, s)) return;
     if (i >= p.D) {
         if (dw2) dw2[i - p.D] = s;
         return;
@@ -372,8 +264,6 @@ const char *norm_check(const fi_norm_desc *q) {
         if (v) return "reserved is not zero";
     return nullptr;
 }
-
-int team_waves(int D) { return (D + 64 * kNormLane - 1) / (64 * kNormLane); }
 
 // Backwards, rows of five or six waves at 16 values a lane leave a CU's eight
 // places partly empty and its four SIMDs unevenly loaded: 8 values a lane then, and
@@ -459,7 +349,7 @@ void launch(const NormArgs &a, bool backward, unsigned groups, hipStream_t st) {
     constexpr int CH = sizeof(W) == 2 ? 8 : 4;
     const int waves = team_waves(a.D);
     if (backward && half_lanes(a.D))
-        launch<V, W, CH, kNormLane / 2 / CH, true, kNormHalf>(a, backward, groups, (a.D + 511) / 512 * 64, st);
+        launch<V, W, CH, kRowLane / 2 / CH, true, kNormHalf>(a, backward, groups, (a.D + 511) / 512 * 64, st);
     else if (a.D < CH)
         launch<V, W, 1, 1, false, 256>(a, backward, groups, 256, st);
     else if (a.D <= 64 * CH)
@@ -467,11 +357,11 @@ void launch(const NormArgs &a, bool backward, unsigned groups, hipStream_t st) {
     else if (a.D <= 128 * CH)
         launch<V, W, CH, 2, false, 256>(a, backward, groups, 256, st);
     else if (waves == 1)
-        launch<V, W, CH, kNormLane / CH, false, 256>(a, backward, groups, 256, st);
+        launch<V, W, CH, kRowLane / CH, false, 256>(a, backward, groups, 256, st);
     else if (waves <= 8)
-        launch<V, W, CH, kNormLane / CH, true, 512>(a, backward, groups, waves * 64, st);
+        launch<V, W, CH, kRowLane / CH, true, 512>(a, backward, groups, waves * 64, st);
     else
-        launch<V, W, CH, kNormLane / CH, true, 1024>(a, backward, groups, waves * 64, st);
+        launch<V, W, CH, kRowLane / CH, true, 1024>(a, backward, groups, waves * 64, st);
 }
 
 void launch(const fi_norm_desc *q, const NormArgs &a, bool backward, unsigned groups, hipStream_t st) {

@@ -1,0 +1,315 @@
+// Products in 8-bit integers (fi_q8_*): y[m][n] = sa[m] sw[n] sum_k a[m][k] w[n][k] + bias[n].
+// Both matrices lie in the order in which the matrix instruction
+// v_mfma_i32_16x16x64_i8 takes them: a piece of 16 rows x 64 values along k is 1 KB,
+// lane l's 16 bytes are the values 16 (l / 16) .. + 15 of row l % 16; the pieces of
+// 16 rows follow each other along k.  So a wave reads a piece as 1 KB in a row, from
+// memory into LDS and from LDS into registers, without bank conflicts.  Sums are
+// whole numbers of 32 bits and exact: 128 * 128 * K < 2^31 for K < 2^17.
+#include "fi_ops.h"
+
+namespace fi {
+
+namespace {
+
+constexpr int kQ8MaxK = 131071;        // 128 * 128 * K < 2^31
+constexpr int64_t kQ8MaxRows = int64_t(1) << 24;
+constexpr int kQ8Piece = 1024;         // bytes of 16 rows x 64 values
+
+using i32x4 = int __attribute__((ext_vector_type(4)));
+
+// Values along k as they are kept, zeros behind K: whole pairs of pieces.
+__host__ __device__ inline int64_t q8_padded(int K) { return (K + 127) / 128 * 128; }
+inline int64_t q8_code_bytes(int64_t rows, int K) { return (rows + 15) / 16 * 16 * q8_padded(K); }
+
+// Where the 16 values from k on (a multiple of 16) of a row lie.
+__device__ __forceinline__ size_t q8_at(int64_t row, int k, int64_t kp) {
+    return (size_t)(row >> 4) * 16 * kp + (size_t)(k >> 6) * kQ8Piece + ((k >> 4) & 3) * 256 + (row & 15) * 16;
+}
+
+__device__ __forceinline__ void put16(int8_t *to, const int (&c)[16]) {
+    i32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v[j] = (c[4 * j] & 255) | (c[4 * j + 1] & 255) << 8 | (c[4 * j + 2] & 255) << 16 | c[4 * j + 3] << 24;
+    *reinterpret_cast<i32x4 *>(to) = v;
+}
+
+// Codes [rows][K] into order, 16 values a thread; the rows and values behind the
+// matrix are zeros.  Scales follow the codes.
+__global__ void __launch_bounds__(256) k_q8_pack(const int8_t *codes, const float *scales, int64_t rows, int K,
+                                                 int8_t *packed, float *out) {
+    const int64_t kp = q8_padded(K), units = kp / 16, total = (rows + 15) / 16 * 16 * units;
+    for (int64_t u = blockIdx.x * (int64_t)256 + threadIdx.x; u < total; u += gridDim.x * (int64_t)256) {
+        const int64_t row = u / units;
+        const int k = (int)(u - row * units) * 16;
+        int c[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c[i] = row < rows && k + i < K ? codes[row * K + k + i] : 0;
+        put16(packed + q8_at(row, k, kp), c);
+        if (k == 0 && row < rows) out[row] = scales[row];
+    }
+}
+
+// A row's largest |x| as the bits of a float: NaN and infinity pass every number.
+template <typename T>
+__device__ __forceinline__ unsigned magnitude(T v) { return __float_as_uint((float)v) & 0x7fffffffu; }
+
+// The scale of a row whose largest |x| has these bits.
+__device__ __forceinline__ float q8_scale(unsigned top) {
+    return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.f;
+}
+
+__device__ __forceinline__ int q8_code(float x, float scale) {
+    // a scale of zero or NaN gives zeros; one below the normal numbers has lost
+    // digits, so the quotient may pass 127
+    const float c = scale > 0.f ? rintf(x / scale) : 0.f;
+    return (int)fminf(fmaxf(c, -127.f), 127.f);
+}
+
+// Scales and codes of rows of values, a wave a row: once over the row for its
+// largest value, once more (from the caches) for its codes.
+template <typename T>
+__global__ void __launch_bounds__(256) k_q8_quantize(const T *x, int64_t ld, int64_t rows, int K, int8_t *packed,
+                                                     float *scales) {
+    const int lane = threadIdx.x & 63;
+    const int64_t kp = q8_padded(K), padded = (rows + 15) / 16 * 16;
+    for (int64_t row = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6); row < padded; row += gridDim.x * (int64_t)4) {
+        const T *from = x + row * ld;
+        unsigned top = 0;
+        if (row < rows)
+            for (int k = lane; k < K; k += 64) top = max(top, magnitude(from[k]));
+#pragma unroll
+        for (int s = 32; s; s >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, s, 64));
+        const float scale = q8_scale(top);
+        if (lane == 0 && row < rows) scales[row] = scale;
+        for (int k = lane * 16; k < kp; k += 64 * 16) {
+            int c[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) c[i] = row < rows && k + i < K ? q8_code((float)from[k + i], scale) : 0;
+            put16(packed + q8_at(row, k, kp), c);
+        }
+    }
+}
+
+struct Q8Args {
+    const int8_t *a, *w;
+    const float *sa, *sw, *bias;
+    void *y;
+    int64_t M, N, ldy, kp;
+};
+
+// Outputs [BM rows][BN columns] of a workgroup, WM x WN waves; a stage of 128 values
+// along k of both sides in LDS while the next is on its way.
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
+    constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;      // pieces of a wave
+    constexpr int PIECES = (BM + BN) / 16 * 2, EACH = PIECES / (WM * WN);
+    static_assert(PIECES % (WM * WN) == 0, "the waves bring equal shares");
+    extern __shared__ __align__(16) int8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int64_t tiles = (p.M + BM - 1) / BM;
+    const int64_t m0 = blockIdx.x % tiles * (BM / 16), n0 = blockIdx.x / tiles * (BN / 16);   // in pieces
+    const int64_t mp = (p.M + 15) / 16, np = (p.N + 15) / 16;
+    const int steps = (int)(p.kp / 128);
+
+    const auto bring = [&](int step, int buffer) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int piece = wave * EACH + i, row = piece / 2;
+            // rows behind the matrix: the last one again
+            const int8_t *from;
+            if (row < BM / 16)
+                from = p.a + min(m0 + row, mp - 1) * 16 * p.kp;
+            else
+                from = p.w + min(n0 + row - BM / 16, np - 1) * 16 * p.kp;
+            from += (size_t)step * (2 * kQ8Piece) + (piece & 1) * kQ8Piece + lane * 16;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                             (__attribute__((address_space(3))) void *)(lds + buffer * PIECES * kQ8Piece +
+                                                                                        piece * kQ8Piece),
+                                             16, 0, 0);
+        }
+    };
+
+    i32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    bring(0, 0);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) bring(s + 1, (s + 1) & 1);
+        const int8_t *at = lds + (s & 1) * PIECES * kQ8Piece + lane * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            i32x4 fa[FM], fw[FN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                fa[i] = *reinterpret_cast<const i32x4 *>(at + ((wm * FM + i) * 2 + h) * kQ8Piece);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                fw[j] = *reinterpret_cast<const i32x4 *>(at + ((BM / 16 + wn * FN + j) * 2 + h) * kQ8Piece);
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
+        }
+        __syncthreads();
+    }
+    // lane l holds outputs n = 4 (l / 16) .. + 3 of row m = l % 16
+    T *y = static_cast<T *>(p.y);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t m = (m0 + wm * FM + i) * 16 + (lane & 15);
+        if (m >= p.M) continue;
+        const float sa = p.sa[m];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int64_t n = (n0 + wn * FN + j) * 16 + (lane >> 4) * 4;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (n + r < p.N)
+                    y[m * p.ldy + n + r] =
+                        (T)fmaf((float)acc[i][j][r] * sa, p.sw[n + r], p.bias ? p.bias[n + r] : 0.f);
+        }
+    }
+}
+
+// Up to 16 rows: 16 outputs a workgroup, its four waves share k.
+template <typename T>
+__global__ void __launch_bounds__(256) k_q8_few(Q8Args p) {
+    __shared__ i32x4 join[3][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int steps = (int)(p.kp / 64);
+    const int row = min(lane & 15, (int)p.M - 1);             // of a: the rows behind it give outputs that are not kept
+    const int8_t *a = p.a + (lane >> 4) * 256 + row * 16, *w = p.w + (size_t)blockIdx.x * 16 * p.kp + lane * 16;
+    i32x4 acc{0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = wave; s < steps; s += 4)
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4 *>(w + (size_t)s * kQ8Piece),
+                                                    *reinterpret_cast<const i32x4 *>(a + (size_t)s * kQ8Piece), acc, 0, 0,
+                                                    0);
+    if (wave) join[wave - 1][lane] = acc;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) acc += join[i][lane];
+    const int64_t m = lane & 15, n = blockIdx.x * (int64_t)16 + (lane >> 4) * 4;
+    if (m >= p.M) return;
+    const float sa = p.sa[m];
+    T *y = static_cast<T *>(p.y) + m * p.ldy;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (n + r < p.N) y[n + r] = (T)fmaf((float)acc[r] * sa, p.sw[n + r], p.bias ? p.bias[n + r] : 0.f);
+}
+
+template <typename T>
+void launch_product(const Q8Args &p, hipStream_t st) {
+    if (p.M <= 16) {
+        hipLaunchKernelGGL((k_q8_few<T>), dim3((unsigned)((p.N + 15) / 16)), dim3(256), 0, st, p);
+        return;
+    }
+    constexpr int BM = 128, BN = 128;
+    hipLaunchKernelGGL((k_q8_product<T, BM, BN, 2, 2>), dim3((unsigned)(((p.N + BN - 1) / BN) * ((p.M + BM - 1) / BM))),
+                       dim3(256), 2 * (BM + BN) / 16 * 2 * kQ8Piece, st, p);
+}
+
+const char *q8_check(int64_t rows, int K) {
+    if (rows < 0 || rows > kQ8MaxRows) return "rows is not in 0 .. 2^24";
+    if (K < 1 || K > kQ8MaxK) return "K is not in 1 .. 131071";
+    return nullptr;
+}
+
+}  // namespace
+
+}  // namespace fi
+
+using namespace fi;
+
+extern "C" {
+
+size_t fi_q8_bytes(int64_t rows, int K) {
+    if (q8_check(rows, K)) return 0;
+    return up256((size_t)q8_code_bytes(rows, K)) + up256((size_t)rows * 4);
+}
+
+fi_status fi_q8_pack(int64_t rows, int K, const int8_t *codes, const float *scales, void *packed, void *stream) {
+    static const char *call = "fi_q8_pack";
+    if (const char *why = q8_check(rows, K)) return op_fail(FI_EINVAL, call, why);
+    if (rows == 0) return FI_OK;
+    if (!codes || !scales || !packed || (uintptr_t)packed % 256)
+        return op_fail(FI_EINVAL, call, "codes, scales and packed memory aligned to 256 bytes are required");
+    if (!aligned(4, {scales})) return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
+    const size_t bytes = fi_q8_bytes(rows, K);
+    const View out = {packed, 1, bytes, bytes};
+    const View in[] = {{codes, 1, (size_t)rows * K, (size_t)rows * K}, {scales, 1, (size_t)rows * 4, (size_t)rows * 4}};
+    if (outputs_meet(&out, 1, in, 2)) return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
+    const int64_t units = q8_code_bytes(rows, K) / 16;
+    hipLaunchKernelGGL(k_q8_pack, dim3((unsigned)std::min<int64_t>((units + 255) / 256, 1 << 16)), dim3(256), 0,
+                       (hipStream_t)stream, codes, scales, rows, K, (int8_t *)packed,
+                       (float *)((char *)packed + up256((size_t)q8_code_bytes(rows, K))));
+    return op_launched(call);
+}
+
+fi_status fi_q8_quantize(int64_t rows, int K, int dtype, const void *x, int64_t ld_x, void *packed, void *stream) {
+    static const char *call = "fi_q8_quantize";
+    if (const char *why = q8_check(rows, K)) return op_fail(FI_EINVAL, call, why);
+    if (!value_type(dtype)) return op_fail(FI_EINVAL, call, "dtype is none of FI_F32, FI_BF16, FI_F16");
+    if (ld_x != 0 && (ld_x < K || ld_x > (int64_t(1) << 40))) return op_fail(FI_EINVAL, call, "a row pitch is less than K");
+    if (rows == 0) return FI_OK;
+    if (!x || !packed || (uintptr_t)packed % 256)
+        return op_fail(FI_EINVAL, call, "x and packed memory aligned to 256 bytes are required");
+    const size_t es = value_bytes(dtype), bytes = fi_q8_bytes(rows, K);
+    if (!aligned(es, {x})) return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
+    const int64_t ld = pitch_or(ld_x, K);
+    const View out = {packed, 1, bytes, bytes}, in = {x, rows, K * es, ld * es};
+    if (outputs_meet(&out, 1, &in, 1)) return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
+    const unsigned groups = (unsigned)std::min<int64_t>((rows + 15) / 16 * 4, 1 << 16);
+    int8_t *codes = (int8_t *)packed;
+    float *scales = (float *)((char *)packed + up256((size_t)q8_code_bytes(rows, K)));
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == FI_F32)
+        hipLaunchKernelGGL((k_q8_quantize<float>), dim3(groups), dim3(256), 0, st, (const float *)x, ld, rows, K, codes,
+                           scales);
+    else if (dtype == FI_BF16)
+        hipLaunchKernelGGL((k_q8_quantize<bf16_t>), dim3(groups), dim3(256), 0, st, (const bf16_t *)x, ld, rows, K, codes,
+                           scales);
+    else
+        hipLaunchKernelGGL((k_q8_quantize<f16_t>), dim3(groups), dim3(256), 0, st, (const f16_t *)x, ld, rows, K, codes,
+                           scales);
+    return op_launched(call);
+}
+
+fi_status fi_q8_product(int64_t rows, int64_t N, int K, const void *a, const void *w, const float *bias, int dtype,
+                        void *y, int64_t ld_y, void *stream) {
+    static const char *call = "fi_q8_product";
+    if (const char *why = q8_check(rows, K)) return op_fail(FI_EINVAL, call, why);
+    if (N < 1 || N > kQ8MaxRows) return op_fail(FI_EINVAL, call, "N is not in 1 .. 2^24");
+    if (rows * N > int64_t(1) << 42) return op_fail(FI_EINVAL, call, "rows * N is over 2^42");
+    if (!value_type(dtype)) return op_fail(FI_EINVAL, call, "dtype is none of FI_F32, FI_BF16, FI_F16");
+    if (ld_y != 0 && (ld_y < N || ld_y > (int64_t(1) << 40))) return op_fail(FI_EINVAL, call, "a row pitch is less than N");
+    if (rows == 0) return FI_OK;
+    if (!a || !w || !y || (uintptr_t)a % 256 || (uintptr_t)w % 256)
+        return op_fail(FI_EINVAL, call, "a, w (aligned to 256 bytes) and y are required");
+    const size_t es = value_bytes(dtype);
+    if (!aligned(es, {y}) || !aligned(4, {bias})) return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
+    const int64_t ld = pitch_or(ld_y, N);
+    const size_t ba = fi_q8_bytes(rows, K), bw = fi_q8_bytes(N, K);
+    const View out = {y, rows, (size_t)N * es, (size_t)ld * es};
+    const View in[] = {{a, 1, ba, ba}, {w, 1, bw, bw}, {bias, 1, (size_t)N * 4, (size_t)N * 4}};
+    if (outputs_meet(&out, 1, in, 3)) return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
+    Q8Args p = {};
+    p.a = (const int8_t *)a, p.w = (const int8_t *)w, p.bias = bias, p.y = y;
+    p.sa = (const float *)((const char *)a + up256((size_t)q8_code_bytes(rows, K)));
+    p.sw = (const float *)((const char *)w + up256((size_t)q8_code_bytes(N, K)));
+    p.M = rows, p.N = N, p.ldy = ld, p.kp = q8_padded(K);
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == FI_F32) launch_product<float>(p, st);
+    else if (dtype == FI_BF16) launch_product<bf16_t>(p, st);
+    else launch_product<f16_t>(p, st);
+    return op_launched(call);
+}
+
+}  // extern "C"

@@ -109,6 +109,17 @@ def load_library():
         "fi_norm_workspace_bytes": (S, [P]),
         "fi_norm_forward": (I, [P] * 11),
         "fi_norm_backward": (I, [P] * 18),
+        "fi_delta_saved_bytes": (S, [P]),
+        "fi_delta_workspace_bytes": (S, [P, I]),
+        "fi_delta_forward": (I, [P] * 13),
+        "fi_delta_backward": (I, [P] * 19),
+        "fi_layer_workspace_bytes": (S, [P]),
+        "fi_layer_forward": (I, [P] * 9),
+        "fi_layer_backward": (I, [P] * 13),
+        "fi_q8_bytes": (S, [I64, I]),
+        "fi_q8_pack": (I, [I64, I, P, P, P, P]),
+        "fi_q8_quantize": (I, [I64, I, I, P, I64, P, P]),
+        "fi_q8_product": (I, [I64, I64, I, P, P, P, I, P, I64, P]),
         "fi_q4_packed_bytes": (S, [P]),
         "fi_q4_pack": (I, [P] * 6),
         "fi_q4_quantize": (I, [P, I, P, I64, P, P, P]),

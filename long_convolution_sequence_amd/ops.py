@@ -37,6 +37,8 @@ _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 # The descriptors of include/fi.h, packed (reserved fields zero).
 _SCAN_DESC = struct.Struct("=q4i6q16x")       # T batch channels dtype input ld_x ld_gate ld_y ld_dy ld_dx ld_dgate
 _NORM_DESC = struct.Struct("=q5if10q16x")     # rows channels dtype res_dtype post_norm act eps ld_o .. ld_dres
+_DELTA_DESC = struct.Struct("=q7if12q16x")     # T batch key_heads heads dk dv dtype unit scale ld_q .. ld_dbeta
+_LAYER_DESC = struct.Struct("=q3if8q16x")      # rows channels dtype res_dtype eps ld_x .. ld_dres
 _Q4_DESC = struct.Struct("=5i12x")            # N K group scale_dtype has_zeros
 
 
@@ -263,6 +265,151 @@ def gated_scan_backward(dy, x, gate, saved, bias=None, state=None, lengths=None,
     return dx, dgate, dbias, dstate
 
 
+# ---- gated delta rule ------------------------------------------------------------
+
+class DeltaGradients(NamedTuple):
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    decay: torch.Tensor
+    beta: torch.Tensor
+    state: Optional[torch.Tensor]
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_sizes(*head):
+    """Bytes of the forward pass's workspace, the backward pass's, and of what is saved."""
+    lib = load_library()
+    d = _pack(_DELTA_DESC, *head, 0.0, *([0] * 12))
+    return lib.fi_delta_workspace_bytes(d, 0), lib.fi_delta_workspace_bytes(d, 1), lib.fi_delta_saved_bytes(d)
+
+
+_DELTA_STEPS = 8           # positions up to which a forward call that saves nothing takes no workspace
+
+
+def _heads(t, shape, dtype, device, name):
+    """As _rows of a tensor [T][B][heads][d]: a row is all its heads."""
+    if t is None:
+        _bad(f"{name}: required")
+    if _packed(t, shape, dtype, device):
+        return t.data_ptr(), 0
+    _fits(t, shape, dtype, device, name)
+    if t.stride(-2) != shape[-1] and shape[-2] != 1:
+        _bad(f"{name}: the heads of a row are not packed")
+    return _rows(t.flatten(-2) if shape[-2] != 1 else t.squeeze(-2), (*shape[:-2], shape[-2] * shape[-1]), dtype, device,
+                 name)
+
+
+def _delta_inputs(q, k, v, decay, beta, state, lengths, scale, unit, positions=True):
+    device = _device(v, "v")
+    dtype = v.dtype
+    dt = _type(v, "v")
+    if not positions:
+        q, k, v, decay, beta = (t.unsqueeze(0) if isinstance(t, torch.Tensor) else t for t in (q, k, v, decay, beta))
+    dims = "[T][B]" if positions else "[B]"
+    if v.dim() != 4 or not v.shape[1] or not v.shape[2] or not v.shape[3]:
+        _bad(f"v: shape {tuple(v.shape)}, expected {dims}[heads][dv]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not q.shape[2] or not q.shape[3]:
+        _bad(f"q: expected a tensor {dims}[key heads][dk]")
+    T, B, H, dv = v.shape
+    HK, dk = q.shape[2:]
+    scale = dk ** -0.5 if scale is None else scale
+    keys = (T, B, HK, dk)
+    pq, ldq = _heads(q, keys, dtype, device, "q")
+    pk, ldk = _heads(k, keys, dtype, device, "k")
+    pv, ldv = _heads(v, v.shape, dtype, device, "v")
+    pg, ldg = _rows(decay, (T, B, H), torch.float32, device, "decay")
+    pb, ldb = _rows(beta, (T, B, H), torch.float32, device, "beta")
+    if decay is None or beta is None:
+        _bad("decay and beta: required")
+    return (device, dtype, keys, v.shape, (T, B, HK, H, dk, dv, dt, int(bool(unit))), scale, (ldq, ldk, ldv, ldg, ldb),
+            (pq, pk, pv, pg, pb, _dense(state, (B, H, dk, dv), torch.float32, device, "state"),
+             _dense(lengths, (B,), torch.int32, device, "lengths")))
+
+
+def gated_delta(q, k, v, decay, beta, state=None, lengths=None, *, scale=None, unit=False, save=False, y=None, final=None):
+    """The gated delta rule over a sequence (fi_delta_forward).
+
+    S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T with a_t = e^decay_t, y_t = scale S_t^T q_t.
+    unit: k and q are divided by their lengths (k / sqrt(sum k^2 + 1e-6)); scale None: 1 / sqrt(dk).
+
+    q, k [T][B][key heads][dk] and v [T][B][heads][dv] of one type, heads a multiple of key heads (groups
+    of neighbouring heads share one); decay (a logarithm, at most 0) and beta [T][B][heads] fp32; state
+    [B][heads][dk][dv] fp32 (before the first position) or None for zeros; lengths as in gated_scan.  dk
+    up to 128, dv to 1024.  Returns (y like v, final like state), with save=True also what
+    gated_delta_backward needs.  final may be given as the state itself.  Autograd does not see it."""
+    if not save and _any_requires_grad(q, k, v, decay, beta, state):
+        _not_recorded("gated_delta")
+    device, dtype, _, shape, head, scale, ld, args = _delta_inputs(q, k, v, decay, beta, state, lengths, scale, unit)
+    if y is None:
+        y = _like(v)
+        py, ldy = y.data_ptr(), 0
+    else:
+        py, ldy = _heads(y, shape, dtype, device, "y")
+    T, B, _, H, dk, dv = head[:6]
+    if final is None:
+        final = _like(state) if state is not None else v.new_empty((B, H, dk, dv), dtype=torch.float32)
+        pf = final.data_ptr()
+    else:
+        pf = _dense(final, (B, H, dk, dv), torch.float32, device, "final")
+    work, _, kept = _delta_sizes(*head)
+    work = _bytes(work, v) if save or T > _DELTA_STEPS else None
+    saved = _bytes(kept, v) if save else None
+    _call(device, load_library().fi_delta_forward, _pack(_DELTA_DESC, *head, scale, *ld, ldy, 0, 0, 0, 0, 0, 0), *args, py,
+          pf, saved.data_ptr() if save else None, work.data_ptr() if work is not None else None)
+    return (y, final, saved) if save else (y, final)
+
+
+def gated_delta_step(q, k, v, decay, beta, state, lengths=None, *, scale=None, unit=False, y=None):
+    """One position: q, k [B][key heads][dk], v [B][heads][dv], decay, beta [B][heads]; state
+    [B][heads][dk][dv] fp32 is updated in place.  lengths [B] int32 or None: a row with 0 is an empty slot
+    (y = 0, its state stays).  Returns y.  Autograd does not see it."""
+    if _any_requires_grad(q, k, v, decay, beta, state):
+        _not_recorded("gated_delta_step")
+    device, dtype, _, shape, head, scale, ld, args = _delta_inputs(q, k, v, decay, beta, state, lengths, scale, unit,
+                                                                   positions=False)
+    if state is None:
+        _bad("state: required")
+    if y is None:
+        y = _like(v)
+        py, ldy = y.data_ptr(), 0
+    else:
+        if not isinstance(y, torch.Tensor):
+            _bad(f"y: expected a torch tensor, got {type(y).__name__}")
+        py, ldy = _heads(y.unsqueeze(0), shape, dtype, device, "y")
+    _call(device, load_library().fi_delta_forward, _pack(_DELTA_DESC, *head, scale, *ld, ldy, 0, 0, 0, 0, 0, 0), *args, py,
+          args[5], None, None)
+    return y
+
+
+def gated_delta_backward(dy, q, k, v, decay, beta, saved, state=None, lengths=None, *, dfinal=None, scale=None, unit=False,
+                         dq=None, dk=None, dv=None):
+    """Gradients of gated_delta (fi_delta_backward): the forward call's arguments, its `saved`, and the
+    gradients dy like v and dfinal like state (or None) of its outputs.  Returns DeltaGradients; state's
+    is None where state is."""
+    device, dtype, keys, shape, head, scale, ld, args = _delta_inputs(q, k, v, decay, beta, state, lengths, scale, unit)
+    if dy is None or saved is None:
+        _bad("dy and saved are required")
+    T, B, _, H = head[:4]
+    pdy, lddy = _heads(dy, shape, dtype, device, "dy")
+    pdf = _dense(dfinal, (B, H, *head[4:6]), torch.float32, device, "dfinal")
+    dq = _like(q) if dq is None else dq
+    dk = _like(k) if dk is None else dk
+    dv = _like(v) if dv is None else dv
+    pdq, lddq = _heads(dq, keys, dtype, device, "dq")
+    pdk, lddk = _heads(dk, keys, dtype, device, "dk")
+    pdv, lddv = _heads(dv, shape, dtype, device, "dv")
+    ddecay, dbeta = (v.new_empty((T, B, H), dtype=torch.float32) for _ in range(2))
+    dstate = _like(state) if state is not None else None
+    _, work, kept = _delta_sizes(*head)
+    psv = _dense(saved, (kept,), torch.uint8, device, "saved")
+    work = _bytes(work, v)
+    _call(device, load_library().fi_delta_backward,
+          _pack(_DELTA_DESC, *head, scale, *ld, 0, lddy, lddq, lddk, lddv, 0, 0), *args, psv, pdy, pdf, pdq, pdk, pdv,
+          ddecay.data_ptr(), dbeta.data_ptr(), dstate.data_ptr() if dstate is not None else None, work.data_ptr())
+    return DeltaGradients(dq, dk, dv, ddecay, dbeta, dstate)
+
+
 # ---- norms around a block --------------------------------------------------------
 
 class NormGradients(NamedTuple):
@@ -364,6 +511,114 @@ def block_norm_backward(dr, da, o, res, gate, saved, *, post_weight=None, scale=
     return NormGradients(do, dres, dgate, *w)
 
 
+# ---- layer norm --------------------------------------------------------------------
+
+class LayerGradients(NamedTuple):
+    x: torch.Tensor
+    res: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+
+
+def _layer_inputs(x, res, weight, bias, eps, dtype):
+    """As the C call takes them: without a residual, an fp32 x that is normed into another type is its `res`."""
+    device = _device(x, "x")
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        _bad(f"x: shape {tuple(shape)}, expected [..., D]")
+    D = shape[-1]
+    dt = x.dtype if dtype is None else dtype
+    if dt not in _TYPES:
+        _bad(f"dtype: {dtype}, expected float32, bfloat16 or float16")
+    alone = None
+    if dt is not x.dtype:
+        if res is not None or x.dtype is not torch.float32:
+            _bad(f"dtype: {dt}, expected x's {x.dtype} (only an fp32 x without res is normed into another type)")
+        alone, x, res = x, None, x
+    rt = res.dtype if isinstance(res, torch.Tensor) else dt
+    if rt is not dt and rt is not torch.float32:
+        _bad(f"res: dtype {rt}, expected {dt} or torch.float32")
+    px, ldx = _rows(x, shape, dt, device, "x")
+    pr, ldr = _rows(res, shape, rt, device, "res")
+    rows = (x if x is not None else res).numel() // D
+    _type(x if x is not None else res, "x")
+    head = (rows, D, _TYPES[dt], _TYPES[rt], eps, ldx, ldr)
+    return (device, shape, dt, rt, rows, alone, head,
+            (px, pr, _dense(weight, (D,), torch.float32, device, "weight")),
+            _dense(bias, (D,), torch.float32, device, "bias"))
+
+
+def layer_norm(x, res=None, *, weight=None, bias=None, eps=1e-5, dtype=None, save=False, r=None, a=None):
+    """The layer norm with a residual (fi_layer_forward).
+
+    r = res + x, a = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) * weight + bias; what is None is
+    left out.  x, a [..., D] of one type; res, r of that type or fp32; weight and bias fp32 [D].
+    Without res an fp32 x can be normed into 16 bits (dtype).  r may be given as res itself.  Returns
+    (r, a), r being x where there is no res; with save=True also what layer_norm_backward needs.
+    Autograd does not see it."""
+    if not save and _any_requires_grad(x, res, weight, bias):
+        _not_recorded("layer_norm")
+    device, shape, dt, rt, rows, alone, head, args, pb = _layer_inputs(x, res, weight, bias, eps, dtype)
+    if res is None:
+        if r is not None:
+            _bad("r: without res it is x itself")
+        pr, ldr, r = None, 0, x
+    elif r is None:
+        r = _like(res)
+        pr, ldr = r.data_ptr(), 0
+    else:
+        pr, ldr = _rows(r, shape, rt, device, "r")
+    if a is None:
+        a = _like(x) if alone is None else x.new_empty(shape, dtype=dt)
+        pa, lda = a.data_ptr(), 0
+    else:
+        pa, lda = _rows(a, shape, dt, device, "a")
+    saved = torch.empty((2, rows), dtype=torch.float32, device=x.device) if save else None
+    _call(device, load_library().fi_layer_forward, _pack(_LAYER_DESC, *head, ldr, lda, 0, 0, 0, 0), *args, pb, pr, pa,
+          saved.data_ptr() if save else None)
+    return (r, a, saved) if save else (r, a)
+
+
+@functools.lru_cache(maxsize=256)
+def _layer_workspace(rows, D, dtype, res_dtype):
+    return load_library().fi_layer_workspace_bytes(_pack(_LAYER_DESC, rows, D, dtype, res_dtype, 0.0, *([0] * 8)))
+
+
+def layer_norm_backward(dr, da, x, res, saved, *, weight=None, bias=None, eps=1e-5, dtype=None, dx=None, dres=None):
+    """Gradients of layer_norm (fi_layer_backward) from those of r and a (either may be None): the
+    forward call's arguments and its `saved`.  Returns LayerGradients, None where the input is None (x
+    and res have the same gradient, each in its type).  dres may be given as dr itself."""
+    device, shape, dt, rt, rows, alone, head, args, _ = _layer_inputs(x, res, weight, bias, eps, dtype)
+    if saved is None:
+        _bad("saved: required")
+    psv = _dense(saved, (2, rows), torch.float32, device, "saved")
+    pdr, lddr = _rows(dr, shape, rt, device, "dr")
+    pda, ldda = _rows(da, shape, dt, device, "da")
+    if res is None and dres is not None:
+        _bad("dres: without res there is none")
+    if alone is not None:                        # x's gradient is the C call's dres
+        dx = _like(x) if dx is None else dx
+        (pdx, lddx), (pdres, lddres) = (None, 0), _rows(dx, shape, rt, device, "dx")
+    else:
+        dx = _like(x) if dx is None else dx
+        dres = _like(res) if res is not None and dres is None else dres
+        pdx, lddx = _rows(dx, shape, dt, device, "dx")
+        pdres, lddres = _rows(dres, shape, rt, device, "dres")
+    D = shape[-1]
+    cols = torch.empty((2, D), dtype=torch.float32, device=x.device)
+    w = [cols[i] if t is not None else None for i, t in enumerate((weight, bias))]
+    ptr = [t.data_ptr() if t is not None else None for t in w]
+    if da is None:
+        for t in w:
+            if t is not None:
+                t.zero_()
+        ptr = [None, None]
+    work = _bytes(_layer_workspace(rows, D, head[2], head[3]), x)
+    _call(device, load_library().fi_layer_backward, _pack(_LAYER_DESC, *head, 0, 0, lddr, ldda, lddx, lddres), *args, psv,
+          pdr, pda, pdx, pdres, *ptr, work.data_ptr())
+    return LayerGradients(dx, dres, *w)
+
+
 # ---- 4-bit products ----------------------------------------------------------------
 
 class Q4Weight:
@@ -439,4 +694,98 @@ def q4_matvec(w, x, y=None):
     else:
         py, ldy = _rows(y, (rows, w.N), dtype, device, "y")
     _call(device, load_library().fi_q4_matvec, w._desc, w.packed.data_ptr(), rows, dt, px, ldx, py, ldy)
+    return y
+
+
+# ---- 8-bit products ----------------------------------------------------------------
+
+class Q8Rows:
+    """A matrix [rows][K] in 8-bit integers with an fp32 scale a row, laid out for q8_product
+    (fi_q8_pack): activations, or a weight [N][K].
+
+    codes [rows][K] int8, scales [rows] fp32; Q8Rows.quantize makes them from values."""
+
+    def __init__(self, codes, scales):
+        self._make(codes, "codes")
+        rows, K = codes.shape
+        pc = _dense(codes, codes.shape, torch.int8, self._index, "codes")
+        ps = _dense(scales, (rows,), torch.float32, self._index, "scales")
+        if ps is None:
+            _bad("scales: required")
+        _call(self._index, load_library().fi_q8_pack, rows, K, pc, ps, self.packed.data_ptr())
+
+    def _make(self, t, name):
+        device = _device(t, name)
+        if t.dim() != 2 or t.shape[1] < 1:
+            _bad(f"{name}: shape {tuple(t.shape)}, expected [rows][K]")
+        rows, K = t.shape
+        if rows > 1 << 24 or K > 131071:
+            _bad(f"unsupported rows={rows} K={K}")
+        self.rows, self.K, self.device, self._index = rows, K, t.device, device
+        self.packed = _bytes(load_library().fi_q8_bytes(rows, K), t)
+
+    @classmethod
+    def quantize(cls, x):
+        """From values x [rows][K]: scale = max|x| / 127 of each row, codes rounded to nearest."""
+        out = cls.__new__(cls)
+        out._make(x, "x")
+        dt = _type(x, "x")
+        px, ld = _rows(x, x.shape, x.dtype, out._index, "x")
+        _call(out._index, load_library().fi_q8_quantize, out.rows, out.K, dt, px, ld, out.packed.data_ptr())
+        return out
+
+    @property
+    def codes(self):
+        """The codes [rows][K] int8 (a copy in their plain order)."""
+        r, k = -(-self.rows // 16), -(-self.K // 128) * 2
+        c = self.packed[:r * 16 * k * 64].view(torch.int8).view(r, k, 4, 16, 16).permute(0, 3, 1, 2, 4)
+        return c.reshape(r * 16, k * 64)[:self.rows, :self.K].contiguous()
+
+    @property
+    def scales(self):
+        """The scales [rows] fp32 (a view)."""
+        r, k = -(-self.rows // 16) * 16, -(-self.K // 128) * 128
+        at = -(-r * k // 256) * 256
+        return self.packed[at:at + 4 * self.rows].view(torch.float32)
+
+
+class Q8Weight(Q8Rows):
+    """A weight matrix [N][K] in 8-bit integers with a scale an output."""
+
+    @property
+    def N(self):
+        return self.rows
+
+
+def q8_product(w, x, bias=None, *, dtype=None, y=None):
+    """y [rows][N] = x [rows][K] times a Q8Weight, plus bias [N] fp32 (fi_q8_product).  x is a tensor,
+    which is brought to 8 bits with a scale a row first, or Q8Rows (one quantization for several weights;
+    then dtype says y's type, else it is x's).  Autograd does not see it."""
+    if not isinstance(w, Q8Rows):
+        _bad(f"w: expected a Q8Weight, got {type(w).__name__}")
+    if isinstance(x, Q8Rows):
+        dt = torch.bfloat16 if dtype is None else dtype
+    else:
+        device = _device(x, "x")
+        if _any_requires_grad(x, bias):
+            _not_recorded("q8_product")
+        if device != w._index:
+            _bad(f"x: on {x.device}, expected {w.device}")
+        if x.dim() != 2 or x.shape[1] != w.K:
+            _bad(f"x: shape {tuple(x.shape)}, expected [rows][{w.K}]")
+        dt = x.dtype if dtype is None else dtype
+        x = Q8Rows.quantize(x)
+    if dt not in _TYPES:
+        _bad(f"dtype: {dt}, expected float32, bfloat16 or float16")
+    device = w._index
+    if x._index != device or x.K != w.K:
+        _bad(f"x: [{x.rows}][{x.K}] on {x.device}, expected [rows][{w.K}] on {w.device}")
+    pb = _dense(bias, (w.rows,), torch.float32, device, "bias")
+    if y is None:
+        y = torch.empty((x.rows, w.rows), dtype=dt, device=w.device)
+        py, ldy = y.data_ptr(), 0
+    else:
+        py, ldy = _rows(y, (x.rows, w.rows), dt, device, "y")
+    _call(device, load_library().fi_q8_product, x.rows, w.rows, w.K, x.packed.data_ptr(), w.packed.data_ptr(), pb,
+          _TYPES[dt], py, ldy)
     return y
