@@ -24,12 +24,11 @@
 
 namespace fi {
 
-namespace {
-
 constexpr int kDeltaMaxK = 128;        // channels of a key at most
 constexpr int kDeltaMaxV = 1024;       // of a value
 constexpr float kDeltaUnit = 1e-6f;    // k / sqrt(sum k^2 + this)
 constexpr int kPiece = 1024;           // bytes of an operand's piece
+constexpr int kDeltaFactors = 9;
 constexpr float kLog2e = 1.44269504088896f;
 
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
@@ -68,7 +67,7 @@ struct DeltaArgs {
     float scale;
     // [chunk][B][H] of each
     char *images;                          // M and P of a chunk (backwards N^T and P^T)
-    float *factors;                        // [5][C]
+    float *factors;                        // [kDeltaFactors][C]
     float *states;                         // [dk][dv] before each chunk, and [B][H] of them after the last
     float *ends;                           // backwards [dk][dv] after each chunk
     float *w, *x;                          // [C][dv]
@@ -231,8 +230,9 @@ constexpr int image_bytes() {          // of a chunk: M in three terms and P
 // P_ij = scale E_ij (q_i . k_j) b_j, and the factors e^G_i of k_i S, scale e^G_i of
 // q_i S, e^(G_C - G_i) b_i of k_i, e^(G_C).  Backwards those of N^T, N = (I + A')^-1
 // with A'_ij = b_i E_ij (k_i . k_j), and of P^T without the b_j, and e^(G_C - G_i),
-// scale e^G_i, e^G_i b_i, b_i, e^(G_C).  "unit" divides k and q by their lengths in
-// these factors, so the operands stay the inputs themselves.
+// scale e^G_i, e^G_i b_i, b_i, e^(G_C), both lengths' reciprocals and G in two floats.
+// "unit" divides k and q by their lengths in these factors, so the operands stay the
+// inputs themselves.
 // The inverse: lane j solves for column j, row by row from registers, the rows of A
 // read from LDS for all lanes at once.
 template <typename T, int KT, bool BACK>
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
         const float a = both_halves(ssk[mt]), c = both_halves(ssq[mt]);
         if (half == 0) {
             fk[mt * 32 + col] = p.unit ? 1.f / sqrtf(a + kDeltaUnit) : 1.f;
-            fq[mt * 32 + col] = p.scale * (p.unit ? 1.f / sqrtf(c + kDeltaUnit) : 1.f);
+            fq[mt * 32 + col] = p.unit ? 1.f / sqrtf(c + kDeltaUnit) : 1.f;
         }
     }
     __syncthreads();
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
                 if (j <= i && row >= c) {
                     e = exp2f((float)(sum[row] - sum[c])) * fk[c];
                     if (row > c) a = e * fk[row] * fb[BACK ? row : c] * kk[i][j <= i ? j : 0][r];
-                    e *= fq[row] * (BACK ? 1.f : fb[c]);
+                    e *= p.scale * fq[row] * (BACK ? 1.f : fb[c]);
                 }
                 m[row * LD + c] = a;
                 if (j <= i) qk[i][j <= i ? j : 0][r] *= e;       // P
@@ -384,13 +384,17 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
     __syncthreads();
     flush(image + 3 * C * C * 2, std::integral_constant<int, PT>());
     if (lane < C) {
-        float *f = p.factors + at * 5 * C;
+        float *f = p.factors + at * kDeltaFactors * C;
         const float rise = exp2f((float)sum[lane]), fall = exp2f((float)(sum[C - 1] - sum[lane]));
         f[lane] = fk[lane] * (BACK ? fall : rise);
-        f[C + lane] = fq[lane] * rise;
+        f[C + lane] = p.scale * fq[lane] * rise;
         f[2 * C + lane] = fk[lane] * (BACK ? rise : fall) * fb[lane];
         f[3 * C + lane] = fb[lane];
         f[4 * C + lane] = exp2f((float)sum[C - 1]);
+        f[5 * C + lane] = fk[lane];
+        f[6 * C + lane] = fq[lane];
+        f[7 * C + lane] = (float)sum[lane];
+        f[8 * C + lane] = (float)(sum[lane] - (double)(float)sum[lane]);
     }
 }
 
@@ -423,7 +427,7 @@ inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
     const size_t all = (size_t)d.chunks * heads, C = d.C, sk = (size_t)q->dk * q->dv * 4;
     const size_t out = backward || q->dtype == FI_F32 ? 3 : 2;
     d.images = up256(all * C * C * 2 * (3 + out));
-    d.factors = up256(all * 5 * C * 4);
+    d.factors = up256(all * kDeltaFactors * C * 4);
     d.states = up256(all * sk);
     d.ends = up256(all * sk);
     d.rows = up256(all * C * q->dv * 4);
@@ -432,8 +436,6 @@ inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
     d.maps = up256(parts * q->dk * q->dk * 4);
     return d;
 }
-
-}  // namespace
 
 const char *delta_check(const fi_delta_desc *q);
 void delta_args(const fi_delta_desc *q, const DeltaPlan &plan, DeltaArgs &a);

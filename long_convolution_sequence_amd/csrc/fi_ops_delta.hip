@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
         stage<T, C>(k + (t0 * p.B + b) * p.ldk, p.B * p.ldk, p.dk, DK, live, ik, ikt);
         if (FULL) stage<T, C>(q + (t0 * p.B + b) * p.ldq, p.B * p.ldq, p.dk, DK, live, iq, nullptr);
         copy_in(im, p.images + at * image_bytes<T, false>(), FULL ? (3 + NY) * MB : 3 * MB);
-        copy_in((char *)f, (const char *)(p.factors + at * 5 * C), 5 * C * 4);
+        copy_in((char *)f, (const char *)(p.factors + at * kDeltaFactors * C), 5 * C * 4);
         __syncthreads();
 
         if (FULL && p.states) keep(p.states + at * p.dk * p.dv, p.dv);
@@ -320,7 +320,9 @@ void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
     hipLaunchKernelGGL((k_delta_prep<T, KT, false>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
     if (a.segments > 1) {
         const int all = tiles + KT;
-        hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_LOCAL>), dim3((unsigned)((a.segments - 1) * heads), (all + 3) / 4),
+        // the last segment's map is the backward pass's alone
+        const int parts = a.states ? a.segments : a.segments - 1;
+        hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_LOCAL>), dim3((unsigned)(parts * heads), (all + 3) / 4),
                            dim3(std::min(4, all) * 64), N * KB * 2 + 3 * MB + 5 * C * 4, st, a);
         delta_join(a, a.state, false, st);
     }

@@ -1,5 +1,497 @@
+// The gated delta rule's gradients.  Per chunk, with D the gradient of the state
+// behind it, w and S as the forward pass kept them, N = (I + A')^-1,
+// A'_ij = b_i E_ij (k_i . k_j) (i > j) and dy scaled:
+//   x = N^T (P^T dy + e^(G_C - G) K D),  dv = b x,  dbeta_i = x_i . w_i,
+//   the gradient before it  e^(G_C) D + (e^G Q)^T dy - (e^G K)^T dv,
+// which again passes from chunk to chunk column by column, from the last to the
+// first.  The rest is a chunk's own, with H_ij = -b_i b_j E_ij (x_i . w_j) (i > j) and
+// J_ij = b_j E_ij (dy_i . w_j) (i >= j):
+//   dq_i = sum_j J_ij k_j + e^G_i S dy_i,
+//   dk_i = sum_j (H_ij + H_ji) k_j + sum_j J_ji q_j - e^G_i S dv_i + e^(G_C - G_i) b_i D w_i,
+//   ddecay_t = <D, S'> + sum_{i >= t} (q_i . dq_i - v_i . dv_i)  with S' the state behind the
+// chunk: y is linear in q, and a decay scales what was written before it against
+// what is written after.
 #include "fi_delta.h"
-extern "C" fi_status fi_delta_backward(const fi_delta_desc *desc, const void *q, const void *k, const void *v, const float *decay,
-                            const float *beta, const float *state, const int32_t *lengths, const void *saved,
-                            const void *dy, const float *dfinal, void *dq, void *dk, void *dv, float *ddecay,
-                            float *dbeta, float *dstate, void *workspace, void *stream) { return FI_EINVAL; }
+
+namespace fi {
+
+namespace {
+
+// The gradient of the state through a segment's chunks, 32 columns a wave, backwards.
+// FULL: from the gradient behind the segment; dv, x and the gradients behind each
+// chunk.  Else from nothing, only the gradient before the segment.
+template <typename T, int KT, bool FULL>
+__global__ void __launch_bounds__(256) k_delta_back_chain(DeltaArgs p) {
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
+    constexpr int MT = C / 32, CS = C / 16, KS = KT * 2, DK = KT * 32;
+    constexpr int KB = C * DK * 2, MB = C * C * 2;
+    extern __shared__ __align__(16) char lds[];
+    char *const ik = lds, *const ikt = ik + N * KB, *const iqt = ikt + N * KB, *const in = iqt + N * KB, *const ip = in + 3 * MB;
+    float *const f = reinterpret_cast<float *>(ip + 3 * MB);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int heads = p.B * p.H, seg = blockIdx.x / heads + (FULL ? 0 : 1), bh = blockIdx.x % heads, b = bh / p.H, h = bh % p.H;
+    const int column = (blockIdx.y * 4 + wave) * 32 + (lane & 31);
+    const bool mine = column < p.dv;
+    const int64_t length = delta_length(p, b), size = (int64_t)p.dk * p.dv;
+    const int hk = h / (p.H / p.HK);
+
+    f32x16 D[KT];
+    const float *from = !FULL ? nullptr : p.segments > 1 ? p.starts + ((int64_t)seg * heads + bh) * size
+                                        : p.dfinal       ? p.dfinal + bh * size
+                                                         : nullptr;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = t * 32 + acc_row(r);
+            D[t][r] = from && mine && row < p.dk ? from[(int64_t)row * p.dv + column] : 0.f;
+        }
+    const auto keep = [&](float *to) {
+        if (!mine) return;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = t * 32 + acc_row(r);
+                if (row < p.dk) to[(int64_t)row * p.dv + column] = D[t][r];
+            }
+    };
+    const T *const q = static_cast<const T *>(p.q) + hk * p.dk, *const k = static_cast<const T *>(p.k) + hk * p.dk;
+    const T *const dy = static_cast<const T *>(p.dy) + (int64_t)h * p.dv;
+    T *const dv = FULL ? static_cast<T *>(p.dv_out) + (int64_t)h * p.dv : nullptr;
+    const int64_t first = seg * p.per, last = min(p.chunks, first + p.per);
+    for (int64_t c = last - 1; c >= first; --c) {
+        const int64_t t0 = c * C, n = length - t0, at = c * heads + bh;
+        const int rows = (int)min<int64_t>(C, p.T - t0), live = n < 0 ? 0 : n < rows ? (int)n : rows;
+        if (live == 0) {
+            if (FULL && mine)
+                for (int i = lane >> 5; i < rows; i += 2) dv[((t0 + i) * p.B + b) * p.lddv + column] = (T)0.f;
+            continue;
+        }
+        __syncthreads();
+        stage<T, C>(k + (t0 * p.B + b) * p.ldk, p.B * p.ldk, p.dk, DK, live, ik, ikt);
+        stage<T, C>(q + (t0 * p.B + b) * p.ldq, p.B * p.ldq, p.dk, DK, live, nullptr, iqt);
+        copy_in(in, p.images + at * image_bytes<T, true>(), 6 * MB);
+        copy_in((char *)f, (const char *)(p.factors + at * kDeltaFactors * C), 5 * C * 4);
+        __syncthreads();
+
+        if (FULL) keep(p.ends + at * size);
+        f32x16 X[MT], Y[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            X[i] = zeros16();
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = i * 32 + acc_row(r);
+                Y[i][r] = mine && row < live ? (float)dy[((t0 + row) * p.B + b) * p.lddy + column] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const Frag<3> s = step_of<3>(D[ks / 2], ks & 1);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) multiply<2>(X[i], piece<N>(ik, i * KS + ks, KB), s);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) X[i][r] *= f[i * 32 + acc_row(r)];
+#pragma unroll
+        for (int cs = 0; cs < CS; ++cs) {
+            const Frag<N> s = step_of<N>(Y[cs / 2], cs & 1);
+#pragma unroll
+            for (int i = 0; i <= cs / 2; ++i) multiply<2>(X[i], piece<3>(ip, i * CS + cs, MB), s);
+        }
+        f32x16 Z[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) Z[i] = zeros16();
+#pragma unroll
+        for (int cs = 0; cs < CS; ++cs) {
+            const Frag<3> s = step_of<3>(X[cs / 2], cs & 1);
+#pragma unroll
+            for (int i = 0; i <= cs / 2; ++i) multiply<2>(Z[i], piece<3>(in, i * CS + cs, MB), s);
+        }
+        if (FULL && mine) {
+            float *to = p.x + at * C * p.dv + column;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = i * 32 + acc_row(r);
+                    to[row * p.dv] = Z[i][r];
+                    if (row < rows) dv[((t0 + row) * p.B + b) * p.lddv + column] = (T)(row < live ? Z[i][r] * f[3 * C + row] : 0.f);
+                }
+        }
+        const float decay = f[4 * C];
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) D[t][r] *= decay;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = i * 32 + acc_row(r);
+                Y[i][r] *= f[C + row];
+                Z[i][r] *= -f[2 * C + row];
+            }
+#pragma unroll
+        for (int cs = 0; cs < CS; ++cs) {
+            const Frag<3> sy = step_of<3>(Y[cs / 2], cs & 1), sz = step_of<3>(Z[cs / 2], cs & 1);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                multiply<2>(D[t], piece<N>(iqt, t * CS + cs, KB), sy);
+                multiply<2>(D[t], piece<N>(ikt, t * CS + cs, KB), sz);
+            }
+        }
+    }
+    if (!FULL)
+        keep(p.local + ((int64_t)seg * heads + bh) * size);
+    else if (seg == 0 && p.dstate)
+        keep(p.dstate + bh * size);
+}
+
+// Sum over the 32 lanes of a half, in every lane of it.
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) v += __shfl_xor(v, s, 64);
+    return v;
+}
+
+// What is a chunk's own, for a key head and the heads that share it: a workgroup a
+// chunk, a wave 32 channels of the keys.
+template <typename T, int KT>
+__global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
+    constexpr int MT = C / 32, CS = C / 16, DK = KT * 32, KB = C * DK * 2, LD = C + 4, SB = MT * 2 * kPiece;
+    extern __shared__ __align__(16) char lds[];
+    char *const ix = lds, *const iw = ix + 3 * SB, *const iy = iw + 3 * SB, *const ikt = iy + N * SB, *const iqt = ikt + N * KB;
+    float *const Hm = reinterpret_cast<float *>(iqt + N * KB), *const Jm = Hm + C * LD;
+    __shared__ double G[C];
+    __shared__ float beta[C], rk[C], rq[C], dotb[C], dotv[C], dotq[4][C], dotk[4][C], total[2][4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5, col = lane & 31;
+    const int hk = blockIdx.x % p.HK, b = blockIdx.x / p.HK % p.B, share = p.H / p.HK, heads = p.B * p.H;
+    const int64_t c = blockIdx.x / p.HK / p.B, t0 = c * C, n = delta_length(p, b) - t0;
+    const int rows = (int)min<int64_t>(C, p.T - t0), live = n < 0 ? 0 : n < rows ? (int)n : rows;
+    T *const dq = static_cast<T *>(p.dq) + hk * p.dk, *const dk = static_cast<T *>(p.dk_out) + hk * p.dk;
+    if (live == 0) {
+        for (int u = tid; u < rows * p.dk; u += 256) {
+            const int64_t row = (t0 + u / p.dk) * p.B + b;
+            dq[row * p.lddq + u % p.dk] = (T)0.f;
+            dk[row * p.lddk + u % p.dk] = (T)0.f;
+        }
+        for (int u = tid; u < rows * share; u += 256) {
+            const int64_t row = (t0 + u / share) * p.B + b;
+            p.dg[row * p.lddg + hk * share + u % share] = 0.f;
+            p.dbeta[row * p.lddb + hk * share + u % share] = 0.f;
+        }
+        return;
+    }
+    const int64_t row0 = t0 * p.B + b;
+    stage<T, C>(static_cast<const T *>(p.k) + hk * p.dk + row0 * p.ldk, p.B * p.ldk, p.dk, DK, live, nullptr, ikt);
+    stage<T, C>(static_cast<const T *>(p.q) + hk * p.dk + row0 * p.ldq, p.B * p.ldq, p.dk, DK, live, nullptr, iqt);
+    // four positions of this lane's channel, of an image of k or q
+    const auto four = [&](const char *image, int i, float (&x)[4]) {
+        x[0] = x[1] = x[2] = x[3] = 0.f;
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            const bf16x4 v = *reinterpret_cast<const bf16x4 *>(image + t * KB + image_at(wave * 32 + col, i, CS));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] += (float)v[j];
+        }
+    };
+    const int d = wave * 32 + col;                       // this lane's channel
+    f32x16 allq[MT], allk[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) allq[i] = allk[i] = zeros16();
+    float sumq = 0.f;                                    // q . dq of row `lane`, over the heads
+
+    for (int s = 0; s < share; ++s) {
+        const int h = hk * share + s;
+        const int64_t at = c * heads + b * p.H + h;
+        __syncthreads();
+        if (tid < C) {
+            const float *f = p.factors + at * kDeltaFactors * C;
+            beta[tid] = f[3 * C + tid], rk[tid] = f[5 * C + tid], rq[tid] = f[6 * C + tid];
+            G[tid] = (double)f[7 * C + tid] + (double)f[8 * C + tid];
+        }
+        const float *const x = p.x + at * C * p.dv, *const w = p.w + at * C * p.dv;
+        const float *const S = p.states + at * p.dk * p.dv, *const D = p.ends + at * p.dk * p.dv;
+        const T *const v = static_cast<const T *>(p.v) + row0 * p.ldv + (int64_t)h * p.dv;
+        const T *const dy = static_cast<const T *>(p.dy) + row0 * p.lddy + (int64_t)h * p.dv;
+        f32x16 ys[MT], xs[MT], wd[MT], xw = zeros16(), yw = zeros16();
+#pragma unroll
+        for (int i = 0; i < MT; ++i) ys[i] = xs[i] = wd[i] = zeros16();
+        float db[MT], dw[MT], inner = 0.f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) db[i] = dw[i] = 0.f;
+        for (int c0 = 0; c0 < p.dv; c0 += 32) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < MT; ++e) {
+                const int i = e * 32 + tid / 8, cc = c0 + tid % 8 * 4, to = image_at(i, tid % 8 * 4, 2);
+                float a[4], u[4], z[4], y[4];
+                load4(a, x + i * p.dv, cc, p.dv, i < live);
+                load4(u, w + i * p.dv, cc, p.dv, i < live);
+                load4(z, v + (int64_t)i * p.B * p.ldv, cc, p.dv, i < live);
+                load4(y, dy + (int64_t)i * p.B * p.lddy, cc, p.dv, i < live);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) db[e] = fmaf(a[j], u[j], db[e]), dw[e] = fmaf(a[j], z[j], dw[e]);
+                put_terms<3>(ix, to, SB, a);
+                put_terms<3>(iw, to, SB, u);
+                put_terms<N>(iy, to, SB, y);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                if (wave < KT) {
+                    const auto fetch = [&](const float *from, float (&v8)[8]) {
+                        float lo[4], hi[4];
+                        load4(lo, from + (int64_t)d * p.dv, c0 + st * 16 + 4 * half, p.dv, d < p.dk);
+                        load4(hi, from + (int64_t)d * p.dv, c0 + st * 16 + 4 * half + 8, p.dv, d < p.dk);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v8[j] = lo[j], v8[4 + j] = hi[j];
+                    };
+                    float s8[8], d8[8];
+                    fetch(S, s8), fetch(D, d8);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) inner = fmaf(s8[j], d8[j], inner);
+                    const Frag<3> fs = split<3>(s8), fd = split<3>(d8);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        multiply<2>(ys[i], piece<N>(iy, i * 2 + st, SB), fs);
+                        multiply<2>(xs[i], piece<3>(ix, i * 2 + st, SB), fs);
+                        multiply<2>(wd[i], piece<3>(iw, i * 2 + st, SB), fd);
+                    }
+                }
+                if (wave < MT * MT) {
+                    const Frag<3> fw = piece<3>(iw, wave % MT * 2 + st, SB);
+                    multiply<2>(xw, piece<3>(ix, wave / MT * 2 + st, SB), fw);
+                    multiply<2>(yw, piece<N>(iy, wave / MT * 2 + st, SB), fw);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < MT; ++e) {
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) db[e] += __shfl_xor(db[e], o, 64), dw[e] += __shfl_xor(dw[e], o, 64);
+            if (tid % 8 == 0) dotb[e * 32 + tid / 8] = db[e], dotv[e * 32 + tid / 8] = dw[e];
+        }
+        if (wave < MT * MT) {
+            const int j = wave % MT * 32 + col;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int i = wave / MT * 32 + acc_row(r);
+                float e = 0.f;
+                if (i >= j) e = exp2f((float)(G[i] - G[j])) * beta[j];
+                Hm[i * LD + j] = i > j ? -beta[i] * e * xw[r] : 0.f;
+                Jm[i * LD + j] = p.scale * e * yw[r];
+            }
+        }
+        __syncthreads();
+        float part = 0.f;
+        if (wave < KT) {
+            f32x16 gq[MT], gk[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) gq[i] = gk[i] = zeros16();
+#pragma unroll
+            for (int cs = 0; cs < CS; ++cs) {
+                const Frag<N> fk = piece<N>(ikt, wave * CS + cs, KB), fq = piece<N>(iqt, wave * CS + cs, KB);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    float a[8], e[8], u[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = i * 32 + col, t = cs * 16 + 8 * (j >> 2) + 4 * half + (j & 3);
+                        a[j] = Jm[r * LD + t] * rk[t];
+                        e[j] = Jm[t * LD + r] * rq[t];
+                        u[j] = (r > t ? Hm[r * LD + t] : Hm[t * LD + r]) * rk[t];
+                    }
+                    multiply<2>(gq[i], split<3>(a), fk);
+                    multiply<2>(gk[i], split<3>(e), fq);
+                    multiply<2>(gk[i], split<3>(u), fk);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    float qv[4], kv[4];
+                    four(iqt, i * 32 + acc_row(r4 * 4), qv);
+                    four(ikt, i * 32 + acc_row(r4 * 4), kv);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
+                        const float rise = exp2f((float)G[row]), fall = exp2f((float)(G[C - 1] - G[row])) * beta[row];
+                        const float g = fmaf(p.scale * rise, ys[i][r], gq[i][r]);
+                        part = fmaf(rk[row] * fall * kv[j], wd[i][r], part);
+                        allq[i][r] += g;
+                        allk[i][r] += fmaf(fall, wd[i][r], fmaf(-rise * beta[row], xs[i][r], gk[i][r]));
+                        const float dot = half_sum(rq[row] * qv[j] * g);
+                        if (col == 0) dotq[wave][row] = dot;
+                    }
+                }
+        }
+        inner = lanes_sum(inner), part = lanes_sum(part);
+        if (lane == 0) total[0][wave] = inner, total[1][wave] = part;
+        __syncthreads();
+        if (wave == 0) {
+            float all = 0.f, end = 0.f, qd = 0.f, g = 0.f;
+#pragma unroll
+            for (int i = 0; i < KT; ++i) all += total[0][i], end += total[1][i];
+            all = fmaf(exp2f((float)G[C - 1]), all, end);
+            if (lane < C) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) qd += dotq[i][lane];
+                g = fmaf(-beta[lane], dotv[lane], qd);
+            }
+            sumq += qd;
+#pragma unroll
+            for (int o = 1; o < C; o *= 2) {
+                const float z = __shfl_down(g, o, 64);
+                if (lane + o < C) g += z;
+            }
+            if (lane < rows) {
+                const int64_t row = row0 + (int64_t)lane * p.B;
+                p.dg[row * p.lddg + h] = lane < live ? g + all : 0.f;
+                p.dbeta[row * p.lddb + h] = lane < live ? dotb[lane] : 0.f;
+            }
+        }
+    }
+    // over the lengths: d = r (d^ - x^ (x^ . d^)), x^ = r x
+    if (p.unit) {
+        __syncthreads();
+        if (wave == 0 && lane < C) dotv[lane] = sumq;
+        if (wave < KT)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    float kv[4];
+                    four(ikt, i * 32 + acc_row(r4 * 4), kv);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
+                        const float dot = half_sum(rk[row] * kv[j] * allk[i][r]);
+                        if (col == 0) dotk[wave][row] = dot;
+                    }
+                }
+        __syncthreads();
+    }
+    if (wave >= KT || d >= p.dk) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            float qv[4], kv[4];
+            four(iqt, i * 32 + acc_row(r4 * 4), qv);
+            four(ikt, i * 32 + acc_row(r4 * 4), kv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
+                if (row >= rows) continue;
+                float gq = allq[i][r], gk = allk[i][r];
+                if (p.unit) {
+                    float dot = 0.f;
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) dot += dotk[t][row];
+                    gq = rq[row] * fmaf(-rq[row] * qv[j], dotv[row], gq);
+                    gk = rk[row] * fmaf(-rk[row] * kv[j], dot, gk);
+                }
+                const int64_t to = row0 + (int64_t)row * p.B;
+                dq[to * p.lddq + d] = (T)(row < live ? gq : 0.f);
+                dk[to * p.lddk + d] = (T)(row < live ? gk : 0.f);
+            }
+        }
+}
+
+template <typename T, int KT>
+void backward(const DeltaArgs &a, hipStream_t st) {
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, KB = C * KT * 64, MB = C * C * 2;
+    const int heads = a.B * a.H, tiles = (a.dv + 31) / 32;
+    const dim3 block(std::min(4, tiles) * 64);
+    const int chain = N * KB * 3 + 6 * MB + 5 * C * 4;
+    hipLaunchKernelGGL((k_delta_prep<T, KT, true>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
+    if (a.segments > 1) {
+        hipLaunchKernelGGL((k_delta_back_chain<T, KT, false>), dim3((unsigned)((a.segments - 1) * heads), (tiles + 3) / 4), block,
+                           chain, st, a);
+        delta_join(a, a.dfinal, true, st);
+    }
+    hipLaunchKernelGGL((k_delta_back_chain<T, KT, true>), dim3((unsigned)(a.segments * heads), (tiles + 3) / 4), block, chain, st,
+                       a);
+    hipLaunchKernelGGL((k_delta_grads<T, KT>), dim3((unsigned)(a.chunks * a.B * a.HK)), dim3(256),
+                       (6 + N) * C / 32 * 2 * kPiece + 2 * N * KB + 2 * C * (C + 4) * 4, st, a);
+}
+
+template <typename T>
+void backward(const DeltaArgs &a, hipStream_t st) {
+    switch ((a.dk + 31) / 32) {
+        case 1: return backward<T, 1>(a, st);
+        case 2: return backward<T, 2>(a, st);
+        case 3: return backward<T, 3>(a, st);
+        default: return backward<T, 4>(a, st);
+    }
+}
+
+// No positions: the gradient passes through.
+__global__ void __launch_bounds__(256) k_delta_pass(const float *from, float *to, int64_t n) {
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += gridDim.x * (int64_t)256) to[i] = from ? from[i] : 0.f;
+}
+
+}  // namespace
+
+}  // namespace fi
+
+using namespace fi;
+
+extern "C" fi_status fi_delta_backward(const fi_delta_desc *desc, const void *q, const void *k, const void *v,
+                                       const float *decay, const float *beta, const float *state, const int32_t *lengths,
+                                       const void *saved, const void *dy, const float *dfinal, void *dq, void *dk, void *dv,
+                                       float *ddecay, float *dbeta, float *dstate, void *workspace, void *stream) {
+    static const char *call = "fi_delta_backward";
+    if (const char *why = delta_check(desc)) return op_fail(FI_EINVAL, call, why);
+    if (desc->T > 0 && (!q || !k || !v || !decay || !beta || !saved || !dy || !dq || !dk || !dv || !ddecay || !dbeta || !workspace))
+        return op_fail(FI_EINVAL, call, "q, k, v, decay, beta, saved, dy, their gradients and the workspace are required");
+    const size_t es = value_bytes(desc->dtype);
+    if (!aligned(es, {q, k, v, dy, dq, dk, dv}) || !aligned(4, {decay, beta, state, lengths, dfinal, ddecay, dbeta, dstate}) ||
+        !aligned(256, {saved, workspace}))
+        return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
+    const DeltaPlan d = delta_plan(desc, true);
+    DeltaArgs a = {};
+    delta_args(desc, d, a);
+    const int64_t rows = a.T * a.B;
+    const size_t qk = (size_t)a.HK * a.dk * es, vb = (size_t)a.H * a.dv * es, hb = (size_t)a.H * 4;
+    const size_t sb = (size_t)a.B * a.H * a.dk * a.dv * 4, lb = (size_t)a.B * 4;
+    const size_t sv = fi_delta_saved_bytes(desc), ws = fi_delta_workspace_bytes(desc, 1);
+    const View out[] = {{dq, rows, qk, (size_t)a.lddq * es}, {dk, rows, qk, (size_t)a.lddk * es}, {dv, rows, vb, (size_t)a.lddv * es},
+                        {ddecay, rows, hb, (size_t)a.lddg * 4}, {dbeta, rows, hb, (size_t)a.lddb * 4}, {dstate, 1, sb, sb},
+                        {workspace, 1, ws, ws}};
+    const View in[] = {{q, rows, qk, (size_t)a.ldq * es}, {k, rows, qk, (size_t)a.ldk * es}, {v, rows, vb, (size_t)a.ldv * es},
+                       {decay, rows, hb, (size_t)a.ldg * 4}, {beta, rows, hb, (size_t)a.ldb * 4}, {state, 1, sb, sb},
+                       {lengths, 1, lb, lb}, {saved, 1, sv, sv}, {dy, rows, vb, (size_t)a.lddy * es}, {dfinal, 1, sb, sb}};
+    if (outputs_meet(out, 7, in, 10)) return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
+    const hipStream_t st = (hipStream_t)stream;
+    if (a.T == 0) {
+        if (dstate)
+            hipLaunchKernelGGL(k_delta_pass, dim3((unsigned)std::min<size_t>((sb / 4 + 255) / 256, 4096)), dim3(256), 0, st, dfinal,
+                               dstate, (int64_t)(sb / 4));
+        return op_launched(call);
+    }
+    a.q = q, a.k = k, a.v = v, a.g = decay, a.beta = beta, a.lengths = lengths, a.dy = dy, a.dfinal = dfinal;
+    a.dq = dq, a.dk_out = dk, a.dv_out = dv, a.dg = ddecay, a.dbeta = dbeta, a.dstate = dstate;
+    char *w = (char *)workspace;
+    a.images = w, w += d.images;
+    a.factors = (float *)w, w += d.factors;
+    a.ends = (float *)w, w += d.ends;
+    a.x = (float *)w, w += d.rows;
+    a.starts = (float *)w, w += d.local;
+    a.local = (float *)w;
+    char *s = (char *)saved;
+    a.states = (float *)s, s += d.states + up256(sb);
+    a.w = (float *)s, s += d.rows;
+    a.maps = (float *)s;
+    if (desc->dtype == FI_F32) backward<float>(a, st);
+    else if (desc->dtype == FI_BF16) backward<bf16_t>(a, st);
+    else backward<f16_t>(a, st);
+    return op_launched(call);
+}
