@@ -766,9 +766,9 @@ def q8_product(w, x, bias=None, *, dtype=None, y=None):
     if isinstance(x, Q8Rows):
         dt = torch.bfloat16 if dtype is None else dtype
     else:
-        device = _device(x, "x")
         if _any_requires_grad(x, bias):
             _not_recorded("q8_product")
+        device = _device(x, "x")
         if device != w._index:
             _bad(f"x: on {x.device}, expected {w.device}")
         if x.dim() != 2 or x.shape[1] != w.K:
