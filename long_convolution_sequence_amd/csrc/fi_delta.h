@@ -77,6 +77,22 @@ struct DeltaArgs {
     float *starts;                         // [dk][dv] the state before it (backwards: the gradient behind it)
 };
 
+// Loads from LDS are not moved across: all at once they would spill.
+__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
+
+// A number for the whole wave or a lane that the compiler takes for a new one: what is
+// made of it (a chunk's offsets and masks, 32 registers each) is made where it is used
+// and not kept from chunk to chunk.
+template <typename I>
+__device__ __forceinline__ I anew(I v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+__device__ __forceinline__ unsigned anew_lane(unsigned v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // ---- operands ------------------------------------------------------------------
 
 template <int N>
@@ -157,50 +173,172 @@ __device__ __forceinline__ void put_terms(char *image, int at, int stride, const
 // Row of register r of an accumulator, for the lane's half.
 __device__ __forceinline__ int acc_row(int r) { return 8 * (r >> 2) + 4 * ((threadIdx.x >> 5) & 1) + (r & 3); }
 
-// Four values of a row from d on, zeros behind D and where the row does not count.
-template <typename T>
+// Four values of a row from d on, zeros behind D and where the row does not count
+// (it is read all the same).  No lane branches: a load in a branch of its own would be
+// waited for there.  VEC: D is a multiple of four.
+template <bool VEC, typename T>
 __device__ __forceinline__ void load4(float (&x)[4], const T *row, int d, int D, bool live) {
-    if (live && d + 4 <= D) {
-        const Chunk<T, 4> v = *reinterpret_cast<const Chunk<T, 4> *>(row + d);
+    if (VEC) {
+        const Chunk<T, 4> v = *reinterpret_cast<const Chunk<T, 4> *>(row + min(d, D - 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (float)v[i];
+        for (int i = 0; i < 4; ++i) x[i] = live && d < D ? (float)v[i] : 0.f;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = live && d + i < D ? (float)row[d + i] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const T v = row[min(d + i, D - 1)];
+            x[i] = live && d + i < D ? (float)v : 0.f;
+        }
     }
 }
+template <typename T>
+__device__ __forceinline__ void load4(float (&x)[4], const T *row, int d, int D, bool live) {
+    if ((D & 3) == 0) load4<true>(x, row, d, D, live);
+    else load4<false>(x, row, d, D, live);
+}
 
-// C rows of a tensor as images: `rows` with the channels as the summed index,
-// `cols` (the transpose) with the positions; either may be null.  Rows from `live`
-// on are zeros.  A thread takes four rows of four channels.
-template <typename T, int C>
-__device__ __forceinline__ void stage(const T *x, int64_t pitch, int D, int padded, int live, char *rows, char *cols) {
-    constexpr int N = DeltaType<T>::terms;
-    const int runs = padded / 4, rstep = padded / 16, image = C * padded * 2;
-    for (int u = threadIdx.x; u < C / 4 * runs; u += blockDim.x) {
-        const int i = u / runs * 4, d = (u - u / runs * runs) * 4;
-        float m[4][4];
+// C rows of a tensor on their way into images: a thread of 256 takes four rows of four
+// channels.  load() reads them ahead, rows from `live` (at least one) on and channels
+// from D on as zeros; put() writes images: `rows` with the channels as the summed
+// index, `cols` (the transpose) with the positions, either null.
+template <typename T, int C, int DK>
+struct Stage {
+    static constexpr int N = DeltaType<T>::terms, RUNS = DK / 4, UNITS = C / 4 * RUNS, EACH = (UNITS + 255) / 256;
+    Chunk<T, 4> raw[EACH][4];
+
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T *x, unsigned pitch, int D, int live) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) load4(m[r], x + (i + r) * pitch, d, D, i + r < live);
-        if (rows) {
+        for (int e = 0; e < EACH; ++e) {
+            const int u = e * 256 + threadIdx.x, i = u / RUNS * 4, d = u % RUNS * 4;
+            if (u >= UNITS) break;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) put_terms<N>(rows, image_at(i + r, d, rstep), image, m[r]);
-        }
-        if (cols) {
+            for (int r = 0; r < 4; ++r) {
+                const unsigned row = min(i + r, live - 1) * pitch;
+                if (VEC)
+                    raw[e][r] = *reinterpret_cast<const Chunk<T, 4> *>(in_row(x, row + min(d, D - 4)));
+                else
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float t[4] = {m[0][c], m[1][c], m[2][c], m[3][c]};
-                put_terms<N>(cols, image_at(d + c, i, C / 16), image, t);
+                    for (int j = 0; j < 4; ++j) raw[e][r][j] = *in_row(x, row + min(d + j, D - 1));
             }
         }
     }
+    __device__ __forceinline__ void load(const T *x, unsigned pitch, int D, int live) {
+        if ((D & 3) == 0) load<true>(x, pitch, D, live);
+        else load<false>(x, pitch, D, live);
+    }
+    __device__ __forceinline__ void put(int D, int live, char *rows, char *cols) const {
+        D = anew(D), live = anew(live);
+        constexpr int STEPS = DK / 16, IMAGE = C * DK * 2;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const int u = e * 256 + threadIdx.x, i = u / RUNS * 4, d = u % RUNS * 4;
+            if (u >= UNITS) break;
+            float m[4][4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m[r][j] = i + r < live && d + j < D ? (float)raw[e][r][j] : 0.f;
+            if (rows) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) put_terms<N>(rows, image_at(i + r, d, STEPS), IMAGE, m[r]);
+            }
+            if (cols) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float t[4] = {m[0][c], m[1][c], m[2][c], m[3][c]};
+                    put_terms<N>(cols, image_at(d + c, i, C / 16), IMAGE, t);
+                }
+            }
+        }
+    }
+};
+
+// Addresses below are an address for the whole wave and a 32-bit byte offset of the
+// lane: a chunk's rows lie within 2^32 bytes (delta_check).
+
+// A column of C rows in the places of an accumulator, `at` for the whole wave.  Rows
+// from `live` (at least one) on read the last one.
+template <typename T, int MT>
+__device__ __forceinline__ void load_column(T (&v)[MT][16], const T *at, unsigned column, unsigned pitch, int live) {
+    column = anew_lane(column), pitch = anew(pitch), live = anew(live);
+    if (live == MT * 32) {
+        const unsigned mine = column + acc_row(0) * pitch;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[i][r] = *in_row(at, mine + (i * 32 + 8 * (r >> 2) + (r & 3)) * pitch);
+    } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[i][r] = *in_row(at, column + min(i * 32 + acc_row(r), live - 1) * pitch);
+    }
 }
 
-// Bytes from memory into LDS, 16 a thread and turn.
-__device__ __forceinline__ void copy_in(char *to, const char *from, int bytes) {
-    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
-        *reinterpret_cast<float4 *>(to + i) = *reinterpret_cast<const float4 *>(from + i);
+// The way back: `rows` rows are there, those from `live` on get zeros.
+template <typename T, int MT>
+__device__ __forceinline__ void store_column(T *at, unsigned column, unsigned pitch, const f32x16 (&v)[MT], int rows, int live) {
+    column = anew_lane(column), pitch = anew(pitch), live = anew(live), rows = anew(rows);
+    if (live == MT * 32) {
+        const unsigned mine = column + acc_row(0) * pitch;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) *in_row(at, mine + (i * 32 + 8 * (r >> 2) + (r & 3)) * pitch) = (T)v[i][r];
+    } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = i * 32 + acc_row(r);
+                if (row < rows) *in_row(at, column + row * pitch) = (T)(row < live ? v[i][r] : 0.f);
+            }
+    }
 }
+
+// A state [dk][width] as accumulators and back; nothing lies past its edges.
+template <int KT>
+__device__ __forceinline__ void load_state(f32x16 (&S)[KT], const float *from, int dk, int width, int column) {
+    const unsigned at = min(column, width - 1);
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = t * 32 + acc_row(r);
+            const float s = *in_row(from, at + (unsigned)(min(row, dk - 1) * width));
+            S[t][r] = row < dk && column < width ? s : 0.f;
+        }
+}
+template <int KT>
+__device__ __forceinline__ void store_state(float *to, const f32x16 (&S)[KT], int dk, int width, int column) {
+    if (column >= width) return;
+    width = anew(width), dk = anew(dk), column = (int)anew_lane(column);
+    const unsigned mine = column + acc_row(0) * width;
+    if (dk == KT * 32) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) *in_row(to, mine + (unsigned)((t * 32 + 8 * (r >> 2) + (r & 3)) * width)) = S[t][r];
+    } else {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = t * 32 + acc_row(r);
+                if (row < dk) *in_row(to, (unsigned)(column + row * width)) = S[t][r];
+            }
+    }
+}
+
+// Bytes (a multiple of 1 KB) from memory into LDS past the registers, by 256 threads:
+// each wave brings 1 KB at a time.  arrived() waits for this thread's share.
+__device__ __forceinline__ void bring(char *to, const char *from, int bytes) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    for (int i = wave * kPiece; i < bytes; i += 4 * kPiece)
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(from + i + lane * 16),
+                                         (__attribute__((address_space(3))) void *)(to + i), 16, 0, 0);
+}
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ int64_t delta_length(const DeltaArgs &p, int b) {
     if (!p.lengths) return p.T;
@@ -220,10 +358,15 @@ __device__ __forceinline__ f32x16 zeros16() {
 // Sum over a wave's lanes of the same half-position (lanes l and l ^ 32).
 __device__ __forceinline__ float both_halves(float v) { return v + __shfl_xor(v, 32, 64); }
 
+// A chunk's triangular matrices as images, the pieces that hold zeros alone left out:
+// row tiles `i` and steps `cs` along the summed index, of which forwards (below the
+// diagonal) the first 2 (i + 1) count and backwards (above it) those from 2 i on.
+template <int C>
+constexpr int tri_pieces() { return C == 64 ? 6 : 2; }
+__device__ __forceinline__ constexpr int tri_at(int i, int cs) { return i * 2 + cs; }
 template <typename T, bool BACK>
 constexpr int image_bytes() {          // of a chunk: M in three terms and P
-    constexpr int C = DeltaType<T>::chunk;
-    return C * C * 2 * (3 + (BACK ? 3 : DeltaType<T>::out));
+    return tri_pieces<DeltaType<T>::chunk>() * kPiece * (3 + (BACK ? 3 : DeltaType<T>::out));
 }
 
 // A wave a chunk and head.  Forwards the images of M = (I + A)^-1 and of
@@ -233,12 +376,13 @@ constexpr int image_bytes() {          // of a chunk: M in three terms and P
 // scale e^G_i, e^G_i b_i, b_i, e^(G_C), both lengths' reciprocals and G in two floats.
 // "unit" divides k and q by their lengths in these factors, so the operands stay the
 // inputs themselves.
-// The inverse: lane j solves for column j, row by row from registers, the rows of A
-// read from LDS for all lanes at once.
+// The inverse: a lane solves for a column of a diagonal block of 32, row by row from
+// registers, the rows of A read from LDS for all lanes of a block at once; the block
+// below them is -N22 (A21 N11).
 template <typename T, int KT, bool BACK>
 __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, MT = C / 32, CS = C / 16, KS = KT * 2, LD = C + 4;
-    constexpr int PT = BACK ? 3 : DeltaType<T>::out;
+    constexpr int PT = BACK ? 3 : DeltaType<T>::out, MB = tri_pieces<C>() * kPiece;
     __shared__ __align__(16) float m[C * LD];
     __shared__ double sum[C];
     __shared__ float fb[C], fk[C], fq[C];
@@ -251,12 +395,9 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
 
     // decays, in 64 bits: differences of sums keep their digits next to a large one
     if (lane < C) {
-        const int64_t row = (t0 + lane) * p.B + b;
-        float g = 0.f, beta = 0.f;
-        if (lane < live) {
-            g = p.g[row * p.ldg + h];
-            beta = p.beta[row * p.ldb + h];
-        }
+        const int64_t row = (t0 + min(lane, live - 1)) * p.B + b;
+        float g = p.g[row * p.ldg + h], beta = p.beta[row * p.ldb + h];
+        if (lane >= live) g = beta = 0.f;
         g = g < -1e4f ? -1e4f : g;                       // e^-10^4 is 0 in any case, -inf would be NaN in differences
         double s = (double)g * 1.4426950408889634;
 #pragma unroll
@@ -268,12 +409,11 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
         fb[lane] = beta;
     }
     // k and q as operands, straight from memory
-    Frag<N> fk_[MT][KS];
+    Frag<N> ks_[MT][KS];
     float ssk[MT], ssq[MT];
-    const T *k = static_cast<const T *>(p.k) + hk * p.dk, *q = static_cast<const T *>(p.q) + hk * p.dk;
     const auto fetch = [&](const T *from, int64_t ld, int mt, int ks, float &ss) {
         const int i = mt * 32 + col;
-        const T *row = from + ((t0 + i) * p.B + b) * ld;
+        const T *row = from + ((t0 + min(i, live - 1)) * p.B + b) * ld;
         float x[8], y[4], z[4];
         load4(y, row, ks * 16 + 4 * half, p.dk, i < live);
         load4(z, row, ks * 16 + 4 * half + 8, p.dk, i < live);
@@ -285,11 +425,12 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
         }
         return split<N>(x);
     };
+    const T *k = static_cast<const T *>(p.k) + hk * p.dk, *q = static_cast<const T *>(p.q) + hk * p.dk;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         ssk[mt] = ssq[mt] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) fk_[mt][ks] = fetch(k, p.ldk, mt, ks, ssk[mt]);
+        for (int ks = 0; ks < KS; ++ks) ks_[mt][ks] = fetch(k, p.ldk, mt, ks, ssk[mt]);
     }
     f32x16 kk[MT][MT], qk[MT][MT];
 #pragma unroll
@@ -303,8 +444,8 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
             const Frag<N> fq_ = fetch(q, p.ldq, i, ks, ssq[i]);
 #pragma unroll
             for (int j = 0; j <= i; ++j) {
-                multiply<2>(kk[i][j], fk_[i][ks], fk_[j][ks]);
-                multiply<2>(qk[i][j], fq_, fk_[j][ks]);
+                multiply<2>(kk[i][j], ks_[i][ks], ks_[j][ks]);
+                multiply<2>(qk[i][j], fq_, ks_[j][ks]);
             }
         }
 #pragma unroll
@@ -317,7 +458,7 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
     }
     __syncthreads();
 
-    // A in rows
+    // A in rows (its upper half: zeros), P in its registers
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -326,63 +467,87 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
             for (int r = 0; r < 16; ++r) {
                 const int row = i * 32 + acc_row(r), c = j * 32 + col;
                 float a = 0.f, e = 0.f;
-                if (j <= i && row >= c) {
-                    e = exp2f((float)(sum[row] - sum[c])) * fk[c];
-                    if (row > c) a = e * fk[row] * fb[BACK ? row : c] * kk[i][j <= i ? j : 0][r];
-                    e *= p.scale * fq[row] * (BACK ? 1.f : fb[c]);
+                if (j <= i) {
+                    e = row >= c ? exp2f((float)(sum[row] - sum[c])) * fk[c] : 0.f;
+                    a = row > c ? e * fk[row] * fb[BACK ? row : c] * kk[i][j <= i ? j : 0][r] : 0.f;
+                    qk[i][j <= i ? j : 0][r] *= e * p.scale * fq[row] * (BACK ? 1.f : fb[c]);
                 }
                 m[row * LD + c] = a;
-                if (j <= i) qk[i][j <= i ? j : 0][r] *= e;       // P
             }
     __syncthreads();
-    float x[C];
+    float x[32];
+    const int block = MT == 2 ? half * 32 : 0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        float s0 = lane == i ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    for (int i = 0; i < 32; ++i) {
+        float s0 = col == i ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
         for (int j = 0; j < i; j += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(m + i * LD + j);
+            const float4 a = *reinterpret_cast<const float4 *>(m + (block + i) * LD + block + j);
             s0 = fmaf(-a.x, x[j], s0);
             if (j + 1 < i) s1 = fmaf(-a.y, x[j + 1], s1);
             if (j + 2 < i) s2 = fmaf(-a.z, x[j + 2], s2);
             if (j + 3 < i) s3 = fmaf(-a.w, x[j + 3], s3);
         }
         x[i] = (s0 + s1) + (s2 + s3);
-        asm volatile("" ::: "memory");                   // the rows' loads stay in order: ahead of it they would spill
+        if (i % 4 == 3) asm volatile("" ::: "memory");   // not all rows' loads at once: they would spill
     }
     __syncthreads();
+    if (MT == 2 || half == 0) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m[(block + i) * LD + block + col] = x[i];
+    }
+    __syncthreads();
+    if constexpr (MT == 2) {
+        const auto rows = [&](int r0, int c0, int s) {   // a left operand of m
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = m[(r0 + col) * LD + c0 + s * 16 + 8 * (j >> 2) + 4 * half + (j & 3)];
+            return split<3>(v);
+        };
+        f32x16 t = zeros16(), n21 = zeros16();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = m[(s * 16 + 8 * (j >> 2) + 4 * half + (j & 3)) * LD + col];
+            multiply<2>(t, rows(32, 0, s), split<3>(v));
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) multiply<2>(n21, rows(32, 32, s), step_of<3>(t, s));
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) m[(32 + acc_row(r)) * LD + col] = -n21[r];
+        __syncthreads();
+    }
     const auto flush = [&](char *image, auto terms) {      // m (or its transpose) as an image
         constexpr int NT = decltype(terms)::value;
-        for (int mt = 0; mt < MT; ++mt)
-            for (int cs = 0; cs < CS; ++cs) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int cs = BACK ? 2 * i : 0; cs < (BACK ? CS : 2 * i + 2); ++cs) {
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int r = mt * 32 + col, c = cs * 16 + 8 * (j >> 2) + 4 * half + (j & 3);
+                    const int r = i * 32 + col, c = cs * 16 + 8 * (j >> 2) + 4 * half + (j & 3);
                     v[j] = BACK ? m[c * LD + r] : m[r * LD + c];
                 }
                 const Frag<NT> f = split<NT>(v);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    *reinterpret_cast<bf16x8 *>(image + t * C * C * 2 + (mt * CS + cs) * kPiece + lane * 16) = f.t[t];
+                    *reinterpret_cast<bf16x8 *>(image + t * MB + tri_at(i, cs) * kPiece + lane * 16) = f.t[t];
             }
     };
     char *image = p.images + at * image_bytes<T, BACK>();
-    if (lane < C) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) m[i * LD + lane] = x[i];
-    }
-    __syncthreads();
     flush(image, std::integral_constant<int, 3>());
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
+        for (int j = 0; j <= i; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) m[(i * 32 + acc_row(r)) * LD + j * 32 + col] = j <= i ? qk[i][j <= i ? j : 0][r] : 0.f;
+            for (int r = 0; r < 16; ++r) m[(i * 32 + acc_row(r)) * LD + j * 32 + col] = qk[i][j][r];
     __syncthreads();
-    flush(image + 3 * C * C * 2, std::integral_constant<int, PT>());
+    flush(image + 3 * MB, std::integral_constant<int, PT>());
     if (lane < C) {
         float *f = p.factors + at * kDeltaFactors * C;
         const float rise = exp2f((float)sum[lane]), fall = exp2f((float)(sum[C - 1] - sum[lane]));
@@ -426,7 +591,7 @@ inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
     d.segments = (int)std::max<int64_t>(1, (d.chunks + d.per - 1) / d.per);
     const size_t all = (size_t)d.chunks * heads, C = d.C, sk = (size_t)q->dk * q->dv * 4;
     const size_t out = backward || q->dtype == FI_F32 ? 3 : 2;
-    d.images = up256(all * C * C * 2 * (3 + out));
+    d.images = up256(all * (C == 64 ? tri_pieces<64>() : tri_pieces<32>()) * kPiece * (3 + out));
     d.factors = up256(all * kDeltaFactors * C * 4);
     d.states = up256(all * sk);
     d.ends = up256(all * sk);

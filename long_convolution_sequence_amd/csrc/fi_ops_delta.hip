@@ -12,12 +12,14 @@ enum { CHAIN_LOCAL, CHAIN_FULL };
 // columns).  FULL: from the state before the segment; y, the states before each chunk
 // and w where they are kept, the last state.  LOCAL: from nothing, only the state at
 // the end; the columns behind the state's are those of the map (v = 0, from a unit
-// column).
+// column).  Two workgroups share a CU, so that the products of one run under the loads
+// and the cutting into terms of the other; k and q of the next chunk are on their way
+// in registers, M and P go into LDS under the products with S.
 template <typename T, int KT, int MODE>
-__global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
+__global__ void __launch_bounds__(256, 2) k_delta_chain(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
     constexpr int MT = C / 32, CS = C / 16, KS = KT * 2, DK = KT * 32;
-    constexpr int KB = C * DK * 2, MB = C * C * 2;           // bytes of a term
+    constexpr int KB = C * DK * 2, MB = tri_pieces<C>() * kPiece;    // bytes of a term
     constexpr bool FULL = MODE == CHAIN_FULL;
     extern __shared__ __align__(16) char lds[];
     char *const ik = lds, *const ikt = ik + N * KB, *const im = ikt + N * KB;
@@ -26,56 +28,51 @@ __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = p.B * p.H, seg = blockIdx.x / heads, bh = blockIdx.x % heads, b = bh / p.H, h = bh % p.H;
     const int tiles = (p.dv + 31) / 32, tile = blockIdx.y * 4 + wave;
-    const bool map = !FULL && tile >= tiles;
+    const bool map = !FULL && tile >= tiles, idle = map ? tile - tiles >= KT : tile >= tiles;
     const int column = (map ? tile - tiles : tile) * 32 + (lane & 31), width = map ? p.dk : p.dv;
-    const bool mine = column < width && (!map || tile - tiles < KT);
+    const bool mine = column < width && !idle;
     const int64_t length = delta_length(p, b);
     const int hk = h / (p.H / p.HK);
+    const int64_t size = (int64_t)p.dk * p.dv;
 
     f32x16 S[KT];
-    const float *from = FULL ? (p.segments > 1 ? p.starts + ((int64_t)seg * heads + bh) * p.dk * p.dv
-                                               : p.state ? p.state + (int64_t)bh * p.dk * p.dv : nullptr)
-                             : nullptr;
+    const float *from = !FULL ? nullptr : p.segments > 1 ? p.starts + ((int64_t)seg * heads + bh) * size
+                                        : p.state        ? p.state + bh * size
+                                                         : nullptr;
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = t * 32 + acc_row(r);
-            S[t][r] = map ? (row == column ? 1.f : 0.f) : from && mine && row < p.dk ? from[(int64_t)row * p.dv + column] : 0.f;
-        }
-    const auto keep = [&](float *to, int w) {
-        if (!mine) return;
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = t * 32 + acc_row(r);
-                if (row < p.dk) to[(int64_t)row * w + column] = S[t][r];
-            }
-    };
+        for (int r = 0; r < 16; ++r) S[t][r] = map && t * 32 + acc_row(r) == column ? 1.f : 0.f;
+    if (from) load_state<KT>(S, from, p.dk, p.dv, column);
+    const auto keep = [&](float *to, int w) { store_state<KT>(to, S, p.dk, w, idle ? w : column); };
+
     const T *const q = static_cast<const T *>(p.q) + hk * p.dk, *const k = static_cast<const T *>(p.k) + hk * p.dk;
     const T *const v = static_cast<const T *>(p.v) + (int64_t)h * p.dv;
     const int64_t first = seg * p.per, last = min(p.chunks, first + p.per);
-    for (int64_t c = first; c < last; ++c) {
-        const int64_t t0 = c * C, n = length - t0;
-        const int rows = (int)min<int64_t>(C, p.T - t0), live = n < 0 ? 0 : n < rows ? (int)n : rows;
-        T *const y = FULL ? static_cast<T *>(p.y) + (int64_t)h * p.dv : nullptr;
-        if (live == 0) {
-            if (!FULL) break;
-            if (p.states) keep(p.states + (c * heads + bh) * p.dk * p.dv, p.dv);
-            if (mine)
-                for (int i = lane >> 5; i < rows; i += 2) y[((t0 + i) * p.B + b) * p.ldy + column] = (T)0.f;
-            continue;
-        }
-        const int64_t at = c * heads + bh;
+    const int64_t stop = min(last, (length + C - 1) / C);      // chunks behind it hold nothing
+    Stage<T, C, DK> sk, sq;
+    const auto ahead = [&](int64_t c) {
+        const int64_t t0 = c * C;
+        const int live = (int)min<int64_t>(C, length - t0);
+        sk.load(k + (t0 * p.B + b) * p.ldk, (unsigned)(p.B * p.ldk), p.dk, live);
+        if (FULL) sq.load(q + (t0 * p.B + b) * p.ldq, (unsigned)(p.B * p.ldq), p.dk, live);
+    };
+    if (first < stop) ahead(first);
+    for (int64_t c = first; c < stop; ++c) {
+        const int64_t t0 = c * C, at = c * heads + bh;
+        const int rows = (int)min<int64_t>(C, p.T - t0), live = (int)min<int64_t>(C, length - t0);
         __syncthreads();
-        stage<T, C>(k + (t0 * p.B + b) * p.ldk, p.B * p.ldk, p.dk, DK, live, ik, ikt);
-        if (FULL) stage<T, C>(q + (t0 * p.B + b) * p.ldq, p.B * p.ldq, p.dk, DK, live, iq, nullptr);
-        copy_in(im, p.images + at * image_bytes<T, false>(), FULL ? (3 + NY) * MB : 3 * MB);
-        copy_in((char *)f, (const char *)(p.factors + at * kDeltaFactors * C), 5 * C * 4);
+        bring(im, p.images + at * image_bytes<T, false>(), (FULL ? 3 + NY : 3) * MB);
+        if (threadIdx.x < 5 * C) f[threadIdx.x] = p.factors[at * kDeltaFactors * C + threadIdx.x];
+        if (5 * C > 256 && threadIdx.x < 5 * C - 256) f[256 + threadIdx.x] = p.factors[at * kDeltaFactors * C + 256 + threadIdx.x];
+        sk.put(p.dk, live, ik, ikt);
+        if (FULL) sq.put(p.dk, live, iq, nullptr);
         __syncthreads();
+        T vs[MT][16];
+        if (!map) load_column<T, MT>(vs, v + (t0 * p.B + b) * p.ldv, min(column, p.dv - 1), (unsigned)(p.B * p.ldv), live);
+        if (c + 1 < stop) ahead(c + 1);
+        if (FULL && p.states) keep(p.states + at * size, p.dv);
 
-        if (FULL && p.states) keep(p.states + at * p.dk * p.dv, p.dv);
         f32x16 R[MT], Y[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) R[i] = Y[i] = zeros16();
@@ -90,16 +87,20 @@ __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
                 multiply<2>(R[i], piece<N>(ik, i * KS + ks, KB), s);
                 if (FULL) multiply<NY - 1>(Y[i], piece<N>(iq, i * KS + ks, KB), sy);
             }
+            in_order();
         }
         // v - e^G K S, and w = M of it
+        const int vlive = anew(map ? 0 : live);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int row = i * 32 + acc_row(r);
-                const float x = !map && mine && row < live ? (float)v[((t0 + row) * p.B + b) * p.ldv + column] : 0.f;
+                const float x = row < vlive ? (float)vs[i][r] : 0.f;
                 R[i][r] = fmaf(-f[row], R[i][r], x);
             }
+        arrived();
+        __syncthreads();
         f32x16 W[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) W[i] = zeros16();
@@ -107,16 +108,11 @@ __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
         for (int cs = 0; cs < CS; ++cs) {
             const Frag<3> s = step_of<3>(R[cs / 2], cs & 1);
 #pragma unroll
-            for (int i = cs / 2; i < MT; ++i) multiply<2>(W[i], piece<3>(im, i * CS + cs, MB), s);
+            for (int i = cs / 2; i < MT; ++i) multiply<2>(W[i], piece<3>(im, tri_at(i, cs), MB), s);
+            in_order();
         }
         if (FULL) {
-            if (p.w && mine) {
-                float *to = p.w + at * C * p.dv + column;
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) to[(i * 32 + acc_row(r)) * p.dv] = W[i][r];
-            }
+            if (p.w && mine) store_column<float, MT>(p.w + at * C * p.dv, column, p.dv, W, C, C);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -125,16 +121,12 @@ __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
             for (int cs = 0; cs < CS; ++cs) {
                 const Frag<NY> s = step_of<NY>(W[cs / 2], cs & 1);
 #pragma unroll
-                for (int i = cs / 2; i < MT; ++i) multiply<NY - 1>(Y[i], piece<NY>(ip, i * CS + cs, MB), s);
+                for (int i = cs / 2; i < MT; ++i) multiply<NY - 1>(Y[i], piece<NY>(ip, tri_at(i, cs), MB), s);
+                in_order();
             }
             if (mine)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int row = i * 32 + acc_row(r);
-                        if (row < rows) y[((t0 + row) * p.B + b) * p.ldy + column] = (T)(row < live ? Y[i][r] : 0.f);
-                    }
+                store_column<T, MT>(static_cast<T *>(p.y) + (int64_t)h * p.dv + (t0 * p.B + b) * p.ldy, column,
+                                    (unsigned)(p.B * p.ldy), Y, rows, live);
         }
         const float decay = f[4 * C];
 #pragma unroll
@@ -150,74 +142,92 @@ __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs p) {
             const Frag<3> s = step_of<3>(W[cs / 2], cs & 1);
 #pragma unroll
             for (int t = 0; t < KT; ++t) multiply<2>(S[t], piece<N>(ikt, t * CS + cs, KB), s);
+            in_order();
         }
     }
     if (!FULL) {
-        if (map) {
-            if (tile - tiles < KT) keep(p.maps + ((int64_t)seg * heads + bh) * p.dk * p.dk, p.dk);
-        } else
-            keep(p.local + ((int64_t)seg * heads + bh) * p.dk * p.dv, p.dv);
+        if (map) keep(p.maps + ((int64_t)seg * heads + bh) * p.dk * p.dk, p.dk);
+        else keep(p.local + ((int64_t)seg * heads + bh) * size, p.dv);
         return;
     }
-    if (seg == p.segments - 1) {
-        if (p.states) keep(p.states + (p.chunks * heads + bh) * p.dk * p.dv, p.dv);
-        if (p.final) keep(p.final + (int64_t)bh * p.dk * p.dv, p.dv);
+    // behind the sequence's end: y = 0, the state as it is
+    for (int64_t c = max(first, stop); c < last; ++c) {
+        const int64_t t0 = c * C;
+        const int rows = (int)min<int64_t>(C, p.T - t0);
+        T *const y = static_cast<T *>(p.y) + (int64_t)h * p.dv + (t0 * p.B + b) * p.ldy + column;
+        if (p.states && c == stop) keep(p.states + (c * heads + bh) * size, p.dv);
+        if (mine)
+            for (int i = lane >> 5; i < rows; i += 2) y[i * p.B * p.ldy] = (T)0.f;
     }
+    if (seg == p.segments - 1 && p.final) keep(p.final + bh * size, p.dv);
 }
 
 // starts[s + 1] = maps[s] starts[s] + local[s] (backwards starts[s - 1] = maps[s]^T
-// starts[s] + local[s]), 32 columns a wave.
-template <int KT>
-__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs p, const float *first, bool back) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-    const int heads = p.B * p.H, bh = blockIdx.x, column = (blockIdx.y * 4 + wave) * 32 + (lane & 31);
-    const bool mine = column < p.dv;
-    const int64_t size = (int64_t)p.dk * p.dv;
-    f32x16 S[KT];
+// starts[s] + local[s]): a workgroup 32 columns of a head, a wave 32 rows, whose share
+// of the next map is on its way meanwhile; the state passes through LDS as an image.
+template <int KT, bool BACK>
+__global__ void __launch_bounds__(KT * 64) k_delta_join(DeltaArgs p, const float *first) {
+    constexpr int KS = KT * 2;
+    __shared__ __align__(16) char image[2][3 * KS * kPiece];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    const int heads = p.B * p.H, bh = blockIdx.x, column = blockIdx.y * 32 + (lane & 31), at = min(column, p.dv - 1);
+    const int64_t size = (int64_t)p.dk * p.dv, msize = (int64_t)p.dk * p.dk;
+    const int row = min(wave * 32 + (lane & 31), p.dk - 1);
+    const bool in = wave * 32 + (lane & 31) < p.dk;
+    f32x16 S;
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int r = 0; r < 16; ++r) {
+        const int d = wave * 32 + acc_row(r);
+        const float s = first ? first[bh * size + (int64_t)min(d, p.dk - 1) * p.dv + at] : 0.f;
+        S[r] = d < p.dk ? s : 0.f;
+    }
+    float map[KS][8], local[16];
+    const auto ahead = [&](int s) {
+        const float *m = p.maps + ((int64_t)s * heads + bh) * msize, *l = p.local + ((int64_t)s * heads + bh) * size + at;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = min(ks * 16 + 8 * (j >> 2) + 4 * half + (j & 3), p.dk - 1);
+                map[ks][j] = m[BACK ? k * p.dk + row : row * p.dk + k];
+            }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) local[r] = l[min(wave * 32 + acc_row(r), p.dk - 1) * p.dv];
+    };
+    const int s0 = BACK ? p.segments - 1 : 0, step = BACK ? -1 : 1;
+    ahead(s0);
+    for (int n = 0; n < p.segments; ++n) {
+        const int s = s0 + n * step;
+        float *to = p.starts + ((int64_t)s * heads + bh) * size;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int row = t * 32 + acc_row(r);
-            S[t][r] = first && mine && row < p.dk ? first[bh * size + (int64_t)row * p.dv + column] : 0.f;
+            const int d = wave * 32 + acc_row(r);
+            if (d < p.dk && column < p.dv) to[d * p.dv + column] = S[r];
         }
-    for (int n = 0; n < p.segments; ++n) {
-        const int s = back ? p.segments - 1 - n : n;
-        const int64_t at = (int64_t)s * heads + bh;
-        if (mine)
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = t * 32 + acc_row(r);
-                    if (row < p.dk) p.starts[at * size + (int64_t)row * p.dv + column] = S[t][r];
-                }
         if (n + 1 == p.segments) break;
-        f32x16 next[KT];
+        char *const im = image[n & 1];
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+        for (int r = 0; r < 16; r += 4) {
+            const float x[4] = {S[r], S[r + 1], S[r + 2], S[r + 3]};
+            put_terms<3>(im, image_at(lane & 31, wave * 32 + acc_row(r), KS), KS * kPiece, x);
+        }
+        f32x16 part[2] = {zeros16(), zeros16()};
+        Frag<3> fm[KS];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = t * 32 + acc_row(r);
-                next[t][r] = mine && row < p.dk ? p.local[at * size + (int64_t)row * p.dv + column] : 0.f;
-            }
-        const float *map = p.maps + at * p.dk * p.dk;
+        for (int ks = 0; ks < KS; ++ks) {
+            float x[8];
 #pragma unroll
-        for (int ks = 0; ks < KT * 2; ++ks) {
-            const Frag<3> b = step_of<3>(S[ks / 2], ks & 1);
-#pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int row = t * 32 + (lane & 31), k = ks * 16 + 8 * (j >> 2) + 4 * half + (j & 3);
-                    x[j] = row < p.dk && k < p.dk ? map[back ? (int64_t)k * p.dk + row : (int64_t)row * p.dk + k] : 0.f;
-                }
-                multiply<2>(next[t], split<3>(x), b);
-            }
+            for (int j = 0; j < 8; ++j) x[j] = in && ks * 16 + 8 * (j >> 2) + 4 * half + (j & 3) < p.dk ? map[ks][j] : 0.f;
+            fm[ks] = split<3>(x);
         }
 #pragma unroll
-        for (int t = 0; t < KT; ++t) S[t] = next[t];
+        for (int r = 0; r < 16; ++r) part[0][r] = wave * 32 + acc_row(r) < p.dk ? local[r] : 0.f;
+        if (n + 2 < p.segments) ahead(s + step);
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) multiply<2>(part[ks & 1], fm[ks], piece<3>(im, ks, KS * kPiece));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[r] = part[0][r] + part[1][r];
     }
 }
 
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(256) k_delta_steps(DeltaArgs p) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int row = rg + i * 32;
-        if (from) load4(S[i], from + (int64_t)row * p.dv, column, p.dv, row < p.dk);
+        if (from) load4(S[i], from + (int64_t)min(row, p.dk - 1) * p.dv, column, p.dv, row < p.dk);
         else S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
     }
     for (int64_t t = 0; t < p.T; ++t) {
@@ -315,7 +325,7 @@ constexpr int64_t kDeltaSteps = 8;
 template <typename T, int KT>
 void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
-    constexpr int KB = C * KT * 64, MB = C * C * 2;
+    constexpr int KB = C * KT * 64, MB = tri_pieces<C>() * kPiece;
     const int heads = a.B * a.H, tiles = (a.dv + 31) / 32;
     hipLaunchKernelGGL((k_delta_prep<T, KT, false>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
     if (a.segments > 1) {
@@ -323,11 +333,11 @@ void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
         // the last segment's map is the backward pass's alone
         const int parts = a.states ? a.segments : a.segments - 1;
         hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_LOCAL>), dim3((unsigned)(parts * heads), (all + 3) / 4),
-                           dim3(std::min(4, all) * 64), N * KB * 2 + 3 * MB + 5 * C * 4, st, a);
+                           dim3(256), N * KB * 2 + 3 * MB + 5 * C * 4, st, a);
         delta_join(a, a.state, false, st);
     }
     hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_FULL>), dim3((unsigned)(a.segments * heads), (tiles + 3) / 4),
-                       dim3(std::min(4, tiles) * 64), N * KB * 3 + (3 + NY) * MB + 5 * C * 4, st, a);
+                       dim3(256), N * KB * 3 + (3 + NY) * MB + 5 * C * 4, st, a);
 }
 
 template <typename T>
@@ -359,8 +369,11 @@ const char *delta_check(const fi_delta_desc *q) {
     const int64_t ld[][2] = {{q->ld_q, qk}, {q->ld_k, qk}, {q->ld_v, v}, {q->ld_decay, h}, {q->ld_beta, h}, {q->ld_y, v},
                              {q->ld_dy, v}, {q->ld_dq, qk}, {q->ld_dk, qk}, {q->ld_dv, v}, {q->ld_ddecay, h},
                              {q->ld_dbeta, h}};
-    for (auto &l : ld)
-        if (l[0] != 0 && (l[0] < l[1] || l[0] > (int64_t(1) << 40))) return "a row pitch is less than its row";
+    for (auto &l : ld) {
+        if (l[0] != 0 && l[0] < l[1]) return "a row pitch is less than its row";
+        if (l[0] > (int64_t(1) << 24) / q->batch || l[1] > (int64_t(1) << 24) / q->batch)
+            return "the rows of a position are over 2^24 elements";
+    }
     for (int v : q->reserved)
         if (v) return "reserved is not zero";
     return nullptr;
@@ -376,14 +389,19 @@ void delta_args(const fi_delta_desc *q, const DeltaPlan &d, DeltaArgs &a) {
     a.lddv = pitch_or(q->ld_dv, v), a.lddg = pitch_or(q->ld_ddecay, a.H), a.lddb = pitch_or(q->ld_dbeta, a.H);
 }
 
+template <int KT>
+static void join(const DeltaArgs &a, const float *first, bool back, hipStream_t st) {
+    const dim3 grid(a.B * a.H, (a.dv + 31) / 32), block(KT * 64);
+    if (back) hipLaunchKernelGGL((k_delta_join<KT, true>), grid, block, 0, st, a, first);
+    else hipLaunchKernelGGL((k_delta_join<KT, false>), grid, block, 0, st, a, first);
+}
+
 void delta_join(const DeltaArgs &a, const float *first, bool back, hipStream_t st) {
-    const int tiles = (a.dv + 31) / 32;
-    const dim3 grid(a.B * a.H, (tiles + 3) / 4), block(std::min(4, tiles) * 64);
     switch ((a.dk + 31) / 32) {
-        case 1: hipLaunchKernelGGL((k_delta_join<1>), grid, block, 0, st, a, first, back); break;
-        case 2: hipLaunchKernelGGL((k_delta_join<2>), grid, block, 0, st, a, first, back); break;
-        case 3: hipLaunchKernelGGL((k_delta_join<3>), grid, block, 0, st, a, first, back); break;
-        default: hipLaunchKernelGGL((k_delta_join<4>), grid, block, 0, st, a, first, back);
+        case 1: return join<1>(a, first, back, st);
+        case 2: return join<2>(a, first, back, st);
+        case 3: return join<3>(a, first, back, st);
+        default: return join<4>(a, first, back, st);
     }
 }
 

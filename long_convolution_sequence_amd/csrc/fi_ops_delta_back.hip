@@ -19,14 +19,16 @@ namespace {
 
 // The gradient of the state through a segment's chunks, 32 columns a wave, backwards.
 // FULL: from the gradient behind the segment; dv, x and the gradients behind each
-// chunk.  Else from nothing, only the gradient before the segment.
+// chunk.  Else from nothing, only the gradient before the segment.  Loads as in the
+// forward pass; q's transpose takes the place of k in LDS after k's last use, so that two
+// workgroups share a CU.
 template <typename T, int KT, bool FULL>
-__global__ void __launch_bounds__(256) k_delta_back_chain(DeltaArgs p) {
+__global__ void __launch_bounds__(256, 2) k_delta_back_chain(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
     constexpr int MT = C / 32, CS = C / 16, KS = KT * 2, DK = KT * 32;
-    constexpr int KB = C * DK * 2, MB = C * C * 2;
+    constexpr int KB = C * DK * 2, MB = tri_pieces<C>() * kPiece;
     extern __shared__ __align__(16) char lds[];
-    char *const ik = lds, *const ikt = ik + N * KB, *const iqt = ikt + N * KB, *const in = iqt + N * KB, *const ip = in + 3 * MB;
+    char *const ik = lds, *const iqt = lds, *const ikt = ik + N * KB, *const in = ikt + N * KB, *const ip = in + 3 * MB;
     float *const f = reinterpret_cast<float *>(ip + 3 * MB);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = p.B * p.H, seg = blockIdx.x / heads + (FULL ? 0 : 1), bh = blockIdx.x % heads, b = bh / p.H, h = bh % p.H;
@@ -40,67 +42,67 @@ __global__ void __launch_bounds__(256) k_delta_back_chain(DeltaArgs p) {
                                         : p.dfinal       ? p.dfinal + bh * size
                                                          : nullptr;
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = t * 32 + acc_row(r);
-            D[t][r] = from && mine && row < p.dk ? from[(int64_t)row * p.dv + column] : 0.f;
-        }
-    const auto keep = [&](float *to) {
-        if (!mine) return;
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = t * 32 + acc_row(r);
-                if (row < p.dk) to[(int64_t)row * p.dv + column] = D[t][r];
-            }
-    };
+    for (int t = 0; t < KT; ++t) D[t] = zeros16();
+    if (from) load_state<KT>(D, from, p.dk, p.dv, column);
     const T *const q = static_cast<const T *>(p.q) + hk * p.dk, *const k = static_cast<const T *>(p.k) + hk * p.dk;
     const T *const dy = static_cast<const T *>(p.dy) + (int64_t)h * p.dv;
     T *const dv = FULL ? static_cast<T *>(p.dv_out) + (int64_t)h * p.dv : nullptr;
     const int64_t first = seg * p.per, last = min(p.chunks, first + p.per);
-    for (int64_t c = last - 1; c >= first; --c) {
-        const int64_t t0 = c * C, n = length - t0, at = c * heads + bh;
-        const int rows = (int)min<int64_t>(C, p.T - t0), live = n < 0 ? 0 : n < rows ? (int)n : rows;
-        if (live == 0) {
-            if (FULL && mine)
-                for (int i = lane >> 5; i < rows; i += 2) dv[((t0 + i) * p.B + b) * p.lddv + column] = (T)0.f;
-            continue;
+    const int64_t stop = min(last, (length + C - 1) / C);
+    if (FULL && mine)
+        for (int64_t c = max(first, stop); c < last; ++c) {
+            const int rows = (int)min<int64_t>(C, p.T - c * C);
+            for (int i = lane >> 5; i < rows; i += 2) dv[((c * C + i) * p.B + b) * p.lddv + column] = (T)0.f;
         }
+    Stage<T, C, DK> sk, sq;
+    const auto rows_from = [&](const T *x, int64_t ld, int64_t c) { return x + (c * C * p.B + b) * ld; };
+    const auto live_of = [&](int64_t c) { return (int)min<int64_t>(C, length - c * C); };
+    if (first < stop) {
+        sk.load(rows_from(k, p.ldk, stop - 1), (unsigned)(p.B * p.ldk), p.dk, live_of(stop - 1));
+        sq.load(rows_from(q, p.ldq, stop - 1), (unsigned)(p.B * p.ldq), p.dk, live_of(stop - 1));
+    }
+    for (int64_t c = stop - 1; c >= first; --c) {
+        const int64_t t0 = c * C, at = c * heads + bh;
+        const int rows = (int)min<int64_t>(C, p.T - t0), live = live_of(c);
         __syncthreads();
-        stage<T, C>(k + (t0 * p.B + b) * p.ldk, p.B * p.ldk, p.dk, DK, live, ik, ikt);
-        stage<T, C>(q + (t0 * p.B + b) * p.ldq, p.B * p.ldq, p.dk, DK, live, nullptr, iqt);
-        copy_in(in, p.images + at * image_bytes<T, true>(), 6 * MB);
-        copy_in((char *)f, (const char *)(p.factors + at * kDeltaFactors * C), 5 * C * 4);
+        bring(in, p.images + at * image_bytes<T, true>(), 6 * MB);
+        if (threadIdx.x < 5 * C) f[threadIdx.x] = p.factors[at * kDeltaFactors * C + threadIdx.x];
+        if (5 * C > 256 && threadIdx.x < 5 * C - 256) f[256 + threadIdx.x] = p.factors[at * kDeltaFactors * C + 256 + threadIdx.x];
+        sk.put(p.dk, live, ik, ikt);
         __syncthreads();
-
-        if (FULL) keep(p.ends + at * size);
+        T ys[MT][16];
+        load_column<T, MT>(ys, dy + (t0 * p.B + b) * p.lddy, min(column, p.dv - 1), (unsigned)(p.B * p.lddy), live);
+        if (c > first) sk.load(rows_from(k, p.ldk, c - 1), (unsigned)(p.B * p.ldk), p.dk, live_of(c - 1));
+        if (FULL) store_state<KT>(p.ends + at * size, D, p.dk, p.dv, column);
         f32x16 X[MT], Y[MT];
+        const int ylive = anew(live);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            X[i] = zeros16();
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = i * 32 + acc_row(r);
-                Y[i][r] = mine && row < live ? (float)dy[((t0 + row) * p.B + b) * p.lddy + column] : 0.f;
-            }
-        }
+        for (int i = 0; i < MT; ++i) X[i] = zeros16();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const Frag<3> s = step_of<3>(D[ks / 2], ks & 1);
 #pragma unroll
             for (int i = 0; i < MT; ++i) multiply<2>(X[i], piece<N>(ik, i * KS + ks, KB), s);
+            in_order();
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) X[i][r] *= f[i * 32 + acc_row(r)];
+            for (int r = 0; r < 16; ++r) {
+                const int row = i * 32 + acc_row(r);
+                X[i][r] *= f[row];
+                Y[i][r] = row < ylive ? (float)ys[i][r] : 0.f;
+            }
+        arrived();
+        __syncthreads();
+        sq.put(p.dk, live, nullptr, iqt);
+        if (c > first) sq.load(rows_from(q, p.ldq, c - 1), (unsigned)(p.B * p.ldq), p.dk, live_of(c - 1));
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
             const Frag<N> s = step_of<N>(Y[cs / 2], cs & 1);
 #pragma unroll
-            for (int i = 0; i <= cs / 2; ++i) multiply<2>(X[i], piece<3>(ip, i * CS + cs, MB), s);
+            for (int i = 0; i <= cs / 2; ++i) multiply<2>(X[i], piece<3>(ip, tri_at(i, cs), MB), s);
+            in_order();
         }
         f32x16 Z[MT];
 #pragma unroll
@@ -109,18 +111,16 @@ __global__ void __launch_bounds__(256) k_delta_back_chain(DeltaArgs p) {
         for (int cs = 0; cs < CS; ++cs) {
             const Frag<3> s = step_of<3>(X[cs / 2], cs & 1);
 #pragma unroll
-            for (int i = 0; i <= cs / 2; ++i) multiply<2>(Z[i], piece<3>(in, i * CS + cs, MB), s);
+            for (int i = 0; i <= cs / 2; ++i) multiply<2>(Z[i], piece<3>(in, tri_at(i, cs), MB), s);
+            in_order();
         }
         if (FULL && mine) {
-            float *to = p.x + at * C * p.dv + column;
+            store_column<float, MT>(p.x + at * C * p.dv, column, p.dv, Z, C, C);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = i * 32 + acc_row(r);
-                    to[row * p.dv] = Z[i][r];
-                    if (row < rows) dv[((t0 + row) * p.B + b) * p.lddv + column] = (T)(row < live ? Z[i][r] * f[3 * C + row] : 0.f);
-                }
+                for (int r = 0; r < 16; ++r) X[i][r] = Z[i][r] * f[3 * C + i * 32 + acc_row(r)];
+            store_column<T, MT>(dv + (t0 * p.B + b) * p.lddv, column, (unsigned)(p.B * p.lddv), X, rows, live);
         }
         const float decay = f[4 * C];
 #pragma unroll
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(256) k_delta_back_chain(DeltaArgs p) {
                 Y[i][r] *= f[C + row];
                 Z[i][r] *= -f[2 * C + row];
             }
+        __syncthreads();
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
             const Frag<3> sy = step_of<3>(Y[cs / 2], cs & 1), sz = step_of<3>(Z[cs / 2], cs & 1);
@@ -143,12 +144,13 @@ __global__ void __launch_bounds__(256) k_delta_back_chain(DeltaArgs p) {
                 multiply<2>(D[t], piece<N>(iqt, t * CS + cs, KB), sy);
                 multiply<2>(D[t], piece<N>(ikt, t * CS + cs, KB), sz);
             }
+            in_order();
         }
     }
     if (!FULL)
-        keep(p.local + ((int64_t)seg * heads + bh) * size);
+        store_state<KT>(p.local + ((int64_t)seg * heads + bh) * size, D, p.dk, p.dv, column);
     else if (seg == 0 && p.dstate)
-        keep(p.dstate + bh * size);
+        store_state<KT>(p.dstate + bh * size, D, p.dk, p.dv, column);
 }
 
 // Sum over the 32 lanes of a half, in every lane of it.
@@ -188,8 +190,13 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
         return;
     }
     const int64_t row0 = t0 * p.B + b;
-    stage<T, C>(static_cast<const T *>(p.k) + hk * p.dk + row0 * p.ldk, p.B * p.ldk, p.dk, DK, live, nullptr, ikt);
-    stage<T, C>(static_cast<const T *>(p.q) + hk * p.dk + row0 * p.ldq, p.B * p.ldq, p.dk, DK, live, nullptr, iqt);
+    {
+        Stage<T, C, DK> sk, sq;
+        sk.load(static_cast<const T *>(p.k) + hk * p.dk + row0 * p.ldk, (unsigned)(p.B * p.ldk), p.dk, live);
+        sq.load(static_cast<const T *>(p.q) + hk * p.dk + row0 * p.ldq, (unsigned)(p.B * p.ldq), p.dk, live);
+        sk.put(p.dk, live, nullptr, ikt);
+        sq.put(p.dk, live, nullptr, iqt);
+    }
     // four positions of this lane's channel, of an image of k or q
     const auto four = [&](const char *image, int i, float (&x)[4]) {
         x[0] = x[1] = x[2] = x[3] = 0.f;
@@ -231,10 +238,11 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
             for (int e = 0; e < MT; ++e) {
                 const int i = e * 32 + tid / 8, cc = c0 + tid % 8 * 4, to = image_at(i, tid % 8 * 4, 2);
                 float a[4], u[4], z[4], y[4];
-                load4(a, x + i * p.dv, cc, p.dv, i < live);
-                load4(u, w + i * p.dv, cc, p.dv, i < live);
-                load4(z, v + (int64_t)i * p.B * p.ldv, cc, p.dv, i < live);
-                load4(y, dy + (int64_t)i * p.B * p.lddy, cc, p.dv, i < live);
+                const int64_t ii = min(i, live - 1);
+                load4(a, x + ii * p.dv, cc, p.dv, i < live);
+                load4(u, w + ii * p.dv, cc, p.dv, i < live);
+                load4(z, v + ii * p.B * p.ldv, cc, p.dv, i < live);
+                load4(y, dy + ii * p.B * p.lddy, cc, p.dv, i < live);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) db[e] = fmaf(a[j], u[j], db[e]), dw[e] = fmaf(a[j], z[j], dw[e]);
                 put_terms<3>(ix, to, SB, a);
@@ -247,8 +255,9 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
                 if (wave < KT) {
                     const auto fetch = [&](const float *from, float (&v8)[8]) {
                         float lo[4], hi[4];
-                        load4(lo, from + (int64_t)d * p.dv, c0 + st * 16 + 4 * half, p.dv, d < p.dk);
-                        load4(hi, from + (int64_t)d * p.dv, c0 + st * 16 + 4 * half + 8, p.dv, d < p.dk);
+                        const float *row = from + (int64_t)min(d, p.dk - 1) * p.dv;
+                        load4(lo, row, c0 + st * 16 + 4 * half, p.dv, d < p.dk);
+                        load4(hi, row, c0 + st * 16 + 4 * half + 8, p.dv, d < p.dk);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v8[j] = lo[j], v8[4 + j] = hi[j];
                     };
@@ -407,10 +416,10 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
 
 template <typename T, int KT>
 void backward(const DeltaArgs &a, hipStream_t st) {
-    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, KB = C * KT * 64, MB = C * C * 2;
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, KB = C * KT * 64, MB = tri_pieces<C>() * kPiece;
     const int heads = a.B * a.H, tiles = (a.dv + 31) / 32;
-    const dim3 block(std::min(4, tiles) * 64);
-    const int chain = N * KB * 3 + 6 * MB + 5 * C * 4;
+    const dim3 block(256);
+    const int chain = N * KB * 2 + 6 * MB + 5 * C * 4;
     hipLaunchKernelGGL((k_delta_prep<T, KT, true>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
     if (a.segments > 1) {
         hipLaunchKernelGGL((k_delta_back_chain<T, KT, false>), dim3((unsigned)((a.segments - 1) * heads), (tiles + 3) / 4), block,
