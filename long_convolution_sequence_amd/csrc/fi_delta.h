@@ -20,6 +20,8 @@
 // and j with i + j <= 2 are taken (<= 1 where the result is rounded to 16 bits and
 // nothing else is made of it: 2^-17 there).  bf16 inputs are one term, fp16 two, fp32 three.
 #pragma once
+#include <type_traits>
+
 #include "fi_ops.h"
 
 namespace fi {
@@ -100,20 +102,36 @@ struct Frag {
     bf16x8 t[N];
 };
 
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using f32x2 = float __attribute__((ext_vector_type(2)));
+
+// One term of two values, and what is left of them: x - t as the dot product
+// t . (-1, 0) + x of bf16 pairs, exact, in one instruction a value (unpacking and
+// subtracting take two).  The factors come from registers: as immediates of a packed
+// instruction they would have to differ in their halves.
+__device__ __forceinline__ bf16x2 term(float &x, float &y, bool more) {
+    const bf16x2 t = __builtin_convertvector((f32x2{x, y}), bf16x2);
+    if (more) {
+        unsigned lo = 0x0000bf80u, hi = 0xbf800000u;
+        asm("" : "+s"(lo));
+        asm("" : "+s"(hi));
+        x = __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(bf16x2, lo), x, false);
+        y = __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(bf16x2, hi), y, false);
+    }
+    return t;
+}
+
 // Terms of eight values.
 template <int N>
 __device__ __forceinline__ Frag<N> split(const float (&x)[8]) {
     Frag<N> f;
-    float r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = x[i];
+    for (int i = 0; i < 8; i += 2) {
+        float u = x[i], v = x[i + 1];
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f.t[t][i] = (__bf16)r[i];
-        if (t + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] -= (float)f.t[t][i];
+        for (int t = 0; t < N; ++t) {
+            const bf16x2 two = term(u, v, t + 1 < N);
+            f.t[t][i] = two[0], f.t[t][i + 1] = two[1];
         }
     }
     return f;
@@ -159,15 +177,14 @@ __device__ __forceinline__ void put_terms(char *image, int at, int stride, const
     float r[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-        bf16x4 v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (__bf16)r[i];
-        *reinterpret_cast<bf16x4 *>(image + t * stride + at) = v;
-        if (t + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] -= (float)v[i];
-        }
+        const bf16x2 a = term(r[0], r[1], t + 1 < N), b = term(r[2], r[3], t + 1 < N);
+        *reinterpret_cast<bf16x4 *>(image + t * stride + at) = bf16x4{a[0], a[1], b[0], b[1]};
     }
+}
+// Values that are their own term.
+template <int N>
+__device__ __forceinline__ void put_terms(char *image, int at, int, const bf16_t (&x)[4]) {
+    *reinterpret_cast<bf16x4 *>(image + at) = bf16x4{x[0], x[1], x[2], x[3]};
 }
 
 // Row of register r of an accumulator, for the lane's half.
@@ -207,9 +224,10 @@ struct Stage {
 
     template <bool VEC>
     __device__ __forceinline__ void load(const T *x, unsigned pitch, int D, int live) {
+        const unsigned tid = anew_lane(threadIdx.x);
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int u = e * 256 + threadIdx.x, i = u / RUNS * 4, d = u % RUNS * 4;
+            const int u = e * 256 + (int)tid, i = u / RUNS * 4, d = u % RUNS * 4;
             if (u >= UNITS) break;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -226,18 +244,20 @@ struct Stage {
         if ((D & 3) == 0) load<true>(x, pitch, D, live);
         else load<false>(x, pitch, D, live);
     }
+    template <bool FULL>
     __device__ __forceinline__ void put(int D, int live, char *rows, char *cols) const {
-        D = anew(D), live = anew(live);
         constexpr int STEPS = DK / 16, IMAGE = C * DK * 2;
+        using V = std::conditional_t<N == 1, T, float>;
+        const unsigned tid = anew_lane(threadIdx.x);
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int u = e * 256 + threadIdx.x, i = u / RUNS * 4, d = u % RUNS * 4;
+            const int u = e * 256 + (int)tid, i = u / RUNS * 4, d = u % RUNS * 4;
             if (u >= UNITS) break;
-            float m[4][4];
+            V m[4][4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m[r][j] = i + r < live && d + j < D ? (float)raw[e][r][j] : 0.f;
+                for (int j = 0; j < 4; ++j) m[r][j] = FULL || (i + r < live && d + j < D) ? (V)raw[e][r][j] : (V)0.f;
             if (rows) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) put_terms<N>(rows, image_at(i + r, d, STEPS), IMAGE, m[r]);
@@ -245,11 +265,16 @@ struct Stage {
             if (cols) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float t[4] = {m[0][c], m[1][c], m[2][c], m[3][c]};
+                    const V t[4] = {m[0][c], m[1][c], m[2][c], m[3][c]};
                     put_terms<N>(cols, image_at(d + c, i, C / 16), IMAGE, t);
                 }
             }
         }
+    }
+    __device__ __forceinline__ void put(int D, int live, char *rows, char *cols) const {
+        D = anew(D), live = anew(live);
+        if (live == C && D == DK) put<true>(D, live, rows, cols);
+        else put<false>(D, live, rows, cols);
     }
 };
 

@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(256, 2) k_delta_chain(DeltaArgs p) {
         __syncthreads();
         T vs[MT][16];
         if (!map) load_column<T, MT>(vs, v + (t0 * p.B + b) * p.ldv, min(column, p.dv - 1), (unsigned)(p.B * p.ldv), live);
-        if (c + 1 < stop) ahead(c + 1);
         if (FULL && p.states) keep(p.states + at * size, p.dv);
 
         f32x16 R[MT], Y[MT];
@@ -111,6 +110,7 @@ __global__ void __launch_bounds__(256, 2) k_delta_chain(DeltaArgs p) {
             for (int i = cs / 2; i < MT; ++i) multiply<2>(W[i], piece<3>(im, tri_at(i, cs), MB), s);
             in_order();
         }
+        if (c + 1 < stop) ahead(c + 1);
         if (FULL) {
             if (p.w && mine) store_column<float, MT>(p.w + at * C * p.dv, column, p.dv, W, C, C);
 #pragma unroll

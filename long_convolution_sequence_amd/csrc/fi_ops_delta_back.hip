@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(256, 2) k_delta_back_chain(DeltaArgs p) {
         __syncthreads();
         T ys[MT][16];
         load_column<T, MT>(ys, dy + (t0 * p.B + b) * p.lddy, min(column, p.dv - 1), (unsigned)(p.B * p.lddy), live);
-        if (c > first) sk.load(rows_from(k, p.ldk, c - 1), (unsigned)(p.B * p.ldk), p.dk, live_of(c - 1));
         if (FULL) store_state<KT>(p.ends + at * size, D, p.dk, p.dv, column);
         f32x16 X[MT], Y[MT];
         const int ylive = anew(live);
@@ -96,7 +95,6 @@ __global__ void __launch_bounds__(256, 2) k_delta_back_chain(DeltaArgs p) {
         arrived();
         __syncthreads();
         sq.put(p.dk, live, nullptr, iqt);
-        if (c > first) sq.load(rows_from(q, p.ldq, c - 1), (unsigned)(p.B * p.ldq), p.dk, live_of(c - 1));
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
             const Frag<N> s = step_of<N>(Y[cs / 2], cs & 1);
@@ -114,6 +112,8 @@ __global__ void __launch_bounds__(256, 2) k_delta_back_chain(DeltaArgs p) {
             for (int i = 0; i <= cs / 2; ++i) multiply<2>(Z[i], piece<3>(in, tri_at(i, cs), MB), s);
             in_order();
         }
+        if (c > first) sk.load(rows_from(k, p.ldk, c - 1), (unsigned)(p.B * p.ldk), p.dk, live_of(c - 1));
+        if (c > first) sq.load(rows_from(q, p.ldq, c - 1), (unsigned)(p.B * p.ldq), p.dk, live_of(c - 1));
         if (FULL && mine) {
             store_column<float, MT>(p.x + at * C * p.dv, column, p.dv, Z, C, C);
 #pragma unroll
