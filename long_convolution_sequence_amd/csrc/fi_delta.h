@@ -30,12 +30,13 @@ constexpr int kDeltaMaxK = 128;        // channels of a key at most
 constexpr int kDeltaMaxV = 1024;       // of a value
 constexpr float kDeltaUnit = 1e-6f;    // k / sqrt(sum k^2 + this)
 constexpr int kPiece = 1024;           // bytes of an operand's piece
-constexpr int kDeltaFactors = 9;
+constexpr int kDeltaFactors = 16;      // floats a position, of which nine are used: whole pieces
 constexpr float kLog2e = 1.44269504088896f;
 
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using bf16x4 = __bf16 __attribute__((ext_vector_type(4)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
 
 // Terms of an input, positions of a chunk and terms of what only y is made of.
 // Chunks of fp16 and fp32 are 32 long: the images of two and three terms of 64
@@ -187,6 +188,31 @@ __device__ __forceinline__ void put_terms(char *image, int at, int, const bf16_t
     *reinterpret_cast<bf16x4 *>(image + at) = bf16x4{x[0], x[1], x[2], x[3]};
 }
 
+// The chains' operands: v_mfma_f32_16x16x32_bf16, so that a wave takes 16 columns and
+// four waves share a SIMD: what one waits for (a product that adds to the last, LDS,
+// memory) runs under the others.  A piece is 16 rows x 32 values of the summed index,
+// lane l's 16 bytes the values 16 (j / 4) + 4 (l / 16) + j % 4, j < 8, of row l % 16; an
+// accumulator (lane l: rows 4 (l / 16) + r of column l % 16) is half a right operand.
+__device__ __forceinline__ int tile_at(int row, int k, int steps) {
+    return ((row >> 4) * steps + (k >> 5)) * kPiece + (((k >> 2) & 3) * 16 + (row & 15)) * 16 + ((k >> 4) & 1) * 8;
+}
+__device__ __forceinline__ int tile_row(int r) { return 4 * ((threadIdx.x >> 4) & 3) + r; }
+template <int N, int M>
+__device__ __forceinline__ Frag<N> step_of(const f32x4 (&v)[M], int s) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v[2 * s][i], x[4 + i] = v[2 * s + 1][i];
+    return split<N>(x);
+}
+template <int ORDER, int NA, int NB>
+__device__ __forceinline__ void multiply(f32x4 &acc, const Frag<NA> &a, const Frag<NB> &b) {
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = NB - 1; j >= 0; --j)
+            if (i + j <= ORDER) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.t[i], b.t[j], acc, 0, 0, 0);
+}
+
 // Row of register r of an accumulator, for the lane's half.
 __device__ __forceinline__ int acc_row(int r) { return 8 * (r >> 2) + 4 * ((threadIdx.x >> 5) & 1) + (r & 3); }
 
@@ -213,13 +239,14 @@ __device__ __forceinline__ void load4(float (&x)[4], const T *row, int d, int D,
     else load4<false>(x, row, d, D, live);
 }
 
-// C rows of a tensor on their way into images: a thread of 256 takes four rows of four
-// channels.  load() reads them ahead, rows from `live` (at least one) on and channels
+// C rows of a tensor on their way into images (TILES: of 16-row pieces): a thread takes
+// four rows of four channels, with TILES one such block (chain_grid), else of 256 as many
+// as it takes.  load() reads them ahead, rows from `live` (at least one) on and channels
 // from D on as zeros; put() writes images: `rows` with the channels as the summed
 // index, `cols` (the transpose) with the positions, either null.
-template <typename T, int C, int DK>
+template <typename T, int C, int DK, bool TILES>
 struct Stage {
-    static constexpr int N = DeltaType<T>::terms, RUNS = DK / 4, UNITS = C / 4 * RUNS, EACH = (UNITS + 255) / 256;
+    static constexpr int N = DeltaType<T>::terms, RUNS = DK / 4, UNITS = C / 4 * RUNS, EACH = TILES ? 1 : (UNITS + 255) / 256;
     Chunk<T, 4> raw[EACH][4];
 
     template <bool VEC>
@@ -227,7 +254,7 @@ struct Stage {
         const unsigned tid = anew_lane(threadIdx.x);
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int u = e * 256 + (int)tid, i = u / RUNS * 4, d = u % RUNS * 4;
+            const int u = e * (int)blockDim.x + (int)tid, i = u / RUNS * 4, d = u % RUNS * 4;
             if (u >= UNITS) break;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -246,12 +273,12 @@ struct Stage {
     }
     template <bool FULL>
     __device__ __forceinline__ void put(int D, int live, char *rows, char *cols) const {
-        constexpr int STEPS = DK / 16, IMAGE = C * DK * 2;
+        constexpr int IMAGE = C * DK * 2;
         using V = std::conditional_t<N == 1, T, float>;
         const unsigned tid = anew_lane(threadIdx.x);
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const int u = e * 256 + (int)tid, i = u / RUNS * 4, d = u % RUNS * 4;
+            const int u = e * (int)blockDim.x + (int)tid, i = u / RUNS * 4, d = u % RUNS * 4;
             if (u >= UNITS) break;
             V m[4][4];
 #pragma unroll
@@ -260,13 +287,13 @@ struct Stage {
                 for (int j = 0; j < 4; ++j) m[r][j] = FULL || (i + r < live && d + j < D) ? (V)raw[e][r][j] : (V)0.f;
             if (rows) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) put_terms<N>(rows, image_at(i + r, d, STEPS), IMAGE, m[r]);
+                for (int r = 0; r < 4; ++r) put_terms<N>(rows, TILES ? tile_at(i + r, d, DK / 32) : image_at(i + r, d, DK / 16), IMAGE, m[r]);
             }
             if (cols) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const V t[4] = {m[0][c], m[1][c], m[2][c], m[3][c]};
-                    put_terms<N>(cols, image_at(d + c, i, C / 16), IMAGE, t);
+                    put_terms<N>(cols, TILES ? tile_at(d + c, i, C / 32) : image_at(d + c, i, C / 16), IMAGE, t);
                 }
             }
         }
@@ -281,85 +308,85 @@ struct Stage {
 // Addresses below are an address for the whole wave and a 32-bit byte offset of the
 // lane: a chunk's rows lie within 2^32 bytes (delta_check).
 
-// A column of C rows in the places of an accumulator, `at` for the whole wave.  Rows
-// from `live` (at least one) on read the last one.
-template <typename T, int MT>
-__device__ __forceinline__ void load_column(T (&v)[MT][16], const T *at, unsigned column, unsigned pitch, int live) {
+// A column of C rows in the places of accumulators, `at` for the whole wave.  Rows from
+// `live` (at least one) on read the last one.
+template <typename T, int M>
+__device__ __forceinline__ void load_column(T (&v)[M][4], const T *at, unsigned column, unsigned pitch, int live) {
     column = anew_lane(column), pitch = anew(pitch), live = anew(live);
-    if (live == MT * 32) {
-        const unsigned mine = column + acc_row(0) * pitch;
+    if (live == M * 16) {
+        const unsigned mine = column + tile_row(0) * pitch;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < M; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) v[i][r] = *in_row(at, mine + (i * 32 + 8 * (r >> 2) + (r & 3)) * pitch);
+            for (int r = 0; r < 4; ++r) v[i][r] = *in_row(at, mine + (i * 16 + r) * pitch);
     } else {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < M; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) v[i][r] = *in_row(at, column + min(i * 32 + acc_row(r), live - 1) * pitch);
+            for (int r = 0; r < 4; ++r) v[i][r] = *in_row(at, column + min(i * 16 + tile_row(r), live - 1) * pitch);
     }
 }
 
 // The way back: `rows` rows are there, those from `live` on get zeros.
-template <typename T, int MT>
-__device__ __forceinline__ void store_column(T *at, unsigned column, unsigned pitch, const f32x16 (&v)[MT], int rows, int live) {
+template <typename T, int M>
+__device__ __forceinline__ void store_column(T *at, unsigned column, unsigned pitch, const f32x4 (&v)[M], int rows, int live) {
     column = anew_lane(column), pitch = anew(pitch), live = anew(live), rows = anew(rows);
-    if (live == MT * 32) {
-        const unsigned mine = column + acc_row(0) * pitch;
+    if (live == M * 16) {
+        const unsigned mine = column + tile_row(0) * pitch;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < M; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) *in_row(at, mine + (i * 32 + 8 * (r >> 2) + (r & 3)) * pitch) = (T)v[i][r];
+            for (int r = 0; r < 4; ++r) *in_row(at, mine + (i * 16 + r) * pitch) = (T)v[i][r];
     } else {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < M; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = i * 32 + acc_row(r);
+            for (int r = 0; r < 4; ++r) {
+                const int row = i * 16 + tile_row(r);
                 if (row < rows) *in_row(at, column + row * pitch) = (T)(row < live ? v[i][r] : 0.f);
             }
     }
 }
 
 // A state [dk][width] as accumulators and back; nothing lies past its edges.
-template <int KT>
-__device__ __forceinline__ void load_state(f32x16 (&S)[KT], const float *from, int dk, int width, int column) {
+template <int M>
+__device__ __forceinline__ void load_state(f32x4 (&S)[M], const float *from, int dk, int width, int column) {
     const unsigned at = min(column, width - 1);
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < M; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = t * 32 + acc_row(r);
+        for (int r = 0; r < 4; ++r) {
+            const int row = t * 16 + tile_row(r);
             const float s = *in_row(from, at + (unsigned)(min(row, dk - 1) * width));
             S[t][r] = row < dk && column < width ? s : 0.f;
         }
 }
-template <int KT>
-__device__ __forceinline__ void store_state(float *to, const f32x16 (&S)[KT], int dk, int width, int column) {
+template <int M>
+__device__ __forceinline__ void store_state(float *to, const f32x4 (&S)[M], int dk, int width, int column) {
     if (column >= width) return;
     width = anew(width), dk = anew(dk), column = (int)anew_lane(column);
-    const unsigned mine = column + acc_row(0) * width;
-    if (dk == KT * 32) {
+    const unsigned mine = column + tile_row(0) * width;
+    if (dk == M * 16) {
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+        for (int t = 0; t < M; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) *in_row(to, mine + (unsigned)((t * 32 + 8 * (r >> 2) + (r & 3)) * width)) = S[t][r];
+            for (int r = 0; r < 4; ++r) *in_row(to, mine + (unsigned)((t * 16 + r) * width)) = S[t][r];
     } else {
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+        for (int t = 0; t < M; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = t * 32 + acc_row(r);
+            for (int r = 0; r < 4; ++r) {
+                const int row = t * 16 + tile_row(r);
                 if (row < dk) *in_row(to, (unsigned)(column + row * width)) = S[t][r];
             }
     }
 }
 
-// Bytes (a multiple of 1 KB) from memory into LDS past the registers, by 256 threads:
-// each wave brings 1 KB at a time.  arrived() waits for this thread's share.
+// Bytes (a multiple of 1 KB) from memory into LDS past the registers: each wave brings
+// 1 KB at a time.  arrived() waits for this thread's share.
 __device__ __forceinline__ void bring(char *to, const char *from, int bytes) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    for (int i = wave * kPiece; i < bytes; i += 4 * kPiece)
+    for (int i = wave * kPiece; i < bytes; i += (int)(blockDim.x >> 6) * kPiece)
         __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(from + i + lane * 16),
                                          (__attribute__((address_space(3))) void *)(to + i), 16, 0, 0);
 }
@@ -383,12 +410,20 @@ __device__ __forceinline__ f32x16 zeros16() {
 // Sum over a wave's lanes of the same half-position (lanes l and l ^ 32).
 __device__ __forceinline__ float both_halves(float v) { return v + __shfl_xor(v, 32, 64); }
 
-// A chunk's triangular matrices as images, the pieces that hold zeros alone left out:
-// row tiles `i` and steps `cs` along the summed index, of which forwards (below the
-// diagonal) the first 2 (i + 1) count and backwards (above it) those from 2 i on.
+// A chunk's triangular matrices as images of 16-row pieces, those that hold zeros alone
+// left out: of 64 positions, forwards (below the diagonal) rows 0 .. 31 have their first
+// step alone, backwards (above it) rows 32 .. 63 their second.
 template <int C>
 constexpr int tri_pieces() { return C == 64 ? 6 : 2; }
-__device__ __forceinline__ constexpr int tri_at(int i, int cs) { return i * 2 + cs; }
+template <int C, bool BACK>
+__device__ __forceinline__ constexpr bool tri_in(int i, int s) { return C == 32 || (BACK ? i < 2 || s == 1 : i >= 2 || s == 0); }
+template <int C, bool BACK>
+__device__ __forceinline__ constexpr int tri_at(int i, int s) {
+    return C == 32 ? i : BACK ? (i < 2 ? i * 2 + s : i + 2) : (i < 2 ? i : i * 2 - 2 + s);
+}
+// The factors that a chain reads, in whole pieces.
+template <int C>
+constexpr int factor_bytes() { return (5 * C * 4 + kPiece - 1) / kPiece * kPiece; }
 template <typename T, bool BACK>
 constexpr int image_bytes() {          // of a chunk: M in three terms and P
     return tri_pieces<DeltaType<T>::chunk>() * kPiece * (3 + (BACK ? 3 : DeltaType<T>::out));
@@ -547,19 +582,20 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
     const auto flush = [&](char *image, auto terms) {      // m (or its transpose) as an image
         constexpr int NT = decltype(terms)::value;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < C / 16; ++i)
 #pragma unroll
-            for (int cs = BACK ? 2 * i : 0; cs < (BACK ? CS : 2 * i + 2); ++cs) {
+            for (int s = 0; s < C / 32; ++s) {
+                if (!tri_in<C, BACK>(i, s)) continue;
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int r = i * 32 + col, c = cs * 16 + 8 * (j >> 2) + 4 * half + (j & 3);
+                    const int r = i * 16 + (lane & 15), c = s * 32 + 16 * (j >> 2) + 4 * (lane >> 4) + (j & 3);
                     v[j] = BACK ? m[c * LD + r] : m[r * LD + c];
                 }
                 const Frag<NT> f = split<NT>(v);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    *reinterpret_cast<bf16x8 *>(image + t * MB + tri_at(i, cs) * kPiece + lane * 16) = f.t[t];
+                    *reinterpret_cast<bf16x8 *>(image + t * MB + tri_at<C, BACK>(i, s) * kPiece + lane * 16) = f.t[t];
             }
     };
     char *image = p.images + at * image_bytes<T, BACK>();
@@ -591,6 +627,17 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
 // ---- host side -----------------------------------------------------------------
 
 constexpr int kDeltaSIMDs = 1024;      // waves that run side by side
+
+// Workgroups of a chain over `tiles` sets of 16 columns: up to eight waves each, as
+// evenly as they go, and as many at least as bring a chunk's keys with a block of four
+// rows x four channels a thread.
+struct ChainGrid {
+    unsigned groups, threads;
+};
+inline ChainGrid chain_grid(int tiles, int C, int KT) {
+    const int groups = (tiles + 7) / 8, waves = (tiles + groups - 1) / groups;
+    return {(unsigned)groups, (unsigned)std::max(64 * waves, C / 4 * KT * 8)};
+}
 
 struct DeltaPlan {
     int C, KT;

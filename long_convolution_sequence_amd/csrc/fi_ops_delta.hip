@@ -8,106 +8,110 @@ namespace {
 
 enum { CHAIN_LOCAL, CHAIN_FULL };
 
-// The sequence of a segment's chunks, 32 columns a wave (blockIdx.y: four waves'
-// columns).  FULL: from the state before the segment; y, the states before each chunk
-// and w where they are kept, the last state.  LOCAL: from nothing, only the state at
-// the end; the columns behind the state's are those of the map (v = 0, from a unit
-// column).  Two workgroups share a CU, so that the products of one run under the loads
-// and the cutting into terms of the other; k and q of the next chunk are on their way
-// in registers, M and P go into LDS under the products with S.
+// The sequence of a segment's chunks, 16 columns a wave (blockIdx.y: a workgroup's).
+// FULL: from the state before the segment; y, the states before each chunk and w where
+// they are kept, the last state.  LOCAL: from nothing, only the state at the end; the
+// columns behind the state's are those of the map (v = 0, from a unit column).
+// What a chunk needs is on its way while the one before it runs: k and q in registers,
+// M, P and the factors past them into LDS as soon as nobody reads the last ones.
 template <typename T, int KT, int MODE>
-__global__ void __launch_bounds__(256, 2) k_delta_chain(DeltaArgs p) {
+__global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
-    constexpr int MT = C / 32, CS = C / 16, KS = KT * 2, DK = KT * 32;
+    constexpr int MT = C / 16, CS = C / 32, DT = KT * 2, DK = KT * 32;
     constexpr int KB = C * DK * 2, MB = tri_pieces<C>() * kPiece;    // bytes of a term
     constexpr bool FULL = MODE == CHAIN_FULL;
     extern __shared__ __align__(16) char lds[];
     char *const ik = lds, *const ikt = ik + N * KB, *const im = ikt + N * KB;
     char *const ip = im + 3 * MB, *const iq = ip + NY * MB;   // FULL only
-    float *const f = reinterpret_cast<float *>(FULL ? iq + N * KB : ip);
+    char *const ff = FULL ? iq + N * KB : ip;
+    const float *const f = reinterpret_cast<const float *>(ff);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = p.B * p.H, seg = blockIdx.x / heads, bh = blockIdx.x % heads, b = bh / p.H, h = bh % p.H;
-    const int tiles = (p.dv + 31) / 32, tile = blockIdx.y * 4 + wave;
-    const bool map = !FULL && tile >= tiles, idle = map ? tile - tiles >= KT : tile >= tiles;
-    const int column = (map ? tile - tiles : tile) * 32 + (lane & 31), width = map ? p.dk : p.dv;
+    const int tiles = (p.dv + 15) / 16, tile = blockIdx.y * (int)(blockDim.x >> 6) + wave;
+    const bool map = !FULL && tile >= tiles, idle = map ? (tile - tiles) * 16 >= p.dk : tile >= tiles;
+    const int column = (map ? tile - tiles : tile) * 16 + (lane & 15), width = map ? p.dk : p.dv;
     const bool mine = column < width && !idle;
     const int64_t length = delta_length(p, b);
     const int hk = h / (p.H / p.HK);
     const int64_t size = (int64_t)p.dk * p.dv;
 
-    f32x16 S[KT];
+    f32x4 S[DT];
     const float *from = !FULL ? nullptr : p.segments > 1 ? p.starts + ((int64_t)seg * heads + bh) * size
                                         : p.state        ? p.state + bh * size
                                                          : nullptr;
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = map && t * 32 + acc_row(r) == column ? 1.f : 0.f;
-    if (from) load_state<KT>(S, from, p.dk, p.dv, column);
-    const auto keep = [&](float *to, int w) { store_state<KT>(to, S, p.dk, w, idle ? w : column); };
+        for (int r = 0; r < 4; ++r) S[t][r] = map && t * 16 + tile_row(r) == column ? 1.f : 0.f;
+    if (from) load_state(S, from, p.dk, p.dv, column);
+    const auto keep = [&](float *to, int w) { store_state(to, S, p.dk, w, idle ? w : column); };
 
     const T *const q = static_cast<const T *>(p.q) + hk * p.dk, *const k = static_cast<const T *>(p.k) + hk * p.dk;
     const T *const v = static_cast<const T *>(p.v) + (int64_t)h * p.dv;
     const int64_t first = seg * p.per, last = min(p.chunks, first + p.per);
     const int64_t stop = min(last, (length + C - 1) / C);      // chunks behind it hold nothing
-    Stage<T, C, DK> sk, sq;
+    Stage<T, C, DK, true> sk, sq;
+    T vs[MT][4];
     const auto ahead = [&](int64_t c) {
         const int64_t t0 = c * C;
         const int live = (int)min<int64_t>(C, length - t0);
         sk.load(k + (t0 * p.B + b) * p.ldk, (unsigned)(p.B * p.ldk), p.dk, live);
         if (FULL) sq.load(q + (t0 * p.B + b) * p.ldq, (unsigned)(p.B * p.ldq), p.dk, live);
     };
-    if (first < stop) ahead(first);
+    const auto matrices = [&](int64_t c) {                     // M, P and the factors; v
+        const int64_t at = c * heads + bh;
+        bring(im, p.images + at * image_bytes<T, false>(), (FULL ? 3 + NY : 3) * MB);
+        bring(ff, (const char *)(p.factors + at * kDeltaFactors * C), factor_bytes<C>());
+        if (!map)
+            load_column<T, MT>(vs, v + (c * C * p.B + b) * p.ldv, min(column, p.dv - 1), (unsigned)(p.B * p.ldv),
+                               (int)min<int64_t>(C, length - c * C));
+    };
+    if (first < stop) ahead(first), matrices(first);
     for (int64_t c = first; c < stop; ++c) {
         const int64_t t0 = c * C, at = c * heads + bh;
         const int rows = (int)min<int64_t>(C, p.T - t0), live = (int)min<int64_t>(C, length - t0);
         __syncthreads();
-        bring(im, p.images + at * image_bytes<T, false>(), (FULL ? 3 + NY : 3) * MB);
-        if (threadIdx.x < 5 * C) f[threadIdx.x] = p.factors[at * kDeltaFactors * C + threadIdx.x];
-        if (5 * C > 256 && threadIdx.x < 5 * C - 256) f[256 + threadIdx.x] = p.factors[at * kDeltaFactors * C + 256 + threadIdx.x];
         sk.put(p.dk, live, ik, ikt);
         if (FULL) sq.put(p.dk, live, iq, nullptr);
         __syncthreads();
-        T vs[MT][16];
-        if (!map) load_column<T, MT>(vs, v + (t0 * p.B + b) * p.ldv, min(column, p.dv - 1), (unsigned)(p.B * p.ldv), live);
         if (FULL && p.states) keep(p.states + at * size, p.dv);
 
-        f32x16 R[MT], Y[MT];
+        f32x4 R[MT], Y[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) R[i] = Y[i] = zeros16();
+        for (int i = 0; i < MT; ++i) R[i] = Y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const Frag<3> s = step_of<3>(S[ks / 2], ks & 1);
+        for (int ks = 0; ks < KT; ++ks) {
+            const Frag<3> s = step_of<3>(S, ks);
             Frag<NY> sy;
 #pragma unroll
             for (int i = 0; i < NY; ++i) sy.t[i] = s.t[i];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                multiply<2>(R[i], piece<N>(ik, i * KS + ks, KB), s);
-                if (FULL) multiply<NY - 1>(Y[i], piece<N>(iq, i * KS + ks, KB), sy);
+                multiply<2>(R[i], piece<N>(ik, i * KT + ks, KB), s);
+                if (FULL) multiply<NY - 1>(Y[i], piece<N>(iq, i * KT + ks, KB), sy);
             }
             in_order();
         }
+        arrived();
+        __syncthreads();
         // v - e^G K S, and w = M of it
         const int vlive = anew(map ? 0 : live);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = i * 32 + acc_row(r);
-                const float x = row < vlive ? (float)vs[i][r] : 0.f;
-                R[i][r] = fmaf(-f[row], R[i][r], x);
+            for (int r = 0; r < 4; ++r) {
+                const int row = i * 16 + tile_row(r);
+                R[i][r] = fmaf(-f[row], R[i][r], row < vlive ? (float)vs[i][r] : 0.f);
             }
-        arrived();
-        __syncthreads();
-        f32x16 W[MT];
+        f32x4 W[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) W[i] = zeros16();
+        for (int i = 0; i < MT; ++i) W[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
-            const Frag<3> s = step_of<3>(R[cs / 2], cs & 1);
+            const Frag<3> s = step_of<3>(R, cs);
 #pragma unroll
-            for (int i = cs / 2; i < MT; ++i) multiply<2>(W[i], piece<3>(im, tri_at(i, cs), MB), s);
+            for (int i = 0; i < MT; ++i)
+                if (tri_in<C, false>(i, cs)) multiply<2>(W[i], piece<3>(im, tri_at<C, false>(i, cs), MB), s);
             in_order();
         }
         if (c + 1 < stop) ahead(c + 1);
@@ -116,12 +120,13 @@ __global__ void __launch_bounds__(256, 2) k_delta_chain(DeltaArgs p) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) Y[i][r] *= f[C + i * 32 + acc_row(r)];
+                for (int r = 0; r < 4; ++r) Y[i][r] *= f[C + i * 16 + tile_row(r)];
 #pragma unroll
             for (int cs = 0; cs < CS; ++cs) {
-                const Frag<NY> s = step_of<NY>(W[cs / 2], cs & 1);
+                const Frag<NY> s = step_of<NY>(W, cs);
 #pragma unroll
-                for (int i = cs / 2; i < MT; ++i) multiply<NY - 1>(Y[i], piece<NY>(ip, tri_at(i, cs), MB), s);
+                for (int i = 0; i < MT; ++i)
+                    if (tri_in<C, false>(i, cs)) multiply<NY - 1>(Y[i], piece<NY>(ip, tri_at<C, false>(i, cs), MB), s);
                 in_order();
             }
             if (mine)
@@ -130,18 +135,18 @@ __global__ void __launch_bounds__(256, 2) k_delta_chain(DeltaArgs p) {
         }
         const float decay = f[4 * C];
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) S[t][r] *= decay;
+        for (int t = 0; t < DT; ++t) S[t] *= decay;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) W[i][r] *= f[2 * C + i * 32 + acc_row(r)];
+            for (int r = 0; r < 4; ++r) W[i][r] *= f[2 * C + i * 16 + tile_row(r)];
+        __syncthreads();
+        if (c + 1 < stop) matrices(c + 1);
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
-            const Frag<3> s = step_of<3>(W[cs / 2], cs & 1);
+            const Frag<3> s = step_of<3>(W, cs);
 #pragma unroll
-            for (int t = 0; t < KT; ++t) multiply<2>(S[t], piece<N>(ikt, t * CS + cs, KB), s);
+            for (int t = 0; t < DT; ++t) multiply<2>(S[t], piece<N>(ikt, t * CS + cs, KB), s);
             in_order();
         }
     }
@@ -155,9 +160,8 @@ __global__ void __launch_bounds__(256, 2) k_delta_chain(DeltaArgs p) {
         const int64_t t0 = c * C;
         const int rows = (int)min<int64_t>(C, p.T - t0);
         T *const y = static_cast<T *>(p.y) + (int64_t)h * p.dv + (t0 * p.B + b) * p.ldy + column;
-        if (p.states && c == stop) keep(p.states + (c * heads + bh) * size, p.dv);
         if (mine)
-            for (int i = lane >> 5; i < rows; i += 2) y[i * p.B * p.ldy] = (T)0.f;
+            for (int i = lane >> 4; i < rows; i += 4) y[i * p.B * p.ldy] = (T)0.f;
     }
     if (seg == p.segments - 1 && p.final) keep(p.final + bh * size, p.dv);
 }
@@ -325,19 +329,20 @@ constexpr int64_t kDeltaSteps = 8;
 template <typename T, int KT>
 void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
-    constexpr int KB = C * KT * 64, MB = tri_pieces<C>() * kPiece;
-    const int heads = a.B * a.H, tiles = (a.dv + 31) / 32;
+    constexpr int KB = C * KT * 64, MB = tri_pieces<C>() * kPiece, FB = factor_bytes<C>();
+    const int heads = a.B * a.H;
     hipLaunchKernelGGL((k_delta_prep<T, KT, false>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
     if (a.segments > 1) {
-        const int all = tiles + KT;
         // the last segment's map is the backward pass's alone
         const int parts = a.states ? a.segments : a.segments - 1;
-        hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_LOCAL>), dim3((unsigned)(parts * heads), (all + 3) / 4),
-                           dim3(256), N * KB * 2 + 3 * MB + 5 * C * 4, st, a);
+        const ChainGrid g = chain_grid((a.dv + 15) / 16 + (a.dk + 15) / 16, C, KT);
+        hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_LOCAL>), dim3((unsigned)(parts * heads), g.groups), dim3(g.threads),
+                           N * KB * 2 + 3 * MB + FB, st, a);
         delta_join(a, a.state, false, st);
     }
-    hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_FULL>), dim3((unsigned)(a.segments * heads), (tiles + 3) / 4),
-                       dim3(256), N * KB * 3 + (3 + NY) * MB + 5 * C * 4, st, a);
+    const ChainGrid g = chain_grid((a.dv + 15) / 16, C, KT);
+    hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_FULL>), dim3((unsigned)(a.segments * heads), g.groups), dim3(g.threads),
+                       N * KB * 3 + (3 + NY) * MB + FB, st, a);
 }
 
 template <typename T>

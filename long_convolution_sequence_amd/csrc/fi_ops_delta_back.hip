@@ -17,33 +17,33 @@ namespace fi {
 
 namespace {
 
-// The gradient of the state through a segment's chunks, 32 columns a wave, backwards.
+// The gradient of the state through a segment's chunks, 16 columns a wave, backwards.
 // FULL: from the gradient behind the segment; dv, x and the gradients behind each
 // chunk.  Else from nothing, only the gradient before the segment.  Loads as in the
-// forward pass; q's transpose takes the place of k in LDS after k's last use, so that two
-// workgroups share a CU.
+// forward pass; q's transpose takes the place of k in LDS after k's last use.
 template <typename T, int KT, bool FULL>
-__global__ void __launch_bounds__(256, 2) k_delta_back_chain(DeltaArgs p) {
+__global__ void __launch_bounds__(512, 4) k_delta_back_chain(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
-    constexpr int MT = C / 32, CS = C / 16, KS = KT * 2, DK = KT * 32;
+    constexpr int MT = C / 16, CS = C / 32, DT = KT * 2, DK = KT * 32;
     constexpr int KB = C * DK * 2, MB = tri_pieces<C>() * kPiece;
     extern __shared__ __align__(16) char lds[];
     char *const ik = lds, *const iqt = lds, *const ikt = ik + N * KB, *const in = ikt + N * KB, *const ip = in + 3 * MB;
-    float *const f = reinterpret_cast<float *>(ip + 3 * MB);
+    char *const ff = ip + 3 * MB;
+    const float *const f = reinterpret_cast<const float *>(ff);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = p.B * p.H, seg = blockIdx.x / heads + (FULL ? 0 : 1), bh = blockIdx.x % heads, b = bh / p.H, h = bh % p.H;
-    const int column = (blockIdx.y * 4 + wave) * 32 + (lane & 31);
+    const int column = (blockIdx.y * (int)(blockDim.x >> 6) + wave) * 16 + (lane & 15);
     const bool mine = column < p.dv;
     const int64_t length = delta_length(p, b), size = (int64_t)p.dk * p.dv;
     const int hk = h / (p.H / p.HK);
 
-    f32x16 D[KT];
+    f32x4 D[DT];
     const float *from = !FULL ? nullptr : p.segments > 1 ? p.starts + ((int64_t)seg * heads + bh) * size
                                         : p.dfinal       ? p.dfinal + bh * size
                                                          : nullptr;
 #pragma unroll
-    for (int t = 0; t < KT; ++t) D[t] = zeros16();
-    if (from) load_state<KT>(D, from, p.dk, p.dv, column);
+    for (int t = 0; t < DT; ++t) D[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (from) load_state(D, from, p.dk, p.dv, column);
     const T *const q = static_cast<const T *>(p.q) + hk * p.dk, *const k = static_cast<const T *>(p.k) + hk * p.dk;
     const T *const dy = static_cast<const T *>(p.dy) + (int64_t)h * p.dv;
     T *const dv = FULL ? static_cast<T *>(p.dv_out) + (int64_t)h * p.dv : nullptr;
@@ -52,105 +52,109 @@ __global__ void __launch_bounds__(256, 2) k_delta_back_chain(DeltaArgs p) {
     if (FULL && mine)
         for (int64_t c = max(first, stop); c < last; ++c) {
             const int rows = (int)min<int64_t>(C, p.T - c * C);
-            for (int i = lane >> 5; i < rows; i += 2) dv[((c * C + i) * p.B + b) * p.lddv + column] = (T)0.f;
+            for (int i = lane >> 4; i < rows; i += 4) dv[((c * C + i) * p.B + b) * p.lddv + column] = (T)0.f;
         }
-    Stage<T, C, DK> sk, sq;
+    Stage<T, C, DK, true> sk, sq;
+    T ys[MT][4];
     const auto rows_from = [&](const T *x, int64_t ld, int64_t c) { return x + (c * C * p.B + b) * ld; };
     const auto live_of = [&](int64_t c) { return (int)min<int64_t>(C, length - c * C); };
-    if (first < stop) {
-        sk.load(rows_from(k, p.ldk, stop - 1), (unsigned)(p.B * p.ldk), p.dk, live_of(stop - 1));
-        sq.load(rows_from(q, p.ldq, stop - 1), (unsigned)(p.B * p.ldq), p.dk, live_of(stop - 1));
-    }
+    const auto ahead = [&](int64_t c) {
+        sk.load(rows_from(k, p.ldk, c), (unsigned)(p.B * p.ldk), p.dk, live_of(c));
+        sq.load(rows_from(q, p.ldq, c), (unsigned)(p.B * p.ldq), p.dk, live_of(c));
+    };
+    const auto matrices = [&](int64_t c) {                    // N, P and the factors; dy
+        const int64_t at = c * heads + bh;
+        bring(in, p.images + at * image_bytes<T, true>(), 6 * MB);
+        bring(ff, (const char *)(p.factors + at * kDeltaFactors * C), factor_bytes<C>());
+        load_column<T, MT>(ys, rows_from(dy, p.lddy, c), min(column, p.dv - 1), (unsigned)(p.B * p.lddy), live_of(c));
+    };
+    if (first < stop) ahead(stop - 1), matrices(stop - 1);
     for (int64_t c = stop - 1; c >= first; --c) {
         const int64_t t0 = c * C, at = c * heads + bh;
         const int rows = (int)min<int64_t>(C, p.T - t0), live = live_of(c);
         __syncthreads();
-        bring(in, p.images + at * image_bytes<T, true>(), 6 * MB);
-        if (threadIdx.x < 5 * C) f[threadIdx.x] = p.factors[at * kDeltaFactors * C + threadIdx.x];
-        if (5 * C > 256 && threadIdx.x < 5 * C - 256) f[256 + threadIdx.x] = p.factors[at * kDeltaFactors * C + 256 + threadIdx.x];
         sk.put(p.dk, live, ik, ikt);
         __syncthreads();
-        T ys[MT][16];
-        load_column<T, MT>(ys, dy + (t0 * p.B + b) * p.lddy, min(column, p.dv - 1), (unsigned)(p.B * p.lddy), live);
-        if (FULL) store_state<KT>(p.ends + at * size, D, p.dk, p.dv, column);
-        f32x16 X[MT], Y[MT];
-        const int ylive = anew(live);
+        if (FULL) store_state(p.ends + at * size, D, p.dk, p.dv, column);
+        f32x4 X[MT], Y[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) X[i] = zeros16();
+        for (int i = 0; i < MT; ++i) X[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const Frag<3> s = step_of<3>(D[ks / 2], ks & 1);
+        for (int ks = 0; ks < KT; ++ks) {
+            const Frag<3> s = step_of<3>(D, ks);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) multiply<2>(X[i], piece<N>(ik, i * KS + ks, KB), s);
+            for (int i = 0; i < MT; ++i) multiply<2>(X[i], piece<N>(ik, i * KT + ks, KB), s);
             in_order();
         }
+        arrived();
+        __syncthreads();
+        const int ylive = anew(live);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = i * 32 + acc_row(r);
+            for (int r = 0; r < 4; ++r) {
+                const int row = i * 16 + tile_row(r);
                 X[i][r] *= f[row];
                 Y[i][r] = row < ylive ? (float)ys[i][r] : 0.f;
             }
-        arrived();
-        __syncthreads();
         sq.put(p.dk, live, nullptr, iqt);
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
-            const Frag<N> s = step_of<N>(Y[cs / 2], cs & 1);
+            const Frag<N> s = step_of<N>(Y, cs);
 #pragma unroll
-            for (int i = 0; i <= cs / 2; ++i) multiply<2>(X[i], piece<3>(ip, tri_at(i, cs), MB), s);
+            for (int i = 0; i < MT; ++i)
+                if (tri_in<C, true>(i, cs)) multiply<2>(X[i], piece<3>(ip, tri_at<C, true>(i, cs), MB), s);
             in_order();
         }
-        f32x16 Z[MT];
+        f32x4 Z[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) Z[i] = zeros16();
+        for (int i = 0; i < MT; ++i) Z[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
-            const Frag<3> s = step_of<3>(X[cs / 2], cs & 1);
+            const Frag<3> s = step_of<3>(X, cs);
 #pragma unroll
-            for (int i = 0; i <= cs / 2; ++i) multiply<2>(Z[i], piece<3>(in, tri_at(i, cs), MB), s);
+            for (int i = 0; i < MT; ++i)
+                if (tri_in<C, true>(i, cs)) multiply<2>(Z[i], piece<3>(in, tri_at<C, true>(i, cs), MB), s);
             in_order();
         }
-        if (c > first) sk.load(rows_from(k, p.ldk, c - 1), (unsigned)(p.B * p.ldk), p.dk, live_of(c - 1));
-        if (c > first) sq.load(rows_from(q, p.ldq, c - 1), (unsigned)(p.B * p.ldq), p.dk, live_of(c - 1));
+        if (c > first) ahead(c - 1);
         if (FULL && mine) {
             store_column<float, MT>(p.x + at * C * p.dv, column, p.dv, Z, C, C);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) X[i][r] = Z[i][r] * f[3 * C + i * 32 + acc_row(r)];
+                for (int r = 0; r < 4; ++r) X[i][r] = Z[i][r] * f[3 * C + i * 16 + tile_row(r)];
             store_column<T, MT>(dv + (t0 * p.B + b) * p.lddv, column, (unsigned)(p.B * p.lddv), X, rows, live);
         }
         const float decay = f[4 * C];
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) D[t][r] *= decay;
+        for (int t = 0; t < DT; ++t) D[t] *= decay;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = i * 32 + acc_row(r);
+            for (int r = 0; r < 4; ++r) {
+                const int row = i * 16 + tile_row(r);
                 Y[i][r] *= f[C + row];
                 Z[i][r] *= -f[2 * C + row];
             }
         __syncthreads();
+        if (c > first) matrices(c - 1);
 #pragma unroll
         for (int cs = 0; cs < CS; ++cs) {
-            const Frag<3> sy = step_of<3>(Y[cs / 2], cs & 1), sz = step_of<3>(Z[cs / 2], cs & 1);
+            const Frag<3> sy = step_of<3>(Y, cs);
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                multiply<2>(D[t], piece<N>(iqt, t * CS + cs, KB), sy);
-                multiply<2>(D[t], piece<N>(ikt, t * CS + cs, KB), sz);
-            }
+            for (int t = 0; t < DT; ++t) multiply<2>(D[t], piece<N>(iqt, t * CS + cs, KB), sy);
+            in_order();
+            const Frag<3> sz = step_of<3>(Z, cs);
+#pragma unroll
+            for (int t = 0; t < DT; ++t) multiply<2>(D[t], piece<N>(ikt, t * CS + cs, KB), sz);
             in_order();
         }
     }
     if (!FULL)
-        store_state<KT>(p.local + ((int64_t)seg * heads + bh) * size, D, p.dk, p.dv, column);
+        store_state(p.local + ((int64_t)seg * heads + bh) * size, D, p.dk, p.dv, column);
     else if (seg == 0 && p.dstate)
-        store_state<KT>(p.dstate + bh * size, D, p.dk, p.dv, column);
+        store_state(p.dstate + bh * size, D, p.dk, p.dv, column);
 }
 
 // Sum over the 32 lanes of a half, in every lane of it.
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
     }
     const int64_t row0 = t0 * p.B + b;
     {
-        Stage<T, C, DK> sk, sq;
+        Stage<T, C, DK, false> sk, sq;
         sk.load(static_cast<const T *>(p.k) + hk * p.dk + row0 * p.ldk, (unsigned)(p.B * p.ldk), p.dk, live);
         sq.load(static_cast<const T *>(p.q) + hk * p.dk + row0 * p.ldq, (unsigned)(p.B * p.ldq), p.dk, live);
         sk.put(p.dk, live, nullptr, ikt);
@@ -417,16 +421,16 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
 template <typename T, int KT>
 void backward(const DeltaArgs &a, hipStream_t st) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, KB = C * KT * 64, MB = tri_pieces<C>() * kPiece;
-    const int heads = a.B * a.H, tiles = (a.dv + 31) / 32;
-    const dim3 block(256);
-    const int chain = N * KB * 2 + 6 * MB + 5 * C * 4;
+    const int heads = a.B * a.H;
+    const ChainGrid g = chain_grid((a.dv + 15) / 16, C, KT);
+    const int chain = N * KB * 2 + 6 * MB + factor_bytes<C>();
     hipLaunchKernelGGL((k_delta_prep<T, KT, true>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
     if (a.segments > 1) {
-        hipLaunchKernelGGL((k_delta_back_chain<T, KT, false>), dim3((unsigned)((a.segments - 1) * heads), (tiles + 3) / 4), block,
+        hipLaunchKernelGGL((k_delta_back_chain<T, KT, false>), dim3((unsigned)((a.segments - 1) * heads), g.groups), dim3(g.threads),
                            chain, st, a);
         delta_join(a, a.dfinal, true, st);
     }
-    hipLaunchKernelGGL((k_delta_back_chain<T, KT, true>), dim3((unsigned)(a.segments * heads), (tiles + 3) / 4), block, chain, st,
+    hipLaunchKernelGGL((k_delta_back_chain<T, KT, true>), dim3((unsigned)(a.segments * heads), g.groups), dim3(g.threads), chain, st,
                        a);
     hipLaunchKernelGGL((k_delta_grads<T, KT>), dim3((unsigned)(a.chunks * a.B * a.HK)), dim3(256),
                        (6 + N) * C / 32 * 2 * kPiece + 2 * N * KB + 2 * C * (C + 4) * 4, st, a);
