@@ -76,7 +76,7 @@ struct DeltaArgs {
     float *w, *x;                          // [C][dv]
     // [segment][B][H]
     float *local;                          // [dk][dv] what a segment makes of nothing
-    float *maps;                           // [dk][dk] what it makes of a state
+    float *maps, *mapst;                   // [dk][dk] what it makes of a state, and its transpose
     float *starts;                         // [dk][dv] the state before it (backwards: the gradient behind it)
 };
 
@@ -233,10 +233,13 @@ __device__ __forceinline__ void load4(float (&x)[4], const T *row, int d, int D,
         }
     }
 }
-template <typename T>
-__device__ __forceinline__ void load4(float (&x)[4], const T *row, int d, int D, bool live) {
-    if ((D & 3) == 0) load4<true>(x, row, d, D, live);
-    else load4<false>(x, row, d, D, live);
+template <bool VEC, typename T>
+__device__ __forceinline__ Chunk<T, 4> raw4(const T *row, int d, int D) {
+    if (VEC) return *reinterpret_cast<const Chunk<T, 4> *>(row + min(d, D - 4));
+    Chunk<T, 4> v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = row[min(d + i, D - 1)];
+    return v;
 }
 
 // C rows of a tensor on their way into images (TILES: of 16-row pieces): a thread takes
@@ -439,7 +442,7 @@ constexpr int image_bytes() {          // of a chunk: M in three terms and P
 // The inverse: a lane solves for a column of a diagonal block of 32, row by row from
 // registers, the rows of A read from LDS for all lanes of a block at once; the block
 // below them is -N22 (A21 N11).
-template <typename T, int KT, bool BACK>
+template <typename T, int KT, bool BACK, bool VEC>
 __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, MT = C / 32, CS = C / 16, KS = KT * 2, LD = C + 4;
     constexpr int PT = BACK ? 3 : DeltaType<T>::out, MB = tri_pieces<C>() * kPiece;
@@ -468,29 +471,38 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
         sum[lane] = s;
         fb[lane] = beta;
     }
-    // k and q as operands, straight from memory
-    Frag<N> ks_[MT][KS];
-    float ssk[MT], ssq[MT];
-    const auto fetch = [&](const T *from, int64_t ld, int mt, int ks, float &ss) {
-        const int i = mt * 32 + col;
-        const T *row = from + ((t0 + min(i, live - 1)) * p.B + b) * ld;
-        float x[8], y[4], z[4];
-        load4(y, row, ks * 16 + 4 * half, p.dk, i < live);
-        load4(z, row, ks * 16 + 4 * half + 8, p.dk, i < live);
+    // k and q as operands, straight from memory: all of their loads together
+    const T *k = static_cast<const T *>(p.k) + hk * p.dk, *q = static_cast<const T *>(p.q) + hk * p.dk;
+    Chunk<T, 4> rawk[MT][KS][2], rawq[MT][KS][2];
+    const auto fetch = [&](Chunk<T, 4> (&raw)[MT][KS][2], const T *from, int64_t ld) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = y[j], x[4 + j] = z[j];
-            ss = fmaf(y[j], y[j], ss);
-            ss = fmaf(z[j], z[j], ss);
+        for (int mt = 0; mt < MT; ++mt) {
+            const T *row = from + ((t0 + min(mt * 32 + col, live - 1)) * p.B + b) * ld;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) raw[mt][ks][e] = raw4<VEC>(row, ks * 16 + 4 * half + 8 * e, p.dk);
+        }
+    };
+    fetch(rawk, k, p.ldk);
+    fetch(rawq, q, p.ldq);
+    float ssk[MT], ssq[MT];
+    const auto operand = [&](const Chunk<T, 4> (&raw)[2], int mt, int ks, float &ss) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = mt * 32 + col < live && ks * 16 + 4 * half + 8 * (j >> 2) + (j & 3) < p.dk;
+            x[j] = in ? (float)raw[j >> 2][j & 3] : 0.f;
+            ss = fmaf(x[j], x[j], ss);
         }
         return split<N>(x);
     };
-    const T *k = static_cast<const T *>(p.k) + hk * p.dk, *q = static_cast<const T *>(p.q) + hk * p.dk;
+    Frag<N> ks_[MT][KS];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         ssk[mt] = ssq[mt] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) ks_[mt][ks] = fetch(k, p.ldk, mt, ks, ssk[mt]);
+        for (int ks = 0; ks < KS; ++ks) ks_[mt][ks] = operand(rawk[mt][ks], mt, ks, ssk[mt]);
     }
     f32x16 kk[MT][MT], qk[MT][MT];
 #pragma unroll
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const Frag<N> fq_ = fetch(q, p.ldq, i, ks, ssq[i]);
+            const Frag<N> fq_ = operand(rawq[i][ks], i, ks, ssq[i]);
 #pragma unroll
             for (int j = 0; j <= i; ++j) {
                 multiply<2>(kk[i][j], ks_[i][ks], ks_[j][ks]);
@@ -626,7 +638,7 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
 
 // ---- host side -----------------------------------------------------------------
 
-constexpr int kDeltaSIMDs = 1024;      // waves that run side by side
+constexpr int kDeltaWaves = 1536;      // sets of 32 columns that fill the card
 
 // Workgroups of a chain over `tiles` sets of 16 columns: up to eight waves each, as
 // evenly as they go, and as many at least as bring a chunk's keys with a block of four
@@ -657,7 +669,7 @@ inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
     d.KT = (q->dk + 31) / 32;
     d.chunks = (q->T + d.C - 1) / d.C;
     const int64_t heads = (int64_t)q->batch * q->heads, waves = heads * ((q->dv + 31) / 32);
-    int64_t want = std::min<int64_t>(kDeltaSIMDs / std::max<int64_t>(1, waves), d.chunks / 8);
+    int64_t want = std::min<int64_t>(kDeltaWaves / std::max<int64_t>(1, waves), d.chunks / 8);
     if (want < 4) want = 1;
     d.per = std::max<int64_t>(1, (d.chunks + want - 1) / want);
     d.segments = (int)std::max<int64_t>(1, (d.chunks + d.per - 1) / d.per);

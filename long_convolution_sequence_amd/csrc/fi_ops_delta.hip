@@ -151,8 +151,18 @@ __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
         }
     }
     if (!FULL) {
-        if (map) keep(p.maps + ((int64_t)seg * heads + bh) * p.dk * p.dk, p.dk);
-        else keep(p.local + ((int64_t)seg * heads + bh) * size, p.dv);
+        // the map as it is for the backward pass, transposed for joining forwards: either
+        // way a wave then reads it along its lanes
+        if (map) {
+            const int64_t to = ((int64_t)seg * heads + bh) * p.dk * p.dk;
+            if (p.states) keep(p.maps + to, p.dk);
+            if (!idle && column < p.dk)
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (t * 16 + tile_row(r) < p.dk) p.mapst[to + column * p.dk + t * 16 + tile_row(r)] = S[t][r];
+        } else keep(p.local + ((int64_t)seg * heads + bh) * size, p.dv);
         return;
     }
     // behind the sequence's end: y = 0, the state as it is
@@ -187,13 +197,13 @@ __global__ void __launch_bounds__(KT * 64) k_delta_join(DeltaArgs p, const float
     }
     float map[KS][8], local[16];
     const auto ahead = [&](int s) {
-        const float *m = p.maps + ((int64_t)s * heads + bh) * msize, *l = p.local + ((int64_t)s * heads + bh) * size + at;
+        const float *m = (BACK ? p.maps : p.mapst) + ((int64_t)s * heads + bh) * msize, *l = p.local + ((int64_t)s * heads + bh) * size + at;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int k = min(ks * 16 + 8 * (j >> 2) + 4 * half + (j & 3), p.dk - 1);
-                map[ks][j] = m[BACK ? k * p.dk + row : row * p.dk + k];
+                map[ks][j] = m[k * p.dk + row];
             }
 #pragma unroll
         for (int r = 0; r < 16; ++r) local[r] = l[min(wave * 32 + acc_row(r), p.dk - 1) * p.dv];
@@ -248,12 +258,14 @@ __global__ void __launch_bounds__(256) k_delta_steps(DeltaArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, cg = tid & 7, rg = tid >> 3;
     const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.HK), column = blockIdx.y * 32 + cg * 4;
     const int64_t length = delta_length(p, b);
+    const bool vec = (p.dv & 3) == 0;
     float S[ROWS][4];
     const float *from = p.state ? p.state + (int64_t)bh * p.dk * p.dv : nullptr;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int row = rg + i * 32;
-        if (from) load4(S[i], from + (int64_t)min(row, p.dk - 1) * p.dv, column, p.dv, row < p.dk);
+        if (from && vec) load4<true>(S[i], from + (int64_t)min(row, p.dk - 1) * p.dv, column, p.dv, row < p.dk);
+        else if (from) load4<false>(S[i], from + (int64_t)min(row, p.dk - 1) * p.dv, column, p.dv, row < p.dk);
         else S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
     }
     for (int64_t t = 0; t < p.T; ++t) {
@@ -297,7 +309,7 @@ __global__ void __launch_bounds__(256) k_delta_steps(DeltaArgs p) {
         }
         __syncthreads();
         float v[4];
-        load4(v, static_cast<const T *>(p.v) + row * p.ldv + (int64_t)h * p.dv, column, p.dv, true);
+        load4<false>(v, static_cast<const T *>(p.v) + row * p.ldv + (int64_t)h * p.dv, column, p.dv, true);
         const float g = p.g[row * p.ldg + h], beta = p.beta[row * p.ldb + h], a = exp2f(g * kLog2e);
         const float cross = (dots[2][0] + dots[2][1]) * rk * rq;
 #pragma unroll
@@ -331,7 +343,9 @@ void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
     constexpr int KB = C * KT * 64, MB = tri_pieces<C>() * kPiece, FB = factor_bytes<C>();
     const int heads = a.B * a.H;
-    hipLaunchKernelGGL((k_delta_prep<T, KT, false>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
+    const dim3 all((unsigned)(a.chunks * heads));
+    if (a.dk % 4 == 0) hipLaunchKernelGGL((k_delta_prep<T, KT, false, true>), all, dim3(64), 0, st, a);
+    else hipLaunchKernelGGL((k_delta_prep<T, KT, false, false>), all, dim3(64), 0, st, a);
     if (a.segments > 1) {
         // the last segment's map is the backward pass's alone
         const int parts = a.states ? a.segments : a.segments - 1;
@@ -464,7 +478,7 @@ fi_status fi_delta_forward(const fi_delta_desc *desc, const void *q, const void 
     a.factors = (float *)w, w += d.factors;
     a.starts = (float *)w, w += d.local;
     a.local = (float *)w, w += d.local;
-    a.maps = (float *)w;
+    a.mapst = (float *)w;
     if (saved) {
         char *s = (char *)saved;
         const size_t last = up256((size_t)a.B * a.H * a.dk * a.dv * 4);

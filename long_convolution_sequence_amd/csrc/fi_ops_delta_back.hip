@@ -166,7 +166,7 @@ __device__ __forceinline__ float half_sum(float v) {
 
 // What is a chunk's own, for a key head and the heads that share it: a workgroup a
 // chunk, a wave 32 channels of the keys.
-template <typename T, int KT>
+template <typename T, int KT, bool VEC>
 __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
     constexpr int MT = C / 32, CS = C / 16, DK = KT * 32, KB = C * DK * 2, LD = C + 4, SB = MT * 2 * kPiece;
@@ -243,10 +243,10 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
                 const int i = e * 32 + tid / 8, cc = c0 + tid % 8 * 4, to = image_at(i, tid % 8 * 4, 2);
                 float a[4], u[4], z[4], y[4];
                 const int64_t ii = min(i, live - 1);
-                load4(a, x + ii * p.dv, cc, p.dv, i < live);
-                load4(u, w + ii * p.dv, cc, p.dv, i < live);
-                load4(z, v + ii * p.B * p.ldv, cc, p.dv, i < live);
-                load4(y, dy + ii * p.B * p.lddy, cc, p.dv, i < live);
+                load4<VEC>(a, x + ii * p.dv, cc, p.dv, i < live);
+                load4<VEC>(u, w + ii * p.dv, cc, p.dv, i < live);
+                load4<VEC>(z, v + ii * p.B * p.ldv, cc, p.dv, i < live);
+                load4<VEC>(y, dy + ii * p.B * p.lddy, cc, p.dv, i < live);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) db[e] = fmaf(a[j], u[j], db[e]), dw[e] = fmaf(a[j], z[j], dw[e]);
                 put_terms<3>(ix, to, SB, a);
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
                     const auto fetch = [&](const float *from, float (&v8)[8]) {
                         float lo[4], hi[4];
                         const float *row = from + (int64_t)min(d, p.dk - 1) * p.dv;
-                        load4(lo, row, c0 + st * 16 + 4 * half, p.dv, d < p.dk);
-                        load4(hi, row, c0 + st * 16 + 4 * half + 8, p.dv, d < p.dk);
+                        load4<VEC>(lo, row, c0 + st * 16 + 4 * half, p.dv, d < p.dk);
+                        load4<VEC>(hi, row, c0 + st * 16 + 4 * half + 8, p.dv, d < p.dk);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v8[j] = lo[j], v8[4 + j] = hi[j];
                     };
@@ -424,7 +424,9 @@ void backward(const DeltaArgs &a, hipStream_t st) {
     const int heads = a.B * a.H;
     const ChainGrid g = chain_grid((a.dv + 15) / 16, C, KT);
     const int chain = N * KB * 2 + 6 * MB + factor_bytes<C>();
-    hipLaunchKernelGGL((k_delta_prep<T, KT, true>), dim3((unsigned)(a.chunks * heads)), dim3(64), 0, st, a);
+    const dim3 all((unsigned)(a.chunks * heads));
+    if (a.dk % 4 == 0) hipLaunchKernelGGL((k_delta_prep<T, KT, true, true>), all, dim3(64), 0, st, a);
+    else hipLaunchKernelGGL((k_delta_prep<T, KT, true, false>), all, dim3(64), 0, st, a);
     if (a.segments > 1) {
         hipLaunchKernelGGL((k_delta_back_chain<T, KT, false>), dim3((unsigned)((a.segments - 1) * heads), g.groups), dim3(g.threads),
                            chain, st, a);
@@ -432,8 +434,10 @@ void backward(const DeltaArgs &a, hipStream_t st) {
     }
     hipLaunchKernelGGL((k_delta_back_chain<T, KT, true>), dim3((unsigned)(a.segments * heads), g.groups), dim3(g.threads), chain, st,
                        a);
-    hipLaunchKernelGGL((k_delta_grads<T, KT>), dim3((unsigned)(a.chunks * a.B * a.HK)), dim3(256),
-                       (6 + N) * C / 32 * 2 * kPiece + 2 * N * KB + 2 * C * (C + 4) * 4, st, a);
+    const dim3 own((unsigned)(a.chunks * a.B * a.HK));
+    const int lds = (6 + N) * C / 32 * 2 * kPiece + 2 * N * KB + 2 * C * (C + 4) * 4;
+    if (a.dv % 4 == 0) hipLaunchKernelGGL((k_delta_grads<T, KT, true>), own, dim3(256), lds, st, a);
+    else hipLaunchKernelGGL((k_delta_grads<T, KT, false>), own, dim3(256), lds, st, a);
 }
 
 template <typename T>
