@@ -66,28 +66,77 @@ __device__ __forceinline__ int q8_code(float x, float scale) {
     return (int)fminf(fmaxf(c, -127.f), 127.f);
 }
 
-// Scales and codes of rows of values, a wave a row: once over the row for its
-// largest value, once more (from the caches) for its codes.
+// Sixteen values of a row from k on, zeros behind K.
 template <typename T>
-__global__ void __launch_bounds__(256) k_q8_quantize(const T *x, int64_t ld, int64_t rows, int K, int8_t *packed,
-                                                     float *scales) {
-    const int lane = threadIdx.x & 63;
-    const int64_t kp = q8_padded(K), padded = (rows + 15) / 16 * 16;
-    for (int64_t row = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6); row < padded; row += gridDim.x * (int64_t)4) {
-        const T *from = x + row * ld;
-        unsigned top = 0;
-        if (row < rows)
-            for (int k = lane; k < K; k += 64) top = max(top, magnitude(from[k]));
+__device__ __forceinline__ void values16(T (&v)[16], const T *row, int k, int K) {
+    if (k + 16 <= K) {
+        constexpr int CH = 16 / sizeof(T);
 #pragma unroll
-        for (int s = 32; s; s >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, s, 64));
-        const float scale = q8_scale(top);
-        if (lane == 0 && row < rows) scales[row] = scale;
-        for (int k = lane * 16; k < kp; k += 64 * 16) {
-            int c[16];
+        for (int i = 0; i < 16; i += CH) {
+            const Chunk<T, CH> c = *reinterpret_cast<const Chunk<T, CH> *>(row + k + i);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) c[i] = row < rows && k + i < K ? q8_code((float)from[k + i], scale) : 0;
-            put16(packed + q8_at(row, k, kp), c);
+            for (int j = 0; j < CH; ++j) v[i + j] = c[j];
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = k + i < K ? row[k + i] : (T)0.f;
+    }
+}
+
+// Scales and codes of rows of values: WAVES waves a row, a lane 16 neighbouring values
+// at a time; the first HELD of them stay in registers from the search for the largest
+// to the codes, what is behind is read again.
+template <typename T, int WAVES>
+__global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) k_q8_quantize(const T *x, int64_t ld, int64_t rows, int K,
+                                                                           int8_t *packed, float *scales) {
+    constexpr int HELD = sizeof(T) == 2 ? 4 : 2;
+    __shared__ unsigned tops[WAVES];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t kp = q8_padded(K), padded = (rows + 15) / 16 * 16;
+    const int64_t row = WAVES == 1 ? blockIdx.x * (int64_t)4 + wave : blockIdx.x;
+    if (row >= padded) return;
+    const int first = ((WAVES == 1 ? 0 : wave * 64) + lane) * 16;
+    constexpr int step = WAVES * 64 * 16;
+    const T *from = x + row * ld;
+    T held[HELD][16];
+    unsigned top = 0;
+    if (row < rows) {
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) values16(held[h], from, min(first + h * step, K), K);
+#pragma unroll
+        for (int h = 0; h < HELD; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = max(top, magnitude(held[h][i]));
+        for (int k = first + HELD * step; k < K; k += step) {
+            T v[16];
+            values16(v, from, k, K);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = max(top, magnitude(v[i]));
+        }
+    }
+#pragma unroll
+    for (int s = 32; s; s >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, s, 64));
+    if (WAVES > 1) {
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) top = max(top, tops[w]);
+    }
+    const float scale = q8_scale(top);
+    if (first == 0 && row < rows) scales[row] = scale;
+    const auto codes = [&](const T (&v)[16], int k) {
+        int c[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c[i] = row < rows ? q8_code((float)v[i], scale) : 0;
+        put16(packed + q8_at(row, k, kp), c);
+    };
+#pragma unroll
+    for (int h = 0; h < HELD; ++h)
+        if (first + h * step < kp) codes(held[h], first + h * step);
+    for (int k = first + HELD * step; k < kp; k += step) {
+        T v[16];
+        if (row < rows) values16(v, from, min(k, K), K);
+        codes(v, k);
     }
 }
 
@@ -99,7 +148,9 @@ struct Q8Args {
 };
 
 // Outputs [BM rows][BN columns] of a workgroup, WM x WN waves; a stage of 128 values
-// along k of both sides in LDS while the next is on its way.
+// along k of both sides in LDS while the next is on its way.  Workgroup i runs on XCD
+// i % 8: each XCD takes a run of tiles in groups of eight rows of tiles, so that what
+// its workgroups read at a time meets in its L2.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
     constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;      // pieces of a wave
@@ -108,8 +159,11 @@ __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
     extern __shared__ __align__(16) int8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int64_t tiles = (p.M + BM - 1) / BM;
-    const int64_t m0 = blockIdx.x % tiles * (BM / 16), n0 = blockIdx.x / tiles * (BN / 16);   // in pieces
+    const unsigned tm = (unsigned)((p.M + BM - 1) / BM), tn = (unsigned)((p.N + BN - 1) / BN);
+    const unsigned tile = blockIdx.x % 8 * ((tm * tn + 7) / 8) + blockIdx.x / 8;
+    if (tile >= tm * tn || blockIdx.x / 8 >= (tm * tn + 7) / 8) return;
+    const unsigned group = tile / (8 * tn), high = min(8u, tm - group * 8), at = tile - group * 8 * tn;
+    const int64_t m0 = (group * 8 + at % high) * (int64_t)(BM / 16), n0 = at / high * (int64_t)(BN / 16);   // in pieces
     const int64_t mp = (p.M + 15) / 16, np = (p.N + 15) / 16;
     const int steps = (int)(p.kp / 128);
 
@@ -137,6 +191,7 @@ __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     bring(0, 0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     for (int s = 0; s < steps; ++s) {
         if (s + 1 < steps) bring(s + 1, (s + 1) & 1);
@@ -156,6 +211,7 @@ __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
                 for (int j = 0; j < FN; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the next stage has arrived
         __syncthreads();
     }
     // lane l holds outputs n = 4 (l / 16) .. + 3 of row m = l % 16
@@ -211,9 +267,23 @@ void launch_product(const Q8Args &p, hipStream_t st) {
         hipLaunchKernelGGL((k_q8_few<T>), dim3((unsigned)((p.N + 15) / 16)), dim3(256), 0, st, p);
         return;
     }
-    constexpr int BM = 128, BN = 128;
-    hipLaunchKernelGGL((k_q8_product<T, BM, BN, 2, 2>), dim3((unsigned)(((p.N + BN - 1) / BN) * ((p.M + BM - 1) / BM))),
-                       dim3(256), 2 * (BM + BN) / 16 * 2 * kQ8Piece, st, p);
+    const auto tiles = [&](int64_t b) { return ((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
+    const auto run = [&](auto kernel, int64_t b, int waves) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((tiles(b) + 7) / 8 * 8)), dim3(waves * 64), 2 * (2 * b) / 16 * 2 * kQ8Piece, st, p);
+    };
+    if (tiles(256) >= 192) run(k_q8_product<T, 256, 256, 2, 4>, 256, 8);
+    else if (tiles(128) >= 192) run(k_q8_product<T, 128, 128, 2, 2>, 128, 4);
+    else run(k_q8_product<T, 64, 64, 2, 2>, 64, 4);
+}
+
+// Eight waves a row where there are few of them or they are long.
+template <typename T>
+void quantize(const T *x, int64_t ld, int64_t rows, int K, int8_t *codes, float *scales, hipStream_t st) {
+    const int64_t padded = (rows + 15) / 16 * 16;
+    if (rows < 2048 || K > 16384)
+        hipLaunchKernelGGL((k_q8_quantize<T, 8>), dim3((unsigned)padded), dim3(512), 0, st, x, ld, rows, K, codes, scales);
+    else
+        hipLaunchKernelGGL((k_q8_quantize<T, 1>), dim3((unsigned)(padded / 4)), dim3(256), 0, st, x, ld, rows, K, codes, scales);
 }
 
 const char *q8_check(int64_t rows, int K) {
@@ -266,19 +336,12 @@ fi_status fi_q8_quantize(int64_t rows, int K, int dtype, const void *x, int64_t 
     const int64_t ld = pitch_or(ld_x, K);
     const View out = {packed, 1, bytes, bytes}, in = {x, rows, K * es, ld * es};
     if (outputs_meet(&out, 1, &in, 1)) return op_fail(FI_EINVAL, call, "an output shares memory with another argument");
-    const unsigned groups = (unsigned)std::min<int64_t>((rows + 15) / 16 * 4, 1 << 16);
     int8_t *codes = (int8_t *)packed;
     float *scales = (float *)((char *)packed + up256((size_t)q8_code_bytes(rows, K)));
     const hipStream_t st = (hipStream_t)stream;
-    if (dtype == FI_F32)
-        hipLaunchKernelGGL((k_q8_quantize<float>), dim3(groups), dim3(256), 0, st, (const float *)x, ld, rows, K, codes,
-                           scales);
-    else if (dtype == FI_BF16)
-        hipLaunchKernelGGL((k_q8_quantize<bf16_t>), dim3(groups), dim3(256), 0, st, (const bf16_t *)x, ld, rows, K, codes,
-                           scales);
-    else
-        hipLaunchKernelGGL((k_q8_quantize<f16_t>), dim3(groups), dim3(256), 0, st, (const f16_t *)x, ld, rows, K, codes,
-                           scales);
+    if (dtype == FI_F32) quantize((const float *)x, ld, rows, K, codes, scales, st);
+    else if (dtype == FI_BF16) quantize((const bf16_t *)x, ld, rows, K, codes, scales, st);
+    else quantize((const f16_t *)x, ld, rows, K, codes, scales, st);
     return op_launched(call);
 }
 
