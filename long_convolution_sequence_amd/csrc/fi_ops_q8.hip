@@ -214,22 +214,46 @@ __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the next stage has arrived
         __syncthreads();
     }
-    // lane l holds outputs n = 4 (l / 16) .. + 3 of row m = l % 16
+    // Lane l holds outputs n = 4 (l / 16) .. + 3 of row m = l % 16: 16 rows at a time go
+    // through a wave's own part of LDS, so that their stores are whole lines.
     T *y = static_cast<T *>(p.y);
+    constexpr int W = FN * 16, PITCH = W + 16 / sizeof(T), CH = 16 / sizeof(T), LANES = W / CH;
+    static_assert(WM * WN * 16 * PITCH * sizeof(T) <= 2 * PIECES * kQ8Piece, "the waves' parts fit");
+    T *const mine = reinterpret_cast<T *>(lds) + wave * 16 * PITCH;
+    const int64_t nw = (n0 + wn * FN) * 16;
+    const bool whole = nw + W <= p.N;
+    float sw[FN][4], bias[FN][4];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t n = min(nw + j * 16 + (lane >> 4) * 4 + r, p.N - 1);
+            sw[j][r] = p.sw[n];
+            bias[j][r] = p.bias ? p.bias[n] : 0.f;
+        }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int64_t m = (m0 + wm * FM + i) * 16 + (lane & 15);
-        if (m >= p.M) continue;
-        const float sa = p.sa[m];
+        const int64_t mw = (m0 + wm * FM + i) * 16;
+        const float sa = p.sa[min(mw + (lane & 15), p.M - 1)];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int64_t n = (n0 + wn * FN + j) * 16 + (lane >> 4) * 4;
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (n + r < p.N)
-                    y[m * p.ldy + n + r] =
-                        (T)fmaf((float)acc[i][j][r] * sa, p.sw[n + r], p.bias ? p.bias[n + r] : 0.f);
+                mine[(lane & 15) * PITCH + j * 16 + (lane >> 4) * 4 + r] =
+                    (T)fmaf((float)acc[i][j][r] * sa, sw[j][r], bias[j][r]);
+        __builtin_amdgcn_wave_barrier();
+        for (int u = lane; u < 16 * LANES; u += 64) {
+            const int64_t m = mw + u / LANES, n = nw + u % LANES * CH;
+            if (m >= p.M) continue;
+            const Chunk<T, CH> v = *reinterpret_cast<const Chunk<T, CH> *>(mine + u / LANES * PITCH + u % LANES * CH);
+            if (whole)
+                *reinterpret_cast<Chunk<T, CH> *>(y + m * p.ldy + n) = v;
+            else
+#pragma unroll
+                for (int e = 0; e < CH; ++e)
+                    if (n + e < p.N) y[m * p.ldy + n + e] = v[e];
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
