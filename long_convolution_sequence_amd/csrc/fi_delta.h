@@ -443,7 +443,7 @@ constexpr int image_bytes() {          // of a chunk: M in three terms and P
 // registers, the rows of A read from LDS for all lanes of a block at once; the block
 // below them is -N22 (A21 N11).
 template <typename T, int KT, bool BACK, bool VEC>
-__global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
+__global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_prep(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, MT = C / 32, CS = C / 16, KS = KT * 2, LD = C + 4;
     constexpr int PT = BACK ? 3 : DeltaType<T>::out, MB = tri_pieces<C>() * kPiece;
     __shared__ __align__(16) float m[C * LD];
@@ -504,47 +504,66 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) ks_[mt][ks] = operand(rawk[mt][ks], mt, ks, ssk[mt]);
     }
-    f32x16 kk[MT][MT], qk[MT][MT];
+    // A in rows (its upper half: zeros)
+    {
+        f32x16 kk[MT][MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j <= i; ++j) kk[i][j] = zeros16();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j <= i; ++j) multiply<2>(kk[i][j], ks_[i][ks], ks_[j][ks]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const float a = both_halves(ssk[mt]);
+            if (half == 0) fk[mt * 32 + col] = p.unit ? 1.f / sqrtf(a + kDeltaUnit) : 1.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = i * 32 + acc_row(r), c = j * 32 + col;
+                    m[row * LD + c] = j <= i && row > c ? exp2f((float)(sum[row] - sum[c])) * fk[c] * fk[row] * fb[BACK ? row : c] *
+                                                              kk[i][j <= i ? j : 0][r]
+                                                        : 0.f;
+                }
+    }
+    // P in its registers
+    f32x16 qk[MT][MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j <= i; ++j) kk[i][j] = qk[i][j] = zeros16();
+        for (int j = 0; j <= i; ++j) qk[i][j] = zeros16();
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int ks = 0; ks < KS; ++ks) {
             const Frag<N> fq_ = operand(rawq[i][ks], i, ks, ssq[i]);
 #pragma unroll
-            for (int j = 0; j <= i; ++j) {
-                multiply<2>(kk[i][j], ks_[i][ks], ks_[j][ks]);
-                multiply<2>(qk[i][j], fq_, ks_[j][ks]);
-            }
+            for (int j = 0; j <= i; ++j) multiply<2>(qk[i][j], fq_, ks_[j][ks]);
         }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const float a = both_halves(ssk[mt]), c = both_halves(ssq[mt]);
-        if (half == 0) {
-            fk[mt * 32 + col] = p.unit ? 1.f / sqrtf(a + kDeltaUnit) : 1.f;
-            fq[mt * 32 + col] = p.unit ? 1.f / sqrtf(c + kDeltaUnit) : 1.f;
-        }
+        const float c = both_halves(ssq[mt]);
+        if (half == 0) fq[mt * 32 + col] = p.unit ? 1.f / sqrtf(c + kDeltaUnit) : 1.f;
     }
     __syncthreads();
-
-    // A in rows (its upper half: zeros), P in its registers
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
+        for (int j = 0; j <= i; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int row = i * 32 + acc_row(r), c = j * 32 + col;
-                float a = 0.f, e = 0.f;
-                if (j <= i) {
-                    e = row >= c ? exp2f((float)(sum[row] - sum[c])) * fk[c] : 0.f;
-                    a = row > c ? e * fk[row] * fb[BACK ? row : c] * kk[i][j <= i ? j : 0][r] : 0.f;
-                    qk[i][j <= i ? j : 0][r] *= e * p.scale * fq[row] * (BACK ? 1.f : fb[c]);
-                }
-                m[row * LD + c] = a;
+                const float e = row >= c ? exp2f((float)(sum[row] - sum[c])) * fk[c] : 0.f;
+                qk[i][j][r] *= e * p.scale * fq[row] * (BACK ? 1.f : fb[c]);
             }
     __syncthreads();
     float x[32];
@@ -561,7 +580,7 @@ __global__ void __launch_bounds__(64) k_delta_prep(DeltaArgs p) {
             if (j + 3 < i) s3 = fmaf(-a.w, x[j + 3], s3);
         }
         x[i] = (s0 + s1) + (s2 + s3);
-        if (i % 4 == 3) asm volatile("" ::: "memory");   // not all rows' loads at once: they would spill
+        if (i % 2) __builtin_amdgcn_sched_barrier(0);    // not all rows' loads at once: they would spill
     }
     __syncthreads();
     if (MT == 2 || half == 0) {

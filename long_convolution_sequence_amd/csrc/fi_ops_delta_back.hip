@@ -157,22 +157,32 @@ __global__ void __launch_bounds__(512, 4) k_delta_back_chain(DeltaArgs p) {
         store_state(p.dstate + bh * size, D, p.dk, p.dv, column);
 }
 
-// Sum over the 32 lanes of a half, in every lane of it.
+// Sum over the 32 lanes of a half, in its last lane: shifts within rows of 16 lanes,
+// then the lower row's last lane into the upper row.
 __device__ __forceinline__ float half_sum(float v) {
-#pragma unroll
-    for (int s = 1; s < 32; s *= 2) v += __shfl_xor(v, s, 64);
+#define FI_LANE_ADD(ctrl, rows) \
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false))
+    FI_LANE_ADD(0x111, 0xf);
+    FI_LANE_ADD(0x112, 0xf);
+    FI_LANE_ADD(0x114, 0xf);
+    FI_LANE_ADD(0x118, 0xf);
+    FI_LANE_ADD(0x142, 0xa);
+#undef FI_LANE_ADD
     return v;
 }
 
 // What is a chunk's own, for a key head and the heads that share it: a workgroup a
-// chunk, a wave 32 channels of the keys.
-template <typename T, int KT, bool VEC>
-__global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
+// chunk, a wave 32 channels of the keys.  The values' channels pass in slabs of 32,
+// the next one's rows on their way; H and J then take the slabs' place in LDS, so that
+// two workgroups share a CU (one where heads share a key head: SHARED, their sums take
+// 64 registers more).
+template <typename T, int KT, bool VEC, bool SHARED>
+__global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
     constexpr int MT = C / 32, CS = C / 16, DK = KT * 32, KB = C * DK * 2, LD = C + 4, SB = MT * 2 * kPiece;
     extern __shared__ __align__(16) char lds[];
-    char *const ix = lds, *const iw = ix + 3 * SB, *const iy = iw + 3 * SB, *const ikt = iy + N * SB, *const iqt = ikt + N * KB;
-    float *const Hm = reinterpret_cast<float *>(iqt + N * KB), *const Jm = Hm + C * LD;
+    char *const ikt = lds, *const iqt = ikt + N * KB, *const ix = iqt + N * KB, *const iw = ix + 3 * SB, *const iy = iw + 3 * SB;
+    float *const Hm = reinterpret_cast<float *>(ix), *const Jm = Hm + C * LD;
     __shared__ double G[C];
     __shared__ float beta[C], rk[C], rq[C], dotb[C], dotv[C], dotq[4][C], dotk[4][C], total[2][4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5, col = lane & 31;
@@ -212,9 +222,10 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
         }
     };
     const int d = wave * 32 + col;                       // this lane's channel
-    f32x16 allq[MT], allk[MT];
+    f32x16 ys[MT], xs[MT], sums[2][SHARED ? MT : 1];
+    f32x16 *const allq = SHARED ? sums[0] : ys, *const allk = SHARED ? sums[1] : xs;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) allq[i] = allk[i] = zeros16();
+    for (int i = 0; i < (SHARED ? MT : 1); ++i) sums[0][i] = sums[1][i] = zeros16();
     float sumq = 0.f;                                    // q . dq of row `lane`, over the heads
 
     for (int s = 0; s < share; ++s) {
@@ -230,29 +241,44 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
         const float *const S = p.states + at * p.dk * p.dv, *const D = p.ends + at * p.dk * p.dv;
         const T *const v = static_cast<const T *>(p.v) + row0 * p.ldv + (int64_t)h * p.dv;
         const T *const dy = static_cast<const T *>(p.dy) + row0 * p.lddy + (int64_t)h * p.dv;
-        f32x16 ys[MT], xs[MT], wd[MT], xw = zeros16(), yw = zeros16();
+        f32x16 wd[MT], xw = zeros16(), yw = zeros16();
 #pragma unroll
         for (int i = 0; i < MT; ++i) ys[i] = xs[i] = wd[i] = zeros16();
         float db[MT], dw[MT], inner = 0.f;
 #pragma unroll
         for (int i = 0; i < MT; ++i) db[i] = dw[i] = 0.f;
+        Chunk<float, 4> na[MT], nu[MT];
+        Chunk<T, 4> nz[MT], ny[MT];
+        const auto ahead = [&](int c0) {
+#pragma unroll
+            for (int e = 0; e < MT; ++e) {
+                const int cc = c0 + tid % 8 * 4;
+                const int64_t i = min(e * 32 + tid / 8, live - 1);
+                na[e] = raw4<VEC>(x + i * p.dv, cc, p.dv);
+                nu[e] = raw4<VEC>(w + i * p.dv, cc, p.dv);
+                nz[e] = raw4<VEC>(v + i * p.B * p.ldv, cc, p.dv);
+                ny[e] = raw4<VEC>(dy + i * p.B * p.lddy, cc, p.dv);
+            }
+        };
+        ahead(0);
         for (int c0 = 0; c0 < p.dv; c0 += 32) {
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < MT; ++e) {
                 const int i = e * 32 + tid / 8, cc = c0 + tid % 8 * 4, to = image_at(i, tid % 8 * 4, 2);
-                float a[4], u[4], z[4], y[4];
-                const int64_t ii = min(i, live - 1);
-                load4<VEC>(a, x + ii * p.dv, cc, p.dv, i < live);
-                load4<VEC>(u, w + ii * p.dv, cc, p.dv, i < live);
-                load4<VEC>(z, v + ii * p.B * p.ldv, cc, p.dv, i < live);
-                load4<VEC>(y, dy + ii * p.B * p.lddy, cc, p.dv, i < live);
+                float a[4], u[4], y[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) db[e] = fmaf(a[j], u[j], db[e]), dw[e] = fmaf(a[j], z[j], dw[e]);
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = i < live && cc + j < p.dv;
+                    a[j] = in ? na[e][j] : 0.f, u[j] = in ? nu[e][j] : 0.f, y[j] = in ? (float)ny[e][j] : 0.f;
+                    db[e] = fmaf(a[j], u[j], db[e]);
+                    dw[e] = fmaf(a[j], in ? (float)nz[e][j] : 0.f, dw[e]);
+                }
                 put_terms<3>(ix, to, SB, a);
                 put_terms<3>(iw, to, SB, u);
                 put_terms<N>(iy, to, SB, y);
             }
+            if (c0 + 32 < p.dv) ahead(c0 + 32);
             __syncthreads();
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
@@ -290,23 +316,38 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
             for (int o = 1; o < 8; o *= 2) db[e] += __shfl_xor(db[e], o, 64), dw[e] += __shfl_xor(dw[e], o, 64);
             if (tid % 8 == 0) dotb[e * 32 + tid / 8] = db[e], dotv[e * 32 + tid / 8] = dw[e];
         }
+        __syncthreads();                                 // the slabs have been read
         if (wave < MT * MT) {
             const int j = wave % MT * 32 + col;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int i = wave / MT * 32 + acc_row(r);
-                float e = 0.f;
-                if (i >= j) e = exp2f((float)(G[i] - G[j])) * beta[j];
+                const float e = i >= j ? exp2f((float)(G[i] - G[j])) * beta[j] : 0.f;
                 Hm[i * LD + j] = i > j ? -beta[i] * e * xw[r] : 0.f;
                 Jm[i * LD + j] = p.scale * e * yw[r];
             }
         }
-        __syncthreads();
+        // the states' shares, with their rows' factors, where the pairs' are added
         float part = 0.f;
         if (wave < KT) {
-            f32x16 gq[MT], gk[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) gq[i] = gk[i] = zeros16();
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    float kv[4];
+                    four(ikt, i * 32 + acc_row(r4 * 4), kv);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
+                        const float rise = exp2f((float)G[row]), fall = exp2f((float)(G[C - 1] - G[row])) * beta[row];
+                        part = fmaf(rk[row] * fall * kv[j], wd[i][r], part);
+                        ys[i][r] *= p.scale * rise;
+                        xs[i][r] = fmaf(fall, wd[i][r], -rise * beta[row] * xs[i][r]);
+                    }
+                }
+        }
+        __syncthreads();
+        if (wave < KT) {
 #pragma unroll
             for (int cs = 0; cs < CS; ++cs) {
                 const Frag<N> fk = piece<N>(ikt, wave * CS + cs, KB), fq = piece<N>(iqt, wave * CS + cs, KB);
@@ -320,28 +361,24 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
                         e[j] = Jm[t * LD + r] * rq[t];
                         u[j] = (r > t ? Hm[r * LD + t] : Hm[t * LD + r]) * rk[t];
                     }
-                    multiply<2>(gq[i], split<3>(a), fk);
-                    multiply<2>(gk[i], split<3>(e), fq);
-                    multiply<2>(gk[i], split<3>(u), fk);
+                    multiply<2>(ys[i], split<3>(a), fk);
+                    multiply<2>(xs[i], split<3>(e), fq);
+                    multiply<2>(xs[i], split<3>(u), fk);
+                    in_order();
                 }
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4) {
-                    float qv[4], kv[4];
+                    float qv[4];
                     four(iqt, i * 32 + acc_row(r4 * 4), qv);
-                    four(ikt, i * 32 + acc_row(r4 * 4), kv);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
-                        const float rise = exp2f((float)G[row]), fall = exp2f((float)(G[C - 1] - G[row])) * beta[row];
-                        const float g = fmaf(p.scale * rise, ys[i][r], gq[i][r]);
-                        part = fmaf(rk[row] * fall * kv[j], wd[i][r], part);
-                        allq[i][r] += g;
-                        allk[i][r] += fmaf(fall, wd[i][r], fmaf(-rise * beta[row], xs[i][r], gk[i][r]));
-                        const float dot = half_sum(rq[row] * qv[j] * g);
-                        if (col == 0) dotq[wave][row] = dot;
+                        if (SHARED) allq[i][r] += ys[i][r], allk[i][r] += xs[i][r];
+                        const float dot = half_sum(rq[row] * qv[j] * ys[i][r]);
+                        if (col == 31) dotq[wave][row] = dot;
                     }
                 }
         }
@@ -386,7 +423,7 @@ __global__ void __launch_bounds__(256) k_delta_grads(DeltaArgs p) {
                     for (int j = 0; j < 4; ++j) {
                         const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
                         const float dot = half_sum(rk[row] * kv[j] * allk[i][r]);
-                        if (col == 0) dotk[wave][row] = dot;
+                        if (col == 31) dotk[wave][row] = dot;
                     }
                 }
         __syncthreads();
@@ -435,9 +472,10 @@ void backward(const DeltaArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((k_delta_back_chain<T, KT, true>), dim3((unsigned)(a.segments * heads), g.groups), dim3(g.threads), chain, st,
                        a);
     const dim3 own((unsigned)(a.chunks * a.B * a.HK));
-    const int lds = (6 + N) * C / 32 * 2 * kPiece + 2 * N * KB + 2 * C * (C + 4) * 4;
-    if (a.dv % 4 == 0) hipLaunchKernelGGL((k_delta_grads<T, KT, true>), own, dim3(256), lds, st, a);
-    else hipLaunchKernelGGL((k_delta_grads<T, KT, false>), own, dim3(256), lds, st, a);
+    const int lds = std::max((6 + N) * C / 32 * 2 * kPiece, 2 * C * (C + 4) * 4) + 2 * N * KB;
+    if (a.dv % 4) hipLaunchKernelGGL((k_delta_grads<T, KT, false, true>), own, dim3(256), lds, st, a);
+    else if (a.H > a.HK) hipLaunchKernelGGL((k_delta_grads<T, KT, true, true>), own, dim3(256), lds, st, a);
+    else hipLaunchKernelGGL((k_delta_grads<T, KT, true, false>), own, dim3(256), lds, st, a);
 }
 
 template <typename T>
