@@ -544,13 +544,13 @@ typedef struct fi_delta_desc {
     int dtype;             /* of q, k, v, y and their gradients */
     int unit;              /* 0 or 1 */
     float scale;
-    int64_t ld_q, ld_k, ld_v, ld_decay, ld_beta, ld_y;   /* row pitches, elements; 0 = a row's own length */
+    int64_t ld_q, ld_k, ld_v, ld_decay, ld_beta, ld_y;   /* row pitches, elements; 0 = a row's own length; B rows at most 2^24 */
     int64_t ld_dy, ld_dq, ld_dk, ld_dv, ld_ddecay, ld_dbeta;
     int reserved[4];       /* must be zero */
 } fi_delta_desc;
 
 /* Bytes of what the forward pass keeps for the backward pass (`saved`), and of the
- * workspace of either pass; 0 for a bad descriptor.  A forward call of up to 8
+ * workspace of either pass; 0 for a bad descriptor.  A forward call of up to 14
  * positions that saves nothing uses no workspace (it may be NULL). */
 size_t fi_delta_saved_bytes(const fi_delta_desc *desc);
 size_t fi_delta_workspace_bytes(const fi_delta_desc *desc, int backward);

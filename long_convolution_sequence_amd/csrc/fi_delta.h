@@ -4,16 +4,18 @@
 // E_ij = e^(G_i - G_j) and S the state before the chunk,
 //   (I + A) w = v - e^G K S,  A_ij = E_ij (k_i . k_j) b_j (i > j),
 //   y = scale (e^G Q S + (E o Q K^T)(b w)),  S' = e^(G_C) S + sum_j e^(G_C - G_j) k_j (b_j w_j)^T.
-// Only S passes from chunk to chunk, and its columns do not meet: a wave runs 32
-// columns of a head along the sequence, with S in the accumulators of the matrix
-// instruction v_mfma_f32_32x32x16_bf16.
+// Only S passes from chunk to chunk, and its columns do not meet: a wave runs 16 columns
+// of a head along the sequence, with S in the accumulators of the matrix instruction
+// v_mfma_f32_16x16x32_bf16 (the chains); what is a chunk's own runs for all chunks at
+// once on v_mfma_f32_32x32x16_bf16.
 //
-// Operands.  The instruction's left operand is kept in LDS or memory as an image: a
-// piece of 32 rows x 16 values of the summed index is 1 KB, lane l's 16 bytes are the
-// values 8 (j / 4) + 4 (l / 32) + j % 4, j < 8, of row l % 32.  In that order of the
-// summed index an accumulator (lane l: rows 8 (r / 4) + 4 (l / 32) + r % 4 of column
-// l % 32) is a right operand as it stands, registers 8 s .. 8 s + 7 its step s: what
-// one product gives goes into the next without leaving the lane.
+// Operands.  An operand is kept in LDS or memory as an image of pieces of 1 KB, lane l's
+// 16 bytes what the instruction takes of it.  Of 32 rows x 16 values of the summed index
+// they are the values 8 (j / 4) + 4 (l / 32) + j % 4, j < 8, of row l % 32.  In that order
+// of the summed index an accumulator (lane l: rows 8 (r / 4) + 4 (l / 32) + r % 4 of column
+// l % 32) is an operand as it stands, registers 8 s .. 8 s + 7 its step s: what one product
+// gives goes into the next without leaving the lane.  The chains' pieces (tile_at) do the
+// same for 16 rows x 32 values.
 //
 // Values in 32 bits are multiplied as terms of bf16 (x = t0 + t1 + t2, each the
 // rounding of what is left, exact to 2^-24): of two factors the products of terms i
@@ -441,7 +443,8 @@ constexpr int image_bytes() {          // of a chunk: M in three terms and P
 // inputs themselves.
 // The inverse: a lane solves for a column of a diagonal block of 32, row by row from
 // registers, the rows of A read from LDS for all lanes of a block at once; the block
-// below them is -N22 (A21 N11).
+// below them is -N22 (A21 N11).  131072 positions of 9 heads of 96 bf16 270 us (1.2 GB
+// moved, 250 at a copy's rate).
 template <typename T, int KT, bool BACK, bool VEC>
 __global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_prep(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, MT = C / 32, CS = C / 16, KS = KT * 2, LD = C + 4;
@@ -677,11 +680,15 @@ struct DeltaPlan {
     size_t images, factors, states, ends, rows, local, maps;   // bytes, each a multiple of 256
 };
 
-// Segments: a wave runs 32 columns of a head along the sequence; where that leaves
-// most of the card idle, the sequence is cut into as many segments as fill it, each
-// run once from nothing (with the columns of the state's own map, dk of them, beside
-// it), joined, and run again from what is before it.  That is 2.4 times the work, so
-// it takes eight segments at least to be worth it, and eight chunks a segment.
+// Segments: a workgroup runs up to 128 columns of a head along the sequence; where that
+// leaves most of the card idle, the sequence is cut into as many segments as fill it,
+// each run once from nothing (with the columns of the state's own map, dk of them, beside
+// it), joined, and run again from what is before it.  That is 2.5 times the work: with
+// four segments a call over 2048 x 4 x 24 heads of 128 takes 388 us against 431 in one
+// piece, over 4096 x 8 x 12 heads 702 against 892, but with two 2048 x 8 x 24 heads 615
+// against 539.  At least eight chunks a segment; more segments than fill the card twice
+// cost more to join (2.7 us each) than they bring (131072 x 9 heads of 96: 1024 sets of
+// columns 1.52 ms, 1536 1.43, 2048 1.50, without a chunk's own matrices).
 inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
     DeltaPlan d = {};
     d.C = delta_chunk(q->dtype);

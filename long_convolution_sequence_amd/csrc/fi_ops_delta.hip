@@ -14,6 +14,12 @@ enum { CHAIN_LOCAL, CHAIN_FULL };
 // columns behind the state's are those of the map (v = 0, from a unit column).
 // What a chunk needs is on its way while the one before it runs: k and q in registers,
 // M, P and the factors past them into LDS as soon as nobody reads the last ones.
+// 131072 positions of 9 heads of 96 bf16: FULL 550 us (55 segments of 37 chunks, two
+// workgroups a CU, 15 us a chunk), LOCAL 760.  Of a chunk's 36000 cycles a wave issues
+// 150 products (2400) and 790 others (3200); the loads account for 100 us of the 550,
+// bringing k and q into LDS for 80; the rest waits in the phases' chain of products,
+// terms and four barriers.  Wider waves (32 columns) ran no faster, nor did all of a
+// step's operands read ahead of it (653) or v and y by whole vectors (585).
 template <typename T, int KT, int MODE>
 __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
@@ -246,7 +252,9 @@ __global__ void __launch_bounds__(KT * 64) k_delta_join(DeltaArgs p, const float
 }
 
 // Position by position, for a few of them: a workgroup 32 columns of a head, a thread
-// four columns of every 32nd row, held in registers.  Both sums over the rows, k . S
+// four columns of every 32nd row, held in registers (one position of 8 x 9 heads of 96
+// 7.1 us, of which the state's 5.3 MB are one: two loads that wait for each other, two
+// sums over the workgroup and the launch).  Both sums over the rows, k . S
 // and q . S, are taken of the state before the position:
 // y = scale (a q.S + (k.q) u), u = b (v - a k.S).
 template <typename T>
@@ -335,8 +343,9 @@ __global__ void __launch_bounds__(256) k_delta_steps(DeltaArgs p) {
     }
 }
 
-// Positions that run one by one: below, the chunk's launches cost more.
-constexpr int64_t kDeltaSteps = 8;
+// Up to as many positions run one by one (9 heads of 96, 1.8 us each: 8 of them 19 us,
+// 16 34); the chunk's two launches take 32 us at any number up to 64.
+constexpr int64_t kDeltaSteps = 14;
 
 template <typename T, int KT>
 void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {

@@ -50,7 +50,8 @@ __device__ __forceinline__ void load_columns(float (&v)[NC * CH], const float *p
 // Forward: a row in registers, every tensor once.  The mean m0 of the fp32 sum is
 // off by its rounding; the mean d of what is left, found along with the squares,
 // takes that away (variance mean c^2 - d^2 of c = r - m0), so rows far from zero
-// keep their digits.
+// keep their digits.  HBM-bound: 131072 x 864 bf16 with fp32 rows 247 us (5.5 TB/s);
+// 1999 x 5001 fp16 without a residual 15 us: few rows, two barriers in each.
 template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, bool STREAM, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_layer(LayerArgs p) {
     constexpr int N = CH * NC;
@@ -120,7 +121,8 @@ __global__ void __launch_bounds__(THREADS) k_layer(LayerArgs p) {
 // Backward: every tensor of the row once, both row means in one step; the column
 // sums of a team's rows in registers, its workgroup's joined in LDS (team after
 // team, so the order is fixed) and written once.  Elements that a lane does not
-// own have weights of zero, so both means pass them by.
+// own have weights of zero, so both means pass them by.  131072 x 768 bf16 with fp32
+// rows 309 us (5.9 TB/s); 1999 x 5001 fp16 21 us and 6 for the column sums.
 template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, bool STREAM, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) k_layer_back(LayerArgs p) {
     constexpr int N = CH * NC;
@@ -229,7 +231,8 @@ const char *layer_check(const fi_layer_desc *q) {
 
 // Workgroups: as many as are resident together, so that a team runs through its
 // rows without a second round of workgroups, and the backward pass has few column
-// sums; the rows are spread evenly.
+// sums; the rows are spread evenly.  The counts are those of the block's norms, whose
+// rows lie in registers alike.
 unsigned layer_groups(const fi_layer_desc *q, bool backward) {
     const int D = q->channels, waves = team_waves(D), ch = value_bytes(q->res_dtype) == 2 ? 8 : 4;
     const int group = waves > 1 ? waves : 4;

@@ -1,5 +1,6 @@
 """Binding of the operators of a recurrent block in ``include/fi.h``: the gated
-linear recurrence, the norms fused with gate and residual, 4-bit products.
+linear recurrence and the gated delta rule, the norms fused with gate and
+residual and the layer norm, 4-bit and 8-bit products.
 
 For a caller that runs its own block between the mixers (``fi.Context`` with
 ``MAP_EXTERNAL``) or trains one.  As in ``fi``: argument marshalling only, no
@@ -12,8 +13,9 @@ tensors that require gradients warns, unless it saves what the backward call
 takes or stands under ``torch.no_grad()``.
 
 Tensors need contiguous rows at one pitch (a column slice of a wider tensor
-is fine); states, weights and ``lengths`` are densely packed.  Sequences are
-``[T][B][D]`` as in ``fi.Context.prefill``.
+is fine; a row of heads is all of them); states, weights and ``lengths`` are
+densely packed.  Sequences are ``[T][B][D]`` as in ``fi.Context.prefill``, with
+heads ``[T][B][heads][d]``.
 """
 from __future__ import annotations
 
@@ -284,7 +286,7 @@ def _delta_sizes(*head):
     return lib.fi_delta_workspace_bytes(d, 0), lib.fi_delta_workspace_bytes(d, 1), lib.fi_delta_saved_bytes(d)
 
 
-_DELTA_STEPS = 8           # positions up to which a forward call that saves nothing takes no workspace
+_DELTA_STEPS = 14          # positions up to which a forward call that saves nothing takes no workspace
 
 
 def _heads(t, shape, dtype, device, name):
@@ -759,8 +761,8 @@ class Q8Weight(Q8Rows):
 
 def q8_product(w, x, bias=None, *, dtype=None, y=None):
     """y [rows][N] = x [rows][K] times a Q8Weight, plus bias [N] fp32 (fi_q8_product).  x is a tensor,
-    which is brought to 8 bits with a scale a row first, or Q8Rows (one quantization for several weights;
-    then dtype says y's type, else it is x's).  Autograd does not see it."""
+    which is brought to 8 bits with a scale a row first, or Q8Rows (one quantization for several weights).
+    dtype: of y; None for x's, with Q8Rows bfloat16.  Autograd does not see it."""
     if not isinstance(w, Q8Rows):
         _bad(f"w: expected a Q8Weight, got {type(w).__name__}")
     if isinstance(x, Q8Rows):

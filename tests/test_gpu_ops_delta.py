@@ -95,7 +95,7 @@ def test_sequences_in_segments(T, lengths, dtype):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_positions_one_by_one_as_a_sequence(dtype):
-    """Steps in place, a sequence of 8 and one in chunks agree within their bounds; an empty slot keeps its state."""
+    """Steps in place, a short sequence and one in chunks agree within their bounds; an empty slot keeps its state."""
     say(f"case delta steps {dtype}")
     v = _inputs(40, 3, 1, 2, 48, 36, dtype, True)
     c = _cuda(v)

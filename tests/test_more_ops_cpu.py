@@ -122,7 +122,7 @@ def test_layer_arguments_are_checked(lib):
     (dict(scale=float("nan")), "scale"), (dict(batch=1 << 19), "2^20"), (dict(T=1 << 23, batch=64), "too large"),
     (dict(ld_q=31), "pitch"), (dict(ld_k=-1), "pitch"), (dict(ld_v=95), "pitch"), (dict(ld_decay=3), "pitch"),
     (dict(ld_beta=1), "pitch"), (dict(ld_y=95), "pitch"), (dict(ld_dy=1), "pitch"), (dict(ld_dq=1), "pitch"), (dict(ld_dk=1), "pitch"),
-    (dict(ld_dv=1), "pitch"), (dict(ld_ddecay=1), "pitch"), (dict(ld_dbeta=3), "pitch")])
+    (dict(ld_v=(1 << 23) + 1), "2^24"), (dict(ld_dq=1 << 40), "2^24"), (dict(dv=1024, heads=16384), "2^24"), (dict(ld_dv=1), "pitch"), (dict(ld_ddecay=1), "pitch"), (dict(ld_dbeta=3), "pitch")])
 def test_delta_descriptors_are_checked(lib, kw, why):
     q = _delta(**kw)
     assert lib.fi_delta_saved_bytes(ctypes.byref(q)) == 0
@@ -156,11 +156,11 @@ def test_delta_arguments_are_checked(lib):
 
 
 def test_few_positions_need_no_workspace(lib):
-    """Up to 8 positions that save nothing: the call gets as far as the next check."""
-    for T, why in ((8, "aligned"), (9, "required")):
+    """Up to 14 positions that save nothing: the call gets as far as the next check."""
+    for T, why in ((14, "aligned"), (15, "required")):
         _delta_refused(lib, _delta(T=T), why, backward=False, workspace=None, saved=None, final=P + 1)
-    assert ops._DELTA_STEPS == 8
-    _delta_refused(lib, _delta(T=8), "required", backward=False, workspace=None)
+    assert ops._DELTA_STEPS == 14
+    _delta_refused(lib, _delta(T=14), "required", backward=False, workspace=None)
 
 
 def test_q8_arguments_are_checked(lib):
