@@ -314,11 +314,12 @@ void launch_product(const Q8Args &p, hipStream_t st) {
 }
 
 // Eight waves a row where one a row would leave the card idle: rows of 4096, 256 of them
-// 6.7 us with eight and 6.8 with one, 1024 of them 13.3 and 7.6.
+// 6.7 us with eight and 6.8 with one, 1024 of them 13.3 and 7.6; 333 rows of 4999 8.9
+// and 10.8.
 template <typename T>
 void quantize(const T *x, int64_t ld, int64_t rows, int K, int8_t *codes, float *scales, hipStream_t st) {
     const int64_t padded = (rows + 15) / 16 * 16;
-    if (rows * 16 < K)
+    if (rows * 12 < K)
         hipLaunchKernelGGL((k_q8_quantize<T, 8>), dim3((unsigned)padded), dim3(512), 0, st, x, ld, rows, K, codes, scales);
     else
         hipLaunchKernelGGL((k_q8_quantize<T, 1>), dim3((unsigned)(padded / 4)), dim3(256), 0, st, x, ld, rows, K, codes, scales);
