@@ -172,12 +172,13 @@ __device__ __forceinline__ float half_sum(float v) {
 }
 
 // What is a chunk's own, for a key head and the heads that share it: a workgroup a
-// chunk, a wave 32 channels of the keys.  The values' channels pass in slabs of 32,
-// the next one's rows on their way; H and J then take the slabs' place in LDS, so that
-// two workgroups share a CU (one where heads share a key head: SHARED, their sums take
-// 64 registers more).  8192 x 4 x 6 heads of 128 bf16 531 us (0.55 GB: 110 at a copy's
-// rate): 123 registers spill, a slab's two barriers and its loads of the states; with
-// one workgroup a CU 933.
+// chunk, a wave 32 channels of the keys.  The values' channels pass in slabs of 32; H
+// and J then take the slabs' place in LDS, so that two workgroups share a CU and one
+// computes while the other waits for its slab (one workgroup where heads share a key
+// head: SHARED, their sums take 64 registers more).  8192 x 4 x 6 heads of 128 bf16
+// 476 us (0.55 GB: 110 at a copy's rate): 90 registers spill, a slab's two barriers and
+// its loads of the states; with the next slab's rows ahead 123 spill and it is 527, with
+// those and one workgroup a CU 565.
 template <typename T, int KT, bool VEC, bool SHARED>
 __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
         for (int i = 0; i < MT; ++i) db[i] = dw[i] = 0.f;
         Chunk<float, 4> na[MT], nu[MT];
         Chunk<T, 4> nz[MT], ny[MT];
-        const auto ahead = [&](int c0) {
+        const auto load = [&](int c0) {
 #pragma unroll
             for (int e = 0; e < MT; ++e) {
                 const int cc = c0 + tid % 8 * 4;
@@ -262,8 +263,8 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
                 ny[e] = raw4<VEC>(dy + i * p.B * p.lddy, cc, p.dv);
             }
         };
-        ahead(0);
         for (int c0 = 0; c0 < p.dv; c0 += 32) {
+            load(c0);
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < MT; ++e) {
@@ -280,7 +281,6 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
                 put_terms<3>(iw, to, SB, u);
                 put_terms<N>(iy, to, SB, y);
             }
-            if (c0 + 32 < p.dv) ahead(c0 + 32);
             __syncthreads();
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
