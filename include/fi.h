@@ -560,12 +560,12 @@ size_t fi_delta_workspace_bytes(const fi_delta_desc *desc, int backward);
  * lengths as in fi_scan_forward.  y [T][B][H][dv] (0 past a row's length) and,
  * where not NULL, final [B][H][dk][dv] fp32 (it may be state) and saved.
  * A decay of -infinity (any below -10^4) forgets everything before its position.
- * Products of the state are of fp32 quality (three bf16 terms a factor), what only
- * a 16-bit y is made of in two terms (2^-17 of it).  Values, sums of squares and
- * products of keys and queries stay below 2^127; of factors below 2^-110 the last
- * terms may be lost.  An infinity or NaN in the state, or at a position that counts,
- * makes its head's values non-finite from the start of its chunk on (64 positions, 32
- * for FI_F16 and FI_F32); other heads and rows are as without it. */
+ * Products are of fp32 quality (three bf16 terms a factor), also those that only a
+ * 16-bit y is made of.  Values, sums of squares and products of keys and queries
+ * stay below 2^127; of factors below 2^-110 the last terms may be lost.  An infinity
+ * or NaN in the state, or at a position that counts, makes its head's values
+ * non-finite from the start of its chunk on (64 positions, 32 for FI_F16 and
+ * FI_F32); other heads and rows are as without it. */
 fi_status fi_delta_forward(const fi_delta_desc *desc, const void *q, const void *k, const void *v, const float *decay,
                            const float *beta, const float *state, const int32_t *lengths, void *y, float *final,
                            void *saved, void *workspace, void *stream);

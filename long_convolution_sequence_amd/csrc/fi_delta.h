@@ -19,8 +19,7 @@
 //
 // Values in 32 bits are multiplied as terms of bf16 (x = t0 + t1 + t2, each the
 // rounding of what is left, exact to 2^-24): of two factors the products of terms i
-// and j with i + j <= 2 are taken (<= 1 where the result is rounded to 16 bits and
-// nothing else is made of it: 2^-17 there).  bf16 inputs are one term, fp16 two, fp32 three.
+// and j with i + j <= 2 are taken.  bf16 inputs are one term, fp16 two, fp32 three.
 #pragma once
 #include <type_traits>
 
@@ -40,22 +39,21 @@ using bf16x4 = __bf16 __attribute__((ext_vector_type(4)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 
-// Terms of an input, positions of a chunk and terms of what only y is made of.
-// Chunks of fp16 and fp32 are 32 long: the images of two and three terms of 64
-// positions leave a CU one workgroup or none.
+// Terms of an input and positions of a chunk.  Chunks of fp16 and fp32 are 32 long: the
+// images of two and three terms of 64 positions leave a CU one workgroup or none.
 template <typename T>
 struct DeltaType;
 template <>
 struct DeltaType<bf16_t> {
-    static constexpr int terms = 1, chunk = 64, out = 2;
+    static constexpr int terms = 1, chunk = 64;
 };
 template <>
 struct DeltaType<f16_t> {
-    static constexpr int terms = 2, chunk = 32, out = 2;
+    static constexpr int terms = 2, chunk = 32;
 };
 template <>
 struct DeltaType<float> {
-    static constexpr int terms = 3, chunk = 32, out = 3;
+    static constexpr int terms = 3, chunk = 32;
 };
 inline int delta_chunk(int dtype) { return dtype == FI_BF16 ? 64 : 32; }
 
@@ -429,10 +427,8 @@ __device__ __forceinline__ constexpr int tri_at(int i, int s) {
 // The factors that a chain reads, in whole pieces.
 template <int C>
 constexpr int factor_bytes() { return (5 * C * 4 + kPiece - 1) / kPiece * kPiece; }
-template <typename T, bool BACK>
-constexpr int image_bytes() {          // of a chunk: M in three terms and P
-    return tri_pieces<DeltaType<T>::chunk>() * kPiece * (3 + (BACK ? 3 : DeltaType<T>::out));
-}
+template <typename T>
+constexpr int image_bytes() { return tri_pieces<DeltaType<T>::chunk>() * kPiece * 6; }   // of a chunk: M and P in three terms
 
 // A wave a chunk and head.  Forwards the images of M = (I + A)^-1 and of
 // P_ij = scale E_ij (q_i . k_j) b_j, and the factors e^G_i of k_i S, scale e^G_i of
@@ -448,7 +444,7 @@ constexpr int image_bytes() {          // of a chunk: M in three terms and P
 template <typename T, int KT, bool BACK, bool VEC>
 __global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_prep(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, MT = C / 32, CS = C / 16, KS = KT * 2, LD = C + 4;
-    constexpr int PT = BACK ? 3 : DeltaType<T>::out, MB = tri_pieces<C>() * kPiece;
+    constexpr int MB = tri_pieces<C>() * kPiece;
     __shared__ __align__(16) float m[C * LD];
     __shared__ double sum[C];
     __shared__ float fb[C], fk[C], fq[C];
@@ -613,8 +609,7 @@ __global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_
         for (int r = 0; r < 16; ++r) m[(32 + acc_row(r)) * LD + col] = -n21[r];
         __syncthreads();
     }
-    const auto flush = [&](char *image, auto terms) {      // m (or its transpose) as an image
-        constexpr int NT = decltype(terms)::value;
+    const auto flush = [&](char *image) {                  // m (or its transpose) as an image
 #pragma unroll
         for (int i = 0; i < C / 16; ++i)
 #pragma unroll
@@ -626,14 +621,14 @@ __global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_
                     const int r = i * 16 + (lane & 15), c = s * 32 + 16 * (j >> 2) + 4 * (lane >> 4) + (j & 3);
                     v[j] = BACK ? m[c * LD + r] : m[r * LD + c];
                 }
-                const Frag<NT> f = split<NT>(v);
+                const Frag<3> f = split<3>(v);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < 3; ++t)
                     *reinterpret_cast<bf16x8 *>(image + t * MB + tri_at<C, BACK>(i, s) * kPiece + lane * 16) = f.t[t];
             }
     };
-    char *image = p.images + at * image_bytes<T, BACK>();
-    flush(image, std::integral_constant<int, 3>());
+    char *image = p.images + at * image_bytes<T>();
+    flush(image);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -642,7 +637,7 @@ __global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_
 #pragma unroll
             for (int r = 0; r < 16; ++r) m[(i * 32 + acc_row(r)) * LD + j * 32 + col] = qk[i][j][r];
     __syncthreads();
-    flush(image + 3 * MB, std::integral_constant<int, PT>());
+    flush(image + 3 * MB);
     if (lane < C) {
         float *f = p.factors + at * kDeltaFactors * C;
         const float rise = exp2f((float)sum[lane]), fall = exp2f((float)(sum[C - 1] - sum[lane]));
@@ -689,7 +684,7 @@ struct DeltaPlan {
 // against 539.  At least eight chunks a segment; more segments than fill the card twice
 // cost more to join (2.7 us each) than they bring (131072 x 9 heads of 96: 1024 sets of
 // columns 1.52 ms, 1536 1.43, 2048 1.50, without a chunk's own matrices).
-inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
+inline DeltaPlan delta_plan(const fi_delta_desc *q) {
     DeltaPlan d = {};
     d.C = delta_chunk(q->dtype);
     d.KT = (q->dk + 31) / 32;
@@ -700,8 +695,7 @@ inline DeltaPlan delta_plan(const fi_delta_desc *q, bool backward) {
     d.per = std::max<int64_t>(1, (d.chunks + want - 1) / want);
     d.segments = (int)std::max<int64_t>(1, (d.chunks + d.per - 1) / d.per);
     const size_t all = (size_t)d.chunks * heads, C = d.C, sk = (size_t)q->dk * q->dv * 4;
-    const size_t out = backward || q->dtype == FI_F32 ? 3 : 2;
-    d.images = up256(all * (C == 64 ? tri_pieces<64>() : tri_pieces<32>()) * kPiece * (3 + out));
+    d.images = up256(all * (C == 64 ? tri_pieces<64>() : tri_pieces<32>()) * kPiece * 6);
     d.factors = up256(all * kDeltaFactors * C * 4);
     d.states = up256(all * sk);
     d.ends = up256(all * sk);

@@ -8,6 +8,21 @@ namespace {
 
 enum { CHAIN_LOCAL, CHAIN_FULL };
 
+// LDS of the whole sequence's kernel, and whether P's last term comes into k's place there
+// after k's last use: with a place of its own it would leave a CU one workgroup where
+// without it there are two (bf16 keys of over 96 channels).
+constexpr int kTwoWorkgroups = 80 * 1024;
+template <typename T, int KT>
+constexpr int full_bytes() {
+    constexpr int C = DeltaType<T>::chunk;
+    return 3 * DeltaType<T>::terms * C * KT * 64 + 6 * tri_pieces<C>() * kPiece + factor_bytes<C>();
+}
+template <typename T, int KT>
+constexpr bool p_late() {
+    return full_bytes<T, KT>() > kTwoWorkgroups &&
+           full_bytes<T, KT>() - tri_pieces<DeltaType<T>::chunk>() * kPiece <= kTwoWorkgroups;
+}
+
 // The sequence of a segment's chunks, 16 columns a wave (blockIdx.y: a workgroup's).
 // FULL: from the state before the segment; y, the states before each chunk and w where
 // they are kept, the last state.  LOCAL: from nothing, only the state at the end; the
@@ -22,13 +37,14 @@ enum { CHAIN_LOCAL, CHAIN_FULL };
 // step's operands read ahead of it (653) or v and y by whole vectors (585).
 template <typename T, int KT, int MODE>
 __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
-    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
     constexpr int MT = C / 16, CS = C / 32, DT = KT * 2, DK = KT * 32;
     constexpr int KB = C * DK * 2, MB = tri_pieces<C>() * kPiece;    // bytes of a term
-    constexpr bool FULL = MODE == CHAIN_FULL;
+    constexpr bool FULL = MODE == CHAIN_FULL, LATE = FULL && p_late<T, KT>();
     extern __shared__ __align__(16) char lds[];
     char *const ik = lds, *const ikt = ik + N * KB, *const im = ikt + N * KB;
-    char *const ip = im + 3 * MB, *const iq = ip + NY * MB;   // FULL only
+    char *const ip = im + 3 * MB, *const iq = ip + (LATE ? 2 : 3) * MB;   // FULL only
+    char *const ip2 = LATE ? ik : ip + 2 * MB;                 // P's last term
     char *const ff = FULL ? iq + N * KB : ip;
     const float *const f = reinterpret_cast<const float *>(ff);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -66,7 +82,7 @@ __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
     };
     const auto matrices = [&](int64_t c) {                     // M, P and the factors; v
         const int64_t at = c * heads + bh;
-        bring(im, p.images + at * image_bytes<T, false>(), (FULL ? 3 + NY : 3) * MB);
+        bring(im, p.images + at * image_bytes<T>(), (LATE ? 5 : FULL ? 6 : 3) * MB);
         bring(ff, (const char *)(p.factors + at * kDeltaFactors * C), factor_bytes<C>());
         if (!map)
             load_column<T, MT>(vs, v + (c * C * p.B + b) * p.ldv, min(column, p.dv - 1), (unsigned)(p.B * p.ldv),
@@ -88,18 +104,16 @@ __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
 #pragma unroll
         for (int ks = 0; ks < KT; ++ks) {
             const Frag<3> s = step_of<3>(S, ks);
-            Frag<NY> sy;
-#pragma unroll
-            for (int i = 0; i < NY; ++i) sy.t[i] = s.t[i];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 multiply<2>(R[i], piece<N>(ik, i * KT + ks, KB), s);
-                if (FULL) multiply<NY - 1>(Y[i], piece<N>(iq, i * KT + ks, KB), sy);
+                if (FULL) multiply<2>(Y[i], piece<N>(iq, i * KT + ks, KB), s);
             }
             in_order();
         }
         arrived();
         __syncthreads();
+        if (LATE) bring(ip2, p.images + at * image_bytes<T>() + 5 * MB, MB);   // k has been read
         // v - e^G K S, and w = M of it
         const int vlive = anew(map ? 0 : live);
 #pragma unroll
@@ -120,7 +134,11 @@ __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
                 if (tri_in<C, false>(i, cs)) multiply<2>(W[i], piece<3>(im, tri_at<C, false>(i, cs), MB), s);
             in_order();
         }
-        if (c + 1 < stop) ahead(c + 1);
+        if (LATE) {
+            arrived();
+            __syncthreads();
+        }
+        if (!FULL && c + 1 < stop) ahead(c + 1);
         if (FULL) {
             if (p.w && mine) store_column<float, MT>(p.w + at * C * p.dv, column, p.dv, W, C, C);
 #pragma unroll
@@ -129,16 +147,22 @@ __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
                 for (int r = 0; r < 4; ++r) Y[i][r] *= f[C + i * 16 + tile_row(r)];
 #pragma unroll
             for (int cs = 0; cs < CS; ++cs) {
-                const Frag<NY> s = step_of<NY>(W, cs);
+                const Frag<3> s = step_of<3>(W, cs);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
-                    if (tri_in<C, false>(i, cs)) multiply<NY - 1>(Y[i], piece<NY>(ip, tri_at<C, false>(i, cs), MB), s);
+                    if (tri_in<C, false>(i, cs)) {
+                        const Frag<2> p01 = piece<2>(ip, tri_at<C, false>(i, cs), MB);
+                        multiply<2>(Y[i], Frag<3>{p01.t[0], p01.t[1], piece<1>(ip2, tri_at<C, false>(i, cs), MB).t[0]}, s);
+                    }
                 in_order();
             }
             if (mine)
                 store_column<T, MT>(static_cast<T *>(p.y) + (int64_t)h * p.dv + (t0 * p.B + b) * p.ldy, column,
                                     (unsigned)(p.B * p.ldy), Y, rows, live);
         }
+        // the whole sequence's next k and q begin behind y: ahead of it they would push v's
+        // loads into scratch memory (131072 positions of 9 heads of 96 1840 us in place of 1650)
+        if (FULL && c + 1 < stop) ahead(c + 1);
         const float decay = f[4 * C];
 #pragma unroll
         for (int t = 0; t < DT; ++t) S[t] *= decay;
@@ -349,7 +373,7 @@ constexpr int64_t kDeltaSteps = 14;
 
 template <typename T, int KT>
 void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
-    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms, NY = DeltaType<T>::out;
+    constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
     constexpr int KB = C * KT * 64, MB = tri_pieces<C>() * kPiece, FB = factor_bytes<C>();
     const int heads = a.B * a.H;
     const dim3 all((unsigned)(a.chunks * heads));
@@ -364,8 +388,9 @@ void forward(const DeltaArgs &a, const DeltaPlan &d, hipStream_t st) {
         delta_join(a, a.state, false, st);
     }
     const ChainGrid g = chain_grid((a.dv + 15) / 16, C, KT);
+    constexpr int full = full_bytes<T, KT>() - (p_late<T, KT>() ? MB : 0);
     hipLaunchKernelGGL((k_delta_chain<T, KT, CHAIN_FULL>), dim3((unsigned)(a.segments * heads), g.groups), dim3(g.threads),
-                       N * KB * 3 + (3 + NY) * MB + FB, st, a);
+                       full, st, a);
 }
 
 template <typename T>
@@ -441,7 +466,7 @@ extern "C" {
 
 size_t fi_delta_saved_bytes(const fi_delta_desc *desc) {
     if (delta_check(desc)) return 0;
-    const DeltaPlan d = delta_plan(desc, false);
+    const DeltaPlan d = delta_plan(desc);
     const size_t last = up256((size_t)desc->batch * desc->heads * desc->dk * desc->dv * 4);
     return d.states + last + d.rows + d.maps + 256;
 }
@@ -449,10 +474,10 @@ size_t fi_delta_saved_bytes(const fi_delta_desc *desc) {
 size_t fi_delta_workspace_bytes(const fi_delta_desc *desc, int backward) {
     if (delta_check(desc)) return 0;
     if (backward) {
-        const DeltaPlan d = delta_plan(desc, true);
+        const DeltaPlan d = delta_plan(desc);
         return d.images + d.factors + d.ends + d.rows + 2 * d.local + 256;
     }
-    const DeltaPlan d = delta_plan(desc, false);
+    const DeltaPlan d = delta_plan(desc);
     return d.images + d.factors + 2 * d.local + d.maps + 256;
 }
 
@@ -467,7 +492,7 @@ fi_status fi_delta_forward(const fi_delta_desc *desc, const void *q, const void 
         return op_fail(FI_EINVAL, call, "q, k, v, decay, beta, y and the workspace are required");
     if (!aligned(es, {q, k, v, y}) || !aligned(4, {decay, beta, state, lengths, final}) || !aligned(256, {saved, workspace}))
         return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
-    const DeltaPlan d = delta_plan(desc, false);
+    const DeltaPlan d = delta_plan(desc);
     DeltaArgs a = {};
     delta_args(desc, d, a);
     const int64_t rows = a.T * a.B;

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(512, 4) k_delta_back_chain(DeltaArgs p) {
     const auto ahead = [&](int64_t c) { sk.load(rows_from(k, p.ldk, c), (unsigned)(p.B * p.ldk), p.dk, live_of(c)); };
     const auto matrices = [&](int64_t c) {                    // N, P and the factors
         const int64_t at = c * heads + bh;
-        bring(in, p.images + at * image_bytes<T, true>(), 6 * MB);
+        bring(in, p.images + at * image_bytes<T>(), 6 * MB);
         bring(ff, (const char *)(p.factors + at * kDeltaFactors * C), factor_bytes<C>());
     };
     if (first < stop) ahead(stop - 1), matrices(stop - 1);
@@ -513,7 +513,7 @@ extern "C" fi_status fi_delta_backward(const fi_delta_desc *desc, const void *q,
     if (!aligned(es, {q, k, v, dy, dq, dk, dv}) || !aligned(4, {decay, beta, state, lengths, dfinal, ddecay, dbeta, dstate}) ||
         !aligned(256, {saved, workspace}))
         return op_fail(FI_EINVAL, call, "a pointer is not aligned to its values");
-    const DeltaPlan d = delta_plan(desc, true);
+    const DeltaPlan d = delta_plan(desc);
     DeltaArgs a = {};
     delta_args(desc, d, a);
     const int64_t rows = a.T * a.B;
