@@ -574,7 +574,8 @@ fi_status fi_delta_forward(const fi_delta_desc *desc, const void *q, const void 
  * summed over the heads that share them), ddecay and dbeta [T][B][H] fp32, all 0
  * past a row's length, and where not NULL dstate [B][H][dk][dv] fp32.  The other
  * arguments are those of the forward call that wrote `saved`; dfinal may be NULL
- * (zeros). */
+ * (zeros).  A decay's gradient is summed of terms that carry the decay, so it keeps
+ * its digits however small it makes them (0 at -infinity). */
 fi_status fi_delta_backward(const fi_delta_desc *desc, const void *q, const void *k, const void *v, const float *decay,
                             const float *beta, const float *state, const int32_t *lengths, const void *saved,
                             const void *dy, const float *dfinal, void *dq, void *dk, void *dv, float *ddecay,

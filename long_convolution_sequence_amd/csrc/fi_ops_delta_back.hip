@@ -8,9 +8,12 @@
 // J_ij = b_j E_ij (dy_i . w_j) (i >= j):
 //   dq_i = sum_j J_ij k_j + e^G_i S dy_i,
 //   dk_i = sum_j (H_ij + H_ji) k_j + sum_j J_ji q_j - e^G_i S dv_i + e^(G_C - G_i) b_i D w_i,
-//   ddecay_t = <D, S'> + sum_{i >= t} (q_i . dq_i - v_i . dv_i)  with S' the state behind the
-// chunk: y is linear in q, and a decay scales what was written before it against
-// what is written after.
+//   ddecay_t = e^(G_C) <D, S> + sum_{i >= t > j} (H_ij k_i . k_j + J_ij q_i . k_j)
+//            + sum_{i >= t} e^G_i (q_i . S dy_i - k_i . S dv_i) + sum_{j < t} e^(G_C - G_j) b_j k_j . D w_j.
+// A decay scales what was before it against what comes after: each of its four parts
+// holds only terms that carry it, so a gate that is nearly shut keeps the digits of its
+// gradient.  (<D, S'> + sum_{i >= t} (q_i . dq_i - v_i . dv_i) is the same number, but as
+// a difference of others that do not carry the decay.)
 #include "fi_delta.h"
 
 namespace fi {
@@ -157,9 +160,9 @@ __global__ void __launch_bounds__(512, 4) k_delta_back_chain(DeltaArgs p) {
         store_state(p.dstate + bh * size, D, p.dk, p.dv, column);
 }
 
-// Sum over the 32 lanes of a half, in its last lane: shifts within rows of 16 lanes,
-// then the lower row's last lane into the upper row.
-__device__ __forceinline__ float half_sum(float v) {
+// Sums over the lanes up to each one of a half (32 lanes): shifts within rows of 16
+// lanes, then the lower row's last lane into the upper row.
+__device__ __forceinline__ float half_sums(float v) {
 #define FI_LANE_ADD(ctrl, rows) \
     v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false))
     FI_LANE_ADD(0x111, 0xf);
@@ -175,10 +178,11 @@ __device__ __forceinline__ float half_sum(float v) {
 // chunk, a wave 32 channels of the keys.  The values' channels pass in slabs of 32; H
 // and J then take the slabs' place in LDS, so that two workgroups share a CU and one
 // computes while the other waits for its slab (one workgroup where heads share a key
-// head: SHARED, their sums take 64 registers more).  8192 x 4 x 6 heads of 128 bf16
-// 476 us (0.55 GB: 110 at a copy's rate): 90 registers spill, a slab's two barriers and
-// its loads of the states; with the next slab's rows ahead 123 spill and it is 527, with
-// those and one workgroup a CU 565.
+// head: SHARED, their sums take 64 registers more).  The decays' pairs of positions are
+// multiplied out there, with k and q read again (as images by rows they would leave a CU
+// one workgroup): 85 us of it.  8192 x 4 x 6 heads of 128 bf16 560 us (0.5 GB: 100 at a
+// copy's rate): 92 registers spill, a slab's two barriers and its loads of the states.
+// The steps of k and q by twos ahead of their products 559, by fours 680.
 template <typename T, int KT, bool VEC, bool SHARED>
 __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
     char *const ikt = lds, *const iqt = ikt + N * KB, *const ix = iqt + N * KB, *const iw = ix + 3 * SB, *const iy = iw + 3 * SB;
     float *const Hm = reinterpret_cast<float *>(ix), *const Jm = Hm + C * LD;
     __shared__ double G[C];
-    __shared__ float beta[C], rk[C], rq[C], dotb[C], dotv[C], dotq[4][C], dotk[4][C], total[2][4];
+    __shared__ float beta[C], rk[C], rq[C], dotb[C], dots[4][C], dote[4][C], pairs[2][C], total[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5, col = lane & 31;
     const int hk = blockIdx.x % p.HK, b = blockIdx.x / p.HK % p.B, share = p.H / p.HK, heads = p.B * p.H;
     const int64_t c = blockIdx.x / p.HK / p.B, t0 = c * C, n = delta_length(p, b) - t0;
@@ -229,7 +233,27 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
     f32x16 *const allq = SHARED ? sums[0] : ys, *const allk = SHARED ? sums[1] : xs;
 #pragma unroll
     for (int i = 0; i < (SHARED ? MT : 1); ++i) sums[0][i] = sums[1][i] = zeros16();
-    float sumq = 0.f;                                    // q . dq of row `lane`, over the heads
+    // kk_ij = k_i . k_j and qk_ij = q_i . k_j of a 32 x 32 block, rows i of block a
+    const auto products = [&](f32x16 &kk, f32x16 &qk, int a, int b32, auto vec) {
+        constexpr bool V = decltype(vec)::value;
+        const T *const k0 = static_cast<const T *>(p.k) + hk * p.dk + row0 * p.ldk;
+        const T *const q0 = static_cast<const T *>(p.q) + hk * p.dk + row0 * p.ldq;
+        const auto operand = [&](const T *from, int64_t ld, int i, int ks) {
+            float lo[4], hi[4], x[8];
+            const T *row = from + (int64_t)min(i, live - 1) * p.B * ld;
+            load4<V>(lo, row, ks * 16 + 4 * half, p.dk, i < live);
+            load4<V>(hi, row, ks * 16 + 4 * half + 8, p.dk, i < live);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = lo[j], x[4 + j] = hi[j];
+            return split<N>(x);
+        };
+#pragma unroll 1
+        for (int ks = 0; ks < KT * 2; ++ks) {
+            const Frag<N> kb = operand(k0, p.ldk, b32 * 32 + col, ks);
+            multiply<2>(kk, operand(k0, p.ldk, a * 32 + col, ks), kb);
+            multiply<2>(qk, operand(q0, p.ldq, a * 32 + col, ks), kb);
+        }
+    };
 
     for (int s = 0; s < share; ++s) {
         const int h = hk * share + s;
@@ -242,16 +266,15 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
         }
         const float *const x = p.x + at * C * p.dv, *const w = p.w + at * C * p.dv;
         const float *const S = p.states + at * p.dk * p.dv, *const D = p.ends + at * p.dk * p.dv;
-        const T *const v = static_cast<const T *>(p.v) + row0 * p.ldv + (int64_t)h * p.dv;
         const T *const dy = static_cast<const T *>(p.dy) + row0 * p.lddy + (int64_t)h * p.dv;
         f32x16 wd[MT], xw = zeros16(), yw = zeros16();
 #pragma unroll
         for (int i = 0; i < MT; ++i) ys[i] = xs[i] = wd[i] = zeros16();
-        float db[MT], dw[MT], inner = 0.f;
+        float db[MT], inner = 0.f;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) db[i] = dw[i] = 0.f;
+        for (int i = 0; i < MT; ++i) db[i] = 0.f;
         Chunk<float, 4> na[MT], nu[MT];
-        Chunk<T, 4> nz[MT], ny[MT];
+        Chunk<T, 4> ny[MT];
         const auto load = [&](int c0) {
 #pragma unroll
             for (int e = 0; e < MT; ++e) {
@@ -259,7 +282,6 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
                 const int64_t i = min(e * 32 + tid / 8, live - 1);
                 na[e] = raw4<VEC>(x + i * p.dv, cc, p.dv);
                 nu[e] = raw4<VEC>(w + i * p.dv, cc, p.dv);
-                nz[e] = raw4<VEC>(v + i * p.B * p.ldv, cc, p.dv);
                 ny[e] = raw4<VEC>(dy + i * p.B * p.lddy, cc, p.dv);
             }
         };
@@ -275,7 +297,6 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
                     const bool in = i < live && cc + j < p.dv;
                     a[j] = in ? na[e][j] : 0.f, u[j] = in ? nu[e][j] : 0.f, y[j] = in ? (float)ny[e][j] : 0.f;
                     db[e] = fmaf(a[j], u[j], db[e]);
-                    dw[e] = fmaf(a[j], in ? (float)nz[e][j] : 0.f, dw[e]);
                 }
                 put_terms<3>(ix, to, SB, a);
                 put_terms<3>(iw, to, SB, u);
@@ -315,36 +336,54 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
 #pragma unroll
         for (int e = 0; e < MT; ++e) {
 #pragma unroll
-            for (int o = 1; o < 8; o *= 2) db[e] += __shfl_xor(db[e], o, 64), dw[e] += __shfl_xor(dw[e], o, 64);
-            if (tid % 8 == 0) dotb[e * 32 + tid / 8] = db[e], dotv[e * 32 + tid / 8] = dw[e];
+            for (int o = 1; o < 8; o *= 2) db[e] += __shfl_xor(db[e], o, 64);
+            if (tid % 8 == 0) dotb[e * 32 + tid / 8] = db[e];
         }
         __syncthreads();                                 // the slabs have been read
         if (wave < MT * MT) {
-            const int j = wave % MT * 32 + col;
+            const int bi = wave / MT, bj = wave % MT, j = bj * 32 + col;
+            f32x16 kk = zeros16(), qk = zeros16();
+            if (bi >= bj) {
+                if ((p.dk & 3) == 0) products(kk, qk, bi, bj, std::true_type());
+                else products(kk, qk, bi, bj, std::false_type());
+            }
+            float before = 0.f;                          // over the pairs i >= j > column, of this block
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int i = wave / MT * 32 + acc_row(r);
+                const int i = bi * 32 + acc_row(r);
                 const float e = i >= j ? exp2f((float)(G[i] - G[j])) * beta[j] : 0.f;
-                Hm[i * LD + j] = i > j ? -beta[i] * e * xw[r] : 0.f;
-                Jm[i * LD + j] = p.scale * e * yw[r];
+                const float hij = i > j ? -beta[i] * e * xw[r] : 0.f, jij = p.scale * e * yw[r];
+                Hm[i * LD + j] = hij;
+                Jm[i * LD + j] = jij;
+                if (bi < bj) continue;
+                const float to = half_sums(fmaf(hij * rk[i], kk[r], jij * rq[i] * qk[r]) * rk[j]);
+                const float under = __shfl_up(to, 1, 32);
+                before += col > 0 && i >= j ? under : 0.f;
+                if (bi > bj && col == 31) pairs[1][i] = to;      // a whole row of the block below
             }
+            before = both_halves(before);
+            if (bi >= bj && half == 0) pairs[bi - bj][j] = before;
         }
         // the states' shares, with their rows' factors, where the pairs' are added
-        float part = 0.f;
         if (wave < KT) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4) {
-                    float kv[4];
+                    float kv[4], qv[4];
                     four(ikt, i * 32 + acc_row(r4 * 4), kv);
+                    four(iqt, i * 32 + acc_row(r4 * 4), qv);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
                         const float rise = exp2f((float)G[row]), fall = exp2f((float)(G[C - 1] - G[row])) * beta[row];
-                        part = fmaf(rk[row] * fall * kv[j], wd[i][r], part);
                         ys[i][r] *= p.scale * rise;
-                        xs[i][r] = fmaf(fall, wd[i][r], -rise * beta[row] * xs[i][r]);
+                        xs[i][r] *= -rise * beta[row];
+                        wd[i][r] *= fall;
+                        const float own = half_sums(fmaf(rq[row] * qv[j], ys[i][r], rk[row] * kv[j] * xs[i][r]));
+                        const float end = half_sums(rk[row] * kv[j] * wd[i][r]);
+                        if (col == 31) dots[wave][row] = own, dote[wave][row] = end;
+                        xs[i][r] += wd[i][r];
                     }
                 }
         }
@@ -369,43 +408,44 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
                     in_order();
                 }
             }
+            if (SHARED) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    float qv[4];
-                    four(iqt, i * 32 + acc_row(r4 * 4), qv);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
-                        if (SHARED) allq[i][r] += ys[i][r], allk[i][r] += xs[i][r];
-                        const float dot = half_sum(rq[row] * qv[j] * ys[i][r]);
-                        if (col == 31) dotq[wave][row] = dot;
-                    }
-                }
+                for (int i = 0; i < MT; ++i) allq[i] += ys[i], allk[i] += xs[i];
+            }
         }
-        inner = lanes_sum(inner), part = lanes_sum(part);
-        if (lane == 0) total[0][wave] = inner, total[1][wave] = part;
+        inner = lanes_sum(inner);
+        if (lane == 0) total[wave] = inner;
         __syncthreads();
         if (wave == 0) {
-            float all = 0.f, end = 0.f, qd = 0.f, g = 0.f;
+            // lane t's decay: own, and of the blocks on the diagonal what is before it; the block
+            // below them adds its columns before t, or its rows from t on
+            float all = 0.f, own = 0.f, ends = 0.f, g = 0.f, under = 0.f;
 #pragma unroll
-            for (int i = 0; i < KT; ++i) all += total[0][i], end += total[1][i];
-            all = fmaf(exp2f((float)G[C - 1]), all, end);
+            for (int i = 0; i < KT; ++i) all += total[i];
             if (lane < C) {
 #pragma unroll
-                for (int i = 0; i < KT; ++i) qd += dotq[i][lane];
-                g = fmaf(-beta[lane], dotv[lane], qd);
+                for (int i = 0; i < KT; ++i) own += dots[i][lane], ends += dote[i][lane];
+                g = pairs[0][lane];
+                if (MT == 2) under = pairs[1][lane];
             }
-            sumq += qd;
 #pragma unroll
             for (int o = 1; o < C; o *= 2) {
-                const float z = __shfl_down(g, o, 64);
-                if (lane + o < C) g += z;
+                const float z = __shfl_down(own, o, 64), u = __shfl_up(ends, o, 64);
+                if (lane + o < C) own += z;
+                if (lane >= o) ends += u;
             }
+            if (MT == 2) {
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const float u = __shfl_down(under, o, 32);
+                    if (half == 1 && col + o < 32) under += u;
+                }
+            }
+            const float z = __shfl_up(ends, 1, 64);
+            g = (g + under) + (own + (lane > 0 ? z : 0.f)) + exp2f((float)G[C - 1]) * all;
             if (lane < rows) {
                 const int64_t row = row0 + (int64_t)lane * p.B;
-                p.dg[row * p.lddg + h] = lane < live ? g + all : 0.f;
+                p.dg[row * p.lddg + h] = lane < live ? g : 0.f;
                 p.dbeta[row * p.lddb + h] = lane < live ? dotb[lane] : 0.f;
             }
         }
@@ -413,19 +453,20 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
     // over the lengths: d = r (d^ - x^ (x^ . d^)), x^ = r x
     if (p.unit) {
         __syncthreads();
-        if (wave == 0 && lane < C) dotv[lane] = sumq;
         if (wave < KT)
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4) {
-                    float kv[4];
+                    float qv[4], kv[4];
+                    four(iqt, i * 32 + acc_row(r4 * 4), qv);
                     four(ikt, i * 32 + acc_row(r4 * 4), kv);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = r4 * 4 + j, row = i * 32 + acc_row(r);
-                        const float dot = half_sum(rk[row] * kv[j] * allk[i][r]);
-                        if (col == 31) dotk[wave][row] = dot;
+                        const float dotq = half_sums(rq[row] * qv[j] * allq[i][r]);
+                        const float dotk = half_sums(rk[row] * kv[j] * allk[i][r]);
+                        if (col == 31) dots[wave][row] = dotq, dote[wave][row] = dotk;
                     }
                 }
         __syncthreads();
@@ -444,11 +485,11 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
                 if (row >= rows) continue;
                 float gq = allq[i][r], gk = allk[i][r];
                 if (p.unit) {
-                    float dot = 0.f;
+                    float dotq = 0.f, dotk = 0.f;
 #pragma unroll
-                    for (int t = 0; t < KT; ++t) dot += dotk[t][row];
-                    gq = rq[row] * fmaf(-rq[row] * qv[j], dotv[row], gq);
-                    gk = rk[row] * fmaf(-rk[row] * kv[j], dot, gk);
+                    for (int t = 0; t < KT; ++t) dotq += dots[t][row], dotk += dote[t][row];
+                    gq = rq[row] * fmaf(-rq[row] * qv[j], dotq, gq);
+                    gk = rk[row] * fmaf(-rk[row] * kv[j], dotk, gk);
                 }
                 const int64_t to = row0 + (int64_t)row * p.B;
                 dq[to * p.lddq + d] = (T)(row < live ? gq : 0.f);
