@@ -296,7 +296,8 @@ def _heads(t, shape, dtype, device, name):
     if _packed(t, shape, dtype, device):
         return t.data_ptr(), 0
     _fits(t, shape, dtype, device, name)
-    if t.stride(-2) != shape[-1] and shape[-2] != 1:
+    # a head's channels side by side too: flattening anything else would make a copy
+    if shape[-2] != 1 and (t.stride(-2) != shape[-1] or (t.stride(-1) != 1 and shape[-1] != 1)):
         _bad(f"{name}: the heads of a row are not packed")
     return _rows(t.flatten(-2) if shape[-2] != 1 else t.squeeze(-2), (*shape[:-2], shape[-2] * shape[-1]), dtype, device,
                  name)
