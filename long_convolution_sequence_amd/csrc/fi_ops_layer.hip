@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(THREADS) k_layer(LayerArgs p) {
     }
 }
 
-// Backward: every tensor of the row once, both row means in one step; the column
+// Backward: every tensor of the row once, its three means in one step: those of e and e u,
+// and that of r - m, which takes the rounding of the mean as it is kept away; the column
 // sums of a team's rows in registers, its workgroup's joined in LDS (team after
 // team, so the order is fixed) and written once.  Elements that a lane does not
 // own have weights of zero, so both means pass them by.  131072 x 768 bf16 with fp32
@@ -127,7 +128,7 @@ template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool AL
 __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) k_layer_back(LayerArgs p) {
     constexpr int N = CH * NC;
     constexpr bool AHEAD = MULTI && THREADS <= 512;
-    __shared__ float slots[2][2][16];
+    __shared__ float slots[2][3][16];
     __shared__ float join[MULTI ? 1 : 2 * 64 * N];
     Team<CH, NC, MULTI> t(p.D);
     Raw<ALL, STREAM, V, CH, NC> raw_x, raw_da;
@@ -153,28 +154,33 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) k_layer_back(
         raw_dr.get(dr);
         if (AHEAD && t.row + t.rows_step < p.rows) fetch(t.row + t.rows_step);
         const float mean = p.saved[t.row], n = p.saved[p.rows + t.row];
-        float s = 0.f, q = 0.f;
+        float s = 0.f, q = 0.f, d = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            float c = 0.f, e = 0.f;
+            float c = 0.f, e = 0.f, m = 0.f;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int at = j * CH + i;
-                r[at] = (r[at] + x[at] - mean) * n;          // unit r
-                c1[at] = fmaf(da[at], r[at], c1[at]);
-                c2[at] += da[at];
-                da[at] *= w[at];
-                c += da[at];
-                e = fmaf(da[at], r[at], e);
+                r[at] = r[at] + x[at] - mean;
+                m += TAIL && i < t.at[j].skip ? 0.f : r[at];
+                const float g = da[at] * w[at];
+                c += g;
+                e = fmaf(g, r[at], e);
             }
             s += t.at[j].skip < CH ? c : 0.f;
             q += t.at[j].skip < CH ? e : 0.f;
+            d += t.at[j].skip < CH ? m : 0.f;
         }
-        if (!p.dx && !p.dres) continue;
-        t.sums(s, q, slots);
-        s *= per, q *= per;
+        t.sums(s, q, d, slots);
+        s *= per, d *= per;
+        q = n * fmaf(-d, s, q * per);
 #pragma unroll
-        for (int i = 0; i < N; ++i) dr[i] = fmaf(n, da[i] - fmaf(r[i], q, s), dr[i]);
+        for (int i = 0; i < N; ++i) {
+            const float u = (r[i] - d) * n;                  // unit r
+            c1[i] = fmaf(da[i], u, c1[i]);
+            c2[i] += da[i];
+            dr[i] = fmaf(n, fmaf(da[i], w[i], -fmaf(u, q, s)), dr[i]);
+        }
         if (p.dres) store_row<TAIL, W>(dr, p.dres, p.lddres, t);
         if (p.dx) store_row<TAIL, V>(dr, p.dx, p.lddx, t);
     }

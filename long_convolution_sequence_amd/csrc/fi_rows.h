@@ -57,6 +57,16 @@ struct Team {
         for (int i = 0; i < waves; ++i) v += slots[turn][0][i], w += slots[turn][1][i];
         turn ^= 1;
     }
+    // Three.
+    __device__ __forceinline__ void sums(float &v, float &w, float &x, float (*slots)[3][16]) {
+        v = lanes_sum(v), w = lanes_sum(w), x = lanes_sum(x);
+        if (!MULTI) return;
+        if (lane == 0) slots[turn][0][wave] = v, slots[turn][1][wave] = w, slots[turn][2][wave] = x;
+        __syncthreads();
+        v = w = x = 0.f;
+        for (int i = 0; i < waves; ++i) v += slots[turn][0][i], w += slots[turn][1][i], x += slots[turn][2][i];
+        turn ^= 1;
+    }
 };
 
 // A row's values as they are loaded.  ALL: the tensor is there; else a null one
