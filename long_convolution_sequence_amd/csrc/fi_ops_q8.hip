@@ -153,6 +153,15 @@ struct Q8Args {
     int64_t M, N, ldy, kp;
 };
 
+// What a wave's lanes wrote to LDS is read by its other lanes: an order for the compiler
+// alone (the wave's accesses to LDS run in order), which must not follow from what it
+// knows of one lane's addresses.
+__device__ __forceinline__ void wave_exchanged() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Outputs [BM rows][BN columns] of a workgroup, WM x WN waves; a stage of 128 values
 // along k of both sides in LDS while the next is on its way.  Workgroup i runs on XCD
 // i % 8: each XCD takes a run of tiles in groups of eight rows of tiles, so that what
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
             for (int r = 0; r < 4; ++r)
                 mine[(lane & 15) * PITCH + j * 16 + (lane >> 4) * 4 + r] =
                     (T)fmaf((float)acc[i][j][r] * sa, sw[j][r], bias[j][r]);
-        __builtin_amdgcn_wave_barrier();
+        wave_exchanged();
         for (int u = lane; u < 16 * LANES; u += 64) {
             const int64_t m = mw + u / LANES, n = nw + u % LANES * CH;
             if (m >= p.M) continue;
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
                 for (int e = 0; e < CH; ++e)
                     if (n + e < p.N) y[m * p.ldy + n + e] = v[e];
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_exchanged();
     }
 }
 
