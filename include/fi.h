@@ -718,7 +718,7 @@ fi_status fi_q4_matvec(const fi_q4_desc *desc, const void *packed, int rows, int
  * the order of the matrix instructions and an fp32 scale a row, laid out from
  * codes and scales (fi_q8_pack) or from values (fi_q8_quantize).  rows and N are
  * up to 2^24, K up to 131071 (the sums are whole numbers of 32 bits and exact),
- * rows * N up to 2^42. */
+ * rows * N up to 2^38. */
 
 /* Device bytes of a packed matrix (256-byte aligned); 0 for a bad size. */
 size_t fi_q8_bytes(int64_t rows, int K);

@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kQ8MaxK = 131071;        // 128 * 128 * K < 2^31
 constexpr int64_t kQ8MaxRows = int64_t(1) << 24;
+constexpr int64_t kQ8MaxOutputs = int64_t(1) << 38;
 constexpr int kQ8Piece = 1024;         // bytes of 16 rows x 64 values
 
 using i32x4 = int __attribute__((ext_vector_type(4)));
@@ -399,6 +400,9 @@ fi_status fi_q8_product(int64_t rows, int64_t N, int K, const void *a, const voi
     if (const char *why = q8_check(rows, K)) return op_fail(FI_EINVAL, call, why);
     if (N < 1 || N > kQ8MaxRows) return op_fail(FI_EINVAL, call, "N is not in 1 .. 2^24");
     if (rows * N > int64_t(1) << 42) return op_fail(FI_EINVAL, call, "rows * N is over 2^42");
+    // tiles of 256 x 256 at 512 threads: with those at the edges 2^22 + 2^17 + 1 of them at most, and a launch
+    // has less than 2^32 threads
+    if (rows * N > kQ8MaxOutputs) return op_fail(FI_EINVAL, call, "too large for a launch: rows * N is over 2^38");
     if (!value_type(dtype)) return op_fail(FI_EINVAL, call, "dtype is none of FI_F32, FI_BF16, FI_F16");
     if (ld_y != 0 && (ld_y < N || ld_y > (int64_t(1) << 40))) return op_fail(FI_EINVAL, call, "a row pitch is less than N");
     if (rows == 0) return FI_OK;

@@ -1,0 +1,16 @@
+"""Sizes of the 8-bit products that no launch can index, without a GPU: refused before
+anything is launched."""
+import pytest
+
+from long_convolution_sequence_amd import fi, ops
+
+P, STEP = 0x100000, 0x10000000        # made-up device addresses
+
+
+@pytest.mark.parametrize("rows,N", [(1 << 20, 1 << 19), ((1 << 24) - 1, 1 << 15), (20000, 1 << 24)])
+@pytest.mark.parametrize("dtype", [ops.F32, ops.BF16, ops.F16])
+def test_outputs_past_a_launch(rows, N, dtype):
+    lib = fi.load_library()
+    a, w, y = P, P + 64 * STEP, P + 128 * STEP
+    assert lib.fi_q8_product(rows, N, 64, a, w, None, dtype, y, 0, None) == fi.FI_EINVAL
+    assert "2^38" in lib.fi_op_last_error().decode()
