@@ -539,7 +539,8 @@ fi_status fi_scan_backward(const fi_scan_desc *desc, const void *x, const void *
 typedef struct fi_delta_desc {
     int64_t T;             /* positions, 0 .. 2^23 */
     int batch;             /* B >= 1 */
-    int key_heads, heads;  /* HK, H >= 1, H a multiple of HK, B H <= 2^20 */
+    int key_heads, heads;  /* HK, H >= 1, H a multiple of HK, B H <= 2^20, and less than 2^24
+                              with the chunks of T: of 64 positions, 32 for FI_F16 and FI_F32 */
     int dk, dv;            /* 1 .. 128, 1 .. 1024 */
     int dtype;             /* of q, k, v, y and their gradients */
     int unit;              /* 0 or 1 */

@@ -417,7 +417,8 @@ const char *delta_check(const fi_delta_desc *q) {
     if (!(q->scale == q->scale)) return "scale is not a number";
     if ((int64_t)q->batch * q->heads > int64_t(1) << 20) return "batch * heads is over 2^20";
     const int C = delta_chunk(q->dtype);
-    if ((q->T + C - 1) / C * q->batch * q->heads > int64_t(1) << 24) return "too large: chunks * batch * heads is over 2^24";
+    // a launch has less than 2^32 threads, 256 of them a chunk and key head backwards
+    if ((q->T + C - 1) / C * q->batch * q->heads >= int64_t(1) << 24) return "too large: chunks * batch * heads is not below 2^24";
     const int64_t qk = (int64_t)q->key_heads * q->dk, v = (int64_t)q->heads * q->dv, h = q->heads;
     const int64_t ld[][2] = {{q->ld_q, qk}, {q->ld_k, qk}, {q->ld_v, v}, {q->ld_decay, h}, {q->ld_beta, h}, {q->ld_y, v},
                              {q->ld_dy, v}, {q->ld_dq, qk}, {q->ld_dk, qk}, {q->ld_dv, v}, {q->ld_ddecay, h},

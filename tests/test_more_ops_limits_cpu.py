@@ -1,5 +1,4 @@
-"""Sizes of the 8-bit products that no launch can index, without a GPU: refused before
-anything is launched."""
+"""Sizes that no launch can index, without a GPU: refused before anything is launched."""
 import pytest
 
 from long_convolution_sequence_amd import fi, ops
@@ -14,3 +13,16 @@ def test_outputs_past_a_launch(rows, N, dtype):
     a, w, y = P, P + 64 * STEP, P + 128 * STEP
     assert lib.fi_q8_product(rows, N, 64, a, w, None, dtype, y, 0, None) == fi.FI_EINVAL
     assert "2^38" in lib.fi_op_last_error().decode()
+
+
+@pytest.mark.parametrize("dtype,C", [(ops.F32, 32), (ops.BF16, 64), (ops.F16, 32)])
+def test_chunks_past_a_launch(dtype, C):
+    """The gradients run 256 threads a chunk and key head, 2^24 of which are one too many."""
+    lib = fi.load_library()
+
+    def desc(T):
+        return ops._pack(ops._DELTA_DESC, T, 1024, 1024, 1024, 1, 1, dtype, 0, 1.0, *([0] * 12))
+    for back in (0, 1):
+        assert lib.fi_delta_workspace_bytes(desc(15 * C), back) > 0
+        assert lib.fi_delta_workspace_bytes(desc(15 * C + 1), back) == 0
+    assert lib.fi_delta_saved_bytes(desc(15 * C + 1)) == 0
