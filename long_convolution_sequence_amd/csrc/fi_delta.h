@@ -71,7 +71,7 @@ struct DeltaArgs {
     // [chunk][B][H] of each
     char *images;                          // M and P of a chunk (backwards N^T and P^T)
     float *factors;                        // [kDeltaFactors][C]
-    float *states;                         // [dk][dv] before each chunk, and [B][H] of them after the last
+    float *states;                         // [dk][dv] before each chunk
     float *ends;                           // backwards [dk][dv] after each chunk
     float *w, *x;                          // [C][dv]
     // [segment][B][H]

@@ -468,8 +468,7 @@ extern "C" {
 size_t fi_delta_saved_bytes(const fi_delta_desc *desc) {
     if (delta_check(desc)) return 0;
     const DeltaPlan d = delta_plan(desc);
-    const size_t last = up256((size_t)desc->batch * desc->heads * desc->dk * desc->dv * 4);
-    return d.states + last + d.rows + d.maps + 256;
+    return d.states + d.rows + d.maps + 256;
 }
 
 size_t fi_delta_workspace_bytes(const fi_delta_desc *desc, int backward) {
@@ -516,8 +515,7 @@ fi_status fi_delta_forward(const fi_delta_desc *desc, const void *q, const void 
     a.mapst = (float *)w;
     if (saved) {
         char *s = (char *)saved;
-        const size_t last = up256((size_t)a.B * a.H * a.dk * a.dv * 4);
-        a.states = (float *)s, s += d.states + last;
+        a.states = (float *)s, s += d.states;
         a.w = (float *)s, s += d.rows;
         a.maps = (float *)s;
     }

@@ -585,7 +585,7 @@ extern "C" fi_status fi_delta_backward(const fi_delta_desc *desc, const void *q,
     a.starts = (float *)w, w += d.local;
     a.local = (float *)w;
     char *s = (char *)saved;
-    a.states = (float *)s, s += d.states + up256(sb);
+    a.states = (float *)s, s += d.states;
     a.w = (float *)s, s += d.rows;
     a.maps = (float *)s;
     if (desc->dtype == FI_F32) backward<float>(a, st);

@@ -26,3 +26,11 @@ def test_chunks_past_a_launch(dtype, C):
         assert lib.fi_delta_workspace_bytes(desc(15 * C), back) > 0
         assert lib.fi_delta_workspace_bytes(desc(15 * C + 1), back) == 0
     assert lib.fi_delta_saved_bytes(desc(15 * C + 1)) == 0
+
+
+def test_what_is_kept_for_the_gradients():
+    """A state before each chunk and a row of w a position, in whole chunks; no more where there is one segment."""
+    kept = fi.load_library().fi_delta_saved_bytes
+    for T, dtype, chunks, C in ((100, ops.BF16, 2, 64), (100, ops.F16, 4, 32), (100, ops.F32, 4, 32)):
+        d = ops._pack(ops._DELTA_DESC, T, 3, 2, 4, 16, 48, dtype, 0, 1.0, *([0] * 12))
+        assert kept(d) == chunks * 12 * (16 * 48 + C * 48) * 4 + 256
