@@ -656,6 +656,7 @@ __global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_
 // ---- host side -----------------------------------------------------------------
 
 constexpr int kDeltaWaves = 1536;      // sets of 32 columns that fill the card
+constexpr int kDeltaLeast = 4;         // chunks of a segment at least
 
 // Workgroups of a chain over `tiles` sets of 16 columns: up to eight waves each, as
 // evenly as they go, and as many at least as bring a chunk's keys with a block of four
@@ -679,18 +680,21 @@ struct DeltaPlan {
 // leaves most of the card idle, the sequence is cut into as many segments as fill it,
 // each run once from nothing (with the columns of the state's own map, dk of them, beside
 // it), joined, and run again from what is before it.  That is 2.5 times the work: with
-// four segments a call over 2048 x 4 x 24 heads of 128 takes 388 us against 431 in one
-// piece, over 4096 x 8 x 12 heads 702 against 892, but with two 2048 x 8 x 24 heads 615
-// against 539.  At least eight chunks a segment; more segments than fill the card twice
-// cost more to join (2.7 us each) than they bring (131072 x 9 heads of 96: 1024 sets of
-// columns 1.52 ms, 1536 1.43, 2048 1.50, without a chunk's own matrices).
+// four segments a call over 2048 x 4 x 24 heads of 128 takes 437 us against 571 in one
+// piece, over 4096 x 8 x 12 heads 798 against 1181, but with two 2048 x 8 x 24 heads 715
+// against 705.  More segments than fill the card cost more to join (2.7 us each) than they
+// bring (768, 1024, 1536, 2048 sets of columns: 131072 x 9 heads of 96 1627, 1777, 1650,
+// 1750 us, 32768 x 6 heads of 128 607, 569, 603, 630).  At least four chunks a segment
+// (two, four, eight, sixteen of them: 1024 x 9 heads of 96 88, 101, 160, 160 us, 4096 x 9
+// heads 178, 149, 167, 261, 2048 x 4 heads of 128 fp32 168, 141, 164, 250, training pass
+// over 1999 x 3 x 4 heads 72 x 41 fp16 345, 341, 388, 865).
 inline DeltaPlan delta_plan(const fi_delta_desc *q) {
     DeltaPlan d = {};
     d.C = delta_chunk(q->dtype);
     d.KT = (q->dk + 31) / 32;
     d.chunks = (q->T + d.C - 1) / d.C;
     const int64_t heads = (int64_t)q->batch * q->heads, waves = heads * ((q->dv + 31) / 32);
-    int64_t want = std::min<int64_t>(kDeltaWaves / std::max<int64_t>(1, waves), d.chunks / 8);
+    int64_t want = std::min<int64_t>(kDeltaWaves / std::max<int64_t>(1, waves), d.chunks / kDeltaLeast);
     if (want < 4) want = 1;
     d.per = std::max<int64_t>(1, (d.chunks + want - 1) / want);
     d.segments = (int)std::max<int64_t>(1, (d.chunks + d.per - 1) / d.per);
