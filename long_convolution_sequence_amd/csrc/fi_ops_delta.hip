@@ -367,8 +367,11 @@ __global__ void __launch_bounds__(256) k_delta_steps(DeltaArgs p) {
     }
 }
 
-// Up to as many positions run one by one (9 heads of 96, 1.8 us each: 8 of them 19 us,
-// 16 34); the chunk's two launches take 32 us at any number up to 64.
+// Up to as many positions run one by one: 1.8 us each, where the chunk's two launches take
+// 31 to 40 us at any number up to 64 (8, 14, 24 positions one by one and in a chunk: 9
+// heads of 96 19 and 32, 30 and 32, 48 and 32 us, 8 x 9 the same, 64 heads of 128 20 and
+// 40, 31 and 40, 49 and 40).  Very many or very narrow heads turn earlier: 32 x 16 heads of
+// 128 55 and 59, 83 and 60, 2 heads of 32 18 and 23, 29 and 23.
 constexpr int64_t kDeltaSteps = 14;
 
 template <typename T, int KT>
