@@ -439,7 +439,7 @@ constexpr int image_bytes() { return tri_pieces<DeltaType<T>::chunk>() * kPiece 
 // inputs themselves.
 // The inverse: a lane solves for a column of a diagonal block of 32, row by row from
 // registers, the rows of A read from LDS for all lanes of a block at once; the block
-// below them is -N22 (A21 N11).  131072 positions of 9 heads of 96 bf16 270 us (1.2 GB
+// below them is -N22 (A21 N11).  131072 positions of 9 heads of 96 bf16 268 us (1.2 GB
 // moved, 250 at a copy's rate).
 template <typename T, int KT, bool BACK, bool VEC>
 __global__ void __launch_bounds__(64, DeltaType<T>::terms == 1 ? 2 : 1) k_delta_prep(DeltaArgs p) {

@@ -29,12 +29,12 @@ constexpr bool p_late() {
 // columns behind the state's are those of the map (v = 0, from a unit column).
 // What a chunk needs is on its way while the one before it runs: k and q in registers,
 // M, P and the factors past them into LDS as soon as nobody reads the last ones.
-// 131072 positions of 9 heads of 96 bf16: FULL 550 us (55 segments of 37 chunks, two
-// workgroups a CU, 15 us a chunk), LOCAL 760.  Of a chunk's 36000 cycles a wave issues
-// 150 products (2400) and 790 others (3200); the loads account for 100 us of the 550,
-// bringing k and q into LDS for 80; the rest waits in the phases' chain of products,
-// terms and four barriers.  Wider waves (32 columns) ran no faster, nor did all of a
-// step's operands read ahead of it (653) or v and y by whole vectors (585).
+// 131072 positions of 9 heads of 96 bf16: FULL 612 us (56 segments of 37 chunks, two
+// workgroups a CU, 16 us a chunk), LOCAL 756.  Of a chunk's 36000 cycles a wave issues
+// 180 products (2900) and 790 others (3200); the loads account for 100 us, bringing k
+// and q into LDS for 80; the rest waits in the phases' chain of products, terms and four
+// barriers.  Wider waves (32 columns) ran no faster, nor did all of a step's operands
+// read ahead of it or v and y by whole vectors (653 and 585 us where it took 550).
 template <typename T, int KT, int MODE>
 __global__ void __launch_bounds__(512, 4) k_delta_chain(DeltaArgs p) {
     constexpr int C = DeltaType<T>::chunk, N = DeltaType<T>::terms;

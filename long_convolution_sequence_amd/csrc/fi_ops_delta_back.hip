@@ -517,7 +517,7 @@ void backward(const DeltaArgs &a, hipStream_t st) {
     const dim3 own((unsigned)(a.chunks * a.B * a.HK));
     const int lds = std::max((6 + N) * C / 32 * 2 * kPiece, 2 * C * (C + 4) * 4) + 2 * N * KB;
     // SHARED where heads share a key head: its sums cost a CU its second workgroup (without them
-    // 8192 x 4 x 6 heads 128 x 130 bf16 1816 -> 1558 us backwards, 4096 x 2 x 6 heads 96 x 97 fp32 548 -> 421)
+    // 8192 x 4 x 6 heads 128 x 130 bf16 1816 -> 1558 us backwards, 4096 x 2 x 6 heads 96 x 97 fp32 548 -> 439)
     const auto run = [&](auto vec, auto shared) {
         hipLaunchKernelGGL((k_delta_grads<T, KT, decltype(vec)::value, decltype(shared)::value>), own, dim3(256), lds, st, a);
     };

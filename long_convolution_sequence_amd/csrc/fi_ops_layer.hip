@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(THREADS) k_layer(LayerArgs p) {
 // sums of a team's rows in registers, its workgroup's joined in LDS (team after
 // team, so the order is fixed) and written once.  Elements that a lane does not
 // own have weights of zero, so both means pass them by.  131072 x 768 bf16 with fp32
-// rows 309 us (5.9 TB/s); 1999 x 5001 fp16 21 us and 6 for the column sums.
+// rows 308 us (5.9 TB/s); 1999 x 5001 fp16 23 us and 6 for the column sums.
 template <typename V, typename W, int CH, int NC, bool MULTI, bool TAIL, bool ALL, bool STREAM, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) k_layer_back(LayerArgs p) {
     constexpr int N = CH * NC;

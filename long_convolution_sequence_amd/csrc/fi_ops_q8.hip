@@ -90,9 +90,10 @@ __device__ __forceinline__ void values16(T (&v)[16], const T *row, int k, int K)
     }
 }
 
-// Scales and codes of rows of values (16384 x 4096 bf16 50 to 64 us, 3 to 4 TB/s): WAVES waves a row, a lane 16 neighbouring values
-// at a time; the first HELD of them stay in registers from the search for the largest
-// to the codes, what is behind is read again.
+// Scales and codes of rows of values: WAVES waves a row, a lane 16 neighbouring values at
+// a time; the first HELD of them stay in registers from the search for the largest to the
+// codes, what is behind is read again.  16384 x 4096 bf16 48 us alone, 70 in turn with the
+// product (4.2 and 2.9 TB/s).
 template <typename T, int WAVES>
 __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) k_q8_quantize(const T *x, int64_t ld, int64_t rows, int K,
                                                                            int8_t *packed, float *scales) {
@@ -166,10 +167,11 @@ __device__ __forceinline__ void wave_exchanged() {
 // Outputs [BM rows][BN columns] of a workgroup, WM x WN waves; a stage of 128 values
 // along k of both sides in LDS while the next is on its way.  Workgroup i runs on XCD
 // i % 8: each XCD takes a run of tiles in groups of eight rows of tiles, so that what
-// its workgroups read at a time meets in its L2.  16384 x 8192 x 4096 500 us, 2.2 POP/s:
-// the matrix units are busy for 57% of the cycles (at the 1.8 GHz that the card keeps up
-// under them), the rest is the barrier a stage with what it waits for; the outputs' stores
-// are 40 us.  All of a stage's operands read ahead of its products: 582 us.
+// its workgroups read at a time meets in its L2.  16384 x 8192 x 4096: 920000 cycles, for
+// 57% of which the matrix units are busy, the rest is the barrier a stage with what it
+// waits for; 450 us (2.4 POP/s) at the clock that the card comes to after forty such
+// products in a row, up to 595 before.  The outputs' stores are 40 us of it; all of a
+// stage's operands read ahead of its products took 582 us where it took 500.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM *WN * 64) k_q8_product(Q8Args p) {
     constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;      // pieces of a wave
