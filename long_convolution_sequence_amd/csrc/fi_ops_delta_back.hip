@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) k_delta_grads(DeltaArgs p
                 if ((p.dk & 3) == 0) products(kk, qk, bi, bj, std::true_type());
                 else products(kk, qk, bi, bj, std::false_type());
             }
-            float before = 0.f;                          // over the pairs i >= j > column, of this block
+            float before = 0.f;                          // of this block: rows from j on, columns before j
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int i = bi * 32 + acc_row(r);

@@ -89,3 +89,45 @@ def test_a_bad_value_reaches_its_own_head_from_its_chunk_on():
     assert torch.equal(got["y"][:, :, 0], clean["y"][:, :, 0]) and torch.equal(got["final"][:, 0], clean["final"][:, 0])
     start = 1500 // 64 * 64
     assert torch.equal(got["y"][:start], clean["y"][:start]) and got["y"][1500:, 0, 1, 3].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_left_out_states_and_slices(dtype):
+    """No state and no gradient of the last one; q, k, v, gates, outputs and gradients as columns of wider tensors,
+    in segments: as packed, and no other column changes."""
+    say(f"case delta segments left out and slices {dtype}")
+    T, HK, H, dk, dv = 36 * one.CHUNK[dtype] + 7, 1, 2, 40, 52
+    v = one._inputs(T, 1, HK, H, dk, dv, dtype, True, state=False, decay=0.03)
+    assert _segments(v) >= 4
+    c = one._cuda(v)
+    want = one._run(c, True, scale=0.3)
+    assert want["dstate"] is None
+    one._check(want, v, True, scale=0.3)
+    sizes, shapes = [HK * dk, HK * dk, H * dv], [(HK, dk), (HK, dk), (H, dv)]
+    wide = torch.full((T, 1, 3 + sum(sizes)), 7.0, dtype=dtype, device="cuda")
+    grads, gates = torch.full_like(wide, 9.0), torch.zeros(T, 1, 2 * H + 1, device="cuda")
+    cut = lambda t: [x.unflatten(-1, s) for x, s in zip(torch.split(t[..., 2:-1], sizes, -1), shapes)]   # noqa: E731
+    s = dict(c)
+    for n, view in zip(("q", "k", "v"), cut(wide)):
+        view.copy_(c[n])
+        s[n] = view
+    s["g"], s["beta"] = gates[..., :H], gates[..., H + 1:]
+    s["g"].copy_(c["g"]), s["beta"].copy_(c["beta"])
+    dq, dk_, dv_ = cut(grads)
+    got = one._run(s, True, scale=0.3, dq=dq, dk=dk_, dv=dv_)
+    assert all(torch.equal(got[k], want[k]) for k in want if want[k] is not None)
+    for t, fill in ((wide, 7), (grads, 9)):
+        assert (t[..., :2] == fill).all() and (t[..., -1] == fill).all()
+
+
+def test_gradients_after_a_state_in_place():
+    """The state overwritten by the last one: the gradients need what was kept, not the state."""
+    say("case delta segments gradients after a state in place")
+    v = one._inputs(2400, 1, 1, 1, 72, 40, BF16, True, decay=0.03)
+    c = one._cuda(v)
+    want = one._run(c, True)
+    state = c["state"].clone()
+    a = [c[n] for n in one.NAMES]
+    _, _, saved = ops.gated_delta(*a, state, unit=True, save=True, final=state)
+    d = ops.gated_delta_backward(c["dy"], *a, saved, state, dfinal=c["dfinal"], unit=True)
+    assert all(torch.equal(x, want[n]) for n, x in (("dq", d.q), ("dk", d.k), ("dg", d.decay), ("dstate", d.state)))
